@@ -37,7 +37,7 @@ def _sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs.append(os.path.join(INCLUDE, "gemm.h"))
+    hs += [os.path.join(INCLUDE, f) for f in ("gemm.h", "ffn.h")]
     return hs
 
 

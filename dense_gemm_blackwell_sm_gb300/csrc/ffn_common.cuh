@@ -1,0 +1,65 @@
+// ffn_common.cuh -- element types and activations (with derivatives) shared by
+// the feed-forward block's kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kernel_common.cuh"
+
+namespace dgb {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// The activation a = act(g) and its derivative d.  SiLU and the tanh form of
+// GeLU go through the logistic function s as in the fused GEMM epilogue:
+//   silu: a = g s(g),   d = s + a (1 - s)
+//   gelu (tanh): a = g s(v), v = 2 sqrt(2/pi) (g + c g^3),  d = s + a (1 - s) v'
+// v' is taken at g clamped to [-16, 16], where s (1 - s) is already exactly 0,
+// so that its square does not overflow; a NaN still arrives through s.
+template <int ACT>
+__device__ __forceinline__ void act_and_slope(float g, float& a, float& d) {
+  if constexpr (ACT == EPI_ACT_RELU) {
+    a = g < 0.f ? 0.f : g;  // (a NaN stays one)
+    d = g > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == EPI_ACT_SILU) {
+    const float s = logistic(g);
+    a = g * s;
+    d = fmaf(a, 1.f - s, s);
+  } else if constexpr (ACT == EPI_ACT_GELU_TANH) {
+    const float k2 = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float s = logistic(k2 * (g + 0.044715f * g * g * g));
+    const float gc = fminf(fmaxf(g, -16.f), 16.f);
+    a = g * s;
+    d = fmaf(gc * s * (1.f - s), k2 * fmaf(3.f * 0.044715f * gc, gc, 1.f), s);
+  } else if constexpr (ACT == EPI_ACT_GELU_ERF) {
+    const float p = 0.5f * (1.f + erff(g * 0.7071067811865476f));
+    a = g * p;
+    d = fmaf(g * 0.3989422804014327f, exp2f(-0.7213475204444817f * g * g), p);  // density e^(-g^2/2) / sqrt(2 pi)
+  } else {
+    a = g;
+    d = 1.f;
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_only(float g) {
+  float a, d;
+  act_and_slope<ACT>(g, a, d);
+  return a;
+}
+
+}  // namespace dgb
