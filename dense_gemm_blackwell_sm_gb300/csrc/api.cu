@@ -1021,6 +1021,12 @@ gemm_status_t run_cached(int64_t M, int64_t N, int64_t K, int64_t ldc, const voi
 
 }  // namespace
 
+bool dgb::encode_rows16(CUtensorMap* m, bool bf16, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+                        uint32_t box_inner, uint32_t box_outer) {
+  return encode_2d(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, inner, outer,
+                   box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+}
+
 extern "C" {
 
 gemm_status_t gemm_auto_variant(int64_t M, int64_t N, int64_t K, gemm_dtype_t dtype, int32_t num_sms,

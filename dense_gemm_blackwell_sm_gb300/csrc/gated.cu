@@ -1,0 +1,224 @@
+// gated.cu -- host side of the gated projections: the choice of tile, TMA maps and
+// launches of the kernels in kernels_gated.cuh and kernel_gated_slopes.cu.
+#include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "ffn_launch.h"
+#include "gated.h"
+#include "idesc.h"
+#include "launch.h"
+
+namespace dgb {
+
+namespace {
+
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int alignment_of(const void* p, int64_t ld) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2);
+  return (bits & 31u) == 0 ? 2 : (bits & 15u) == 0 ? 1 : 0;
+}
+
+// A kernel's shared-memory limit is raised once per device.
+cudaError_t allow_smem_once(const void* func, size_t bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({dev, func})) return cudaSuccess;
+  e = allow_dynamic_smem(func, bytes);
+  if (e == cudaSuccess) done.insert({dev, func});
+  return e;
+}
+
+struct Tiling {
+  int consumers, hw;
+};
+
+// Clocks of a launch whose clusters take `tiles` tiles in waves: per 64-wide block
+// of the reduction the MMAs of a tile (4 hw clocks per consumer), at least what its
+// copies and hand-offs take, and a fixed part per tile.
+double launch_clocks(int64_t tiles, int clusters, int64_t kb, int consumers, int hw) {
+  const double mma = 4.0 * consumers * hw * (consumers == 1 ? 1.12 : 1.0);
+  const double block = std::max(mma, 160.0);
+  return (double)ceil_div64(tiles, clusters) * ((double)kb * block + 2500.0 + 20.0 * hw * consumers);
+}
+
+// The tile that finishes soonest: one or two consumers (256 or 512 rows), hw = 16
+// ... 128 columns of h.  Narrow tiles even out the last wave and spread a weight
+// over more SMs when there are few rows.
+Tiling gated_tiling(int64_t M, int64_t F, int64_t kb, int clusters) {
+  Tiling best{1, 128};
+  double least = 0;
+  for (int consumers = 2; consumers >= 1; --consumers)
+    for (int hw = 128; hw >= 16; hw -= 16) {
+      const int64_t tiles = ceil_div64(M, 256 * consumers) * ceil_div64(F, hw);
+      const double t = launch_clocks(tiles, clusters, kb, consumers, hw);
+      if (least == 0 || t < least) {
+        least = t;
+        best = {consumers, hw};
+      }
+    }
+  return best;
+}
+
+constexpr int stages_of(int consumers) { return consumers == 2 ? 4 : 6; }
+
+void fill_task(GatedTask* t, int64_t rows, int64_t cols, int64_t kb, int tile_m, int tile_n, bool bf16, int mma_n,
+               uint32_t major, void* out, int64_t ld) {
+  t->rows = (int32_t)rows;
+  t->cols = (int32_t)cols;
+  t->kb = (int32_t)kb;
+  t->tiles_m = (int32_t)ceil_div64(rows, tile_m);
+  t->tiles_n = (int32_t)ceil_div64(cols, tile_n);
+  t->raster_group = std::min(8, t->tiles_m);
+  t->a_mn = (major & IDESC_A_MN_MAJOR) != 0;
+  t->idesc = idesc_f16(bf16, 256, mma_n) | major;
+  t->out = out;
+  t->ld_out = ld;
+  t->vec_out = alignment_of(out, ld);
+}
+
+cudaError_t launch_tiles(const void* func, int consumers, int64_t tiles, const FfnDevice& dev, CUtensorMap (&maps)[4],
+                         GatedParams& p, cudaStream_t st) {
+  const size_t smem = gated_smem_bytes(consumers, p.stages);
+  const cudaError_t e = allow_smem_once(func, smem);
+  if (e != cudaSuccess) return e;
+  LaunchSpec s;
+  s.func = func;
+  s.grid = dim3(2u * (unsigned)std::min<int64_t>(tiles, std::max(1, dev.num_sms / 2)), 1, 1);
+  s.block = dim3(kGatedThreads, 1, 1);
+  s.smem = smem;
+  s.cluster = 2;
+  s.pdl = true;
+  void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+  return launch_spec(s, args, st);
+}
+
+template <typename A>
+GatedParams common_params(const A& a, const FfnDevice& dev) {
+  GatedParams p{};
+  p.status = dev.status;
+  p.timeout_ns = a.timeout_ns ? (uint64_t)a.timeout_ns : 2000000000ull;
+  p.debug_flags = (uint32_t)a.debug_flags;
+  return p;
+}
+
+// x w^T for both projections, joined by the epilogue of `func_of`
+template <typename A, typename F>
+cudaError_t launch_pair(const A& a, const FfnDevice& dev, GatedParams& p, void* out, int64_t ld, F func_of,
+                        cudaStream_t st) {
+  const bool bf16 = a.dtype == FFN_BF16;
+  const int clusters = std::max(1, dev.num_sms / 2);
+  const int64_t kb = ceil_div64(a.K, 64);
+  const Tiling t = gated_tiling(a.M, a.F, kb, clusters);
+  fill_task(&p.task[0], a.M, a.F, kb, 256 * t.consumers, t.hw, bf16, 2 * t.hw, 0, out, ld);
+  p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
+  p.hw = t.hw;
+  p.stages = stages_of(t.consumers);
+  CUtensorMap maps[4];
+  if (!encode_rows16(&maps[0], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64, 128) ||
+      !encode_rows16(&maps[1], bf16, a.w, (uint64_t)a.K, (uint64_t)(2 * a.F), (uint64_t)a.ld_w, 64, (uint32_t)t.hw))
+    return cudaErrorInvalidValue;
+  maps[2] = maps[0];
+  maps[3] = maps[1];
+  return launch_tiles(func_of(bf16, t.consumers, a.activation), t.consumers, p.n0, dev, maps, p, st);
+}
+
+// dx = dgu w and dw = dgu^T x in one launch, the product with the longer reduction first
+cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st) {
+  if (!a.dx && !a.dw) return cudaSuccess;
+  const bool bf16 = a.dtype == FFN_BF16;
+  const int clusters = std::max(1, dev.num_sms / 2);
+  const int64_t kb_dx = ceil_div64(2 * a.F, 64), kb_dw = ceil_div64(a.M, 64);
+  // the tile with the least time for both products' work spread over the clusters
+  Tiling best{1, 128};
+  double least = 0;
+  for (int consumers = 2; consumers >= 1; --consumers)
+    for (int hw = 128; hw >= 64; hw -= 64) {
+      double total = 0, longest = 0;
+      auto add = [&](int64_t rows, int64_t kb) {
+        const int64_t tiles = ceil_div64(rows, 256 * consumers) * ceil_div64(a.K, 2 * hw);
+        const double one = launch_clocks(1, 1, kb, consumers, hw);
+        total += one * (double)tiles;
+        longest = std::max(longest, one);
+      };
+      if (a.dx) add(a.M, kb_dx);
+      if (a.dw) add(2 * a.F, kb_dw);
+      const double t = std::max(total / clusters, longest);
+      if (least == 0 || t < least) {
+        least = t;
+        best = {consumers, hw};
+      }
+    }
+  GatedParams p = common_params(a, dev);
+  p.hw = best.hw;
+  p.stages = stages_of(best.consumers);
+  const int tile_m = 256 * best.consumers, tile_n = 2 * best.hw;
+  const bool dx_first = a.dx && (!a.dw || kb_dx >= kb_dw);
+  CUtensorMap maps[4];
+  int n = 0;
+  bool ok = true;
+  auto add_dx = [&] {
+    fill_task(&p.task[n], a.M, a.K, kb_dx, tile_m, tile_n, bf16, tile_n, IDESC_B_MN_MAJOR, a.dx, a.ld_dx);
+    ok = ok &&
+         encode_rows16(&maps[2 * n], bf16, a.dgu, (uint64_t)(2 * a.F), (uint64_t)a.M, (uint64_t)a.ld_dgu, 64, 128) &&
+         encode_rows16(&maps[2 * n + 1], bf16, a.w, (uint64_t)a.K, (uint64_t)(2 * a.F), (uint64_t)a.ld_w, 64, 64);
+    ++n;
+  };
+  if (dx_first) add_dx();
+  if (a.dw) {
+    fill_task(&p.task[n], 2 * a.F, a.K, kb_dw, tile_m, tile_n, bf16, tile_n, IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR, a.dw,
+              a.ld_dw);
+    ok = ok &&
+         encode_rows16(&maps[2 * n], bf16, a.dgu, (uint64_t)(2 * a.F), (uint64_t)a.M, (uint64_t)a.ld_dgu, 64, 64) &&
+         encode_rows16(&maps[2 * n + 1], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64, 64);
+    ++n;
+  }
+  if (a.dx && !dx_first) add_dx();
+  if (!ok) return cudaErrorInvalidValue;
+  p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
+  if (n == 2) {
+    p.n1 = p.task[1].tiles_m * p.task[1].tiles_n;
+    p.fill = (int32_t)(launch_clocks(1, 1, p.task[0].kb, best.consumers, best.hw) /
+                           launch_clocks(1, 1, p.task[1].kb, best.consumers, best.hw) +
+                       0.5);
+  } else {
+    maps[2] = maps[0];
+    maps[3] = maps[1];
+  }
+  return launch_tiles(gated_products_kernel(bf16, best.consumers), best.consumers, (int64_t)p.n0 + p.n1, dev, maps, p,
+                      st);
+}
+
+}  // namespace
+
+cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_t st) {
+  GatedParams p = common_params(a, dev);
+  p.gu = a.gu;
+  p.ld_gu = a.ld_gu;
+  p.vec_gate = alignment_of(a.gu, a.ld_gu);
+  p.vec_up = alignment_of(static_cast<const char*>(a.gu) + 2 * a.F, a.ld_gu);
+  return launch_pair(a, dev, p, a.h, a.ld_h, gated_forward_kernel, st);
+}
+
+cudaError_t launch_gated_backward(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st) {
+  cudaError_t e;
+  if (a.gu != nullptr) {
+    e = launch_gated_slopes(a, dev.num_sms, st);
+  } else {
+    GatedParams p = common_params(a, dev);
+    p.dh = a.dh;
+    p.ld_dh = a.ld_dh;
+    p.vec_dh = alignment_of(a.dh, a.ld_dh);
+    p.vec_up = alignment_of(static_cast<const char*>(a.dgu) + 2 * a.F, a.ld_dgu);
+    e = launch_pair(a, dev, p, a.dgu, a.ld_dgu, gated_slopes_kernel, st);
+  }
+  return e != cudaSuccess ? e : launch_products(a, dev, st);
+}
+
+}  // namespace dgb

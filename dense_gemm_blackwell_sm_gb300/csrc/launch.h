@@ -38,6 +38,11 @@ cudaError_t launch_spec(const LaunchSpec& s, void** args, cudaStream_t st);
 // raise (never lower) a kernel's dynamic shared-memory limit to `bytes`
 cudaError_t allow_dynamic_smem(const void* func, size_t bytes);
 
+// TMA map of a row-major 16-bit array (`outer` rows of `inner` elements, `pitch`
+// elements apart), tiles landing with the 128-byte swizzle and zeros past its ends
+bool encode_rows16(CUtensorMap* m, bool bf16, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+                   uint32_t box_inner, uint32_t box_outer);
+
 // steps 1-3 (thread copies), 4-5 (TMA ring), 6 (persistent + scheduler)
 cudaError_t spec_step123(int M, int N, bool out_f32, LaunchSpec* out);
 cudaError_t spec_step45(int M, int N, int stages, bool out_f32, LaunchSpec* out);
