@@ -1,0 +1,120 @@
+// norm.cu -- host side of the block norms: how rows and columns are split over
+// threads, CTAs and clusters, and the workspace of the column sums.
+#include "norm.h"
+
+#include <algorithm>
+
+#include "ffn_launch.h"
+
+namespace dgb {
+
+namespace {
+
+int elem_bytes(int32_t dtype) { return dtype == FFN_F32 ? 4 : 2; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows that all start on 16-byte boundaries (absent arrays count as aligned)
+bool rows16(const void* p, int64_t ld, int bytes) { return p == nullptr || (aligned16(p) && ld * bytes % 16 == 0); }
+
+int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
+
+}  // namespace
+
+cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
+  const int b = elem_bytes(a.dtype), E = 16 / b;
+  NormShape sh{};
+  const int64_t vectors = (a.D + E - 1) / E;  // of a row
+  const int most = norm_most_vectors(b);
+  if (vectors <= 32 * 4 && a.M > 2 * (int64_t)dev.num_sms) {
+    // short rows: a warp each, no barrier
+    sh.warp_rows = true;
+    sh.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
+    sh.threads = 256;
+    sh.grid = (a.M + 7) / 8;
+  } else {
+    // a CTA per row, with as many threads as let all rows run at once (short rows),
+    // else with as many elements per thread as it can hold, which keeps several rows'
+    // loads in flight on an SM
+    sh.nv = 1;
+    while (sh.nv < most && ((vectors + sh.nv - 1) / sh.nv * a.M > (int64_t)dev.num_sms * 1024 ||
+                            vectors > 512 * (int64_t)sh.nv))
+      sh.nv *= 2;
+    sh.threads = round32((vectors + sh.nv - 1) / sh.nv);
+    sh.grid = a.M;
+  }
+  switch (a.dtype) {
+    case FFN_F16: return norm_forward_f16(a, sh, st);
+    case FFN_BF16: return norm_forward_bf16(a, sh, st);
+    default: return norm_forward_f32(a, sh, st);
+  }
+}
+
+namespace {
+
+// The split of the backward pass; it depends on the sizes alone, so that the
+// workspace can be sized without a device and sums are the same on every call.
+NormGradShape grad_shape(const ffn_norm_grad_t& a) {
+  constexpr int kResident = 304;  // CTAs of 512 threads: two on each of 152 SMs
+  NormGradShape sh{};
+  const int64_t threads = (a.D + kNormGradEach - 1) / kNormGradEach;
+  sh.cluster = (int)((threads + kNormGradThreads - 1) / kNormGradThreads);
+  sh.columns = (a.D + sh.cluster - 1) / sh.cluster;
+  sh.columns = (sh.columns + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
+  sh.threads = round32((sh.columns + kNormGradEach - 1) / kNormGradEach);
+  sh.lanes = sh.threads == 32 ? 8 : 1;
+  const bool gates = a.gate != nullptr || a.dgate != nullptr;
+  const int64_t groups = gates ? a.groups : 1;
+  int64_t parts = (int64_t)kResident * (kNormGradThreads / (sh.threads * sh.lanes)) * sh.lanes / sh.cluster;
+  parts = std::max<int64_t>(1, std::min(parts, a.M));
+  if (groups >= parts && groups > 1) {
+    sh.many = true;
+    sh.parts_per_group = 0;
+  } else {
+    sh.parts_per_group = (int)std::min(parts / groups, a.M / groups);
+    parts = sh.parts_per_group * groups;
+  }
+  sh.parts = (int)parts;
+  sh.bias = a.dpost_bias != nullptr || a.dpre_bias != nullptr || (a.dgate != nullptr && a.post_bias != nullptr);
+  return sh;
+}
+
+int sums_of(const ffn_norm_grad_t& a, const NormGradShape& sh, NormSums* ws, float* base) {
+  int n = 0;
+  const int64_t each = (int64_t)sh.parts * a.D;
+  auto next = [&](bool need, float** p) {
+    *p = nullptr;
+    if (need) *p = base ? base + each * n : nullptr, ++n;
+  };
+  const bool gates = a.dgate != nullptr && !sh.many;
+  next(a.dpost_weight != nullptr || gates, &ws->a);
+  next(a.dpost_bias != nullptr || (gates && a.post_bias != nullptr), &ws->b);
+  next(a.dpre_weight != nullptr, &ws->c);
+  next(a.dpre_bias != nullptr, &ws->e);
+  return n;
+}
+
+}  // namespace
+
+size_t norm_backward_workspace(const ffn_norm_grad_t& a) {
+  const NormGradShape sh = grad_shape(a);
+  NormSums ws{};
+  return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)a.D * 4;
+}
+
+cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice&, cudaStream_t st) {
+  ffn_norm_grad_t a = args;
+  if (a.gate == nullptr && a.dgate == nullptr) a.groups = 1;
+  NormGradShape sh = grad_shape(a);
+  const int b = elem_bytes(a.dtype);
+  sh.aligned = rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) && rows16(a.s, a.ld_s, b);
+  NormSums ws{};
+  sums_of(a, sh, &ws, static_cast<float*>(a.workspace));
+  switch (a.dtype) {
+    case FFN_F16: return norm_backward_f16(a, sh, ws, st);
+    case FFN_BF16: return norm_backward_bf16(a, sh, ws, st);
+    default: return norm_backward_f32(a, sh, ws, st);
+  }
+}
+
+}  // namespace dgb
