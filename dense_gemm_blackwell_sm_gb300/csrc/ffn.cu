@@ -1,10 +1,12 @@
 // ffn.cu -- the C ABI of the feed-forward block's operators (include/ffn.h):
 // argument validation, the per-device state, launches and status checks.
-#include <cstring>
 #include <mutex>
+#include <set>
+#include <utility>
 
 #include "ffn.h"
 #include "ffn_launch.h"
+#include "launch.h"
 
 using namespace dgb;
 
@@ -94,6 +96,24 @@ gemm_status_t norm_grad_sizes(const ffn_norm_grad_t& a) {
 }
 
 }  // namespace
+
+// A kernel's shared-memory limit is raised once per device.
+cudaError_t dgb::allow_smem_once(const void* func, size_t bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({dev, func})) return cudaSuccess;
+    e = allow_dynamic_smem(func, bytes);
+    if (e == cudaSuccess) done.insert({dev, func});
+    return e;
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
+}
 
 extern "C" {
 

@@ -15,6 +15,9 @@ struct FfnDevice {
   uint32_t* status;  // device status word of the bounded waits
 };
 
+// raise a kernel's dynamic shared-memory limit, once per device
+cudaError_t allow_smem_once(const void* func, size_t bytes);
+
 // The pitches below are resolved (never 0).
 cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_t st);
 cudaError_t launch_gated_backward(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st);

@@ -1,9 +1,6 @@
 // gated.cu -- host side of the gated projections: the choice of tile, TMA maps and
 // launches of the kernels in kernels_gated.cuh and kernel_gated_slopes.cu.
 #include <algorithm>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "ffn_launch.h"
 #include "gated.h"
@@ -19,20 +16,6 @@ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int alignment_of(const void* p, int64_t ld) {
   const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2);
   return (bits & 31u) == 0 ? 2 : (bits & 15u) == 0 ? 1 : 0;
-}
-
-// A kernel's shared-memory limit is raised once per device.
-cudaError_t allow_smem_once(const void* func, size_t bytes) {
-  static std::mutex mu;
-  static std::set<std::pair<int, const void*>> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  if (done.count({dev, func})) return cudaSuccess;
-  e = allow_dynamic_smem(func, bytes);
-  if (e == cudaSuccess) done.insert({dev, func});
-  return e;
 }
 
 struct Tiling {

@@ -251,8 +251,8 @@ struct RowSums {
 // ------------------------------------------------------------------- forward
 
 // mean (layer norm) and reciprocal deviation of a row held as v[NV][E]; elements
-// past the row's end are excluded by `at`
-template <bool LAYER, int NV, int E>
+// past the row's end are excluded by `at` (WHOLE: vectors lie wholly in or out)
+template <bool LAYER, bool WHOLE = false, int NV, int E>
 __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places (&at)[NV], int D, float eps,
                                           RowSums<1>& sum) {
   const float inv = 1.f / (float)D;
@@ -272,7 +272,7 @@ __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places 
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float c = v[j][e] - mean;
-      if (!LAYER || at[j].inside(e)) s[0] = fmaf(c, c, s[0]);
+      if (!LAYER || at[j].inside(WHOLE ? 0 : e)) s[0] = fmaf(c, c, s[0]);
     }
   sum(s);
   return make_float2(mean, rsqrtf(s[0] * inv + eps));
@@ -348,6 +348,29 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
 
 // ------------------------------------------------------------------ backward
 
+// the rows of one part
+template <bool MANY>
+__device__ __forceinline__ void norm_part_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, int part, int64_t& r0,
+                                               int64_t& r1) {
+  const int64_t per = a.M / a.groups;
+  if constexpr (MANY) {
+    r0 = a.groups * part / sh.parts * per;
+    r1 = a.groups * (part + 1) / sh.parts * per;
+  } else {
+    const int64_t g = part / sh.parts_per_group, i = part % sh.parts_per_group;
+    r0 = g * per + per * i / sh.parts_per_group;
+    r1 = g * per + per * (i + 1) / sh.parts_per_group;
+  }
+}
+
+// The arithmetic of a row's elements, in one place with every rounding spelt out, so
+// that both forms of the kernel give the same bits.
+__device__ __forceinline__ float unit_value(float v, float mean, float r) { return __fmul_rn(v - mean, r); }
+// r (a - u mean(a u) - mean(a)), added to t
+__device__ __forceinline__ float unit_slope(float t, float r, float a, float u, float mean_au, float mean_a) {
+  return fmaf(r, __fsub_rn(fmaf(-u, mean_au, a), mean_a), t);
+}
+
 // With u = unit(s), v = unit(y), a = dn * pre_weight, t = ds + r_s (a - u mean(a u)
 // [- mean a]) and b = branch_scale * gate * t * post_weight, a thread holds 8
 // columns of each of the rows its part takes, and over those rows the sums
@@ -357,10 +380,10 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
 //   dgate = branch_scale (post_weight A + post_bias B),
 //   dpost_weight = branch_scale sum over groups of gate A, dpost_bias the same of B.
 // A row takes two rounds of sums over its columns (RMS: of s^2, a s and y^2; of
-// b y), three for the layer norm (means first).  The next row's loads are issued
-// before the current row's first round.
+// b y), three for the layer norm (means first).  (This form takes rows that start
+// anywhere; kernels_norm_ring.cuh has the one for aligned rows.)
 template <typename T, typename P, bool LAYER, bool BIAS, bool MANY>
-__global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY && sizeof(T) == 2) ? 2 : 1)
+__global__ void __launch_bounds__(kNormGradThreads, (MANY || sizeof(T) == 4) ? 1 : 2)
     k_norm_grad(const ffn_norm_grad_t a, const NormGradShape sh, const NormSums ws) {
   constexpr int E = kNormGradEach;
   constexpr int K = LAYER ? 4 : 3;
@@ -375,17 +398,9 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
   at.first = (int)(rank * sh.columns) + tid * E;
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   const float inv = 1.f / (float)D;
-  // this part's rows
   const int64_t per = a.M / a.groups;
   int64_t r0, r1;
-  if constexpr (MANY) {
-    r0 = a.groups * part / sh.parts * per;
-    r1 = a.groups * (part + 1) / sh.parts * per;
-  } else {
-    const int64_t g = part / sh.parts_per_group, i = part % sh.parts_per_group;
-    r0 = g * per + per * i / sh.parts_per_group;
-    r1 = g * per + per * (i + 1) / sh.parts_per_group;
-  }
+  norm_part_rows<MANY>(a, sh, part, r0, r1);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (part >= sh.parts) return;          // (whole warps only)
@@ -402,13 +417,11 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
     if (a.y != nullptr) load(q.y, static_cast<const T*>(a.y) + r * a.ld_y, at);
     if (a.ds != nullptr) load(q.ds, static_cast<const T*>(a.ds) + r * a.ld_ds, at);
   };
-  Row next;
-  if (r0 < r1) fetch(next, r0);
   float A[E] = {}, C[E] = {}, B[BIAS ? E : 1] = {}, Eo[BIAS ? E : 1] = {};
   float GA[MANY ? E : 1] = {}, GB[(MANY && BIAS) ? E : 1] = {};
   for (int64_t r = r0; r < r1; ++r) {
-    const Row q = next;
-    if (sh.aligned && r + 1 < r1) fetch(next, r + 1);
+    Row q;
+    fetch(q, r);
     float mean_s = 0.f, mean_y = 0.f;
     float k[K];
     float w[E];
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
       for (int e = 0; e < E; ++e) {
         if (pre) {
           k[0] += element(q.s, e);
-          k[2] += element(q.dn, e) * w[e];
+          k[2] += __fmul_rn(element(q.dn, e), w[e]);
         }
         if (post) k[1] += element(q.y, e);
       }
@@ -437,7 +450,7 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
         if (pre) {
           const float c = element(q.s, e) - mean_s;
           k[0] = fmaf(c, c, k[0]);
-          k[1] = fmaf(c, element(q.dn, e) * w[e], k[1]);
+          k[1] = fmaf(c, __fmul_rn(element(q.dn, e), w[e]), k[1]);
         }
         if (post) {
           const float c = element(q.y, e) - mean_y;
@@ -452,8 +465,8 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
     for (int e = 0; e < E; ++e) {
       t[e] = a.ds != nullptr ? element(q.ds, e) : 0.f;
       if (pre) {
-        const float u = (element(q.s, e) - mean_s) * r_s, dn = element(q.dn, e);
-        t[e] += r_s * (dn * w[e] - u * mean_au - mean_a);
+        const float u = unit_value(element(q.s, e), mean_s, r_s), dn = element(q.dn, e);
+        t[e] = unit_slope(t[e], r_s, __fmul_rn(dn, w[e]), u, mean_au, mean_a);
         if (at.inside(e)) {
           C[e] = fmaf(dn, u, C[e]);
           if constexpr (BIAS) Eo[e] += dn;
@@ -470,7 +483,7 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
     if (a.y != nullptr) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        A[e] = fmaf(t[e], (element(q.y, e) - mean_y) * r_y, A[e]);
+        A[e] = fmaf(t[e], unit_value(element(q.y, e), mean_y, r_y), A[e]);
         if constexpr (BIAS) B[e] += t[e];
       }
     }
@@ -481,7 +494,7 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
     if (a.dy != nullptr) {
       float o[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = a.branch_scale * gate[e] * t[e];
+      for (int e = 0; e < E; ++e) o[e] = __fmul_rn(t[e], __fmul_rn(a.branch_scale, gate[e]));
       if (post) {
         float pw[E];
         parameters<P>(pw, a.post_weight, 1.f, at);
@@ -489,15 +502,15 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
         for (int i = 0; i < K; ++i) k[i] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          o[e] *= pw[e];
-          k[0] = fmaf(o[e], element(q.y, e) - mean_y, k[0]);
+          o[e] = __fmul_rn(o[e], pw[e]);
+          k[0] = fmaf(o[e], unit_value(element(q.y, e), mean_y, r_y), k[0]);
           if constexpr (LAYER) k[1] += o[e];
         }
         sum(k);
-        const float mean_bv = k[0] * inv * r_y, mean_b = LAYER ? k[1] * inv : 0.f;
+        const float mean_bv = k[0] * inv, mean_b = LAYER ? k[1] * inv : 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          o[e] = r_y * (o[e] - (element(q.y, e) - mean_y) * r_y * mean_bv - mean_b);
+          o[e] = unit_slope(0.f, r_y, o[e], unit_value(element(q.y, e), mean_y, r_y), mean_bv, mean_b);
       }
       store(static_cast<T*>(a.dy) + r * a.ld_dy, o, at);
     }
@@ -523,7 +536,6 @@ __global__ void __launch_bounds__(kNormGradThreads, (!LAYER && !BIAS && !MANY &&
         }
       }
     }
-    if (!sh.aligned && r + 1 < r1) fetch(next, r + 1);
   }
   // the sums of this part's rows, for k_norm_column_sums
   const int64_t row = (int64_t)part * D;
@@ -550,7 +562,8 @@ __device__ __forceinline__ float parameter(const void* p, int64_t i, float absen
 }
 
 // Adds the parts' sums, 32 columns and 32 parts' lanes per CTA, always in the same
-// order.  blockIdx.y = 0: the sums over all rows; 1 + g: the gate's group g.
+// order.  blockIdx.y = 0: the sums over all rows (and a single gate's); 1 + g: the gate
+// of group g.
 template <typename P>
 __global__ void __launch_bounds__(1024) k_norm_column_sums(const ffn_norm_grad_t a, const NormGradShape sh,
                                                            const NormSums ws) {
@@ -561,12 +574,14 @@ __global__ void __launch_bounds__(1024) k_norm_column_sums(const ffn_norm_grad_t
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float v[4] = {0.f, 0.f, 0.f, 0.f};
+  const bool weighted = g < 0 && !sh.many && a.groups > 1;  // sums over groups: each part with its gate
   if (i < D) {
     const int p0 = g < 0 ? 0 : g * sh.parts_per_group, p1 = g < 0 ? sh.parts : p0 + sh.parts_per_group;
+#pragma unroll 4
     for (int p = p0 + l; p < p1; p += 32) {
       const int64_t at = (int64_t)p * D + i;
       float f = 1.f;
-      if (g < 0 && !sh.many) f = parameter<P>(a.gate, (int64_t)(p / sh.parts_per_group) * a.ld_gate + i, 1.f);
+      if (weighted) f = parameter<P>(a.gate, (int64_t)(p / sh.parts_per_group) * a.ld_gate + i, 1.f);
       if (ws.a != nullptr) v[0] = fmaf(f, ws.a[at], v[0]);
       if (ws.b != nullptr) v[1] = fmaf(f, ws.b[at], v[1]);
       if (g < 0) {
@@ -591,87 +606,15 @@ __global__ void __launch_bounds__(1024) k_norm_column_sums(const ffn_norm_grad_t
   __syncthreads();
   if (l != 0 || i >= D) return;
   const float A = sums[0][0][c] * a.branch_scale, B = sums[1][0][c] * a.branch_scale;
-  if (g >= 0) {
-    a.dgate[(int64_t)g * D + i] = parameter<P>(a.post_weight, i, 1.f) * A +
-                                  (ws.b != nullptr ? parameter<P>(a.post_bias, i, 0.f) * B : 0.f);
-    return;
-  }
-  if (a.dpost_weight != nullptr) a.dpost_weight[i] = A;
-  if (a.dpost_bias != nullptr) a.dpost_bias[i] = B;
+  if (a.dgate != nullptr && !sh.many && (g >= 0 || a.groups == 1))
+    a.dgate[(int64_t)max(g, 0) * D + i] = parameter<P>(a.post_weight, i, 1.f) * A +
+                                          (ws.b != nullptr ? parameter<P>(a.post_bias, i, 0.f) * B : 0.f);
+  if (g >= 0) return;
+  const float f = !sh.many && a.groups == 1 ? parameter<P>(a.gate, i, 1.f) : 1.f;
+  if (a.dpost_weight != nullptr) a.dpost_weight[i] = f * A;
+  if (a.dpost_bias != nullptr) a.dpost_bias[i] = f * B;
   if (a.dpre_weight != nullptr) a.dpre_weight[i] = sums[2][0][c];
   if (a.dpre_bias != nullptr) a.dpre_bias[i] = sums[3][0][c];
-}
-
-// ------------------------------------------------------------------- launches
-
-inline cudaError_t launch_dependent(const void* f, dim3 grid, int threads, int cluster, void** args, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelExC(&cfg, f, args);
-}
-
-template <typename T, typename P, bool LAYER>
-const void* norm_kernel(const NormShape& sh) {
-  constexpr int MOST = norm_most_vectors((int)sizeof(T));
-  if (sh.warp_rows) {
-    switch (sh.nv) {
-      case 1: return (const void*)k_norm<T, P, LAYER, true, 1, 256>;
-      case 2: return (const void*)k_norm<T, P, LAYER, true, 2, 256>;
-      default: return (const void*)k_norm<T, P, LAYER, true, 4, 256>;
-    }
-  }
-  if (sh.threads > 512) return (const void*)k_norm<T, P, LAYER, false, MOST, 1024>;
-  switch (sh.nv) {
-    case 1: return (const void*)k_norm<T, P, LAYER, false, 1, 512>;
-    case 2: return (const void*)k_norm<T, P, LAYER, false, 2, 512>;
-    case 4: return (const void*)k_norm<T, P, LAYER, false, 4, 512>;
-    default: return (const void*)k_norm<T, P, LAYER, false, MOST, 512>;
-  }
-}
-
-template <typename T, typename P>
-cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& sh, cudaStream_t st) {
-  const void* k = a.kind == FFN_NORM_LAYER ? norm_kernel<T, P, true>(sh) : norm_kernel<T, P, false>(sh);
-  ffn_norm_t args_a = a;
-  void* args[] = {&args_a};
-  return launch_dependent(k, dim3((unsigned)sh.grid), sh.threads, 1, args, st);
-}
-
-template <typename T, typename P, bool LAYER, bool BIAS>
-const void* norm_grad_kernel(bool many) {
-  return many ? (const void*)k_norm_grad<T, P, LAYER, BIAS, true> : (const void*)k_norm_grad<T, P, LAYER, BIAS, false>;
-}
-
-template <typename T, typename P>
-cudaError_t norm_backward(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws, cudaStream_t st) {
-  const bool layer = a.kind == FFN_NORM_LAYER;
-  const void* k = layer ? (sh.bias ? norm_grad_kernel<T, P, true, true>(sh.many)
-                                   : norm_grad_kernel<T, P, true, false>(sh.many))
-                        : (sh.bias ? norm_grad_kernel<T, P, false, true>(sh.many)
-                                   : norm_grad_kernel<T, P, false, false>(sh.many));
-  ffn_norm_grad_t args_a = a;
-  NormGradShape args_sh = sh;
-  NormSums args_ws = ws;
-  void* args[] = {&args_a, &args_sh, &args_ws};
-  const unsigned grid = (unsigned)((sh.parts + sh.lanes - 1) / sh.lanes * sh.cluster);
-  cudaError_t e = launch_dependent(k, dim3(grid), sh.threads * sh.lanes, sh.cluster, args, st);
-  if (e != cudaSuccess) return e;
-  const bool totals = a.dpost_weight || a.dpost_bias || a.dpre_weight || a.dpre_bias;
-  const bool gates = a.dgate != nullptr && !sh.many;
-  if (!totals && !gates) return cudaSuccess;
-  const dim3 sums((unsigned)((a.D + 31) / 32), 1u + (gates ? (unsigned)a.groups : 0u));
-  return launch_dependent((const void*)k_norm_column_sums<P>, sums, 1024, 1, args, st);
 }
 
 }  // namespace

@@ -1,0 +1,11 @@
+// kernels_norm_forward_bf16.cu -- instances of the block norms' forward kernels for bf16 rows.
+#include "kernels_norm_launch.cuh"
+
+namespace dgb {
+
+cudaError_t norm_forward_bf16(const ffn_norm_t& a, const NormShape& sh,
+                         const FfnDevice& dev, cudaStream_t st) {
+  return a.param_dtype == FFN_F32 ? norm_forward<__nv_bfloat16, float>(a, sh, dev, st) : norm_forward<__nv_bfloat16, __nv_bfloat16>(a, sh, dev, st);
+}
+
+}  // namespace dgb

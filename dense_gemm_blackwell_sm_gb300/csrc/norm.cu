@@ -24,6 +24,7 @@ int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
 cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int b = elem_bytes(a.dtype), E = 16 / b;
   NormShape sh{};
+  const int pb = elem_bytes(a.param_dtype);
   const int64_t vectors = (a.D + E - 1) / E;  // of a row
   const int most = norm_most_vectors(b);
   if (vectors <= 32 * 4 && a.M > 2 * (int64_t)dev.num_sms) {
@@ -43,10 +44,29 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
     sh.threads = round32((vectors + sh.nv - 1) / sh.nv);
     sh.grid = a.M;
   }
+  // the ring, where rows allow 16-byte copies and every group has a few of them
+  if (a.D % E == 0 && rows16(a.y, a.ld_y, b) && rows16(a.residual, a.ld_residual, b) && rows16(a.s, a.ld_s, b) &&
+      rows16(a.n, a.ld_n, b) && rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.post_bias) &&
+      aligned16(a.pre_weight) && aligned16(a.pre_bias)) {
+    NormShape ring = sh;
+    ring.ring = true;
+    ring.warp_rows = vectors <= 32 * 4;
+    ring.nv = ring.warp_rows ? (vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4)
+                             : (vectors <= 256 ? 1 : vectors <= 1024 ? 2 : 4);
+    ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
+    const int groups = ring.warp_rows ? 8 : 1;
+    ring.smem = (size_t)groups * kNormStages * (a.residual ? 2 : 1) * (size_t)(a.D * b);
+    if (ring.threads <= 512 && ring.smem <= kNormRingBytes) {
+      const int64_t per_sm =
+          std::max<int64_t>(1, std::min<int64_t>((int64_t)(220 * 1024) / ((int64_t)ring.smem + 2048), 1024 / ring.threads));
+      ring.grid = std::min<int64_t>(per_sm * dev.num_sms, (a.M + groups - 1) / groups);
+      if (a.M >= 2 * ring.grid * groups) sh = ring;
+    }
+  }
   switch (a.dtype) {
-    case FFN_F16: return norm_forward_f16(a, sh, st);
-    case FFN_BF16: return norm_forward_bf16(a, sh, st);
-    default: return norm_forward_f32(a, sh, st);
+    case FFN_F16: return norm_forward_f16(a, sh, dev, st);
+    case FFN_BF16: return norm_forward_bf16(a, sh, dev, st);
+    default: return norm_forward_f32(a, sh, dev, st);
   }
 }
 
@@ -102,18 +122,26 @@ size_t norm_backward_workspace(const ffn_norm_grad_t& a) {
   return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)a.D * 4;
 }
 
-cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice&, cudaStream_t st) {
+cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& dev, cudaStream_t st) {
   ffn_norm_grad_t a = args;
   if (a.gate == nullptr && a.dgate == nullptr) a.groups = 1;
   NormGradShape sh = grad_shape(a);
-  const int b = elem_bytes(a.dtype);
-  sh.aligned = rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) && rows16(a.s, a.ld_s, b);
+  const int b = elem_bytes(a.dtype), pb = elem_bytes(a.param_dtype);
+  const int arrays = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
+  const size_t smem = (size_t)sh.lanes * kNormStages * arrays * (size_t)(sh.columns * b);
+  if (a.D % kNormGradEach == 0 && rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) &&
+      rows16(a.s, a.ld_s, b) && rows16(a.dresidual, a.ld_dresidual, b) && rows16(a.dy, a.ld_dy, b) &&
+      rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.post_bias) && aligned16(a.pre_weight) &&
+      smem <= kNormRingBytes) {
+    sh.ring = true;
+    sh.smem = smem;
+  }
   NormSums ws{};
   sums_of(a, sh, &ws, static_cast<float*>(a.workspace));
   switch (a.dtype) {
-    case FFN_F16: return norm_backward_f16(a, sh, ws, st);
-    case FFN_BF16: return norm_backward_bf16(a, sh, ws, st);
-    default: return norm_backward_f32(a, sh, ws, st);
+    case FFN_F16: return norm_backward_f16(a, sh, ws, dev, st);
+    case FFN_BF16: return norm_backward_bf16(a, sh, ws, dev, st);
+    default: return norm_backward_f32(a, sh, ws, dev, st);
   }
 }
 

@@ -6,15 +6,18 @@
 #include <cuda_runtime.h>
 
 #include "ffn.h"
+#include "ffn_launch.h"
 
 namespace dgb {
 
 // Forward: one row per warp (warp_rows) or per CTA, nv 16-byte vectors per thread.
 struct NormShape {
+  bool ring;       // rows through the shared-memory ring (kernels_norm_ring.cuh)
   bool warp_rows;
   int nv;
   int threads;     // per CTA
   int64_t grid;
+  size_t smem;
 };
 
 // 16-byte vectors a thread can hold of a row: 32 elements
@@ -23,7 +26,8 @@ constexpr int norm_most_vectors(int element_bytes) { return 2 * element_bytes; }
 // Backward: a part (a CTA, a cluster of CTAs sharing the columns, or a warp) takes a
 // run of rows that lies in one of the gate's groups, or several whole groups.
 struct NormGradShape {
-  bool aligned;            // rows start on 16-byte boundaries: the next row's loads are issued ahead
+  bool ring;
+  size_t smem;
   int cluster;             // CTAs that share a row's columns
   int threads;             // per row and CTA
   int lanes;               // rows a CTA takes at once (warps; 1 above 256 columns)
@@ -42,14 +46,19 @@ struct NormSums {
   float* e;  // sums of dn
 };
 
-cudaError_t norm_forward_f16(const ffn_norm_t& a, const NormShape& sh, cudaStream_t st);
-cudaError_t norm_forward_bf16(const ffn_norm_t& a, const NormShape& sh, cudaStream_t st);
-cudaError_t norm_forward_f32(const ffn_norm_t& a, const NormShape& sh, cudaStream_t st);
-cudaError_t norm_backward_f16(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws, cudaStream_t st);
-cudaError_t norm_backward_bf16(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws, cudaStream_t st);
-cudaError_t norm_backward_f32(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws, cudaStream_t st);
+cudaError_t norm_forward_f16(const ffn_norm_t& a, const NormShape& sh, const FfnDevice& dev, cudaStream_t st);
+cudaError_t norm_forward_bf16(const ffn_norm_t& a, const NormShape& sh, const FfnDevice& dev, cudaStream_t st);
+cudaError_t norm_forward_f32(const ffn_norm_t& a, const NormShape& sh, const FfnDevice& dev, cudaStream_t st);
+cudaError_t norm_backward_f16(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
+                              const FfnDevice& dev, cudaStream_t st);
+cudaError_t norm_backward_bf16(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
+                               const FfnDevice& dev, cudaStream_t st);
+cudaError_t norm_backward_f32(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
+                              const FfnDevice& dev, cudaStream_t st);
 
 constexpr int kNormGradThreads = 512;  // most per CTA, 8 columns each
 constexpr int kNormGradEach = 8;
+constexpr int kNormStages = 3;                     // rows of a ring
+constexpr size_t kNormRingBytes = 200 * 1024;      // most of one CTA
 
 }  // namespace dgb
