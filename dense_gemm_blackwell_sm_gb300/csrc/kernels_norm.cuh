@@ -2,10 +2,7 @@
 // the residual stream, one pass over the rows, and their gradients, one pass too.
 //
 // Bound by memory: 4 row reads and writes forward (y, residual, s, n), 6 backward
-// (ds, dn, y, s, dresidual, dy).  A row stays in registers from its load to its
-// stores, all loads of a row are issued before the first sum over it, and sums use
-// the values in registers (the variance is taken around the mean, not from the
-// sum of squares).
+// (ds, dn, y, s, dresidual, dy).  Every row is read once and written once.
 #pragma once
 
 #include <type_traits>
@@ -125,24 +122,31 @@ __device__ __forceinline__ void store_one(T* p, uint32_t word, int odd) {
   }
 }
 
+template <typename T, int E>
+__device__ __forceinline__ Pack<T, E> packed(const float (&f)[E]) {
+  Pack<T, E> p;
+#pragma unroll
+  for (int i = 0; i < Pack<T, E>::W; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      p.w[i] = __float_as_uint(f[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      p.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      p.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return p;
+}
+
 // The same way out: aligned chunks hold the end of a lane's group and the start of
 // the next lane's; the warp's first and last pieces are stored by element.
 template <typename T, int E>
 __device__ __forceinline__ void store(T* row, const float (&f)[E], const Places& at) {
   constexpr int N = 16 / (int)sizeof(T), W = Pack<T, E>::W, PER = 4 / (int)sizeof(T);
-  uint32_t w[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      w[i] = __float_as_uint(f[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
+  const Pack<T, E> pw = packed<T>(f);
+  const uint32_t(&w)[W] = pw.w;
   const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
   if (m == 0) {
 #pragma unroll
@@ -201,91 +205,164 @@ __device__ __forceinline__ void parameters(float (&v)[E], const void* p, float a
   for (int e = 0; e < E; ++e) v[e] = element(raw, e);
 }
 
-// Sums of K values over the threads of a row: one warp; a CTA's warps; or, in a
-// cluster, the warps of all its CTAs.  Every thread gets the same values.  The
-// buffers alternate, so one barrier per sum suffices: a buffer is written again
-// only after the barrier of the sum in between.
-template <int K>
-struct RowSums {
-  float* parts;  // [2][128][K] in shared memory
-  int warps;     // per row and CTA; 1 and cluster 1: the warp alone
-  int cluster, rank, turn;
+// Sums of N values (1, 2 or 4) over a warp, in every lane.  The values are added by
+// halves: each exchange step adds one half of the values in one half of the lanes,
+// so four values take 6 shuffles instead of 20; N more bring them to every lane.
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "values per sum");
+  const uint32_t lane = lane_idx();
+  constexpr int SPAN = 32 / N;  // lanes that share a value
+  float x;
+  if constexpr (N == 4) {
+    const bool hi = (lane & 16u) != 0, odd = (lane & 8u) != 0;
+    float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+    k0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
+    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    x = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
+  } else if constexpr (N == 2) {
+    const bool hi = (lane & 16u) != 0;
+    x = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[1], 16);
+  } else {
+    x = v[0];
+  }
+#pragma unroll
+  for (int o = SPAN / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xffffffffu, x, k * SPAN);
+}
 
-  __device__ __forceinline__ void operator()(float (&v)[K]) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (warps == 1 && cluster == 1) return;
-    float* buf = parts + turn * 128 * K;
+// What the warps of a row tell one another: one warp; a CTA's warps; or, in a
+// cluster, the warps of all its CTAs.  The buffers alternate, so one barrier per
+// exchange suffices: a buffer is written again only after the barrier of the
+// exchange in between.
+struct RowSums {
+  float* parts;  // [2][kFloats] in shared memory
+  int warps;     // per row and CTA
+  int cluster, rank, turn;
+  static constexpr int kFloats = 64 * 8;
+
+  __device__ __forceinline__ bool alone() const { return warps * cluster == 1; }
+
+  // every warp's N values (the same in all its lanes), at [warp * N + k] of the answer
+  template <int N>
+  __device__ __forceinline__ const float* exchange(const float (&v)[N]) {
+    float* buf = parts + turn * kFloats;
     turn ^= 1;
-    const int lane = (int)lane_idx(), warp = (int)(threadIdx.x >> 5);
+    const uint32_t warp = threadIdx.x >> 5, lane = lane_idx();
     if (cluster == 1) {
       if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) buf[warp * K + k] = v[k];
+        for (int k = 0; k < N; ++k) buf[warp * N + k] = v[k];
       }
       __syncthreads();
     } else {
-      if (lane < cluster) {
-        const uint32_t there = mapa_shared(smem_u32(buf + (rank * warps + warp) * K), (uint32_t)lane);
+      if (lane < (uint32_t)cluster) {
+        const uint32_t to = mapa_shared(smem_u32(buf + (rank * warps + warp) * N), lane);
 #pragma unroll
-        for (int k = 0; k < K; ++k) st_cluster_u32(there + 4u * k, __float_as_uint(v[k]));
+        for (int k = 0; k < N; ++k) st_cluster_u32(to + 4u * k, __float_as_uint(v[k]));
       }
       cluster_sync_all();
     }
-    const int n = warps * cluster;
+    return buf;
+  }
+
+  // sums over all the row's threads, in every thread
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    warp_sums(v);
+    if (alone()) return;
+    const float* buf = exchange(v);
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.f;
-    for (int i = lane; i < n; i += 32) {
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    for (int w = (int)lane_idx(); w < warps * cluster; w += 32) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += buf[i * K + k];
+      for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    warp_sums(v);
   }
 };
 
 // ------------------------------------------------------------------- forward
 
-// mean (layer norm) and reciprocal deviation of a row held as v[NV][E]; elements
-// past the row's end are excluded by `at` (WHOLE: vectors lie wholly in or out)
+// the gate of row r, or null
+template <typename P>
+__device__ __forceinline__ const P* gate_row(const void* gate, int64_t ld, int64_t M, int64_t groups, int64_t r) {
+  if (gate == nullptr || groups == 1) return static_cast<const P*>(gate);
+  return static_cast<const P*>(gate) + (int64_t)((uint32_t)r / ((uint32_t)M / (uint32_t)groups)) * ld;
+}
+
+// Mean (layer norm) and reciprocal deviation of a row held as v[NV][E]; elements past
+// the row's end are 0.  The layer norm's variance is taken around the warp's own
+// mean, and the warps' means and variances are then joined exactly,
+//   sum (v - mean)^2 = sum over warps of (its own sum + n_w (mean_w - mean)^2),
+// so one exchange serves both and nothing cancels.  n_w: the warp's elements.
+// WHOLE: vectors lie wholly in or out of the row.
 template <bool LAYER, bool WHOLE = false, int NV, int E>
-__device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places (&at)[NV], int D, float eps,
-                                          RowSums<1>& sum) {
+__device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places (&at)[NV], int D, float n_w, float eps,
+                                          RowSums& sum) {
   const float inv = 1.f / (float)D;
-  float mean = 0.f, s[1];
-  if constexpr (LAYER) {
+  float s[1] = {0.f};
+  if constexpr (!LAYER) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
+    sum(s);
+    return make_float2(0.f, rsqrtf(s[0] * inv + eps));
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] += v[j][e];
+    warp_sums(s);
+    float mean = n_w > 0.f ? s[0] / n_w : 0.f;
     s[0] = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0] += v[j][e];  // elements past the end are 0
-    sum(s);
-    mean = s[0] * inv;
-  }
-  s[0] = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float c = v[j][e] - mean;
-      if (!LAYER || at[j].inside(WHOLE ? 0 : e)) s[0] = fmaf(c, c, s[0]);
+      for (int e = 0; e < E; ++e) {
+        const float c = at[j].inside(WHOLE ? 0 : e) ? v[j][e] - mean : 0.f;
+        s[0] = fmaf(c, c, s[0]);
+      }
+    warp_sums(s);
+    if (!sum.alone()) {
+      const float mine[3] = {n_w, mean, s[0]};
+      const float* all = sum.exchange(mine);
+      float total[1] = {0.f};
+      const int l = (int)lane_idx(), n = sum.warps * sum.cluster;
+      for (int w = l; w < n; w += 32) total[0] = fmaf(all[3 * w], all[3 * w + 1], total[0]);
+      warp_sums(total);
+      mean = total[0] * inv;
+      s[0] = 0.f;
+      for (int w = l; w < n; w += 32) {
+        const float c = all[3 * w + 1] - mean;
+        s[0] += fmaf(all[3 * w] * c, c, all[3 * w + 2]);
+      }
+      warp_sums(s);
     }
-  sum(s);
-  return make_float2(mean, rsqrtf(s[0] * inv + eps));
+    return make_float2(mean, rsqrtf(s[0] * inv + eps));
+  }
+}
+
+// the elements a warp holds of a row
+template <int NV, int E>
+__device__ __forceinline__ float warp_elements(const Places (&at)[NV]) {
+  float n[1] = {0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) n[0] += (float)min(max(at[j].end - at[j].first, 0), E);
+  warp_sums(n);
+  return n[0];
 }
 
 template <typename T, typename P, bool LAYER, bool WARP, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
+__global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_norm_t a) {
   constexpr int E = 16 / (int)sizeof(T);
-  __shared__ float parts[2 * 128];
+  __shared__ float parts[2 * RowSums::kFloats];
   const int tid = WARP ? (int)lane_idx() : (int)threadIdx.x, per_row = WARP ? 32 : (int)blockDim.x;
   const int64_t r = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const int D = (int)a.D;
-  RowSums<1> sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
+  RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
   Places at[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -295,6 +372,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= a.M) return;  // (whole warps only: with a CTA per row every r is a row)
+  const float n_w = LAYER ? warp_elements<NV, E>(at) : 0.f;
   Pack<T, E> y[NV], res[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) load(y[j], static_cast<const T*>(a.y) + r * a.ld_y, at[j]);
@@ -308,7 +386,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[j][e] = element(y[j], e);
   if (a.flags & FFN_NORM_POST) {
-    const float2 st = unit_of<LAYER>(v, at, D, a.eps, sum);
+    const float2 st = unit_of<LAYER>(v, at, D, n_w, a.eps, sum);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[E], b[E];
@@ -318,8 +396,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
       for (int e = 0; e < E; ++e) v[j][e] = fmaf((v[j][e] - st.x) * st.y, w[e], b[e]);
     }
   }
-  const P* gate =
-      a.gate != nullptr ? static_cast<const P*>(a.gate) + (r / (a.M / a.groups)) * a.ld_gate : nullptr;
+  const P* gate = gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     float g[E];
@@ -333,7 +410,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
     if (a.s != nullptr) store(static_cast<T*>(a.s) + r * a.ld_s, v[j], at[j]);
   }
   if (a.flags & FFN_NORM_PRE) {
-    const float2 st = unit_of<LAYER>(v, at, D, a.eps, sum);
+    const float2 st = unit_of<LAYER>(v, at, D, n_w, a.eps, sum);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float w[E], b[E];
@@ -348,23 +425,7 @@ __global__ void __launch_bounds__(THREADS) k_norm(const ffn_norm_t a) {
 
 // ------------------------------------------------------------------ backward
 
-// the rows of one part
-template <bool MANY>
-__device__ __forceinline__ void norm_part_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, int part, int64_t& r0,
-                                               int64_t& r1) {
-  const int64_t per = a.M / a.groups;
-  if constexpr (MANY) {
-    r0 = a.groups * part / sh.parts * per;
-    r1 = a.groups * (part + 1) / sh.parts * per;
-  } else {
-    const int64_t g = part / sh.parts_per_group, i = part % sh.parts_per_group;
-    r0 = g * per + per * i / sh.parts_per_group;
-    r1 = g * per + per * (i + 1) / sh.parts_per_group;
-  }
-}
-
-// The arithmetic of a row's elements, in one place with every rounding spelt out, so
-// that both forms of the kernel give the same bits.
+// The arithmetic of a row's elements.
 __device__ __forceinline__ float unit_value(float v, float mean, float r) { return __fmul_rn(v - mean, r); }
 // r (a - u mean(a u) - mean(a)), added to t
 __device__ __forceinline__ float unit_slope(float t, float r, float a, float u, float mean_au, float mean_a) {
@@ -372,189 +433,285 @@ __device__ __forceinline__ float unit_slope(float t, float r, float a, float u, 
 }
 
 // With u = unit(s), v = unit(y), a = dn * pre_weight, t = ds + r_s (a - u mean(a u)
-// [- mean a]) and b = branch_scale * gate * t * post_weight, a thread holds 8
-// columns of each of the rows its part takes, and over those rows the sums
+// [- mean a]) and b = branch_scale * gate * t * post_weight, a thread holds 16
+// columns (two groups of 8) of each of the rows its part takes, and over those rows
+// the sums
 //   A = sum t v,  B = sum t,  C = sum dn u,  Eo = sum dn,
 // from which every parameter's gradient follows, since gate and post_weight are
 // constant over a group's rows:
 //   dgate = branch_scale (post_weight A + post_bias B),
 //   dpost_weight = branch_scale sum over groups of gate A, dpost_bias the same of B.
 // A row takes two rounds of sums over its columns (RMS: of s^2, a s and y^2; of
-// b y), three for the layer norm (means first).  (This form takes rows that start
-// anywhere; kernels_norm_ring.cuh has the one for aligned rows.)
-template <typename T, typename P, bool LAYER, bool BIAS, bool MANY>
-__global__ void __launch_bounds__(kNormGradThreads, (MANY || sizeof(T) == 4) ? 1 : 2)
-    k_norm_grad(const ffn_norm_grad_t a, const NormGradShape sh, const NormSums ws) {
-  constexpr int E = kNormGradEach;
-  constexpr int K = LAYER ? 4 : 3;
-  __shared__ float parts_smem[2 * 128 * K];
-  const int D = (int)a.D;
-  const int rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const int tid = sh.lanes > 1 ? (int)lane_idx() : (int)threadIdx.x;
-  const int part = sh.lanes > 1 ? (int)blockIdx.x * sh.lanes + (int)(threadIdx.x >> 5) : (int)blockIdx.x / sh.cluster;
-  RowSums<K> sum{parts_smem, sh.threads / 32, sh.cluster, rank, 0};
-  Places at;
-  at.end = min(D, (int)((rank + 1) * sh.columns));
-  at.first = (int)(rank * sh.columns) + tid * E;
+// b v).
+//
+// Rows come through RowsIn, a ring in shared memory (kernels_norm_ring.cuh).
+template <bool LAYER, bool BIAS, bool MANY, typename T, typename P, typename RowsIn>
+__device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
+                                               RowsIn& rows, RowSums& sum, int part, const Places (&at)[2]) {
+  constexpr int E = 8, G = 2;
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
-  const float inv = 1.f / (float)D;
+  const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
   const int64_t per = a.M / a.groups;
-  int64_t r0, r1;
-  norm_part_rows<MANY>(a, sh, part, r0, r1);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (part >= sh.parts) return;          // (whole warps only)
-  if (sh.cluster > 1) cluster_sync_all();  // the cluster's CTAs have started: their shared memory may be written
-
-  struct Row {
-    Pack<T, E> ds, dn, y, s;
-  };
-  auto fetch = [&](Row& q, int64_t r) {
-    if (pre) {
-      load(q.s, static_cast<const T*>(a.s) + r * a.ld_s, at);
-      load(q.dn, static_cast<const T*>(a.dn) + r * a.ld_dn, at);
-    }
-    if (a.y != nullptr) load(q.y, static_cast<const T*>(a.y) + r * a.ld_y, at);
-    if (a.ds != nullptr) load(q.ds, static_cast<const T*>(a.ds) + r * a.ld_ds, at);
-  };
-  float A[E] = {}, C[E] = {}, B[BIAS ? E : 1] = {}, Eo[BIAS ? E : 1] = {};
-  float GA[MANY ? E : 1] = {}, GB[(MANY && BIAS) ? E : 1] = {};
+  int64_t r0, r1, g;
+  if constexpr (MANY) {
+    g = a.groups * part / sh.parts;
+    r0 = g * per;
+    r1 = a.groups * (part + 1) / sh.parts * per;
+  } else {
+    g = part / sh.parts_per_group;
+    const int64_t i = part % sh.parts_per_group;
+    r0 = g * per + per * i / sh.parts_per_group;
+    r1 = g * per + per * (i + 1) / sh.parts_per_group;
+  }
+  int64_t group_end = (g + 1) * per;
+  float A[G][E] = {}, C[G][E] = {}, B[G][BIAS ? E : 1] = {}, Eo[G][BIAS ? E : 1] = {};
+  float GA[G][MANY ? E : 1] = {}, GB[G][(MANY && BIAS) ? E : 1] = {};
+  rows.set_group(g);
+  rows.begin(r0, r1);
   for (int64_t r = r0; r < r1; ++r) {
-    Row q;
-    fetch(q, r);
-    float mean_s = 0.f, mean_y = 0.f;
-    float k[K];
-    float w[E];
-    parameters<P>(w, a.pre_weight, 1.f, at);
+    if (!rows.next(r)) break;
+    float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[4];
     if constexpr (LAYER) {
+      k[0] = k[1] = k[2] = k[3] = 0.f;
 #pragma unroll
-      for (int i = 0; i < K; ++i) k[i] = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
+      for (int j = 0; j < G; ++j) {
         if (pre) {
-          k[0] += element(q.s, e);
-          k[2] += __fmul_rn(element(q.dn, e), w[e]);
-        }
-        if (post) k[1] += element(q.y, e);
-      }
-      sum(k);
-      mean_s = k[0] * inv;
-      mean_y = k[1] * inv;
-    }
-    const float mean_a = LAYER ? k[LAYER ? 2 : 0] * inv : 0.f;
+          float s[E], dn[E];
+          rows.s(s, j);
+          rows.dn(dn, j);
+          rows.scale_pre(dn, j);
 #pragma unroll
-    for (int i = 0; i < K; ++i) k[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (!LAYER || at.inside(e)) {
-        if (pre) {
-          const float c = element(q.s, e) - mean_s;
-          k[0] = fmaf(c, c, k[0]);
-          k[1] = fmaf(c, __fmul_rn(element(q.dn, e), w[e]), k[1]);
+          for (int e = 0; e < E; ++e) {
+            k[0] += s[e];
+            k[2] += dn[e];
+          }
         }
         if (post) {
-          const float c = element(q.y, e) - mean_y;
+          float y[E];
+          rows.y(y, j);
+#pragma unroll
+          for (int e = 0; e < E; ++e) k[1] += y[e];
+        }
+      }
+      warp_sums(k);
+      mean_s = n_w > 0.f ? k[0] / n_w : 0.f;  // the warp's own for now
+      mean_y = n_w > 0.f ? k[1] / n_w : 0.f;
+      mean_a = k[2];
+    }
+    k[0] = k[1] = k[2] = k[3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+      if (pre) {
+        float s[E], dn[E];
+        rows.s(s, j);
+        rows.dn(dn, j);
+        rows.scale_pre(dn, j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float c = !LAYER || at[j].inside(RowsIn::kWhole ? 0 : e) ? s[e] - mean_s : 0.f;
+          k[0] = fmaf(c, c, k[0]);
+          k[1] = fmaf(c, dn[e], k[1]);
+        }
+      }
+      if (post) {
+        float y[E];
+        rows.y(y, j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float c = !LAYER || at[j].inside(RowsIn::kWhole ? 0 : e) ? y[e] - mean_y : 0.f;
           k[2] = fmaf(c, c, k[2]);
         }
       }
-    sum(k);
+    }
+    if constexpr (!LAYER) {
+      sum(k);
+    } else {
+      // the warps' means, squares and products around them, joined exactly (unit_of)
+      warp_sums(k);
+      if (!sum.alone()) {
+        const float mine[7] = {n_w, mean_s, mean_y, mean_a, k[0], k[1], k[2]};
+        const float* all = sum.exchange(mine);
+        const int l = (int)lane_idx(), n = sum.warps * sum.cluster;
+        k[0] = k[1] = k[2] = k[3] = 0.f;
+        for (int w = l; w < n; w += 32) {
+          const float* q = all + 7 * w;
+          k[0] = fmaf(q[0], q[1], k[0]);
+          k[1] = fmaf(q[0], q[2], k[1]);
+          k[2] += q[3];
+        }
+        warp_sums(k);
+        mean_s = k[0] * inv;
+        mean_y = k[1] * inv;
+        mean_a = k[2];
+        k[0] = k[1] = k[2] = 0.f;
+        for (int w = l; w < n; w += 32) {
+          const float* q = all + 7 * w;
+          const float cs = q[1] - mean_s, cy = q[2] - mean_y;
+          k[0] += fmaf(q[0] * cs, cs, q[4]);
+          k[1] += fmaf(q[3], cs, q[5]);
+          k[2] += fmaf(q[0] * cy, cy, q[6]);
+        }
+        warp_sums(k);
+      }
+      mean_a *= inv;
+    }
+    rows.met();
     const float r_s = rsqrtf(k[0] * inv + a.eps), mean_au = k[1] * inv * r_s;
     const float r_y = post ? rsqrtf(k[2] * inv + a.eps) : 1.f;
-    float t[E];
+    float t[G][E];
+    float two[2] = {0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      t[e] = a.ds != nullptr ? element(q.ds, e) : 0.f;
+    for (int j = 0; j < G; ++j) {
+      if (a.ds != nullptr) {
+        rows.ds(t[j], j);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[j][e] = 0.f;
+      }
       if (pre) {
-        const float u = unit_value(element(q.s, e), mean_s, r_s), dn = element(q.dn, e);
-        t[e] = unit_slope(t[e], r_s, __fmul_rn(dn, w[e]), u, mean_au, mean_a);
-        if (at.inside(e)) {
-          C[e] = fmaf(dn, u, C[e]);
-          if constexpr (BIAS) Eo[e] += dn;
-        }
-      }
-      if (!at.inside(e)) t[e] = 0.f;
-    }
-    if (a.dresidual != nullptr) {
-      float o[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[e];
-      store(static_cast<T*>(a.dresidual) + r * a.ld_dresidual, o, at);
-    }
-    if (a.y != nullptr) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        A[e] = fmaf(t[e], unit_value(element(q.y, e), mean_y, r_y), A[e]);
-        if constexpr (BIAS) B[e] += t[e];
-      }
-    }
-    const int64_t g = r / per;
-    float gate[E];
-    if (a.dy != nullptr || MANY)
-      parameters<P>(gate, a.gate != nullptr ? static_cast<const P*>(a.gate) + g * a.ld_gate : nullptr, 1.f, at);
-    if (a.dy != nullptr) {
-      float o[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = __fmul_rn(t[e], __fmul_rn(a.branch_scale, gate[e]));
-      if (post) {
-        float pw[E];
-        parameters<P>(pw, a.post_weight, 1.f, at);
-#pragma unroll
-        for (int i = 0; i < K; ++i) k[i] = 0.f;
+        float s[E], dn[E];
+        rows.s(s, j);
+        rows.dn(dn, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          o[e] = __fmul_rn(o[e], pw[e]);
-          k[0] = fmaf(o[e], unit_value(element(q.y, e), mean_y, r_y), k[0]);
-          if constexpr (LAYER) k[1] += o[e];
+          s[e] = unit_value(s[e], mean_s, r_s);
+          C[j][e] = fmaf(dn[e], s[e], C[j][e]);
+          if constexpr (BIAS) Eo[j][e] += dn[e];
         }
-        sum(k);
-        const float mean_bv = k[0] * inv, mean_b = LAYER ? k[1] * inv : 0.f;
+        rows.scale_pre(dn, j);
+#pragma unroll
+        for (int e = 0; e < E; ++e) t[j][e] = unit_slope(t[j][e], r_s, dn[e], s[e], mean_au, mean_a);
+      }
+      if (LAYER) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          o[e] = unit_slope(0.f, r_y, o[e], unit_value(element(q.y, e), mean_y, r_y), mean_bv, mean_b);
+          if (!at[j].inside(RowsIn::kWhole ? 0 : e)) t[j][e] = 0.f;  // (0 - mean)
       }
-      store(static_cast<T*>(a.dy) + r * a.ld_dy, o, at);
-    }
-    if constexpr (MANY) {
-      if (r + 1 == (g + 1) * per) {  // the group's last row: its gate's gradient is complete
-        if (a.dgate != nullptr) {
-          float pw[E], pb[E], o[E];
-          parameters<P>(pw, a.post_weight, 1.f, at);
-          parameters<P>(pb, a.post_bias, 0.f, at);
+      if (a.dresidual != nullptr) {
+        float o[E];
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            o[e] = a.branch_scale * (pw[e] * A[e] + (BIAS ? pb[e] * B[BIAS ? e : 0] : 0.f));
-          store(a.dgate + g * (int64_t)D, o, at);
-        }
+        for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[j][e];
+        rows.put(static_cast<T*>(a.dresidual) + r * a.ld_dresidual, o, at[j]);
+      }
+      float y[E];
+      if (a.y != nullptr) {
+        rows.y(y, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          GA[e] = fmaf(gate[e], A[e], GA[e]);
-          A[e] = 0.f;
-          if constexpr (BIAS) {
-            GB[BIAS ? e : 0] = fmaf(gate[e], B[e], GB[BIAS ? e : 0]);
-            B[e] = 0.f;
+          y[e] = unit_value(y[e], mean_y, r_y);
+          A[j][e] = fmaf(t[j][e], y[e], A[j][e]);
+          if constexpr (BIAS) B[j][e] += t[j][e];
+        }
+      }
+      if (a.dy != nullptr) {
+        rows.scale_branch(t[j], j);
+        if (post) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            two[0] = fmaf(t[j][e], y[e], two[0]);
+            if constexpr (LAYER) two[1] += t[j][e];
           }
         }
       }
     }
+    if (a.dy != nullptr) {
+      if (post) {
+        if constexpr (LAYER) {
+          sum(two);
+        } else {
+          float one[1] = {two[0]};
+          sum(one);
+          two[0] = one[0];
+        }
+        const float mean_bv = two[0] * inv, mean_b = two[1] * inv;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          float y[E];
+          rows.y(y, j);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            t[j][e] = unit_slope(0.f, r_y, t[j][e], unit_value(y[e], mean_y, r_y), mean_bv, mean_b);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) rows.put(static_cast<T*>(a.dy) + r * a.ld_dy, t[j], at[j]);
+    }
+    rows.done();
+    if constexpr (MANY) {
+      if (r + 1 == group_end) {  // the group's last row: its gate's gradient is complete
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+          if (a.dgate != nullptr) {
+            float o[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = a.branch_scale * A[j][e];
+            float pw[E];
+            parameters<P>(pw, a.post_weight, 1.f, at[j]);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = __fmul_rn(o[e], pw[e]);
+            if constexpr (BIAS) {
+              float pb[E];
+              parameters<P>(pb, a.post_bias, 0.f, at[j]);
+#pragma unroll
+              for (int e = 0; e < E; ++e) o[e] = fmaf(a.branch_scale * B[j][e], pb[e], o[e]);
+            }
+            store(a.dgate + g * (int64_t)a.D, o, at[j]);
+          }
+          float gate[E];
+          parameters<P>(gate, a.gate != nullptr ? static_cast<const P*>(a.gate) + g * a.ld_gate : nullptr, 1.f, at[j]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            GA[j][e] = fmaf(gate[e], A[j][e], GA[j][e]);
+            A[j][e] = 0.f;
+            if constexpr (BIAS) {
+              GB[j][BIAS ? e : 0] = fmaf(gate[e], B[j][e], GB[j][BIAS ? e : 0]);
+              B[j][e] = 0.f;
+            }
+          }
+        }
+        ++g;
+        group_end += per;
+        if (r + 1 < r1) rows.set_group(g);
+      }
+    }
   }
   // the sums of this part's rows, for k_norm_column_sums
-  const int64_t row = (int64_t)part * D;
-  if constexpr (MANY) {
-    if (ws.a != nullptr) store(ws.a + row, GA, at);
-    if constexpr (BIAS) {
-      if (ws.b != nullptr) store(ws.b + row, GB, at);
+  const int64_t out = (int64_t)part * a.D;
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+    if constexpr (MANY) {
+      if (ws.a != nullptr) store(ws.a + out, GA[j], at[j]);
+      if constexpr (BIAS) {
+        if (ws.b != nullptr) store(ws.b + out, GB[j], at[j]);
+      }
+    } else {
+      if (ws.a != nullptr) store(ws.a + out, A[j], at[j]);
+      if constexpr (BIAS) {
+        if (ws.b != nullptr) store(ws.b + out, B[j], at[j]);
+      }
     }
-  } else {
-    if (ws.a != nullptr) store(ws.a + row, A, at);
+    if (ws.c != nullptr) store(ws.c + out, C[j], at[j]);
     if constexpr (BIAS) {
-      if (ws.b != nullptr) store(ws.b + row, B, at);
+      if (ws.e != nullptr) store(ws.e + out, Eo[j], at[j]);
     }
-  }
-  if (ws.c != nullptr) store(ws.c + row, C, at);
-  if constexpr (BIAS) {
-    if (ws.e != nullptr) store(ws.e + row, Eo, at);
   }
 }
+
+// Where a thread of the backward kernel stands: its part and its columns.
+struct NormGradPlace {
+  int rank, tid, group, part, col0, cols;
+  Places at[2];
+  __device__ __forceinline__ NormGradPlace(const ffn_norm_grad_t& a, const NormGradShape& sh) {
+    rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
+    tid = sh.lanes > 1 ? (int)lane_idx() : (int)threadIdx.x;
+    group = sh.lanes > 1 ? (int)(threadIdx.x >> 5) : 0;
+    part = sh.lanes > 1 ? (int)blockIdx.x * sh.lanes + group : (int)blockIdx.x / sh.cluster;
+    col0 = (int)(rank * sh.columns);
+    cols = min((int)a.D - col0, (int)sh.columns);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) at[j] = Places{col0 + (j * sh.threads + tid) * 8, col0 + cols};
+  }
+};
 
 template <typename P>
 __device__ __forceinline__ float parameter(const void* p, int64_t i, float absent) {
@@ -565,8 +722,9 @@ __device__ __forceinline__ float parameter(const void* p, int64_t i, float absen
 // order.  blockIdx.y = 0: the sums over all rows (and a single gate's); 1 + g: the gate
 // of group g.
 template <typename P>
-__global__ void __launch_bounds__(1024) k_norm_column_sums(const ffn_norm_grad_t a, const NormGradShape sh,
-                                                           const NormSums ws) {
+__global__ void __launch_bounds__(1024) k_norm_column_sums(const __grid_constant__ ffn_norm_grad_t a,
+                                                           const __grid_constant__ NormGradShape sh,
+                                                           const __grid_constant__ NormSums ws) {
   __shared__ float sums[4][32][33];
   const int c = (int)lane_idx(), l = (int)(threadIdx.x >> 5), D = (int)a.D;
   const int i = (int)blockIdx.x * 32 + c;

@@ -45,19 +45,19 @@ const void* norm_kernel(const NormShape& sh) {
   }
 }
 
-template <typename T, typename P, bool LAYER>
+template <typename T, typename P, bool ALIGNED, bool LAYER>
 const void* norm_ring_kernel(const NormShape& sh) {
   if (sh.warp_rows) {
     switch (sh.nv) {
-      case 1: return (const void*)k_norm_ring<T, P, LAYER, true, 1>;
-      case 2: return (const void*)k_norm_ring<T, P, LAYER, true, 2>;
-      default: return (const void*)k_norm_ring<T, P, LAYER, true, 4>;
+      case 1: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 1>;
+      case 2: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 2>;
+      default: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 4>;
     }
   }
   switch (sh.nv) {
-    case 1: return (const void*)k_norm_ring<T, P, LAYER, false, 1>;
-    case 2: return (const void*)k_norm_ring<T, P, LAYER, false, 2>;
-    default: return (const void*)k_norm_ring<T, P, LAYER, false, 4>;
+    case 1: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 1>;
+    case 2: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 2>;
+    default: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 4>;
   }
 }
 
@@ -67,18 +67,20 @@ cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& sh, const FfnDevi
   ffn_norm_t args_a = a;
   uint32_t* status = dev.status;
   void* args[] = {&args_a, &status};
-  const void* k = sh.ring ? (layer ? norm_ring_kernel<T, P, true>(sh) : norm_ring_kernel<T, P, false>(sh))
+  const void* k = sh.ring ? (sh.aligned ? (layer ? norm_ring_kernel<T, P, true, true>(sh) : norm_ring_kernel<T, P, true, false>(sh))
+                                        : (layer ? norm_ring_kernel<T, P, false, true>(sh)
+                                                 : norm_ring_kernel<T, P, false, false>(sh)))
                           : (layer ? norm_kernel<T, P, true>(sh) : norm_kernel<T, P, false>(sh));
   return launch_dependent(k, dim3((unsigned)sh.grid), sh.threads, 1, sh.smem, args, st);
 }
 
 template <typename T, typename P, bool LAYER, bool BIAS>
 const void* norm_grad_kernel(const NormGradShape& sh) {
-  if (sh.ring)
-    return sh.many ? (const void*)k_norm_grad_ring<T, P, LAYER, BIAS, true>
-                   : (const void*)k_norm_grad_ring<T, P, LAYER, BIAS, false>;
-  return sh.many ? (const void*)k_norm_grad<T, P, LAYER, BIAS, true>
-                 : (const void*)k_norm_grad<T, P, LAYER, BIAS, false>;
+  if (sh.aligned)
+    return sh.many ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, true>
+                   : (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false>;
+  return sh.many ? (const void*)k_norm_grad<T, P, false, LAYER, BIAS, true>
+                 : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false>;
 }
 
 template <typename T, typename P>

@@ -1,8 +1,8 @@
-// kernels_norm_ring.cuh -- the block norms for rows that start on 16-byte
-// boundaries and have whole 16-byte vectors: rows come through a ring in shared
-// memory filled by bulk copies (cp.async.bulk), so an SM has tens of KB on their
-// way whatever its threads do, and the backward kernel can read a row's values
-// again instead of holding them in registers.
+// kernels_norm_ring.cuh -- the block norms with rows that come through a ring in
+// shared memory filled by bulk copies (cp.async.bulk), so an SM has tens of KB on
+// their way whatever its threads do, and the backward kernel can read a row's values
+// again instead of holding them in registers.  Rows may start anywhere: a copy
+// brings the whole 16-byte pieces a row lies in, and reads shift by its offset.
 //
 // A group (a warp, a CTA, or in the backward kernel a cluster of CTAs that share
 // the columns) walks its rows with `stages` rows ahead.  Every wait is bounded; a
@@ -15,96 +15,243 @@ namespace dgb {
 
 namespace {
 
+// raise the transaction bytes a phase expects, without arriving
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
 
+// (arguments by value: a ring whose address escapes would live in local memory, and
+// every access to it would go there)
+static __device__ __noinline__ bool ring_wait_slow(uint32_t full, uint32_t stage, uint32_t phase, uint32_t stages,
+                                                   volatile uint32_t* abort_flag, uint32_t* status, uint32_t left) {
+  const WaitCtl w{abort_flag, status, 2000000000ull, 0};
+  if (mbar_wait(full + 8u * stage, phase, w, WAIT_MMA_FULL)) return true;
+  volatile uint32_t never = 0u;
+  const WaitCtl wd{&never, nullptr, 2000000ull, 0};
+  for (; left > 0; --left) {
+    mbar_wait(full + 8u * stage, phase, wd, 0u);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  return false;
+}
+
 // The ring of one group: `arrays` rows (or column slices of rows) per stage.
 struct Ring {
-  uint8_t* slots;      // [stages][arrays][bytes]
+  uint8_t* slots;      // [stages][arrays][pitch]
   uint64_t* full;      // [stages]
   volatile uint32_t* abort_flag;
   uint32_t* status;
   uint32_t stages, arrays, bytes, pitch;  // bytes of a row (slice); of a slot
+  uint32_t stage = 0, phase = 0;          // of the row being read
+  uint32_t filled = 0;                    // (the group's first thread) the stage to fill next
 
-  __device__ __forceinline__ uint8_t* slot(uint32_t stage, uint32_t array) const {
-    return slots + (size_t)(stage * arrays + array) * pitch;
+  __device__ __forceinline__ uint8_t* slot(uint32_t st, uint32_t array) const {
+    return slots + (size_t)((st * arrays + array) * pitch);
   }
-  __device__ __forceinline__ WaitCtl ctl() const { return WaitCtl{abort_flag, status, 2000000000ull, 0}; }
-  // all threads: the i-th row of the group has landed
-  __device__ __forceinline__ bool wait(uint32_t i) const {
-    return mbar_wait(smem_u32(full + i % stages), (i / stages) & 1u, ctl(), WAIT_MMA_FULL);
+  // all threads: the row at `stage` has landed.  False where the wait ran out; `left`
+  // copies of this thread's are then in flight, and it sees them land before shared
+  // memory goes.
+  __device__ __forceinline__ bool wait(uint32_t left) const {
+    if (mbar_try_wait(smem_u32(full + stage), phase)) return true;
+    return ring_wait_slow(smem_u32(full), stage, phase, stages, abort_flag, status, left);
   }
-  // after a wait that ran out: the copies still in flight land before shared memory goes
-  __device__ __noinline__ void settle(uint32_t issued, uint32_t from) const {
-    volatile uint32_t never = 0u;
-    const WaitCtl w{&never, nullptr, 2000000ull, 0};
-    for (uint32_t i = from; i < issued; ++i) mbar_wait(smem_u32(full + i % stages), (i / stages) & 1u, w, 0u);
+  __device__ __forceinline__ void advance() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
   }
 };
 
-template <typename T, int E>
-__device__ __forceinline__ void from_slot(float (&v)[E], const uint8_t* slot, int first, bool live) {
-  Pack<T, E> p;
-#pragma unroll
-  for (int i = 0; i < Pack<T, E>::W / 4; ++i) {
-    const uint4 q = live ? reinterpret_cast<const uint4*>(slot + (size_t)first * sizeof(T))[i] : make_uint4(0, 0, 0, 0);
-    p.w[4 * i] = q.x;
-    p.w[4 * i + 1] = q.y;
-    p.w[4 * i + 2] = q.z;
-    p.w[4 * i + 3] = q.w;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = element(p, e);
-}
+// One array of a call: where its rows are, and where they may be read.
+template <typename T, bool ALIGNED>
+struct RingArray {
+  const T* base;  // row 0, from this group's first column on
+  int64_t ld;
+  uintptr_t lo, hi;  // the array's first byte and the end of its last row
 
-template <typename P, int E>
-__device__ __forceinline__ void aligned_parameters(float (&v)[E], const P* p, int first, bool live) {
-  Pack<P, E> raw;
-#pragma unroll
-  for (int i = 0; i < Pack<P, E>::W / 4; ++i) {
-    const uint4 q = live ? __ldg(reinterpret_cast<const uint4*>(p + first) + i) : make_uint4(0, 0, 0, 0);
-    raw.w[4 * i] = q.x;
-    raw.w[4 * i + 1] = q.y;
-    raw.w[4 * i + 2] = q.z;
-    raw.w[4 * i + 3] = q.w;
+  __device__ __forceinline__ RingArray(const void* p, int64_t pitch, int64_t rows, int64_t D, int col0)
+      : base(static_cast<const T*>(p) + col0), ld(pitch), lo(reinterpret_cast<uintptr_t>(p)) {
+    hi = lo + (uintptr_t)(((rows - 1) * pitch + D) * (int64_t)sizeof(T));
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = element(raw, e);
-}
-
-template <typename T, int E>
-__device__ __forceinline__ void aligned_store(T* p, const float (&f)[E], bool live) {
-  if (!live) return;
-  uint32_t w[Pack<T, E>::W];
-#pragma unroll
-  for (int i = 0; i < Pack<T, E>::W; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      w[i] = __float_as_uint(f[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  // how far row r starts past a 16-byte boundary
+  __device__ __forceinline__ uint32_t off(int64_t r) const {
+    if constexpr (ALIGNED) return 0u;
+    return ((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)r * (uint32_t)(ld * (int64_t)sizeof(T))) & 15u;
+  }
+  // The 16-byte pieces row r's `bytes` lie in, [from, to); where the first or last of
+  // them reaches outside the array, only the pieces inside.
+  __device__ __forceinline__ void span(int64_t r, uint32_t bytes, uintptr_t& from, uintptr_t& to) const {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(base + r * ld), end = begin + bytes;
+    from = begin & ~(uintptr_t)15;
+    to = (end + 15) & ~(uintptr_t)15;
+    if (from < lo) from += 16;
+    if (to > hi) to -= 16;
+    if (to < from) to = from;
+  }
+  // Brings row r to `slot`, which keeps its offset to 16-byte boundaries: whole pieces
+  // by a bulk copy, elements of pieces that reach outside the array one by one.
+  __device__ __forceinline__ void copy(int64_t r, uint32_t bytes, uint8_t* slot, uint32_t bar) const {
+    if constexpr (ALIGNED) {
+      bulk_load(smem_u32(slot), base + r * ld, bytes, bar);
+      return;
     }
+    uintptr_t from, to;
+    span(r, bytes, from, to);
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(base + r * ld), end = begin + bytes;
+    const uintptr_t origin = begin & ~(uintptr_t)15;
+    for (uintptr_t q = begin; q < end && q < from; q += sizeof(T))
+      *reinterpret_cast<T*>(slot + (q - origin)) = *reinterpret_cast<const T*>(q);
+    for (uintptr_t q = to > begin ? to : begin; q < end; q += sizeof(T))
+      if (q >= from) *reinterpret_cast<T*>(slot + (q - origin)) = *reinterpret_cast<const T*>(q);
+    if (to > from) bulk_load(smem_u32(slot + (from - origin)), reinterpret_cast<const void*>(from), (uint32_t)(to - from), bar);
   }
+  __device__ __forceinline__ uint32_t copied(int64_t r, uint32_t bytes) const {
+    if constexpr (ALIGNED) return bytes;
+    uintptr_t from, to;
+    span(r, bytes, from, to);
+    return (uint32_t)(to - from);
+  }
+};
+
+// bytes of a slot: a row at any offset, and the piece after it that a shifted read touches
+__host__ __device__ constexpr uint32_t ring_pitch(uint32_t bytes) { return (bytes + 31u) / 32u * 32u + 32u; }
+
+// E elements from element `i` on of the row at offset m of a slot; 0 from element
+// `end` on
+template <typename T, bool ALIGNED, int E>
+__device__ __forceinline__ void from_slot(float (&v)[E], const uint8_t* slot, uint32_t m, int i, int end) {
+  constexpr int W = Pack<T, E>::W;
+  Pack<T, E> p;
+  const uint4* from = reinterpret_cast<const uint4*>(slot + (size_t)i * sizeof(T));
+  if constexpr (ALIGNED) {
+    const bool live = i < end;
 #pragma unroll
-  for (int i = 0; i < Pack<T, E>::W / 4; ++i)
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    for (int k = 0; k < W / 4; ++k) {
+      const uint4 q = live ? from[k] : make_uint4(0u, 0u, 0u, 0u);
+      p.w[4 * k] = q.x;
+      p.w[4 * k + 1] = q.y;
+      p.w[4 * k + 2] = q.z;
+      p.w[4 * k + 3] = q.w;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = element(p, e);
+  } else {
+    uint32_t w[W + 4];
+#pragma unroll
+    for (int k = 0; k < W / 4 + 1; ++k) {
+      const uint4 q = i < end ? from[k] : make_uint4(0u, 0u, 0u, 0u);
+      w[4 * k] = q.x;
+      w[4 * k + 1] = q.y;
+      w[4 * k + 2] = q.z;
+      w[4 * k + 3] = q.w;
+    }
+    shift_down(w, m);
+#pragma unroll
+    for (int k = 0; k < W; ++k) p.w[k] = w[k];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = i + e < end ? element(p, e) : 0.f;
+  }
+}
+
+// a parameter vector's elements; the vectors of an ALIGNED call start on 16-byte boundaries
+template <typename P, bool ALIGNED, int E>
+__device__ __forceinline__ void row_parameters(float (&v)[E], const void* p, float absent, const Places& at) {
+  if constexpr (!ALIGNED) {
+    parameters<P>(v, p, absent, at);
+  } else {
+    if (p == nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = absent;
+      return;
+    }
+    Pack<P, E> raw;
+#pragma unroll
+    for (int k = 0; k < Pack<P, E>::W / 4; ++k) {
+      const uint4 q = at.inside(0) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const P*>(p) + at.first) + k)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+      raw.w[4 * k] = q.x;
+      raw.w[4 * k + 1] = q.y;
+      raw.w[4 * k + 2] = q.z;
+      raw.w[4 * k + 3] = q.w;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = element(raw, e);
+  }
+}
+
+template <typename T, bool ALIGNED, int E>
+__device__ __forceinline__ void row_store(T* row, const float (&f)[E], const Places& at) {
+  if constexpr (!ALIGNED) {
+    store(row, f, at);
+  } else {
+    if (!at.inside(0)) return;
+    const Pack<T, E> w = packed<T>(f);
+#pragma unroll
+    for (int k = 0; k < Pack<T, E>::W / 4; ++k)
+      reinterpret_cast<uint4*>(row + at.first)[k] =
+          make_uint4(w.w[4 * k], w.w[4 * k + 1], w.w[4 * k + 2], w.w[4 * k + 3]);
+  }
 }
 
 // ------------------------------------------------------------------- forward
 
-template <typename T, typename P, bool LAYER, bool WARP, int NV>
-__global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
-    k_norm_ring(const ffn_norm_t a, uint32_t* status) {
+// A thread keeps its columns' parameters in registers where it has at most two
+// vectors (HOLD): with 32-bit parameters they are more bytes than a 16-bit row, and
+// with most of the SM's memory given to the ring they would come from L2 for every
+// row (8192 x 4096: 63 us read per row).
+template <typename P, bool ALIGNED, int NV, int E, bool HOLD>
+struct RowFactors {
+  const P* p;
+  float held[HOLD ? NV : 1][HOLD ? E : 1];
+  __device__ __forceinline__ RowFactors(const void* from, const Places (&at)[NV]) : p(static_cast<const P*>(from)) {
+    if constexpr (HOLD) {
+      if (p != nullptr) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) row_parameters<P, ALIGNED>(held[j], p, 1.f, at[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ void times(float (&v)[E], int j, const Places& at) const {
+    if (p == nullptr) return;
+    float f[E];
+    get(f, j, at);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= f[e];
+  }
+  __device__ __forceinline__ void plus(float (&v)[E], int j, const Places& at) const {
+    if (p == nullptr) return;
+    float f[E];
+    get(f, j, at);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += f[e];
+  }
+  __device__ __forceinline__ void get(float (&f)[E], int j, const Places& at) const {
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = held[j][e];
+    } else {
+      row_parameters<P, ALIGNED>(f, p, 1.f, at);
+    }
+  }
+};
+
+template <typename T, typename P, bool ALIGNED, bool LAYER, bool WARP, int NV>
+__global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(const __grid_constant__ ffn_norm_t a, uint32_t* status) {
   constexpr int E = 16 / (int)sizeof(T);
+  constexpr bool HOLD = !WARP && NV <= 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[8 * kNormStages];
-  __shared__ float parts[2 * 128];
+  __shared__ float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
   const int tid = WARP ? (int)lane_idx() : (int)threadIdx.x, per_row = WARP ? 32 : (int)blockDim.x;
   const int group = WARP ? (int)(threadIdx.x >> 5) : 0, groups = WARP ? (int)(blockDim.x / 32) : 1;
@@ -113,12 +260,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
   ring.stages = kNormStages;
   ring.arrays = a.residual != nullptr ? 2u : 1u;
   ring.bytes = (uint32_t)(D * (int)sizeof(T));
-  ring.pitch = ring.bytes;
+  ring.pitch = ring_pitch(ring.bytes);
   ring.slots = smem + (size_t)group * ring.stages * ring.arrays * ring.pitch;
   ring.full = bars + group * kNormStages;
   ring.abort_flag = &abort_flag;
   ring.status = status;
-  RowSums<1> sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
+  RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
   if (tid == 0) {
     for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), 1);
     fence_mbar_init();
@@ -128,16 +275,22 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t step = (int64_t)gridDim.x * groups, r0 = (int64_t)blockIdx.x * groups + group;
-  uint32_t issued = 0;  // (the group's first thread)
+  int64_t ahead = r0;  // (the group's first thread) the row to fetch next
+  uint32_t in_flight = 0;
+  const RingArray<T, ALIGNED> in_y(a.y, a.ld_y, a.M, D, 0), in_res(a.residual, a.ld_residual, a.M, D, 0);
   auto issue = [&]() {
-    const int64_t r = r0 + (int64_t)issued * step;
-    if (r >= a.M) return;
-    const uint32_t stage = issued % ring.stages, bar = smem_u32(ring.full + stage);
-    mbar_arrive_expect_tx(bar, ring.arrays * ring.bytes);
-    bulk_load(smem_u32(ring.slot(stage, 0)), static_cast<const T*>(a.y) + r * a.ld_y, ring.bytes, bar);
-    if (a.residual != nullptr)
-      bulk_load(smem_u32(ring.slot(stage, 1)), static_cast<const T*>(a.residual) + r * a.ld_residual, ring.bytes, bar);
-    ++issued;
+    if (ahead >= a.M) return;
+    const uint32_t bar = smem_u32(ring.full + ring.filled);
+    const bool two = a.residual != nullptr;
+    // (the elements a copy brings one by one are ordered by this arrival: they come first)
+    const uint32_t bytes = in_y.copied(ahead, ring.bytes) + (two ? in_res.copied(ahead, ring.bytes) : 0u);
+    mbar_expect_tx(bar, bytes);
+    in_y.copy(ahead, ring.bytes, ring.slot(ring.filled, 0), bar);
+    if (two) in_res.copy(ahead, ring.bytes, ring.slot(ring.filled, 1), bar);
+    mbar_arrive(bar);
+    if (++ring.filled == ring.stages) ring.filled = 0;
+    ahead += step;
+    ++in_flight;
   };
   if (tid == 0)
     for (uint32_t s = 0; s < ring.stages; ++s) issue();
@@ -146,91 +299,79 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
   Places at[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) at[j] = Places{(j * per_row + tid) * E, D};
-  uint32_t i = 0;
-  for (int64_t r = r0; r < a.M; r += step, ++i) {
-    if (!ring.wait(i)) {
-      if (tid == 0) ring.settle(issued, i);
-      return;
+  const float n_w = LAYER ? warp_elements<NV, E>(at) : 0.f;
+  const bool one_gate = a.groups == 1;
+  const RowFactors<P, ALIGNED, NV, E, HOLD> post_weight(a.post_weight, at), pre_weight(a.pre_weight, at),
+      shared_gate(one_gate ? a.gate : nullptr, at);
+  const RowFactors<P, ALIGNED, NV, E, HOLD && LAYER> post_bias(a.post_bias, at), pre_bias(a.pre_bias, at);
+  for (int64_t r = r0; r < a.M; r += step) {
+    float own_gate[NV][E];  // (asked for early: it comes from L2)
+    if (a.gate != nullptr && !one_gate) {
+      const P* gate = gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) row_parameters<P, ALIGNED>(own_gate[j], gate, 1.f, at[j]);
     }
-    const uint32_t stage = i % ring.stages;
+    if (!ring.wait(in_flight)) return;
+    const uint32_t off_y = in_y.off(r), off_res = in_res.off(r);
     float v[NV][E];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) from_slot<T>(v[j], ring.slot(stage, 0), at[j].first, at[j].inside(0));
+    for (int j = 0; j < NV; ++j) from_slot<T, ALIGNED>(v[j], ring.slot(ring.stage, 0), off_y, at[j].first, D);
     if (post) {
-      const float2 st = unit_of<LAYER, true>(v, at, D, a.eps, sum);
+      const float2 st = unit_of<LAYER, ALIGNED>(v, at, D, n_w, a.eps, sum);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const bool live = at[j].inside(0);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
-        if (a.post_weight != nullptr) {
-          float w[E];
-          aligned_parameters(w, static_cast<const P*>(a.post_weight), at[j].first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] *= w[e];
-        }
-        if (a.post_bias != nullptr) {
-          float b[E];
-          aligned_parameters(b, static_cast<const P*>(a.post_bias), at[j].first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] += b[e];
-        }
+        post_weight.times(v[j], j, at[j]);
+        post_bias.plus(v[j], j, at[j]);
       }
     }
-    const P* gate =
-        a.gate != nullptr ? static_cast<const P*>(a.gate) + (r / (a.M / a.groups)) * a.ld_gate : nullptr;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const bool live = at[j].inside(0);
-      if (gate != nullptr) {
-        float g[E];
-        aligned_parameters(g, gate, at[j].first, live);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] *= a.branch_scale * g[e];
-      } else {
+      for (int e = 0; e < E; ++e) v[j][e] *= a.branch_scale;
+      if (a.gate != nullptr) {
+        if (one_gate) {
+          shared_gate.times(v[j], j, at[j]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] *= a.branch_scale;
+          for (int e = 0; e < E; ++e) v[j][e] *= own_gate[j][e];
+        }
       }
       if (a.residual != nullptr) {
         float q[E];
-        from_slot<T>(q, ring.slot(stage, 1), at[j].first, live);
+        from_slot<T, ALIGNED>(q, ring.slot(ring.stage, 1), off_res, at[j].first, D);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[j][e] = fmaf(a.residual_scale, q[e], v[j][e]);
       }
-      if (LAYER && !live) {
+      if (!ALIGNED || LAYER) {  // (past the end: a mean or a bias of the post norm)
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = 0.f;  // (0 - mean of the post norm)
+        for (int e = 0; e < E; ++e)
+          if (!at[j].inside(ALIGNED ? 0 : e)) v[j][e] = 0.f;
       }
-      if (a.s != nullptr) aligned_store(static_cast<T*>(a.s) + r * a.ld_s + at[j].first, v[j], live);
+      if (a.s != nullptr) row_store<T, ALIGNED>(static_cast<T*>(a.s) + r * a.ld_s, v[j], at[j]);
     }
     // the group has read the row's slots once it meets at the next barrier
     float2 st = make_float2(0.f, 1.f);
-    if (pre) st = unit_of<LAYER, true>(v, at, D, a.eps, sum);
+    if (pre) st = unit_of<LAYER, ALIGNED>(v, at, D, n_w, a.eps, sum);
     if constexpr (WARP) {
       __syncwarp();
     } else {
       if (!pre || per_row == 32) __syncthreads();
     }
-    if (tid == 0) issue();
+    if (tid == 0) {
+      --in_flight;
+      issue();
+    }
+    ring.advance();
     if (pre) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const bool live = at[j].inside(0);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
-        if (a.pre_weight != nullptr) {
-          float w[E];
-          aligned_parameters(w, static_cast<const P*>(a.pre_weight), at[j].first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] *= w[e];
-        }
-        if (a.pre_bias != nullptr) {
-          float b[E];
-          aligned_parameters(b, static_cast<const P*>(a.pre_bias), at[j].first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] += b[e];
-        }
-        aligned_store(static_cast<T*>(a.n) + r * a.ld_n + at[j].first, v[j], live);
+        pre_weight.times(v[j], j, at[j]);
+        pre_bias.plus(v[j], j, at[j]);
+        row_store<T, ALIGNED>(static_cast<T*>(a.n) + r * a.ld_n, v[j], at[j]);
       }
     }
   }
@@ -238,40 +379,151 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 4 : 2)
 
 // ------------------------------------------------------------------ backward
 
-// k_norm_grad on rows that come through a ring: the same sums (see there), the
-// values read from shared memory where they are used.
-template <typename T, typename P, bool LAYER, bool BIAS, bool MANY>
-__global__ void __launch_bounds__(kNormGradThreads, (MANY || sizeof(T) == 4) ? 1 : 2)
-    k_norm_grad_ring(const ffn_norm_grad_t a, const NormGradShape sh, const NormSums ws, uint32_t* status) {
-  constexpr int E = kNormGradEach;
-  constexpr int K = LAYER ? 4 : 3;
+// Rows of the backward kernel through a ring: s and dn, y, ds, those that are given.
+// The factors of a thread's columns stay in shared memory too, in places only that
+// thread reads and writes: from global memory they came from L2 for every row, since
+// the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us).
+template <typename T, typename P, bool ALIGNED>
+struct RowsRing {
+  static constexpr bool kWhole = ALIGNED;  // groups of 8 columns lie wholly in or out of a row
+  const ffn_norm_grad_t& a;
+  const Places (&at)[2];
+  RingArray<T, ALIGNED> in_s, in_dn, in_y, in_ds;
+  Ring ring;
+  int64_t ahead, r1;
+  uint32_t y_at, ds_at;
+  float* factors;  // [pre_weight, branch][2] groups of 8, `stride` floats apart
+  int stride;
+  int local[2], cols;  // this thread's columns in a slot, and how many a slot has
+  uint32_t off_s, off_dn, off_y, off_ds;  // the row's offsets
+  bool first_thread, alone;
+
+  __device__ __forceinline__ void issue() {
+    if (ahead >= r1) return;
+    const uint32_t bar = smem_u32(ring.full + ring.filled), n = ring.bytes;
+    uint32_t bytes = 0;
+    if (a.dn != nullptr) bytes += in_s.copied(ahead, n) + in_dn.copied(ahead, n);
+    if (a.y != nullptr) bytes += in_y.copied(ahead, n);
+    if (a.ds != nullptr) bytes += in_ds.copied(ahead, n);
+    mbar_expect_tx(bar, bytes);
+    if (a.dn != nullptr) {
+      in_s.copy(ahead, n, ring.slot(ring.filled, 0), bar);
+      in_dn.copy(ahead, n, ring.slot(ring.filled, 1), bar);
+    }
+    if (a.y != nullptr) in_y.copy(ahead, n, ring.slot(ring.filled, y_at), bar);
+    if (a.ds != nullptr) in_ds.copy(ahead, n, ring.slot(ring.filled, ds_at), bar);
+    mbar_arrive(bar);  // (after the elements that were copied one by one)
+    if (++ring.filled == ring.stages) ring.filled = 0;
+    ++ahead;
+  }
+  __device__ __forceinline__ void begin(int64_t from, int64_t to) {
+    ahead = from;
+    r1 = to;
+    if (first_thread)
+      for (uint32_t s = 0; s < ring.stages; ++s) issue();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float w[8];
+      row_parameters<P, ALIGNED>(w, a.pre_weight, 1.f, at[j]);
+      keep(w, j);
+    }
+  }
+  __device__ __forceinline__ void set_group(int64_t g) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float f[8];
+      float w[8];
+      row_parameters<P, ALIGNED>(f, a.gate != nullptr ? static_cast<const P*>(a.gate) + g * a.ld_gate : nullptr, 1.f,
+                                 at[j]);
+      row_parameters<P, ALIGNED>(w, a.post_weight, 1.f, at[j]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn(a.branch_scale, f[e]), w[e]);
+      keep(f, 2 + j);
+    }
+  }
+  __device__ __forceinline__ bool next(int64_t r) {
+    if (!ring.wait(first_thread ? (uint32_t)(ahead - r) : 0u)) return false;
+    off_s = in_s.off(r);
+    off_dn = in_dn.off(r);
+    off_y = in_y.off(r);
+    off_ds = in_ds.off(r);
+    return true;
+  }
+  // every thread of the group has come to this row: the slots of the one before are free
+  __device__ __forceinline__ void met() {
+    if (first_thread && !alone && !first_row) issue();
+    first_row = false;
+  }
+  bool first_row = true;
+  __device__ __forceinline__ void done() {
+    ring.advance();
+    if (!alone) return;  // a lone warp meets no one at the next row's barrier
+    __syncwarp();
+    if (first_thread) issue();
+  }
+  __device__ __forceinline__ void values(float (&v)[8], uint32_t array, uint32_t off, int j) const {
+    from_slot<T, ALIGNED>(v, ring.slot(ring.stage, array), off, local[j], cols);
+  }
+  __device__ __forceinline__ void s(float (&v)[8], int j) const { values(v, 0, off_s, j); }
+  __device__ __forceinline__ void dn(float (&v)[8], int j) const { values(v, 1, off_dn, j); }
+  __device__ __forceinline__ void y(float (&v)[8], int j) const { values(v, y_at, off_y, j); }
+  __device__ __forceinline__ void ds(float (&v)[8], int j) const { values(v, ds_at, off_ds, j); }
+  __device__ __forceinline__ void keep(const float (&v)[8], int k) {
+    float4* to = reinterpret_cast<float4*>(factors + k * stride);
+    to[0] = make_float4(v[0], v[1], v[2], v[3]);
+    to[stride / 8] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void scale(float (&v)[8], int k) const {
+    const float4* from = reinterpret_cast<const float4*>(factors + k * stride);
+    const float4 lo = from[0], hi = from[stride / 8];
+    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], f[e]);
+  }
+  __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const { scale(v, j); }
+  __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const { scale(v, 2 + j); }
+  __device__ __forceinline__ void put(T* to, const float (&v)[8], const Places& w) const {
+    row_store<T, ALIGNED>(to, v, w);
+  }
+};
+
+template <typename T, typename P, bool ALIGNED, bool LAYER, bool BIAS, bool MANY>
+__global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 : 2)
+    k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
+                const __grid_constant__ NormSums ws, uint32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[8 * kNormStages];
-  __shared__ float parts_smem[2 * 128 * K];
+  __shared__ float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
-  const int D = (int)a.D;
-  const int rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
-  const bool lone = sh.lanes > 1;  // a warp per part
-  const int tid = lone ? (int)lane_idx() : (int)threadIdx.x;
-  const int group = lone ? (int)(threadIdx.x >> 5) : 0;
-  const int part = lone ? (int)blockIdx.x * sh.lanes + group : (int)blockIdx.x / sh.cluster;
-  RowSums<K> sum{parts_smem, sh.threads / 32, sh.cluster, rank, 0};
-  const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
-  const int col0 = (int)(rank * sh.columns), cols = min(D - col0, (int)sh.columns);
-  const int first = col0 + tid * E;  // this thread's columns
-  const bool live = tid * E < cols;
-  Ring ring;
-  ring.stages = kNormStages;
-  const uint32_t y_at = pre ? 2u : 0u, ds_at = y_at + (a.y != nullptr ? 1u : 0u);
-  ring.arrays = ds_at + (a.ds != nullptr ? 1u : 0u);
-  ring.bytes = (uint32_t)(cols * (int)sizeof(T));
-  ring.pitch = (uint32_t)(sh.columns * (int64_t)sizeof(T));
-  ring.slots = smem + (size_t)group * ring.stages * ring.arrays * ring.pitch;
-  ring.full = bars + group * kNormStages;
-  ring.abort_flag = &abort_flag;
-  ring.status = status;
-  if (tid == 0) {
-    for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), 1);
+  const NormGradPlace w(a, sh);
+  RowSums sum{parts, sh.threads / 32, sh.cluster, w.rank, 0};
+  RowsRing<T, P, ALIGNED> rows{a,
+                      w.at,
+                      RingArray<T, ALIGNED>(a.s, a.ld_s, a.M, a.D, w.col0),
+                      RingArray<T, ALIGNED>(a.dn, a.ld_dn, a.M, a.D, w.col0),
+                      RingArray<T, ALIGNED>(a.y, a.ld_y, a.M, a.D, w.col0),
+                      RingArray<T, ALIGNED>(a.ds, a.ld_ds, a.M, a.D, w.col0)};
+  rows.y_at = a.dn != nullptr ? 2u : 0u;
+  rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
+  rows.first_thread = w.tid == 0;
+  rows.alone = sum.warps == 1 && sum.cluster == 1;
+  rows.cols = w.cols;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) rows.local[j] = w.at[j].first - w.col0;
+  // thread i's 16-byte pieces of the factors, i pieces in: no bank conflicts
+  rows.stride = 8 * (int)blockDim.x;
+  rows.factors = reinterpret_cast<float*>(smem) + 4 * threadIdx.x;
+  rows.ring.stages = (uint32_t)sh.stages;
+  rows.ring.arrays = rows.ds_at + (a.ds != nullptr ? 1u : 0u);
+  rows.ring.bytes = (uint32_t)(w.cols * (int)sizeof(T));
+  rows.ring.pitch = ring_pitch((uint32_t)(sh.columns * (int64_t)sizeof(T)));
+  rows.ring.slots = smem + (size_t)4 * rows.stride * sizeof(float) +
+                    (size_t)w.group * sh.stages * rows.ring.arrays * rows.ring.pitch;
+  rows.ring.full = bars + w.group * kNormStages;
+  rows.ring.abort_flag = &abort_flag;
+  rows.ring.status = status;
+  if (rows.first_thread) {
+    for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(rows.ring.full + s), 1);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = 0u;
@@ -282,230 +534,8 @@ __global__ void __launch_bounds__(kNormGradThreads, (MANY || sizeof(T) == 4) ? 1
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (part >= sh.parts) return;  // (whole warps only)
-  int64_t r0, r1;
-  const int64_t per = a.M / a.groups;
-  norm_part_rows<MANY>(a, sh, part, r0, r1);
-  uint32_t issued = 0;  // (the group's first thread)
-  auto issue = [&]() {
-    const int64_t r = r0 + issued;
-    if (r >= r1) return;
-    const uint32_t stage = issued % ring.stages, bar = smem_u32(ring.full + stage);
-    mbar_arrive_expect_tx(bar, ring.arrays * ring.bytes);
-    auto copy = [&](uint32_t array, const void* base, int64_t ld) {
-      bulk_load(smem_u32(ring.slot(stage, array)), static_cast<const T*>(base) + r * ld + col0, ring.bytes, bar);
-    };
-    if (pre) {
-      copy(0, a.s, a.ld_s);
-      copy(1, a.dn, a.ld_dn);
-    }
-    if (a.y != nullptr) copy(y_at, a.y, a.ld_y);
-    if (a.ds != nullptr) copy(ds_at, a.ds, a.ld_ds);
-    ++issued;
-  };
-  if (tid == 0)
-    for (uint32_t s = 0; s < ring.stages; ++s) issue();
-
-  const float inv = 1.f / (float)D;
-  const int local = tid * E;  // in a slot
-  const bool alone = sum.warps == 1 && sum.cluster == 1;
-  float A[E] = {}, C[E] = {}, B[BIAS ? E : 1] = {}, Eo[BIAS ? E : 1] = {};
-  float GA[MANY ? E : 1] = {}, GB[(MANY && BIAS) ? E : 1] = {};
-  uint32_t i = 0;
-  for (int64_t r = r0; r < r1; ++r, ++i) {
-    if (!ring.wait(i)) {
-      if (tid == 0) ring.settle(issued, i);
-      break;
-    }
-    const uint32_t stage = i % ring.stages;
-    float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[K];
-    if constexpr (LAYER) {
-#pragma unroll
-      for (int q = 0; q < K; ++q) k[q] = 0.f;
-      if (pre) {
-        float s[E], dn[E];
-        from_slot<T>(s, ring.slot(stage, 0), local, live);
-        from_slot<T>(dn, ring.slot(stage, 1), local, live);
-        if (a.pre_weight != nullptr) {
-          float w[E];
-          aligned_parameters(w, static_cast<const P*>(a.pre_weight), first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) dn[e] = __fmul_rn(dn[e], w[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          k[0] += s[e];
-          k[2] += dn[e];
-        }
-      }
-      if (post) {
-        float y[E];
-        from_slot<T>(y, ring.slot(stage, y_at), local, live);
-#pragma unroll
-        for (int e = 0; e < E; ++e) k[1] += y[e];
-      }
-      sum(k);
-      if (i > 0 && tid == 0 && !alone) issue();  // (every thread is past the row before: its slots are free)
-      mean_s = k[0] * inv;
-      mean_y = k[1] * inv;
-      mean_a = k[2] * inv;
-    }
-#pragma unroll
-    for (int q = 0; q < K; ++q) k[q] = 0.f;
-    if (live && pre) {
-      float s[E], dn[E];
-      from_slot<T>(s, ring.slot(stage, 0), local, true);
-      from_slot<T>(dn, ring.slot(stage, 1), local, true);
-      if (a.pre_weight != nullptr) {
-        float w[E];
-        aligned_parameters(w, static_cast<const P*>(a.pre_weight), first, true);
-#pragma unroll
-        for (int e = 0; e < E; ++e) dn[e] = __fmul_rn(dn[e], w[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float c = s[e] - mean_s;
-        k[0] = fmaf(c, c, k[0]);
-        k[1] = fmaf(c, dn[e], k[1]);
-      }
-    }
-    if (live && post) {
-      float y[E];
-      from_slot<T>(y, ring.slot(stage, y_at), local, true);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float c = y[e] - mean_y;
-        k[2] = fmaf(c, c, k[2]);
-      }
-    }
-    __syncwarp();
-    sum(k);
-    if constexpr (!LAYER) {
-      if (i > 0 && tid == 0 && !alone) issue();
-    }
-    const float r_s = rsqrtf(k[0] * inv + a.eps), mean_au = k[1] * inv * r_s;
-    const float r_y = post ? rsqrtf(k[2] * inv + a.eps) : 1.f;
-    float t[E];
-    if (a.ds != nullptr) {
-      from_slot<T>(t, ring.slot(stage, ds_at), local, live);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = 0.f;
-    }
-    if (pre && live) {
-      float s[E], dn[E];
-      from_slot<T>(s, ring.slot(stage, 0), local, true);
-      from_slot<T>(dn, ring.slot(stage, 1), local, true);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        s[e] = unit_value(s[e], mean_s, r_s);
-        C[e] = fmaf(dn[e], s[e], C[e]);
-        if constexpr (BIAS) Eo[e] += dn[e];
-      }
-      if (a.pre_weight != nullptr) {
-        float w[E];
-        aligned_parameters(w, static_cast<const P*>(a.pre_weight), first, true);
-#pragma unroll
-        for (int e = 0; e < E; ++e) dn[e] = __fmul_rn(dn[e], w[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = unit_slope(t[e], r_s, dn[e], s[e], mean_au, mean_a);
-    }
-    if (a.dresidual != nullptr) {
-      float o[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[e];
-      aligned_store(static_cast<T*>(a.dresidual) + r * a.ld_dresidual + first, o, live);
-    }
-    float y[E];
-    if (a.y != nullptr) {
-      from_slot<T>(y, ring.slot(stage, y_at), local, live);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        y[e] = unit_value(y[e], mean_y, r_y);
-        A[e] = fmaf(t[e], y[e], A[e]);
-        if constexpr (BIAS) B[e] += t[e];
-      }
-    }
-    const int64_t g = r / per;
-    float gate[E];
-    if (a.gate != nullptr) {
-      aligned_parameters(gate, static_cast<const P*>(a.gate) + g * a.ld_gate, first, live);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) gate[e] = 1.f;
-    }
-    if (a.dy != nullptr) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = __fmul_rn(t[e], __fmul_rn(a.branch_scale, gate[e]));
-      if (post) {
-        if (a.post_weight != nullptr) {
-          float w[E];
-          aligned_parameters(w, static_cast<const P*>(a.post_weight), first, live);
-#pragma unroll
-          for (int e = 0; e < E; ++e) t[e] = __fmul_rn(t[e], w[e]);
-        }
-#pragma unroll
-        for (int q = 0; q < K; ++q) k[q] = 0.f;
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            k[0] = fmaf(t[e], y[e], k[0]);
-            if constexpr (LAYER) k[1] += t[e];
-          }
-        }
-        __syncwarp();
-        sum(k);
-        const float mean_bv = k[0] * inv, mean_b = LAYER ? k[1] * inv : 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) t[e] = unit_slope(0.f, r_y, t[e], y[e], mean_bv, mean_b);
-      }
-      aligned_store(static_cast<T*>(a.dy) + r * a.ld_dy + first, t, live);
-    }
-    if (alone) {  // no barrier of the next row to wait for
-      __syncwarp();
-      if (tid == 0) issue();
-    }
-    if constexpr (MANY) {
-      if (r + 1 == (g + 1) * per) {  // the group's last row: its gate's gradient is complete
-        if (a.dgate != nullptr) {
-          float o[E], pw[E], pb[E];
-          parameters<P>(pw, a.post_weight, 1.f, Places{first, col0 + cols});
-          parameters<P>(pb, a.post_bias, 0.f, Places{first, col0 + cols});
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            o[e] = a.branch_scale * (pw[e] * A[e] + (BIAS ? pb[e] * B[BIAS ? e : 0] : 0.f));
-          store(a.dgate + g * (int64_t)D, o, Places{first, col0 + cols});
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          GA[e] = fmaf(gate[e], A[e], GA[e]);
-          A[e] = 0.f;
-          if constexpr (BIAS) {
-            GB[BIAS ? e : 0] = fmaf(gate[e], B[e], GB[BIAS ? e : 0]);
-            B[e] = 0.f;
-          }
-        }
-      }
-    }
-  }
-  // the sums of this part's rows, for k_norm_column_sums
-  const int64_t out = (int64_t)part * D + first;
-  if constexpr (MANY) {
-    if (ws.a != nullptr) aligned_store(ws.a + out, GA, live);
-    if constexpr (BIAS) {
-      if (ws.b != nullptr) aligned_store(ws.b + out, GB, live);
-    }
-  } else {
-    if (ws.a != nullptr) aligned_store(ws.a + out, A, live);
-    if constexpr (BIAS) {
-      if (ws.b != nullptr) aligned_store(ws.b + out, B, live);
-    }
-  }
-  if (ws.c != nullptr) aligned_store(ws.c + out, C, live);
-  if constexpr (BIAS) {
-    if (ws.e != nullptr) aligned_store(ws.e + out, Eo, live);
-  }
+  if (w.part >= sh.parts) return;  // (whole warps only)
+  norm_grad_rows<LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, w.part, w.at);
 }
 
 }  // namespace

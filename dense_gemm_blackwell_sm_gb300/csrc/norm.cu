@@ -24,7 +24,6 @@ int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
 cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int b = elem_bytes(a.dtype), E = 16 / b;
   NormShape sh{};
-  const int pb = elem_bytes(a.param_dtype);
   const int64_t vectors = (a.D + E - 1) / E;  // of a row
   const int most = norm_most_vectors(b);
   if (vectors <= 32 * 4 && a.M > 2 * (int64_t)dev.num_sms) {
@@ -44,10 +43,12 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
     sh.threads = round32((vectors + sh.nv - 1) / sh.nv);
     sh.grid = a.M;
   }
-  // the ring, where rows allow 16-byte copies and every group has a few of them
-  if (a.D % E == 0 && rows16(a.y, a.ld_y, b) && rows16(a.residual, a.ld_residual, b) && rows16(a.s, a.ld_s, b) &&
-      rows16(a.n, a.ld_n, b) && rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.post_bias) &&
-      aligned16(a.pre_weight) && aligned16(a.pre_bias)) {
+  const int pb = elem_bytes(a.param_dtype);
+  sh.aligned = a.D % 8 == 0 && rows16(a.y, a.ld_y, b) && rows16(a.residual, a.ld_residual, b) &&
+               rows16(a.s, a.ld_s, b) && rows16(a.n, a.ld_n, b) && rows16(a.gate, a.ld_gate, pb) &&
+               aligned16(a.post_weight) && aligned16(a.post_bias) && aligned16(a.pre_weight) && aligned16(a.pre_bias);
+  // the ring, where every group has a few rows
+  {
     NormShape ring = sh;
     ring.ring = true;
     ring.warp_rows = vectors <= 32 * 4;
@@ -55,10 +56,11 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
                              : (vectors <= 256 ? 1 : vectors <= 1024 ? 2 : 4);
     ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
     const int groups = ring.warp_rows ? 8 : 1;
-    ring.smem = (size_t)groups * kNormStages * (a.residual ? 2 : 1) * (size_t)(a.D * b);
+    ring.smem = (size_t)groups * kNormStages * (a.residual ? 2 : 1) * norm_slot_bytes(a.D * b);
     if (ring.threads <= 512 && ring.smem <= kNormRingBytes) {
+      // (about 100 registers per thread and 6 KB of static shared memory)
       const int64_t per_sm =
-          std::max<int64_t>(1, std::min<int64_t>((int64_t)(220 * 1024) / ((int64_t)ring.smem + 2048), 1024 / ring.threads));
+          std::max<int64_t>(1, std::min<int64_t>((int64_t)(222 * 1024) / ((int64_t)ring.smem + 6144), 640 / ring.threads));
       ring.grid = std::min<int64_t>(per_sm * dev.num_sms, (a.M + groups - 1) / groups);
       if (a.M >= 2 * ring.grid * groups) sh = ring;
     }
@@ -75,13 +77,12 @@ namespace {
 // The split of the backward pass; it depends on the sizes alone, so that the
 // workspace can be sized without a device and sums are the same on every call.
 NormGradShape grad_shape(const ffn_norm_grad_t& a) {
-  constexpr int kResident = 304;  // CTAs of 512 threads: two on each of 152 SMs
+  constexpr int kResident = 304;  // CTAs of 256 threads: two on each of 152 SMs
   NormGradShape sh{};
   const int64_t threads = (a.D + kNormGradEach - 1) / kNormGradEach;
   sh.cluster = (int)((threads + kNormGradThreads - 1) / kNormGradThreads);
-  sh.columns = (a.D + sh.cluster - 1) / sh.cluster;
-  sh.columns = (sh.columns + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
-  sh.threads = round32((sh.columns + kNormGradEach - 1) / kNormGradEach);
+  sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
+  sh.threads = round32(sh.columns / kNormGradEach);
   sh.lanes = sh.threads == 32 ? 8 : 1;
   const bool gates = a.gate != nullptr || a.dgate != nullptr;
   const int64_t groups = gates ? a.groups : 1;
@@ -127,15 +128,17 @@ cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& d
   if (a.gate == nullptr && a.dgate == nullptr) a.groups = 1;
   NormGradShape sh = grad_shape(a);
   const int b = elem_bytes(a.dtype), pb = elem_bytes(a.param_dtype);
+  sh.aligned = a.D % 8 == 0 && rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) &&
+               rows16(a.s, a.ld_s, b) && rows16(a.dresidual, a.ld_dresidual, b) && rows16(a.dy, a.ld_dy, b) &&
+               rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.pre_weight);
   const int arrays = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
-  const size_t smem = (size_t)sh.lanes * kNormStages * arrays * (size_t)(sh.columns * b);
-  if (a.D % kNormGradEach == 0 && rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) &&
-      rows16(a.s, a.ld_s, b) && rows16(a.dresidual, a.ld_dresidual, b) && rows16(a.dy, a.ld_dy, b) &&
-      rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.post_bias) && aligned16(a.pre_weight) &&
-      smem <= kNormRingBytes) {
-    sh.ring = true;
-    sh.smem = smem;
-  }
+  // three rows ahead where two CTAs still share an SM, else two
+  auto bytes = [&](int stages) {
+    return (size_t)sh.threads * sh.lanes * 32 * 4 +
+           (size_t)sh.lanes * stages * arrays * norm_slot_bytes(sh.columns * elem_bytes(a.dtype));
+  };
+  sh.stages = bytes(kNormStages) <= 108 * 1024 ? kNormStages : 2;
+  sh.smem = bytes(sh.stages);
   NormSums ws{};
   sums_of(a, sh, &ws, static_cast<float*>(a.workspace));
   switch (a.dtype) {
