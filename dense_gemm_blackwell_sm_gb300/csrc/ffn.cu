@@ -1,7 +1,9 @@
 // ffn.cu -- the C ABI of the feed-forward block's operators (include/ffn.h):
 // argument validation, the per-device state, launches and status checks.
+#include <map>
 #include <mutex>
 #include <set>
+#include <tuple>
 #include <utility>
 
 #include "ffn.h"
@@ -109,6 +111,29 @@ cudaError_t dgb::allow_smem_once(const void* func, size_t bytes) {
     if (done.count({dev, func})) return cudaSuccess;
     e = allow_dynamic_smem(func, bytes);
     if (e == cudaSuccess) done.insert({dev, func});
+    return e;
+  } catch (...) {
+    return cudaErrorMemoryAllocation;
+  }
+}
+
+cudaError_t dgb::resident_ctas(const void* func, int threads, size_t smem, size_t most, int* out) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int, size_t>, int> known;
+  cudaError_t e = allow_smem_once(func, most);
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(dev, func, threads, smem);
+    const auto it = known.find(key);
+    if (it != known.end()) {
+      *out = it->second;
+      return cudaSuccess;
+    }
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, func, threads, smem);
+    if (e == cudaSuccess) known[key] = *out;
     return e;
   } catch (...) {
     return cudaErrorMemoryAllocation;

@@ -18,6 +18,10 @@ struct FfnDevice {
 // raise a kernel's dynamic shared-memory limit, once per device
 cudaError_t allow_smem_once(const void* func, size_t bytes);
 
+// CTAs of a kernel an SM holds at once with `smem` bytes of dynamic shared memory (its
+// limit is raised to `most`), asked once per device
+cudaError_t resident_ctas(const void* func, int threads, size_t smem, size_t most, int* out);
+
 // The pitches below are resolved (never 0).
 cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_t st);
 cudaError_t launch_gated_backward(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st);

@@ -36,19 +36,26 @@ __device__ __forceinline__ float element(const Pack<T, E>& p, int e) {
   }
 }
 
-// A thread's elements of a row: E adjacent ones from `first` on, those below `end`;
-// the lanes of a warp hold neighbouring groups.
+// A thread's elements of a row: E adjacent ones from `first` on, those of 0 .. end - 1
+// (`first` may lie before the row: see the shift below); the lanes of a warp hold
+// neighbouring groups.
+//
+// A row that starts `shift` elements past a 16-byte boundary is split over the
+// threads from that boundary on, so every group but the row's first and last is
+// whole 16-byte pieces in memory: odd row lengths cost no more than even ones.
 struct Places {
   int first, end;
-  __device__ __forceinline__ bool inside(int e) const { return first + e < end; }
+  __device__ __forceinline__ bool inside(int e) const { return first + e >= 0 && first + e < end; }
+  template <int E>
+  __device__ __forceinline__ bool whole() const { return first >= 0 && first + E <= end; }
 };
 
-// 16 aligned bytes, elements i .. of a row; those outside 0 .. end - 1 read as 0 and
-// are not touched
+// 16 bytes of a row from element i on; elements outside the row read as 0 and are not
+// touched, pieces off their boundary are read by element
 template <typename T>
-__device__ __forceinline__ void load_chunk(uint32_t* w, const T* row, int i, int end) {
+__device__ __forceinline__ void load_piece(uint32_t* w, const T* row, int i, int end) {
   constexpr int N = 16 / (int)sizeof(T);
-  if (i >= 0 && i + N <= end) {
+  if (i >= 0 && i + N <= end && (reinterpret_cast<uintptr_t>(row + i) & 15u) == 0) {
     const uint4 v = *reinterpret_cast<const uint4*>(row + i);
     w[0] = v.x;
     w[1] = v.y;
@@ -69,57 +76,11 @@ __device__ __forceinline__ void load_chunk(uint32_t* w, const T* row, int i, int
     }
 }
 
-// word i of `v` moved down by `bytes` (1 .. 15, of an element's size): v is shifted in
-// place, its last four words are consumed
-template <int W>
-__device__ __forceinline__ void shift_down(uint32_t (&v)[W], uint32_t bytes) {
-  if (bytes & 8u) {
-#pragma unroll
-    for (int i = 0; i + 2 < W; ++i) v[i] = v[i + 2];
-  }
-  if (bytes & 4u) {
-#pragma unroll
-    for (int i = 0; i + 1 < W; ++i) v[i] = v[i + 1];
-  }
-  if (bytes & 2u) {
-#pragma unroll
-    for (int i = 0; i + 1 < W; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
-  }
-}
-
-// Loads a warp's groups of a row that may start anywhere: where the row is off a
-// 16-byte boundary by m bytes, every lane loads the aligned chunks that its first
-// elements lie in, takes the chunk after them from the next lane, and shifts.  All
-// lanes of the warp call.
 template <typename T, int E>
 __device__ __forceinline__ void load(Pack<T, E>& p, const T* row, const Places& at) {
-  constexpr int N = 16 / (int)sizeof(T), W = Pack<T, E>::W;
-  const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  if (m == 0) {
+  constexpr int N = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int j = 0; j < W / 4; ++j) load_chunk(p.w + 4 * j, row, at.first + j * N, at.end);
-    return;
-  }
-  uint32_t v[W + 4];
-  const int start = at.first - (int)(m / sizeof(T));
-#pragma unroll
-  for (int j = 0; j < W / 4; ++j) load_chunk(v + 4 * j, row, start + j * N, at.end);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[W + k] = __shfl_down_sync(0xffffffffu, v[k], 1);
-  if (lane_idx() == 31) load_chunk(v + W, row, start + E, at.end);
-  shift_down(v, m);
-#pragma unroll
-  for (int i = 0; i < W; ++i) p.w[i] = v[i];
-  // (what follows `end` is 0 already: load_chunk reads nothing there)
-}
-
-template <typename T>
-__device__ __forceinline__ void store_one(T* p, uint32_t word, int odd) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<uint32_t*>(p) = word;
-  } else {
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)(odd ? word >> 16 : word);
-  }
+  for (int j = 0; j < E / N; ++j) load_piece(p.w + 4 * j, row, at.first + j * N, at.end);
 }
 
 template <typename T, int E>
@@ -140,54 +101,27 @@ __device__ __forceinline__ Pack<T, E> packed(const float (&f)[E]) {
   return p;
 }
 
-// The same way out: aligned chunks hold the end of a lane's group and the start of
-// the next lane's; the warp's first and last pieces are stored by element.
 template <typename T, int E>
 __device__ __forceinline__ void store(T* row, const float (&f)[E], const Places& at) {
-  constexpr int N = 16 / (int)sizeof(T), W = Pack<T, E>::W, PER = 4 / (int)sizeof(T);
-  const Pack<T, E> pw = packed<T>(f);
-  const uint32_t(&w)[W] = pw.w;
-  const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-  if (m == 0) {
+  constexpr int N = 16 / (int)sizeof(T), PER = 4 / (int)sizeof(T);
+  const Pack<T, E> p = packed<T>(f);
 #pragma unroll
-    for (int j = 0; j < W / 4; ++j) {
-      const int i = at.first + j * N;
-      if (i + N <= at.end) {
-        *reinterpret_cast<uint4*>(row + i) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (i + e < at.end) store_one(row + i + e, w[4 * j + e / PER], e % PER);
-      }
-    }
-    return;
-  }
-  // the chunks from the first boundary inside this lane's group on: `head` elements in
-  const int head = N - (int)(m / sizeof(T));
-  uint32_t v[W + 4];
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = w[i];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[W + k] = __shfl_down_sync(0xffffffffu, w[k], 1);
-  shift_down(v, 16u - m);
-  const bool last = lane_idx() == 31;
-#pragma unroll
-  for (int j = 0; j < W / 4; ++j) {
-    const int i = at.first + head + j * N;
-    // (the last lane has no next one: its last chunk ends with its group)
-    const int end = last ? min(at.end, at.first + E) : at.end;
-    if (i + N <= end) {
-      *reinterpret_cast<uint4*>(row + i) = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+  for (int j = 0; j < E / N; ++j) {
+    const int i = at.first + j * N;
+    if (i >= 0 && i + N <= at.end && (reinterpret_cast<uintptr_t>(row + i) & 15u) == 0) {
+      *reinterpret_cast<uint4*>(row + i) = make_uint4(p.w[4 * j], p.w[4 * j + 1], p.w[4 * j + 2], p.w[4 * j + 3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (i + e < end) store_one(row + i + e, v[4 * j + e / PER], e % PER);
+      for (int e = 0; e < N; ++e) {
+        const uint32_t w = p.w[4 * j + e / PER];
+        if (i + e < 0 || i + e >= at.end) continue;
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<uint32_t*>(row)[i + e] = w;
+        } else {
+          reinterpret_cast<uint16_t*>(row)[i + e] = (uint16_t)((e & 1) ? w >> 16 : w);
+        }
+      }
     }
-  }
-  if (lane_idx() == 0) {
-#pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (e < head && at.inside(e)) store_one(row + at.first + e, w[e / PER], e % PER);
   }
 }
 
@@ -203,6 +137,12 @@ __device__ __forceinline__ void parameters(float (&v)[E], const void* p, float a
   load(raw, static_cast<const P*>(p), at);
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = element(raw, e);
+}
+
+// a parameter array from element i on, or null
+template <typename P>
+__device__ __forceinline__ const P* from_column(const void* p, int64_t i) {
+  return p == nullptr ? nullptr : static_cast<const P*>(p) + i;
 }
 
 // Sums of N values (1, 2 or 4) over a warp, in every lane.  The values are added by
@@ -275,6 +215,15 @@ struct RowSums {
     const float* buf = exchange(v);
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.f;
+    if (warps * cluster <= 8) {
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (w >= warps * cluster) break;
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
+      }
+      return;
+    }
     for (int w = (int)lane_idx(); w < warps * cluster; w += 32) {
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
@@ -282,6 +231,12 @@ struct RowSums {
     warp_sums(v);
   }
 };
+
+// elements from the 16-byte boundary at or before a row to its start
+template <typename T>
+__device__ __forceinline__ int row_shift(const T* row) {
+  return (int)((uint32_t)reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
+}
 
 // ------------------------------------------------------------------- forward
 
@@ -297,8 +252,7 @@ __device__ __forceinline__ const P* gate_row(const void* gate, int64_t ld, int64
 // mean, and the warps' means and variances are then joined exactly,
 //   sum (v - mean)^2 = sum over warps of (its own sum + n_w (mean_w - mean)^2),
 // so one exchange serves both and nothing cancels.  n_w: the warp's elements.
-// WHOLE: vectors lie wholly in or out of the row.
-template <bool LAYER, bool WHOLE = false, int NV, int E>
+template <bool LAYER, int NV, int E>
 __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places (&at)[NV], int D, float n_w, float eps,
                                           RowSums& sum) {
   const float inv = 1.f / (float)D;
@@ -319,11 +273,20 @@ __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places 
     float mean = n_w > 0.f ? s[0] / n_w : 0.f;
     s[0] = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        if (at[j].template whole<E>()) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float c = at[j].inside(WHOLE ? 0 : e) ? v[j][e] - mean : 0.f;
-        s[0] = fmaf(c, c, s[0]);
+          for (int e = 0; e < E; ++e) {
+            const float c = v[j][e] - mean;
+            s[0] = fmaf(c, c, s[0]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float c = at[j].inside(e) ? v[j][e] - mean : 0.f;
+            s[0] = fmaf(c, c, s[0]);
+          }
+        }
       }
     warp_sums(s);
     if (!sum.alone()) {
@@ -350,7 +313,7 @@ template <int NV, int E>
 __device__ __forceinline__ float warp_elements(const Places (&at)[NV]) {
   float n[1] = {0.f};
 #pragma unroll
-  for (int j = 0; j < NV; ++j) n[0] += (float)min(max(at[j].end - at[j].first, 0), E);
+  for (int j = 0; j < NV; ++j) n[0] += (float)(max(0, min(at[j].end, at[j].first + E)) - max(0, min(at[j].end, at[j].first)));
   warp_sums(n);
   return n[0];
 }
@@ -367,7 +330,9 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_no
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     at[j].end = D;
-    at[j].first = (j * per_row + tid) * E;
+    // (shifted as rows without gaps from a 16-byte boundary on: which elements a thread
+    // adds up depends on the sizes alone)
+    at[j].first = (j * per_row + tid) * E - (int)(((uint32_t)r * (uint32_t)D * (uint32_t)sizeof(T)) & 15u) / (int)sizeof(T);
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -425,6 +390,33 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_no
 
 // ------------------------------------------------------------------ backward
 
+// The rows of one part.  Rows `period` apart start at the same offset to 16-byte
+// boundaries (period = 1 where all do), and a part takes rows of one such class, so
+// that its threads' columns stay the same: parts are numbered slice by slice, and
+// within a slice of a group's rows class by class.
+struct NormWalk {
+  int64_t first, end, step, group;
+};
+template <bool MANY>
+__device__ __forceinline__ NormWalk norm_walk(const ffn_norm_grad_t& a, const NormGradShape& sh, int part) {
+  const int64_t per = a.M / a.groups;
+  NormWalk w;
+  if constexpr (MANY) {
+    w.group = a.groups * part / sh.parts;
+    w.first = w.group * per;
+    w.end = a.groups * (part + 1) / sh.parts * per;
+    w.step = 1;
+  } else {
+    w.group = part / sh.parts_per_group;
+    const int64_t i = part % sh.parts_per_group, slice = i / sh.period, slices = sh.parts_per_group / sh.period;
+    const int64_t blocks = (per + sh.period - 1) / sh.period;  // of `period` rows
+    w.first = w.group * per + blocks * slice / slices * sh.period + i % sh.period;
+    w.end = w.group * per + min(per, blocks * (slice + 1) / slices * sh.period);
+    w.step = sh.period;
+  }
+  return w;
+}
+
 // The arithmetic of a row's elements.
 __device__ __forceinline__ float unit_value(float v, float mean, float r) { return __fmul_rn(v - mean, r); }
 // r (a - u mean(a u) - mean(a)), added to t
@@ -447,28 +439,19 @@ __device__ __forceinline__ float unit_slope(float t, float r, float a, float u, 
 // Rows come through RowsIn, a ring in shared memory (kernels_norm_ring.cuh).
 template <bool LAYER, bool BIAS, bool MANY, typename T, typename P, typename RowsIn>
 __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
-                                               RowsIn& rows, RowSums& sum, int part, const Places (&at)[2]) {
+                                               RowsIn& rows, RowSums& sum, int part, const NormWalk& walk,
+                                               const Places (&at)[2], int col0) {
   constexpr int E = 8, G = 2;
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
   const int64_t per = a.M / a.groups;
-  int64_t r0, r1, g;
-  if constexpr (MANY) {
-    g = a.groups * part / sh.parts;
-    r0 = g * per;
-    r1 = a.groups * (part + 1) / sh.parts * per;
-  } else {
-    g = part / sh.parts_per_group;
-    const int64_t i = part % sh.parts_per_group;
-    r0 = g * per + per * i / sh.parts_per_group;
-    r1 = g * per + per * (i + 1) / sh.parts_per_group;
-  }
-  int64_t group_end = (g + 1) * per;
+  int64_t g = walk.group, group_end = (g + 1) * per;
+  const bool whole[G] = {at[0].template whole<E>(), at[1].template whole<E>()};
   float A[G][E] = {}, C[G][E] = {}, B[G][BIAS ? E : 1] = {}, Eo[G][BIAS ? E : 1] = {};
   float GA[G][MANY ? E : 1] = {}, GB[G][(MANY && BIAS) ? E : 1] = {};
   rows.set_group(g);
-  rows.begin(r0, r1);
-  for (int64_t r = r0; r < r1; ++r) {
+  rows.begin(walk);
+  for (int64_t r = walk.first; r < walk.end; r += walk.step) {
     if (!rows.next(r)) break;
     float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[4];
     if constexpr (LAYER) {
@@ -508,7 +491,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         rows.scale_pre(dn, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float c = !LAYER || at[j].inside(RowsIn::kWhole ? 0 : e) ? s[e] - mean_s : 0.f;
+          const float c = s[e] - (LAYER ? (whole[j] || at[j].inside(e) ? mean_s : 0.f) : 0.f);
           k[0] = fmaf(c, c, k[0]);
           k[1] = fmaf(c, dn[e], k[1]);
         }
@@ -518,7 +501,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         rows.y(y, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float c = !LAYER || at[j].inside(RowsIn::kWhole ? 0 : e) ? y[e] - mean_y : 0.f;
+          const float c = y[e] - (LAYER ? (whole[j] || at[j].inside(e) ? mean_y : 0.f) : 0.f);
           k[2] = fmaf(c, c, k[2]);
         }
       }
@@ -582,16 +565,16 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
 #pragma unroll
         for (int e = 0; e < E; ++e) t[j][e] = unit_slope(t[j][e], r_s, dn[e], s[e], mean_au, mean_a);
       }
-      if (LAYER) {
+      if (LAYER && !whole[j]) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (!at[j].inside(RowsIn::kWhole ? 0 : e)) t[j][e] = 0.f;  // (0 - mean)
+          if (!at[j].inside(e)) t[j][e] = 0.f;  // (0 - mean)
       }
       if (a.dresidual != nullptr) {
         float o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[j][e];
-        rows.put(static_cast<T*>(a.dresidual) + r * a.ld_dresidual, o, at[j]);
+        rows.template put<0>(static_cast<T*>(a.dresidual) + r * a.ld_dresidual + col0, o, j);
       }
       float y[E];
       if (a.y != nullptr) {
@@ -634,7 +617,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         }
       }
 #pragma unroll
-      for (int j = 0; j < G; ++j) rows.put(static_cast<T*>(a.dy) + r * a.ld_dy, t[j], at[j]);
+      for (int j = 0; j < G; ++j) rows.template put<1>(static_cast<T*>(a.dy) + r * a.ld_dy + col0, t[j], j);
     }
     rows.done();
     if constexpr (MANY) {
@@ -646,19 +629,19 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = a.branch_scale * A[j][e];
             float pw[E];
-            parameters<P>(pw, a.post_weight, 1.f, at[j]);
+            parameters<P>(pw, from_column<P>(a.post_weight, col0), 1.f, at[j]);
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = __fmul_rn(o[e], pw[e]);
             if constexpr (BIAS) {
               float pb[E];
-              parameters<P>(pb, a.post_bias, 0.f, at[j]);
+              parameters<P>(pb, from_column<P>(a.post_bias, col0), 0.f, at[j]);
 #pragma unroll
               for (int e = 0; e < E; ++e) o[e] = fmaf(a.branch_scale * B[j][e], pb[e], o[e]);
             }
-            store(a.dgate + g * (int64_t)a.D, o, at[j]);
+            store(a.dgate + g * a.D + col0, o, at[j]);
           }
           float gate[E];
-          parameters<P>(gate, a.gate != nullptr ? static_cast<const P*>(a.gate) + g * a.ld_gate : nullptr, 1.f, at[j]);
+          parameters<P>(gate, from_column<P>(a.gate, g * a.ld_gate + col0), 1.f, at[j]);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             GA[j][e] = fmaf(gate[e], A[j][e], GA[j][e]);
@@ -671,12 +654,12 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         }
         ++g;
         group_end += per;
-        if (r + 1 < r1) rows.set_group(g);
+        if (r + 1 < walk.end) rows.set_group(g);
       }
     }
   }
   // the sums of this part's rows, for k_norm_column_sums
-  const int64_t out = (int64_t)part * a.D;
+  const int64_t out = (int64_t)part * a.D + col0;
 #pragma unroll
   for (int j = 0; j < G; ++j) {
     if constexpr (MANY) {
@@ -696,22 +679,6 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
     }
   }
 }
-
-// Where a thread of the backward kernel stands: its part and its columns.
-struct NormGradPlace {
-  int rank, tid, group, part, col0, cols;
-  Places at[2];
-  __device__ __forceinline__ NormGradPlace(const ffn_norm_grad_t& a, const NormGradShape& sh) {
-    rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
-    tid = sh.lanes > 1 ? (int)lane_idx() : (int)threadIdx.x;
-    group = sh.lanes > 1 ? (int)(threadIdx.x >> 5) : 0;
-    part = sh.lanes > 1 ? (int)blockIdx.x * sh.lanes + group : (int)blockIdx.x / sh.cluster;
-    col0 = (int)(rank * sh.columns);
-    cols = min((int)a.D - col0, (int)sh.columns);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) at[j] = Places{col0 + (j * sh.threads + tid) * 8, col0 + cols};
-  }
-};
 
 template <typename P>
 __device__ __forceinline__ float parameter(const void* p, int64_t i, float absent) {

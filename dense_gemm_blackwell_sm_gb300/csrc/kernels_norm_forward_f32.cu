@@ -3,9 +3,9 @@
 
 namespace dgb {
 
-cudaError_t norm_forward_f32(const ffn_norm_t& a, const NormShape& sh,
+cudaError_t norm_forward_f32(const ffn_norm_t& a, const NormShape& direct, const NormShape* ring,
                          const FfnDevice& dev, cudaStream_t st) {
-  return norm_forward<float, float>(a, sh, dev, st);
+  return norm_forward<float, float>(a, direct, ring, dev, st);
 }
 
 }  // namespace dgb

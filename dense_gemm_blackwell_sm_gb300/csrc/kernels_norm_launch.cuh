@@ -2,6 +2,8 @@
 // type and one parameter type.
 #pragma once
 
+#include <algorithm>
+
 #include "kernels_norm.cuh"
 #include "kernels_norm_ring.cuh"
 #include "launch.h"
@@ -45,42 +47,50 @@ const void* norm_kernel(const NormShape& sh) {
   }
 }
 
-template <typename T, typename P, bool ALIGNED, bool LAYER>
+template <typename T, typename P, bool LAYER>
 const void* norm_ring_kernel(const NormShape& sh) {
   if (sh.warp_rows) {
     switch (sh.nv) {
-      case 1: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 1>;
-      case 2: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 2>;
-      default: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, true, 4>;
+      case 1: return (const void*)k_norm_ring<T, P, LAYER, true, 1>;
+      case 2: return (const void*)k_norm_ring<T, P, LAYER, true, 2>;
+      default: return (const void*)k_norm_ring<T, P, LAYER, true, 4>;
     }
   }
-  switch (sh.nv) {
-    case 1: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 1>;
-    case 2: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 2>;
-    default: return (const void*)k_norm_ring<T, P, ALIGNED, LAYER, false, 4>;
+  if constexpr (!LAYER) {
+    if (sh.nv == 4) return (const void*)k_norm_ring<T, P, false, false, 4>;
   }
+  return (const void*)k_norm_ring<T, P, LAYER, false, 2>;
 }
 
 template <typename T, typename P>
-cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& sh, const FfnDevice& dev, cudaStream_t st) {
+cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& direct, const NormShape* ring, const FfnDevice& dev,
+                         cudaStream_t st) {
   const bool layer = a.kind == FFN_NORM_LAYER;
   ffn_norm_t args_a = a;
   uint32_t* status = dev.status;
-  void* args[] = {&args_a, &status};
-  const void* k = sh.ring ? (sh.aligned ? (layer ? norm_ring_kernel<T, P, true, true>(sh) : norm_ring_kernel<T, P, true, false>(sh))
-                                        : (layer ? norm_ring_kernel<T, P, false, true>(sh)
-                                                 : norm_ring_kernel<T, P, false, false>(sh)))
-                          : (layer ? norm_kernel<T, P, true>(sh) : norm_kernel<T, P, false>(sh));
-  return launch_dependent(k, dim3((unsigned)sh.grid), sh.threads, 1, sh.smem, args, st);
+  if (ring != nullptr) {
+    NormShape sh = *ring;
+    const void* k = layer ? norm_ring_kernel<T, P, true>(sh) : norm_ring_kernel<T, P, false>(sh);
+    int per_sm = 0;
+    const cudaError_t e = resident_ctas(k, sh.threads, sh.smem, kNormRingBytes, &per_sm);
+    if (e != cudaSuccess) return e;
+    // (a CTA of warps holds whole periods of parts: 8 is a multiple of every period)
+    const int64_t unit = sh.warp_rows ? 1 : sh.period, groups = sh.warp_rows ? sh.threads / 32 : 1;
+    sh.grid = std::max<int64_t>(unit, (int64_t)per_sm * dev.num_sms / unit * unit);
+    if (a.M >= 2 * sh.grid * groups) {
+      void* args[] = {&args_a, &sh, &status};
+      return launch_dependent(k, dim3((unsigned)sh.grid), sh.threads, 1, sh.smem, args, st);
+    }
+  }
+  void* args[] = {&args_a};
+  return launch_dependent(layer ? norm_kernel<T, P, true>(direct) : norm_kernel<T, P, false>(direct),
+                          dim3((unsigned)direct.grid), direct.threads, 1, 0, args, st);
 }
 
 template <typename T, typename P, bool LAYER, bool BIAS>
 const void* norm_grad_kernel(const NormGradShape& sh) {
-  if (sh.aligned)
-    return sh.many ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, true>
-                   : (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false>;
-  return sh.many ? (const void*)k_norm_grad<T, P, false, LAYER, BIAS, true>
-                 : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false>;
+  return sh.many ? (const void*)k_norm_grad<T, P, LAYER, BIAS, true>
+                 : (const void*)k_norm_grad<T, P, LAYER, BIAS, false>;
 }
 
 template <typename T, typename P>

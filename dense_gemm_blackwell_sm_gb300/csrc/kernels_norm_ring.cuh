@@ -1,12 +1,12 @@
 // kernels_norm_ring.cuh -- the block norms with rows that come through a ring in
 // shared memory filled by bulk copies (cp.async.bulk), so an SM has tens of KB on
 // their way whatever its threads do, and the backward kernel can read a row's values
-// again instead of holding them in registers.  Rows may start anywhere: a copy
-// brings the whole 16-byte pieces a row lies in, and reads shift by its offset.
+// again instead of holding them in registers.
 //
 // A group (a warp, a CTA, or in the backward kernel a cluster of CTAs that share
-// the columns) walks its rows with `stages` rows ahead.  Every wait is bounded; a
-// wait that runs out is recorded in the device's status word.
+// the columns) walks rows that start at the same offset to 16-byte boundaries, a few
+// rows ahead in the ring.  Every wait is bounded; a wait that runs out is recorded in
+// the device's status word.
 #pragma once
 
 #include "kernels_norm.cuh"
@@ -14,11 +14,6 @@
 namespace dgb {
 
 namespace {
-
-// raise the transaction bytes a phase expects, without arriving
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -50,9 +45,9 @@ struct Ring {
   uint64_t* full;      // [stages]
   volatile uint32_t* abort_flag;
   uint32_t* status;
-  uint32_t stages, arrays, bytes, pitch;  // bytes of a row (slice); of a slot
-  uint32_t stage = 0, phase = 0;          // of the row being read
-  uint32_t filled = 0;                    // (the group's first thread) the stage to fill next
+  uint32_t stages, arrays, pitch;  // bytes of a slot
+  uint32_t stage = 0, phase = 0;   // of the row being read
+  uint32_t filled = 0;             // (the group's first thread) the stage to fill next
 
   __device__ __forceinline__ uint8_t* slot(uint32_t st, uint32_t array) const {
     return slots + (size_t)((st * arrays + array) * pitch);
@@ -72,197 +67,148 @@ struct Ring {
   }
 };
 
-// One array of a call: where its rows are, and where they may be read.
-template <typename T, bool ALIGNED>
-struct RingArray {
-  const T* base;  // row 0, from this group's first column on
-  int64_t ld;
-  uintptr_t lo, hi;  // the array's first byte and the end of its last row
-
-  __device__ __forceinline__ RingArray(const void* p, int64_t pitch, int64_t rows, int64_t D, int col0)
-      : base(static_cast<const T*>(p) + col0), ld(pitch), lo(reinterpret_cast<uintptr_t>(p)) {
-    hi = lo + (uintptr_t)(((rows - 1) * pitch + D) * (int64_t)sizeof(T));
+// Brings row slices that start `shift` elements past a 16-byte boundary to slots, which
+// keep that offset: `pieces` bytes from the boundary on.  In an array's last row the
+// last piece may reach past the array; its elements are then copied one by one, so
+// nothing outside an array is read.
+template <typename T>
+struct RowCopies {
+  uint32_t pieces, tail;  // bytes copied per row; elements of a partial last piece
+  int shift;
+  __device__ __forceinline__ RowCopies(int shift_, int cols, bool ends_row) : shift(shift_) {
+    constexpr uint32_t N = 16 / sizeof(T);
+    const uint32_t n = (uint32_t)(shift + cols);
+    pieces = (n + N - 1) / N * 16u;
+    tail = ends_row ? n % N : 0u;
   }
-  // how far row r starts past a 16-byte boundary
-  __device__ __forceinline__ uint32_t off(int64_t r) const {
-    if constexpr (ALIGNED) return 0u;
-    return ((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)r * (uint32_t)(ld * (int64_t)sizeof(T))) & 15u;
-  }
-  // The 16-byte pieces row r's `bytes` lie in, [from, to); where the first or last of
-  // them reaches outside the array, only the pieces inside.
-  __device__ __forceinline__ void span(int64_t r, uint32_t bytes, uintptr_t& from, uintptr_t& to) const {
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(base + r * ld), end = begin + bytes;
-    from = begin & ~(uintptr_t)15;
-    to = (end + 15) & ~(uintptr_t)15;
-    if (from < lo) from += 16;
-    if (to > hi) to -= 16;
-    if (to < from) to = from;
-  }
-  // Brings row r to `slot`, which keeps its offset to 16-byte boundaries: whole pieces
-  // by a bulk copy, elements of pieces that reach outside the array one by one.
-  __device__ __forceinline__ void copy(int64_t r, uint32_t bytes, uint8_t* slot, uint32_t bar) const {
-    if constexpr (ALIGNED) {
-      bulk_load(smem_u32(slot), base + r * ld, bytes, bar);
-      return;
+  // (n arrays, their rows' first elements in `rows`, the slots `pitch` bytes apart)
+  template <int MOST>
+  __device__ __forceinline__ void issue(const T* const (&rows)[MOST], uint8_t* slot, uint32_t pitch, uint32_t bar,
+                                        bool last_row) const {
+    const uint32_t cut = last_row && tail != 0 ? 16u : 0u;
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) n += rows[k] != nullptr ? 1u : 0u;
+    if (cut != 0) {
+#pragma unroll 1
+      for (int k = 0; k < MOST; ++k) {
+        const T* row = rows[0];
+#pragma unroll
+        for (int q = 1; q < MOST; ++q) row = k == q ? rows[q] : row;
+        if (row == nullptr) continue;
+        T* to = reinterpret_cast<T*>(slot + k * pitch);
+        const int first = (int)((pieces - 16u) / sizeof(T));
+        for (int e = first; e < first + (int)tail; ++e)
+          if (e >= shift) to[e] = row[e - shift];
+      }
     }
-    uintptr_t from, to;
-    span(r, bytes, from, to);
-    const uintptr_t begin = reinterpret_cast<uintptr_t>(base + r * ld), end = begin + bytes;
-    const uintptr_t origin = begin & ~(uintptr_t)15;
-    for (uintptr_t q = begin; q < end && q < from; q += sizeof(T))
-      *reinterpret_cast<T*>(slot + (q - origin)) = *reinterpret_cast<const T*>(q);
-    for (uintptr_t q = to > begin ? to : begin; q < end; q += sizeof(T))
-      if (q >= from) *reinterpret_cast<T*>(slot + (q - origin)) = *reinterpret_cast<const T*>(q);
-    if (to > from) bulk_load(smem_u32(slot + (from - origin)), reinterpret_cast<const void*>(from), (uint32_t)(to - from), bar);
-  }
-  __device__ __forceinline__ uint32_t copied(int64_t r, uint32_t bytes) const {
-    if constexpr (ALIGNED) return bytes;
-    uintptr_t from, to;
-    span(r, bytes, from, to);
-    return (uint32_t)(to - from);
+    mbar_arrive_expect_tx(bar, n * (pieces - cut));  // (after the elements copied one by one)
+    if (pieces == cut) return;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k)
+      if (rows[k] != nullptr) bulk_load(smem_u32(slot + k * pitch), rows[k] - shift, pieces - cut, bar);
   }
 };
 
-// bytes of a slot: a row at any offset, and the piece after it that a shifted read touches
-__host__ __device__ constexpr uint32_t ring_pitch(uint32_t bytes) { return (bytes + 31u) / 32u * 32u + 32u; }
-
-// E elements from element `i` on of the row at offset m of a slot; 0 from element
-// `end` on
-template <typename T, bool ALIGNED, int E>
-__device__ __forceinline__ void from_slot(float (&v)[E], const uint8_t* slot, uint32_t m, int i, int end) {
-  constexpr int W = Pack<T, E>::W;
+// A group's E elements from a slot; `piece` is the thread's first 16-byte piece there.
+template <typename T, int E>
+__device__ __forceinline__ void from_slot(float (&v)[E], const uint8_t* slot, int piece) {
+  const uint4* from = reinterpret_cast<const uint4*>(slot) + piece;
   Pack<T, E> p;
-  const uint4* from = reinterpret_cast<const uint4*>(slot + (size_t)i * sizeof(T));
-  if constexpr (ALIGNED) {
-    const bool live = i < end;
 #pragma unroll
-    for (int k = 0; k < W / 4; ++k) {
-      const uint4 q = live ? from[k] : make_uint4(0u, 0u, 0u, 0u);
-      p.w[4 * k] = q.x;
-      p.w[4 * k + 1] = q.y;
-      p.w[4 * k + 2] = q.z;
-      p.w[4 * k + 3] = q.w;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = element(p, e);
-  } else {
-    uint32_t w[W + 4];
-#pragma unroll
-    for (int k = 0; k < W / 4 + 1; ++k) {
-      const uint4 q = i < end ? from[k] : make_uint4(0u, 0u, 0u, 0u);
-      w[4 * k] = q.x;
-      w[4 * k + 1] = q.y;
-      w[4 * k + 2] = q.z;
-      w[4 * k + 3] = q.w;
-    }
-    shift_down(w, m);
-#pragma unroll
-    for (int k = 0; k < W; ++k) p.w[k] = w[k];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = i + e < end ? element(p, e) : 0.f;
+  for (int k = 0; k < Pack<T, E>::W / 4; ++k) {
+    const uint4 q = from[k];
+    p.w[4 * k] = q.x;
+    p.w[4 * k + 1] = q.y;
+    p.w[4 * k + 2] = q.z;
+    p.w[4 * k + 3] = q.w;
   }
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = element(p, e);
 }
 
-// a parameter vector's elements; the vectors of an ALIGNED call start on 16-byte boundaries
-template <typename P, bool ALIGNED, int E>
-__device__ __forceinline__ void row_parameters(float (&v)[E], const void* p, float absent, const Places& at) {
-  if constexpr (!ALIGNED) {
-    parameters<P>(v, p, absent, at);
-  } else {
-    if (p == nullptr) {
+// A row's first and last group (and those past it) hold elements of other rows or
+// nothing: the thread that reads them makes them 0 in its own piece of the slot, so
+// that no reader has to look.  (Ordered before the bulk copy that refills the slot.)
+template <typename T, int E>
+__device__ __forceinline__ void clean_slot(uint8_t* slot, int piece, const Places& at) {
+  T* to = reinterpret_cast<T*>(slot + (size_t)piece * 16);
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = absent;
-      return;
-    }
-    Pack<P, E> raw;
-#pragma unroll
-    for (int k = 0; k < Pack<P, E>::W / 4; ++k) {
-      const uint4 q = at.inside(0) ? __ldg(reinterpret_cast<const uint4*>(static_cast<const P*>(p) + at.first) + k)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-      raw.w[4 * k] = q.x;
-      raw.w[4 * k + 1] = q.y;
-      raw.w[4 * k + 2] = q.z;
-      raw.w[4 * k + 3] = q.w;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = element(raw, e);
-  }
+  for (int e = 0; e < E; ++e)
+    if (!at.inside(e)) to[e] = from_f32<T>(0.f);
+  fence_proxy_async_smem();
 }
 
-template <typename T, bool ALIGNED, int E>
-__device__ __forceinline__ void row_store(T* row, const float (&f)[E], const Places& at) {
-  if constexpr (!ALIGNED) {
-    store(row, f, at);
-  } else {
-    if (!at.inside(0)) return;
-    const Pack<T, E> w = packed<T>(f);
+// A group's E elements to a row that starts at the shift its places were made for.
+template <typename T, int E>
+__device__ __forceinline__ void to_row(T* row, const float (&f)[E], const Places& at, bool whole) {
+  if (!whole) {
 #pragma unroll
-    for (int k = 0; k < Pack<T, E>::W / 4; ++k)
-      reinterpret_cast<uint4*>(row + at.first)[k] =
-          make_uint4(w.w[4 * k], w.w[4 * k + 1], w.w[4 * k + 2], w.w[4 * k + 3]);
+    for (int e = 0; e < E; ++e)
+      if (at.inside(e)) row[at.first + e] = from_f32<T>(f[e]);
+    return;
   }
+  const Pack<T, E> p = packed<T>(f);
+#pragma unroll
+  for (int k = 0; k < Pack<T, E>::W / 4; ++k)
+    reinterpret_cast<uint4*>(row + at.first)[k] =
+        make_uint4(p.w[4 * k], p.w[4 * k + 1], p.w[4 * k + 2], p.w[4 * k + 3]);
 }
 
 // ------------------------------------------------------------------- forward
 
-// A thread keeps its columns' parameters in registers where it has at most two
-// vectors (HOLD): with 32-bit parameters they are more bytes than a 16-bit row, and
-// with most of the SM's memory given to the ring they would come from L2 for every
-// row (8192 x 4096: 63 us read per row).
-template <typename P, bool ALIGNED, int NV, int E, bool HOLD>
+// A thread keeps its columns' factors in registers where it can (HOLD): with 32-bit
+// parameters they are more bytes than a 16-bit row, and with most of the SM's memory
+// given to the ring they would come from L2 for every row (8192 x 4096: 63 us so).
+//   z -> s:  post_weight * gate * branch_scale, post_bias * gate * branch_scale
+//   s -> n:  pre_weight, pre_bias
+template <typename P, bool LAYER, int NV, int E>
 struct RowFactors {
-  const P* p;
-  float held[HOLD ? NV : 1][HOLD ? E : 1];
-  __device__ __forceinline__ RowFactors(const void* from, const Places (&at)[NV]) : p(static_cast<const P*>(from)) {
-    if constexpr (HOLD) {
-      if (p != nullptr) {
+  static constexpr int NB = LAYER ? NV : 1, EB = LAYER ? E : 1;  // biases are held for the layer norm
+  float branch[NV][E], branch_bias[NB][EB], pre[NV][E], pre_bias[NB][EB];
+
+  __device__ __forceinline__ void for_gate(const ffn_norm_t& a, const P* gate, const Places (&at)[NV]) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) row_parameters<P, ALIGNED>(held[j], p, 1.f, at[j]);
+    for (int j = 0; j < NV; ++j) {
+      float g[E];
+      parameters<P>(g, gate, 1.f, at[j]);
+      parameters<P>(branch[j], a.post_weight, 1.f, at[j]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) branch[j][e] *= a.branch_scale * g[e];
+      if constexpr (LAYER) {
+        parameters<P>(branch_bias[j], a.post_bias, 0.f, at[j]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) branch_bias[j][e] *= a.branch_scale * g[e];
       }
     }
   }
-  __device__ __forceinline__ void times(float (&v)[E], int j, const Places& at) const {
-    if (p == nullptr) return;
-    float f[E];
-    get(f, j, at);
+  __device__ __forceinline__ RowFactors(const ffn_norm_t& a, const Places (&at)[NV]) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= f[e];
-  }
-  __device__ __forceinline__ void plus(float (&v)[E], int j, const Places& at) const {
-    if (p == nullptr) return;
-    float f[E];
-    get(f, j, at);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += f[e];
-  }
-  __device__ __forceinline__ void get(float (&f)[E], int j, const Places& at) const {
-    if constexpr (HOLD) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = held[j][e];
-    } else {
-      row_parameters<P, ALIGNED>(f, p, 1.f, at);
+    for (int j = 0; j < NV; ++j) {
+      parameters<P>(pre[j], a.pre_weight, 1.f, at[j]);
+      if constexpr (LAYER) parameters<P>(pre_bias[j], a.pre_bias, 0.f, at[j]);
     }
   }
 };
 
-template <typename T, typename P, bool ALIGNED, bool LAYER, bool WARP, int NV>
-__global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(const __grid_constant__ ffn_norm_t a, uint32_t* status) {
+// An RMS norm with biases reads them for every row.
+template <typename T, typename P, bool LAYER, bool WARP, int NV>
+__global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) ? 2 : 1)
+    k_norm_ring(const __grid_constant__ ffn_norm_t a, const __grid_constant__ NormShape sh, uint32_t* status) {
   constexpr int E = 16 / (int)sizeof(T);
-  constexpr bool HOLD = !WARP && NV <= 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[8 * kNormStages];
   __shared__ float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
   const int tid = WARP ? (int)lane_idx() : (int)threadIdx.x, per_row = WARP ? 32 : (int)blockDim.x;
-  const int group = WARP ? (int)(threadIdx.x >> 5) : 0, groups = WARP ? (int)(blockDim.x / 32) : 1;
+  const int lane_group = WARP ? (int)(threadIdx.x >> 5) : 0, groups = WARP ? (int)(blockDim.x / 32) : 1;
   const int D = (int)a.D;
   Ring ring;
   ring.stages = kNormStages;
   ring.arrays = a.residual != nullptr ? 2u : 1u;
-  ring.bytes = (uint32_t)(D * (int)sizeof(T));
-  ring.pitch = ring_pitch(ring.bytes);
-  ring.slots = smem + (size_t)group * ring.stages * ring.arrays * ring.pitch;
-  ring.full = bars + group * kNormStages;
+  ring.pitch = (uint32_t)(NV * per_row * 16);
+  ring.slots = smem + (size_t)lane_group * ring.stages * ring.arrays * ring.pitch;
+  ring.full = bars + lane_group * kNormStages;
   ring.abort_flag = &abort_flag;
   ring.status = status;
   RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
@@ -274,20 +220,23 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(co
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t step = (int64_t)gridDim.x * groups, r0 = (int64_t)blockIdx.x * groups + group;
+  // this group's rows: a slice, and in it the rows of one class (see norm_walk)
+  const int64_t part = (int64_t)blockIdx.x * groups + lane_group, slices = (int64_t)gridDim.x * groups / sh.period;
+  const int64_t slice = part / sh.period, blocks = (a.M + sh.period - 1) / sh.period, step = sh.period;
+  if (slice >= slices) return;  // (whole groups: only a CTA of warps has any left over)
+  const int64_t r0 = blocks * slice / slices * step + part % step;
+  const int64_t r1 = min(a.M, blocks * (slice + 1) / slices * step);
+  if (r0 >= r1) return;
+  const int shift = row_shift(static_cast<const T*>(a.y) + r0 * a.ld_y);
   int64_t ahead = r0;  // (the group's first thread) the row to fetch next
   uint32_t in_flight = 0;
-  const RingArray<T, ALIGNED> in_y(a.y, a.ld_y, a.M, D, 0), in_res(a.residual, a.ld_residual, a.M, D, 0);
+  const RowCopies<T> copies(shift, D, true);
   auto issue = [&]() {
-    if (ahead >= a.M) return;
-    const uint32_t bar = smem_u32(ring.full + ring.filled);
-    const bool two = a.residual != nullptr;
-    // (the elements a copy brings one by one are ordered by this arrival: they come first)
-    const uint32_t bytes = in_y.copied(ahead, ring.bytes) + (two ? in_res.copied(ahead, ring.bytes) : 0u);
-    mbar_expect_tx(bar, bytes);
-    in_y.copy(ahead, ring.bytes, ring.slot(ring.filled, 0), bar);
-    if (two) in_res.copy(ahead, ring.bytes, ring.slot(ring.filled, 1), bar);
-    mbar_arrive(bar);
+    if (ahead >= r1) return;
+    const T* const rows[2] = {
+        static_cast<const T*>(a.y) + ahead * a.ld_y,
+        a.residual != nullptr ? static_cast<const T*>(a.residual) + ahead * a.ld_residual : nullptr};
+    copies.issue(rows, ring.slot(ring.filled, 0), ring.pitch, smem_u32(ring.full + ring.filled), ahead == a.M - 1);
     if (++ring.filled == ring.stages) ring.filled = 0;
     ahead += step;
     ++in_flight;
@@ -297,63 +246,67 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(co
 
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   Places at[NV];
+  bool whole[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) at[j] = Places{(j * per_row + tid) * E, D};
+  for (int j = 0; j < NV; ++j) {
+    at[j] = Places{(j * per_row + tid) * E - shift, D};
+    whole[j] = at[j].template whole<E>();
+  }
   const float n_w = LAYER ? warp_elements<NV, E>(at) : 0.f;
-  const bool one_gate = a.groups == 1;
-  const RowFactors<P, ALIGNED, NV, E, HOLD> post_weight(a.post_weight, at), pre_weight(a.pre_weight, at),
-      shared_gate(one_gate ? a.gate : nullptr, at);
-  const RowFactors<P, ALIGNED, NV, E, HOLD && LAYER> post_bias(a.post_bias, at), pre_bias(a.pre_bias, at);
-  for (int64_t r = r0; r < a.M; r += step) {
-    float own_gate[NV][E];  // (asked for early: it comes from L2)
-    if (a.gate != nullptr && !one_gate) {
+  RowFactors<P, LAYER, NV, E> f(a, at);
+  const int64_t per = a.M / a.groups;
+  int64_t gate_end = 0;  // the first row with another gate
+  for (int64_t r = r0; r < r1; r += step) {
+    if (r >= gate_end) {
       const P* gate = gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) row_parameters<P, ALIGNED>(own_gate[j], gate, 1.f, at[j]);
+      gate_end = a.gate == nullptr ? a.M : (r / per + 1) * per;
+      f.for_gate(a, gate, at);
     }
     if (!ring.wait(in_flight)) return;
-    const uint32_t off_y = in_y.off(r), off_res = in_res.off(r);
     float v[NV][E];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) from_slot<T, ALIGNED>(v[j], ring.slot(ring.stage, 0), off_y, at[j].first, D);
-    if (post) {
-      const float2 st = unit_of<LAYER, ALIGNED>(v, at, D, n_w, a.eps, sum);
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
-        post_weight.times(v[j], j, at[j]);
-        post_bias.plus(v[j], j, at[j]);
+    for (int j = 0; j < NV; ++j)
+      if (!whole[j]) {
+        clean_slot<T, E>(ring.slot(ring.stage, 0), j * per_row + tid, at[j]);
+        if (a.residual != nullptr) clean_slot<T, E>(ring.slot(ring.stage, 1), j * per_row + tid, at[j]);
       }
-    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) from_slot<T>(v[j], ring.slot(ring.stage, 0), j * per_row + tid);
+    float2 st = make_float2(0.f, 1.f);
+    if (post) st = unit_of<LAYER>(v, at, D, n_w, a.eps, sum);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (post) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[j][e] *= a.branch_scale;
-      if (a.gate != nullptr) {
-        if (one_gate) {
-          shared_gate.times(v[j], j, at[j]);
-        } else {
+        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
+      }
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] *= own_gate[j][e];
-        }
+      for (int e = 0; e < E; ++e) v[j][e] *= f.branch[j][e];
+      if constexpr (LAYER) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[j][e] += f.branch_bias[j][e];
+      } else if (a.post_bias != nullptr) {
+        float b[E], g[E];
+        parameters<P>(b, a.post_bias, 0.f, at[j]);
+        parameters<P>(g, gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r), 1.f, at[j]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[j][e] = fmaf(b[e], a.branch_scale * g[e], v[j][e]);
       }
       if (a.residual != nullptr) {
         float q[E];
-        from_slot<T, ALIGNED>(q, ring.slot(ring.stage, 1), off_res, at[j].first, D);
+        from_slot<T>(q, ring.slot(ring.stage, 1), j * per_row + tid);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[j][e] = fmaf(a.residual_scale, q[e], v[j][e]);
       }
-      if (!ALIGNED || LAYER) {  // (past the end: a mean or a bias of the post norm)
+      if (LAYER && !whole[j]) {  // (past the row: a mean)
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (!at[j].inside(ALIGNED ? 0 : e)) v[j][e] = 0.f;
+          if (!at[j].inside(e)) v[j][e] = 0.f;
       }
-      if (a.s != nullptr) row_store<T, ALIGNED>(static_cast<T*>(a.s) + r * a.ld_s, v[j], at[j]);
+      if (a.s != nullptr) to_row(static_cast<T*>(a.s) + r * a.ld_s, v[j], at[j], whole[j]);
     }
     // the group has read the row's slots once it meets at the next barrier
-    float2 st = make_float2(0.f, 1.f);
-    if (pre) st = unit_of<LAYER, ALIGNED>(v, at, D, n_w, a.eps, sum);
+    if (pre) st = unit_of<LAYER>(v, at, D, n_w, a.eps, sum);
     if constexpr (WARP) {
       __syncwarp();
     } else {
@@ -368,10 +321,17 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(co
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
-        pre_weight.times(v[j], j, at[j]);
-        pre_bias.plus(v[j], j, at[j]);
-        row_store<T, ALIGNED>(static_cast<T*>(a.n) + r * a.ld_n, v[j], at[j]);
+        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y * f.pre[j][e];
+        if constexpr (LAYER) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] += f.pre_bias[j][e];
+        } else if (a.pre_bias != nullptr) {
+          float b[E];
+          parameters<P>(b, a.pre_bias, 0.f, at[j]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] += b[e];
+        }
+        to_row(static_cast<T*>(a.n) + r * a.ld_n, v[j], at[j], whole[j]);
       }
     }
   }
@@ -380,73 +340,90 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP ? 2 : 1) k_norm_ring(co
 // ------------------------------------------------------------------ backward
 
 // Rows of the backward kernel through a ring: s and dn, y, ds, those that are given.
+// Arrays whose rows do not start at the walk's shift (odd pitches; a walk over whole
+// groups) are brought to their slots by the threads that read them.
 // The factors of a thread's columns stay in shared memory too, in places only that
 // thread reads and writes: from global memory they came from L2 for every row, since
 // the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us).
-template <typename T, typename P, bool ALIGNED>
+template <typename T, typename P>
 struct RowsRing {
-  static constexpr bool kWhole = ALIGNED;  // groups of 8 columns lie wholly in or out of a row
   const ffn_norm_grad_t& a;
   const Places (&at)[2];
-  RingArray<T, ALIGNED> in_s, in_dn, in_y, in_ds;
+  const RowCopies<T> copies;
   Ring ring;
-  int64_t ahead, r1;
+  int64_t ahead, end, step;
   uint32_t y_at, ds_at;
+  uint32_t slow;   // bits of the arrays off the walk's shift: s, dn, y, ds, dresidual, dy
   float* factors;  // [pre_weight, branch][2] groups of 8, `stride` floats apart
-  int stride;
-  int local[2], cols;  // this thread's columns in a slot, and how many a slot has
-  uint32_t off_s, off_dn, off_y, off_ds;  // the row's offsets
-  bool first_thread, alone;
+  int stride, col0, piece[2];
+  bool whole[2], first_thread, alone, first_row;
 
   __device__ __forceinline__ void issue() {
-    if (ahead >= r1) return;
-    const uint32_t bar = smem_u32(ring.full + ring.filled), n = ring.bytes;
-    uint32_t bytes = 0;
-    if (a.dn != nullptr) bytes += in_s.copied(ahead, n) + in_dn.copied(ahead, n);
-    if (a.y != nullptr) bytes += in_y.copied(ahead, n);
-    if (a.ds != nullptr) bytes += in_ds.copied(ahead, n);
-    mbar_expect_tx(bar, bytes);
-    if (a.dn != nullptr) {
-      in_s.copy(ahead, n, ring.slot(ring.filled, 0), bar);
-      in_dn.copy(ahead, n, ring.slot(ring.filled, 1), bar);
-    }
-    if (a.y != nullptr) in_y.copy(ahead, n, ring.slot(ring.filled, y_at), bar);
-    if (a.ds != nullptr) in_ds.copy(ahead, n, ring.slot(ring.filled, ds_at), bar);
-    mbar_arrive(bar);  // (after the elements that were copied one by one)
+    if (ahead >= end) return;
+    auto row = [&](const void* p, int64_t ld, uint32_t bit) {
+      return p == nullptr || (slow & bit) ? nullptr : static_cast<const T*>(p) + ahead * ld + col0;
+    };
+    const bool pre = a.dn != nullptr;
+    // (in the slots' order: s and dn where they are given, then y, then ds)
+    const T *first = pre ? row(a.s, a.ld_s, 1u) : row(a.y, a.ld_y, 4u),
+            *second = pre ? row(a.dn, a.ld_dn, 2u) : a.y != nullptr ? row(a.ds, a.ld_ds, 8u) : nullptr;
+    if (!pre && a.y == nullptr) first = row(a.ds, a.ld_ds, 8u);
+    const T *third = !pre ? nullptr : a.y != nullptr ? row(a.y, a.ld_y, 4u) : row(a.ds, a.ld_ds, 8u),
+            *fourth = !pre || a.y == nullptr ? nullptr : row(a.ds, a.ld_ds, 8u);
+    const T* const rows[4] = {first, second, third, fourth};
+    copies.issue(rows, ring.slot(ring.filled, 0), ring.pitch, smem_u32(ring.full + ring.filled), ahead == a.M - 1);
     if (++ring.filled == ring.stages) ring.filled = 0;
-    ++ahead;
+    ahead += step;
   }
-  __device__ __forceinline__ void begin(int64_t from, int64_t to) {
-    ahead = from;
-    r1 = to;
+  __device__ __forceinline__ void begin(const NormWalk& w) {
+    ahead = w.first;
+    end = w.end;
+    step = w.step;
+    first_row = true;
     if (first_thread)
       for (uint32_t s = 0; s < ring.stages; ++s) issue();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float w[8];
-      row_parameters<P, ALIGNED>(w, a.pre_weight, 1.f, at[j]);
-      keep(w, j);
+      float f[8];
+      parameters<P>(f, from_column<P>(a.pre_weight, col0), 1.f, at[j]);
+      keep(f, j);
     }
   }
   __device__ __forceinline__ void set_group(int64_t g) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float f[8];
-      float w[8];
-      row_parameters<P, ALIGNED>(f, a.gate != nullptr ? static_cast<const P*>(a.gate) + g * a.ld_gate : nullptr, 1.f,
-                                 at[j]);
-      row_parameters<P, ALIGNED>(w, a.post_weight, 1.f, at[j]);
+      float f[8], w[8];
+      parameters<P>(f, from_column<P>(a.gate, g * a.ld_gate + col0), 1.f, at[j]);
+      parameters<P>(w, from_column<P>(a.post_weight, col0), 1.f, at[j]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__fmul_rn(a.branch_scale, f[e]), w[e]);
+      for (int e = 0; e < 8; ++e) f[e] *= a.branch_scale * w[e];
       keep(f, 2 + j);
     }
   }
+  __device__ __forceinline__ void fetch(const void* p, int64_t ld, int64_t r, uint32_t array) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      Pack<T, 8> q;
+      load(q, static_cast<const T*>(p) + r * ld + col0, at[j]);
+      uint4* to = reinterpret_cast<uint4*>(ring.slot(ring.stage, array)) + piece[j];
+#pragma unroll
+      for (int k = 0; k < Pack<T, 8>::W / 4; ++k)
+        to[k] = make_uint4(q.w[4 * k], q.w[4 * k + 1], q.w[4 * k + 2], q.w[4 * k + 3]);
+    }
+  }
   __device__ __forceinline__ bool next(int64_t r) {
-    if (!ring.wait(first_thread ? (uint32_t)(ahead - r) : 0u)) return false;
-    off_s = in_s.off(r);
-    off_dn = in_dn.off(r);
-    off_y = in_y.off(r);
-    off_ds = in_ds.off(r);
+    if (!ring.wait(first_thread ? (uint32_t)((ahead - r) / step) : 0u)) return false;
+    if (slow & 15u) {  // (a thread's own places: no one else reads them)
+      if (a.dn != nullptr && (slow & 1u)) fetch(a.s, a.ld_s, r, 0);
+      if (a.dn != nullptr && (slow & 2u)) fetch(a.dn, a.ld_dn, r, 1);
+      if (a.y != nullptr && (slow & 4u)) fetch(a.y, a.ld_y, r, y_at);
+      if (a.ds != nullptr && (slow & 8u)) fetch(a.ds, a.ld_ds, r, ds_at);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (!whole[j]) {
+        for (uint32_t k = 0; k < ring.arrays; ++k) clean_slot<T, 8>(ring.slot(ring.stage, k), piece[j], at[j]);
+      }
     return true;
   }
   // every thread of the group has come to this row: the slots of the one before are free
@@ -454,20 +431,19 @@ struct RowsRing {
     if (first_thread && !alone && !first_row) issue();
     first_row = false;
   }
-  bool first_row = true;
   __device__ __forceinline__ void done() {
     ring.advance();
     if (!alone) return;  // a lone warp meets no one at the next row's barrier
     __syncwarp();
     if (first_thread) issue();
   }
-  __device__ __forceinline__ void values(float (&v)[8], uint32_t array, uint32_t off, int j) const {
-    from_slot<T, ALIGNED>(v, ring.slot(ring.stage, array), off, local[j], cols);
+  __device__ __forceinline__ void values(float (&v)[8], uint32_t array, int j) const {
+    from_slot<T>(v, ring.slot(ring.stage, array), piece[j]);
   }
-  __device__ __forceinline__ void s(float (&v)[8], int j) const { values(v, 0, off_s, j); }
-  __device__ __forceinline__ void dn(float (&v)[8], int j) const { values(v, 1, off_dn, j); }
-  __device__ __forceinline__ void y(float (&v)[8], int j) const { values(v, y_at, off_y, j); }
-  __device__ __forceinline__ void ds(float (&v)[8], int j) const { values(v, ds_at, off_ds, j); }
+  __device__ __forceinline__ void s(float (&v)[8], int j) const { values(v, 0, j); }
+  __device__ __forceinline__ void dn(float (&v)[8], int j) const { values(v, 1, j); }
+  __device__ __forceinline__ void y(float (&v)[8], int j) const { values(v, y_at, j); }
+  __device__ __forceinline__ void ds(float (&v)[8], int j) const { values(v, ds_at, j); }
   __device__ __forceinline__ void keep(const float (&v)[8], int k) {
     float4* to = reinterpret_cast<float4*>(factors + k * stride);
     to[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -478,16 +454,18 @@ struct RowsRing {
     const float4 lo = from[0], hi = from[stride / 8];
     const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], f[e]);
+    for (int e = 0; e < 8; ++e) v[e] *= f[e];
   }
   __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const { scale(v, j); }
   __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const { scale(v, 2 + j); }
-  __device__ __forceinline__ void put(T* to, const float (&v)[8], const Places& w) const {
-    row_store<T, ALIGNED>(to, v, w);
+  // output 0: dresidual, 1: dy
+  template <int OUTPUT>
+  __device__ __forceinline__ void put(T* row, const float (&v)[8], int j) const {
+    to_row(row, v, at[j], whole[j] && !(slow & (16u << OUTPUT)));
   }
 };
 
-template <typename T, typename P, bool ALIGNED, bool LAYER, bool BIAS, bool MANY>
+template <typename T, typename P, bool LAYER, bool BIAS, bool MANY>
 __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 : 2)
     k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
                 const __grid_constant__ NormSums ws, uint32_t* status) {
@@ -495,31 +473,42 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   __shared__ uint64_t bars[8 * kNormStages];
   __shared__ float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
-  const NormGradPlace w(a, sh);
-  RowSums sum{parts, sh.threads / 32, sh.cluster, w.rank, 0};
-  RowsRing<T, P, ALIGNED> rows{a,
-                      w.at,
-                      RingArray<T, ALIGNED>(a.s, a.ld_s, a.M, a.D, w.col0),
-                      RingArray<T, ALIGNED>(a.dn, a.ld_dn, a.M, a.D, w.col0),
-                      RingArray<T, ALIGNED>(a.y, a.ld_y, a.M, a.D, w.col0),
-                      RingArray<T, ALIGNED>(a.ds, a.ld_ds, a.M, a.D, w.col0)};
+  const int rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
+  const int tid = sh.lanes > 1 ? (int)lane_idx() : (int)threadIdx.x;
+  const int lane_group = sh.lanes > 1 ? (int)(threadIdx.x >> 5) : 0;
+  const int part = sh.lanes > 1 ? (int)blockIdx.x * sh.lanes + lane_group : (int)blockIdx.x / sh.cluster;
+  RowSums sum{parts, sh.threads / 32, sh.cluster, rank, 0};
+  // The walk's shift is that of rows without gaps from a 16-byte boundary on, whatever
+  // the arrays' pitches: which elements a thread adds up, and so the results' last
+  // bits, depend on the sizes alone.
+  const NormWalk walk = norm_walk<MANY>(a, sh, min(part, sh.parts - 1));
+  const int col0 = (int)(rank * sh.columns), cols = min((int)a.D - col0, (int)sh.columns);
+  const int shift =
+      sh.period > 1 ? (int)(((uint32_t)walk.first * (uint32_t)a.D * (uint32_t)sizeof(T)) & 15u) / (int)sizeof(T) : 0;
+  Places at[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
+  RowsRing<T, P> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
   rows.y_at = a.dn != nullptr ? 2u : 0u;
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
-  rows.first_thread = w.tid == 0;
+  rows.first_thread = tid == 0;
   rows.alone = sum.warps == 1 && sum.cluster == 1;
-  rows.cols = w.cols;
+  rows.col0 = col0;
+  rows.slow = sh.slow;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) rows.local[j] = w.at[j].first - w.col0;
+  for (int j = 0; j < 2; ++j) {
+    rows.piece[j] = (j * sh.threads + tid) * (int)sizeof(T) / 2;
+    rows.whole[j] = at[j].template whole<8>();
+  }
   // thread i's 16-byte pieces of the factors, i pieces in: no bank conflicts
   rows.stride = 8 * (int)blockDim.x;
   rows.factors = reinterpret_cast<float*>(smem) + 4 * threadIdx.x;
   rows.ring.stages = (uint32_t)sh.stages;
   rows.ring.arrays = rows.ds_at + (a.ds != nullptr ? 1u : 0u);
-  rows.ring.bytes = (uint32_t)(w.cols * (int)sizeof(T));
-  rows.ring.pitch = ring_pitch((uint32_t)(sh.columns * (int64_t)sizeof(T)));
+  rows.ring.pitch = (uint32_t)(16 * sh.threads * (int)sizeof(T));
   rows.ring.slots = smem + (size_t)4 * rows.stride * sizeof(float) +
-                    (size_t)w.group * sh.stages * rows.ring.arrays * rows.ring.pitch;
-  rows.ring.full = bars + w.group * kNormStages;
+                    (size_t)lane_group * sh.stages * rows.ring.arrays * rows.ring.pitch;
+  rows.ring.full = bars + lane_group * kNormStages;
   rows.ring.abort_flag = &abort_flag;
   rows.ring.status = status;
   if (rows.first_thread) {
@@ -534,8 +523,9 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (w.part >= sh.parts) return;  // (whole warps only)
-  norm_grad_rows<LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, w.part, w.at);
+  if (part >= sh.parts) return;  // (whole warps only)
+  // from here on columns count from the slice's first, in every array
+  norm_grad_rows<LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
 }
 
 }  // namespace

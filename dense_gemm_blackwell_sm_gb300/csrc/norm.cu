@@ -3,6 +3,7 @@
 #include "norm.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "ffn_launch.h"
 
@@ -14,61 +15,62 @@ int elem_bytes(int32_t dtype) { return dtype == FFN_F32 ? 4 : 2; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// rows that all start on 16-byte boundaries (absent arrays count as aligned)
-bool rows16(const void* p, int64_t ld, int bytes) { return p == nullptr || (aligned16(p) && ld * bytes % 16 == 0); }
-
 int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
+
+// rows this far apart start at the same offset to 16-byte boundaries
+int row_period(int64_t pitch_bytes) {
+  int period = 1;
+  while (pitch_bytes * period % 16 != 0) period *= 2;
+  return period;
+}
 
 }  // namespace
 
 cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int b = elem_bytes(a.dtype), E = 16 / b;
-  NormShape sh{};
-  const int64_t vectors = (a.D + E - 1) / E;  // of a row
+  // a row that may start off a boundary takes one vector more
+  const bool aligned = a.D * b % 16 == 0 && aligned16(a.y) && a.ld_y * b % 16 == 0;
+  const int64_t vectors = (a.D + E - 1 + (aligned ? 0 : E - 1)) / E;
   const int most = norm_most_vectors(b);
+  NormShape direct{};
   if (vectors <= 32 * 4 && a.M > 2 * (int64_t)dev.num_sms) {
     // short rows: a warp each, no barrier
-    sh.warp_rows = true;
-    sh.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
-    sh.threads = 256;
-    sh.grid = (a.M + 7) / 8;
+    direct.warp_rows = true;
+    direct.nv = vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4;
+    direct.threads = 256;
+    direct.grid = (a.M + 7) / 8;
   } else {
     // a CTA per row, with as many threads as let all rows run at once (short rows),
     // else with as many elements per thread as it can hold, which keeps several rows'
     // loads in flight on an SM
-    sh.nv = 1;
-    while (sh.nv < most && ((vectors + sh.nv - 1) / sh.nv * a.M > (int64_t)dev.num_sms * 1024 ||
-                            vectors > 512 * (int64_t)sh.nv))
-      sh.nv *= 2;
-    sh.threads = round32((vectors + sh.nv - 1) / sh.nv);
-    sh.grid = a.M;
+    direct.nv = 1;
+    while (direct.nv < most && ((vectors + direct.nv - 1) / direct.nv * a.M > (int64_t)dev.num_sms * 1024 ||
+                                vectors > 512 * (int64_t)direct.nv))
+      direct.nv *= 2;
+    direct.threads = round32((vectors + direct.nv - 1) / direct.nv);
+    direct.grid = a.M;
   }
-  const int pb = elem_bytes(a.param_dtype);
-  sh.aligned = a.D % 8 == 0 && rows16(a.y, a.ld_y, b) && rows16(a.residual, a.ld_residual, b) &&
-               rows16(a.s, a.ld_s, b) && rows16(a.n, a.ld_n, b) && rows16(a.gate, a.ld_gate, pb) &&
-               aligned16(a.post_weight) && aligned16(a.post_bias) && aligned16(a.pre_weight) && aligned16(a.pre_bias);
-  // the ring, where every group has a few rows
-  {
-    NormShape ring = sh;
-    ring.ring = true;
-    ring.warp_rows = vectors <= 32 * 4;
-    ring.nv = ring.warp_rows ? (vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4)
-                             : (vectors <= 256 ? 1 : vectors <= 1024 ? 2 : 4);
-    ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
-    const int groups = ring.warp_rows ? 8 : 1;
-    ring.smem = (size_t)groups * kNormStages * (a.residual ? 2 : 1) * norm_slot_bytes(a.D * b);
-    if (ring.threads <= 512 && ring.smem <= kNormRingBytes) {
-      // (about 100 registers per thread and 6 KB of static shared memory)
-      const int64_t per_sm =
-          std::max<int64_t>(1, std::min<int64_t>((int64_t)(222 * 1024) / ((int64_t)ring.smem + 6144), 640 / ring.threads));
-      ring.grid = std::min<int64_t>(per_sm * dev.num_sms, (a.M + groups - 1) / groups);
-      if (a.M >= 2 * ring.grid * groups) sh = ring;
-    }
-  }
+  // The ring, where the rows of all arrays start alike (and, settled at the launch,
+  // where every group has a few of them).
+  NormShape ring{};
+  ring.period = row_period(a.ld_y * b);
+  auto alike = [&](const void* p, int64_t ld) {
+    return p == nullptr || (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(a.y)) & 15u) == 0 &&
+                            (ld - a.ld_y) * b % 16 == 0);
+  };
+  const bool layer = a.kind == FFN_NORM_LAYER;
+  static const int64_t kNV4 = getenv("NV4") ? atoi(getenv("NV4")) : 512;
+  ring.warp_rows = vectors <= 32 * 4;
+  ring.nv = ring.warp_rows ? (vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4) : (!layer && vectors >= kNV4 ? 4 : 2);
+  ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
+  ring.smem = (size_t)kNormStages * (a.residual ? 2 : 1) * (size_t)(ring.nv * ring.threads * 16);
+  const bool ring_ok = alike(a.residual, a.ld_residual) && alike(a.s, a.ld_s) && alike(a.n, a.ld_n) &&
+                       ring.threads <= 512 && ring.smem <= kNormRingBytes;
+  const NormShape* maybe_ring = ring_ok ? &ring : nullptr;
   switch (a.dtype) {
-    case FFN_F16: return norm_forward_f16(a, sh, dev, st);
-    case FFN_BF16: return norm_forward_bf16(a, sh, dev, st);
-    default: return norm_forward_f32(a, sh, dev, st);
+    case FFN_F16: return norm_forward_f16(a, direct, maybe_ring, dev, st);
+    case FFN_BF16: return norm_forward_bf16(a, direct, maybe_ring, dev, st);
+    default: return norm_forward_f32(a, direct, maybe_ring, dev, st);
   }
 }
 
@@ -79,20 +81,28 @@ namespace {
 NormGradShape grad_shape(const ffn_norm_grad_t& a) {
   constexpr int kResident = 304;  // CTAs of 256 threads: two on each of 152 SMs
   NormGradShape sh{};
-  const int64_t threads = (a.D + kNormGradEach - 1) / kNormGradEach;
-  sh.cluster = (int)((threads + kNormGradThreads - 1) / kNormGradThreads);
-  sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
-  sh.threads = round32(sh.columns / kNormGradEach);
+  sh.period = row_period(a.D * elem_bytes(a.dtype));
+  const int spare = sh.period > 1 ? 8 : 0;  // columns a shifted row may need more
+  for (sh.cluster = 1;; ++sh.cluster) {
+    sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
+    sh.threads = round32((sh.columns + spare + kNormGradEach - 1) / kNormGradEach);
+    if (sh.threads <= kNormGradThreads || sh.cluster == 8) break;
+  }
   sh.lanes = sh.threads == 32 ? 8 : 1;
   const bool gates = a.gate != nullptr || a.dgate != nullptr;
   const int64_t groups = gates ? a.groups : 1;
   int64_t parts = (int64_t)kResident * (kNormGradThreads / (sh.threads * sh.lanes)) * sh.lanes / sh.cluster;
-  parts = std::max<int64_t>(1, std::min(parts, a.M));
+  // two rows at least per part: a part's sums cost about what a row does
+  parts = std::max<int64_t>(1, std::min(parts, (a.M + 1) / 2));
   if (groups >= parts && groups > 1) {
     sh.many = true;
     sh.parts_per_group = 0;
+    sh.period = 1;
+    parts = std::min(groups, parts);
   } else {
-    sh.parts_per_group = (int)std::min(parts / groups, a.M / groups);
+    sh.parts_per_group = (int)std::max<int64_t>(1, std::min(parts / groups, a.M / groups));
+    if (sh.parts_per_group < sh.period) sh.period = 1;
+    sh.parts_per_group = sh.parts_per_group / sh.period * sh.period;
     parts = sh.parts_per_group * groups;
   }
   sh.parts = (int)parts;
@@ -127,15 +137,20 @@ cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& d
   ffn_norm_grad_t a = args;
   if (a.gate == nullptr && a.dgate == nullptr) a.groups = 1;
   NormGradShape sh = grad_shape(a);
-  const int b = elem_bytes(a.dtype), pb = elem_bytes(a.param_dtype);
-  sh.aligned = a.D % 8 == 0 && rows16(a.ds, a.ld_ds, b) && rows16(a.dn, a.ld_dn, b) && rows16(a.y, a.ld_y, b) &&
-               rows16(a.s, a.ld_s, b) && rows16(a.dresidual, a.ld_dresidual, b) && rows16(a.dy, a.ld_dy, b) &&
-               rows16(a.gate, a.ld_gate, pb) && aligned16(a.post_weight) && aligned16(a.pre_weight);
-  const int arrays = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
+  const int b = elem_bytes(a.dtype);
+  const struct {
+    const void* p;
+    int64_t ld;
+  } arrays[6] = {{a.s, a.ld_s}, {a.dn, a.ld_dn}, {a.y, a.ld_y}, {a.ds, a.ld_ds}, {a.dresidual, a.ld_dresidual},
+                 {a.dy, a.ld_dy}};
+  for (int i = 0; i < 6; ++i) {
+    const int64_t off = (sh.period > 1 ? arrays[i].ld - a.D : arrays[i].ld) * b;
+    if (arrays[i].p != nullptr && (!aligned16(arrays[i].p) || off % 16 != 0)) sh.slow |= 1u << i;
+  }
+  const int rows = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
   // three rows ahead where two CTAs still share an SM, else two
   auto bytes = [&](int stages) {
-    return (size_t)sh.threads * sh.lanes * 32 * 4 +
-           (size_t)sh.lanes * stages * arrays * norm_slot_bytes(sh.columns * elem_bytes(a.dtype));
+    return (size_t)sh.threads * sh.lanes * 32 * 4 + (size_t)sh.lanes * stages * rows * (size_t)(16 * sh.threads * b);
   };
   sh.stages = bytes(kNormStages) <= 108 * 1024 ? kNormStages : 2;
   sh.smem = bytes(sh.stages);
