@@ -47,14 +47,14 @@ struct Ring {
   uint32_t* status;
   uint32_t stages, arrays, pitch;  // bytes of a slot
   uint32_t stage = 0, phase = 0;   // of the row being read
-  uint32_t filled = 0;             // (the group's first thread) the stage to fill next
+  uint32_t filled = 0;             // (the lanes that fill) the stage to fill next
 
   __device__ __forceinline__ uint8_t* slot(uint32_t st, uint32_t array) const {
     return slots + (size_t)((st * arrays + array) * pitch);
   }
   // all threads: the row at `stage` has landed.  False where the wait ran out; `left`
-  // copies of this thread's are then in flight, and it sees them land before shared
-  // memory goes.
+  // rows are then in flight, and a lane that filled sees them land before shared memory
+  // goes.
   __device__ __forceinline__ bool wait(uint32_t left) const {
     if (mbar_try_wait(smem_u32(full + stage), phase)) return true;
     return ring_wait_slow(smem_u32(full), stage, phase, stages, abort_flag, status, left);
@@ -81,32 +81,19 @@ struct RowCopies {
     pieces = (n + N - 1) / N * 16u;
     tail = ends_row ? n % N : 0u;
   }
-  // (n arrays, their rows' first elements in `rows`, the slots `pitch` bytes apart)
-  template <int MOST>
-  __device__ __forceinline__ void issue(const T* const (&rows)[MOST], uint8_t* slot, uint32_t pitch, uint32_t bar,
-                                        bool last_row) const {
-    const uint32_t cut = last_row && tail != 0 ? 16u : 0u;
-    uint32_t n = 0;
-#pragma unroll
-    for (int k = 0; k < MOST; ++k) n += rows[k] != nullptr ? 1u : 0u;
-    if (cut != 0) {
-#pragma unroll 1
-      for (int k = 0; k < MOST; ++k) {
-        const T* row = rows[0];
-#pragma unroll
-        for (int q = 1; q < MOST; ++q) row = k == q ? rows[q] : row;
-        if (row == nullptr) continue;
-        T* to = reinterpret_cast<T*>(slot + k * pitch);
-        const int first = (int)((pieces - 16u) / sizeof(T));
-        for (int e = first; e < first + (int)tail; ++e)
-          if (e >= shift) to[e] = row[e - shift];
-      }
+  // One array's row: one arrival on the stage's barrier (which counts the arrays).  A
+  // null row (an array that its readers fetch themselves) only arrives.
+  __device__ __forceinline__ void issue(const T* row, uint8_t* slot, uint32_t bar, bool last_row) const {
+    uint32_t n = row != nullptr ? pieces : 0u;
+    if (last_row && tail != 0 && n != 0) {
+      n -= 16u;
+      T* to = reinterpret_cast<T*>(slot);
+      const int first = (int)(n / sizeof(T));
+      for (int e = first; e < first + (int)tail; ++e)
+        if (e >= shift) to[e] = row[e - shift];
     }
-    mbar_arrive_expect_tx(bar, n * (pieces - cut));  // (after the elements copied one by one)
-    if (pieces == cut) return;
-#pragma unroll
-    for (int k = 0; k < MOST; ++k)
-      if (rows[k] != nullptr) bulk_load(smem_u32(slot + k * pitch), rows[k] - shift, pieces - cut, bar);
+    mbar_arrive_expect_tx(bar, n);  // (after the elements copied one by one)
+    if (n != 0) bulk_load(smem_u32(slot), row - shift, n, bar);
   }
 };
 
@@ -213,7 +200,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   ring.status = status;
   RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
   if (tid == 0) {
-    for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), 1);
+    for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), ring.arrays);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = 0u;
@@ -228,20 +215,22 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   const int64_t r1 = min(a.M, blocks * (slice + 1) / slices * step);
   if (r0 >= r1) return;
   const int shift = row_shift(static_cast<const T*>(a.y) + r0 * a.ld_y);
-  int64_t ahead = r0;  // (the group's first thread) the row to fetch next
+  // the first lanes fill, an array each, so that the rows' copies cost one array's code
+  const bool fills = tid < (int)ring.arrays;
+  const T* in = static_cast<const T*>(tid == 0 ? a.y : a.residual);
+  const int64_t in_ld = tid == 0 ? a.ld_y : a.ld_residual;
+  int64_t ahead = r0;  // (the lanes that fill) the row to fetch next
   uint32_t in_flight = 0;
   const RowCopies<T> copies(shift, D, true);
   auto issue = [&]() {
     if (ahead >= r1) return;
-    const T* const rows[2] = {
-        static_cast<const T*>(a.y) + ahead * a.ld_y,
-        a.residual != nullptr ? static_cast<const T*>(a.residual) + ahead * a.ld_residual : nullptr};
-    copies.issue(rows, ring.slot(ring.filled, 0), ring.pitch, smem_u32(ring.full + ring.filled), ahead == a.M - 1);
+    copies.issue(in + ahead * in_ld, ring.slot(ring.filled, (uint32_t)tid), smem_u32(ring.full + ring.filled),
+                 ahead == a.M - 1);
     if (++ring.filled == ring.stages) ring.filled = 0;
     ahead += step;
     ++in_flight;
   };
-  if (tid == 0)
+  if (fills)
     for (uint32_t s = 0; s < ring.stages; ++s) issue();
 
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
@@ -312,7 +301,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
     } else {
       if (!pre || per_row == 32) __syncthreads();
     }
-    if (tid == 0) {
+    if (fills) {
       --in_flight;
       issue();
     }
@@ -356,22 +345,14 @@ struct RowsRing {
   uint32_t slow;   // bits of the arrays off the walk's shift: s, dn, y, ds, dresidual, dy
   float* factors;  // [pre_weight, branch][2] groups of 8, `stride` floats apart
   int stride, col0, piece[2];
-  bool whole[2], first_thread, alone, first_row;
+  const T* in;     // (the lanes that fill, an array each) its row 0 here, null where it is slow
+  int64_t in_ld;
+  bool whole[2], fills, alone, first_row;
 
   __device__ __forceinline__ void issue() {
     if (ahead >= end) return;
-    auto row = [&](const void* p, int64_t ld, uint32_t bit) {
-      return p == nullptr || (slow & bit) ? nullptr : static_cast<const T*>(p) + ahead * ld + col0;
-    };
-    const bool pre = a.dn != nullptr;
-    // (in the slots' order: s and dn where they are given, then y, then ds)
-    const T *first = pre ? row(a.s, a.ld_s, 1u) : row(a.y, a.ld_y, 4u),
-            *second = pre ? row(a.dn, a.ld_dn, 2u) : a.y != nullptr ? row(a.ds, a.ld_ds, 8u) : nullptr;
-    if (!pre && a.y == nullptr) first = row(a.ds, a.ld_ds, 8u);
-    const T *third = !pre ? nullptr : a.y != nullptr ? row(a.y, a.ld_y, 4u) : row(a.ds, a.ld_ds, 8u),
-            *fourth = !pre || a.y == nullptr ? nullptr : row(a.ds, a.ld_ds, 8u);
-    const T* const rows[4] = {first, second, third, fourth};
-    copies.issue(rows, ring.slot(ring.filled, 0), ring.pitch, smem_u32(ring.full + ring.filled), ahead == a.M - 1);
+    copies.issue(in != nullptr ? in + ahead * in_ld : nullptr, ring.slot(ring.filled, (uint32_t)lane_idx()),
+                 smem_u32(ring.full + ring.filled), ahead == a.M - 1);
     if (++ring.filled == ring.stages) ring.filled = 0;
     ahead += step;
   }
@@ -380,7 +361,7 @@ struct RowsRing {
     end = w.end;
     step = w.step;
     first_row = true;
-    if (first_thread)
+    if (fills)
       for (uint32_t s = 0; s < ring.stages; ++s) issue();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -412,7 +393,7 @@ struct RowsRing {
     }
   }
   __device__ __forceinline__ bool next(int64_t r) {
-    if (!ring.wait(first_thread ? (uint32_t)((ahead - r) / step) : 0u)) return false;
+    if (!ring.wait(fills ? ring.stages : 0u)) return false;
     if (slow & 15u) {  // (a thread's own places: no one else reads them)
       if (a.dn != nullptr && (slow & 1u)) fetch(a.s, a.ld_s, r, 0);
       if (a.dn != nullptr && (slow & 2u)) fetch(a.dn, a.ld_dn, r, 1);
@@ -428,14 +409,14 @@ struct RowsRing {
   }
   // every thread of the group has come to this row: the slots of the one before are free
   __device__ __forceinline__ void met() {
-    if (first_thread && !alone && !first_row) issue();
+    if (fills && !alone && !first_row) issue();
     first_row = false;
   }
   __device__ __forceinline__ void done() {
     ring.advance();
     if (!alone) return;  // a lone warp meets no one at the next row's barrier
     __syncwarp();
-    if (first_thread) issue();
+    if (fills) issue();
   }
   __device__ __forceinline__ void values(float (&v)[8], uint32_t array, int j) const {
     from_slot<T>(v, ring.slot(ring.stage, array), piece[j]);
@@ -491,7 +472,6 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   RowsRing<T, P> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
   rows.y_at = a.dn != nullptr ? 2u : 0u;
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
-  rows.first_thread = tid == 0;
   rows.alone = sum.warps == 1 && sum.cluster == 1;
   rows.col0 = col0;
   rows.slow = sh.slow;
@@ -506,13 +486,23 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   rows.ring.stages = (uint32_t)sh.stages;
   rows.ring.arrays = rows.ds_at + (a.ds != nullptr ? 1u : 0u);
   rows.ring.pitch = (uint32_t)(16 * sh.threads * (int)sizeof(T));
+  rows.fills = tid < (int)rows.ring.arrays;
+  {
+    // lane k fills the k-th array given: s and dn, then y, then ds
+    const bool s = a.dn != nullptr && tid == 0, dn = a.dn != nullptr && tid == 1;
+    const bool y = !s && !dn && a.y != nullptr && tid == (int)rows.y_at;
+    const void* p = s ? a.s : dn ? a.dn : y ? a.y : a.ds;
+    rows.in_ld = s ? a.ld_s : dn ? a.ld_dn : y ? a.ld_y : a.ld_ds;
+    const uint32_t bit = s ? 1u : dn ? 2u : y ? 4u : 8u;
+    rows.in = (p == nullptr || (sh.slow & bit)) ? nullptr : static_cast<const T*>(p) + col0;
+  }
   rows.ring.slots = smem + (size_t)4 * rows.stride * sizeof(float) +
                     (size_t)lane_group * sh.stages * rows.ring.arrays * rows.ring.pitch;
   rows.ring.full = bars + lane_group * kNormStages;
   rows.ring.abort_flag = &abort_flag;
   rows.ring.status = status;
-  if (rows.first_thread) {
-    for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(rows.ring.full + s), 1);
+  if (tid == 0) {
+    for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(rows.ring.full + s), rows.ring.arrays);
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = 0u;

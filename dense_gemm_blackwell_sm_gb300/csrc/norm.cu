@@ -3,7 +3,6 @@
 #include "norm.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "ffn_launch.h"
 
@@ -59,9 +58,8 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
                             (ld - a.ld_y) * b % 16 == 0);
   };
   const bool layer = a.kind == FFN_NORM_LAYER;
-  static const int64_t kNV4 = getenv("NV4") ? atoi(getenv("NV4")) : 512;
   ring.warp_rows = vectors <= 32 * 4;
-  ring.nv = ring.warp_rows ? (vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4) : (!layer && vectors >= kNV4 ? 4 : 2);
+  ring.nv = ring.warp_rows ? (vectors <= 32 ? 1 : vectors <= 64 ? 2 : 4) : (!layer && vectors > 1024 ? 4 : 2);
   ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
   ring.smem = (size_t)kNormStages * (a.residual ? 2 : 1) * (size_t)(ring.nv * ring.threads * 16);
   const bool ring_ok = alike(a.residual, a.ld_residual) && alike(a.s, a.ld_s) && alike(a.n, a.ld_n) &&
