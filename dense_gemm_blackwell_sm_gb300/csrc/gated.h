@@ -82,6 +82,9 @@ const void* gated_products_kernel(bool bf16, int consumers);
 size_t gated_smem_bytes(int consumers, int stages);
 constexpr int kGatedThreads = 384;
 
+// the gated projections for at most 16 tokens (kernel_gated_few.cu)
+cudaError_t launch_gated_few(const ffn_gated_t& a, cudaStream_t st);
+
 // the pre-activations' gradient from kept ones (kernel_gated_slopes.cu)
 cudaError_t launch_gated_slopes(const ffn_gated_grad_t& a, int num_sms, cudaStream_t st);
 

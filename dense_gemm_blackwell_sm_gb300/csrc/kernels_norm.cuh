@@ -125,18 +125,32 @@ __device__ __forceinline__ void store(T* row, const float (&f)[E], const Places&
   }
 }
 
-// a parameter vector's elements, `absent` where there is none
+// A parameter vector's elements, `absent` where there is none.  Places outside the row
+// get the nearest element inside (they meet values that are 0 or not stored), so that
+// the unaligned form needs no predicates: a call's code is fetched cold for few rows.
 template <typename P, int E>
 __device__ __forceinline__ void parameters(float (&v)[E], const void* p, float absent, const Places& at) {
+  const P* from = static_cast<const P*>(p) + at.first;
   if (p == nullptr) {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = absent;
-    return;
-  }
-  Pack<P, E> raw;
-  load(raw, static_cast<const P*>(p), at);
+  } else if (at.template whole<E>() && (reinterpret_cast<uintptr_t>(from) & 15u) == 0) {
+    Pack<P, E> raw;
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = element(raw, e);
+    for (int k = 0; k < Pack<P, E>::W / 4; ++k) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(from) + k);
+      raw.w[4 * k] = q.x;
+      raw.w[4 * k + 1] = q.y;
+      raw.w[4 * k + 2] = q.z;
+      raw.w[4 * k + 3] = q.w;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = element(raw, e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      v[e] = to_f32(static_cast<const P*>(p)[min(max(at.first + e, 0), at.end - 1)]);
+  }
 }
 
 // a parameter array from element i on, or null
@@ -215,15 +229,6 @@ struct RowSums {
     const float* buf = exchange(v);
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = 0.f;
-    if (warps * cluster <= 8) {
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        if (w >= warps * cluster) break;
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
-      }
-      return;
-    }
     for (int w = (int)lane_idx(); w < warps * cluster; w += 32) {
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
@@ -399,22 +404,32 @@ struct NormWalk {
 };
 template <bool MANY>
 __device__ __forceinline__ NormWalk norm_walk(const ffn_norm_grad_t& a, const NormGradShape& sh, int part) {
-  const int64_t per = a.M / a.groups;
   NormWalk w;
   if constexpr (MANY) {
-    w.group = a.groups * part / sh.parts;
-    w.first = w.group * per;
-    w.end = a.groups * (part + 1) / sh.parts * per;
+    const int next = part + 1;
+    w.group = sh.share.begin(part);
+    w.first = w.group * sh.per;
+    w.end = (int64_t)sh.share.begin(next) * sh.per;
     w.step = 1;
   } else {
-    w.group = part / sh.parts_per_group;
-    const int64_t i = part % sh.parts_per_group, slice = i / sh.period, slices = sh.parts_per_group / sh.period;
-    const int64_t blocks = (per + sh.period - 1) / sh.period;  // of `period` rows
-    w.first = w.group * per + blocks * slice / slices * sh.period + i % sh.period;
-    w.end = w.group * per + min(per, blocks * (slice + 1) / slices * sh.period);
+    const int g = part / sh.parts_per_group, i = part - g * sh.parts_per_group;
+    const int slice = i / sh.period, kind = i - slice * sh.period;
+    w.group = g;
+    const int64_t row0 = (int64_t)g * sh.per;
+    w.first = row0 + (int64_t)sh.share.begin(slice) * sh.period + kind;
+    w.end = row0 + min((int64_t)sh.per, (int64_t)sh.share.begin(slice + 1) * sh.period);
     w.step = sh.period;
   }
   return w;
+}
+
+// The shift a part's columns have (see k_norm_grad).
+__device__ __forceinline__ int norm_part_shift(const ffn_norm_grad_t& a, const NormGradShape& sh, int part,
+                                               int element_bytes) {
+  if (sh.period == 1) return 0;
+  const int g = part / sh.parts_per_group, kind = (part - g * sh.parts_per_group) % sh.period;
+  const uint32_t row = (uint32_t)g * (uint32_t)sh.per + (uint32_t)kind;
+  return (int)((row * (uint32_t)a.D * (uint32_t)element_bytes) & 15u) / element_bytes;
 }
 
 // The arithmetic of a row's elements.
@@ -444,7 +459,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
   constexpr int E = 8, G = 2;
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
-  const int64_t per = a.M / a.groups;
+  const int64_t per = sh.per;
   int64_t g = walk.group, group_end = (g + 1) * per;
   const bool whole[G] = {at[0].template whole<E>(), at[1].template whole<E>()};
   float A[G][E] = {}, C[G][E] = {}, B[G][BIAS ? E : 1] = {}, Eo[G][BIAS ? E : 1] = {};
@@ -658,25 +673,25 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
       }
     }
   }
-  // the sums of this part's rows, for k_norm_column_sums
-  const int64_t out = (int64_t)part * a.D + col0;
+  // the sums of this part's rows, for k_norm_column_sums: at the threads' places, whole
+  const int64_t out = rows.sums_at(part);
 #pragma unroll
   for (int j = 0; j < G; ++j) {
+    auto put = [&](float* to, const auto& v) {
+      if (to == nullptr) return;
+      float4* q = reinterpret_cast<float4*>(to + out + j * sh.threads * 8);
+      q[0] = make_float4(v[0], v[1], v[2], v[3]);
+      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    };
     if constexpr (MANY) {
-      if (ws.a != nullptr) store(ws.a + out, GA[j], at[j]);
-      if constexpr (BIAS) {
-        if (ws.b != nullptr) store(ws.b + out, GB[j], at[j]);
-      }
+      put(ws.a, GA[j]);
+      if constexpr (BIAS) put(ws.b, GB[j]);
     } else {
-      if (ws.a != nullptr) store(ws.a + out, A[j], at[j]);
-      if constexpr (BIAS) {
-        if (ws.b != nullptr) store(ws.b + out, B[j], at[j]);
-      }
+      put(ws.a, A[j]);
+      if constexpr (BIAS) put(ws.b, B[j]);
     }
-    if (ws.c != nullptr) store(ws.c + out, C[j], at[j]);
-    if constexpr (BIAS) {
-      if (ws.e != nullptr) store(ws.e + out, Eo[j], at[j]);
-    }
+    put(ws.c, C[j]);
+    if constexpr (BIAS) put(ws.e, Eo[j]);
   }
 }
 
@@ -685,52 +700,59 @@ __device__ __forceinline__ float parameter(const void* p, int64_t i, float absen
   return p == nullptr ? absent : to_f32(static_cast<const P*>(p)[i]);
 }
 
-// Adds the parts' sums, 32 columns and 32 parts' lanes per CTA, always in the same
-// order.  blockIdx.y = 0: the sums over all rows (and a single gate's); 1 + g: the gate
-// of group g.
-template <typename P>
-__global__ void __launch_bounds__(1024) k_norm_column_sums(const __grid_constant__ ffn_norm_grad_t a,
-                                                           const __grid_constant__ NormGradShape sh,
-                                                           const __grid_constant__ NormSums ws) {
-  __shared__ float sums[4][32][33];
-  const int c = (int)lane_idx(), l = (int)(threadIdx.x >> 5), D = (int)a.D;
-  const int i = (int)blockIdx.x * 32 + c;
+// Adds the parts' sums, COLS columns and blockDim / COLS lanes of parts per CTA, always
+// in the same order.  blockIdx.y = 0: the sums over all rows (and a single gate's); 1 + g:
+// the gate of group g.
+template <typename P, int COLS>
+__global__ void __launch_bounds__(1024)
+    k_norm_column_sums(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
+                       const __grid_constant__ NormSums ws, int element_bytes) {
+  const int LANES = (int)blockDim.x / COLS, warps = (int)blockDim.x / 32;
+  __shared__ float sums[32][COLS * 4 + 1];
+  const int c = (int)threadIdx.x % COLS, l = (int)threadIdx.x / COLS, D = (int)a.D;
+  const int i = (int)blockIdx.x * COLS + c;
   const int g = (int)blockIdx.y - 1;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   const bool weighted = g < 0 && !sh.many && a.groups > 1;  // sums over groups: each part with its gate
   if (i < D) {
+    // the column's place: its slice's, and in it the part's shift
+    const int rank = i / (int)sh.columns, place = rank * sh.threads * 16 + i - rank * (int)sh.columns;
+    const int64_t pitch = (int64_t)sh.cluster * sh.threads * 16;
     const int p0 = g < 0 ? 0 : g * sh.parts_per_group, p1 = g < 0 ? sh.parts : p0 + sh.parts_per_group;
 #pragma unroll 4
-    for (int p = p0 + l; p < p1; p += 32) {
-      const int64_t at = (int64_t)p * D + i;
-      float f = 1.f;
-      if (weighted) f = parameter<P>(a.gate, (int64_t)(p / sh.parts_per_group) * a.ld_gate + i, 1.f);
+    for (int p = p0 + l; p < p1; p += LANES) {
+      const int64_t at = p * pitch + place + norm_part_shift(a, sh, p, element_bytes);
+      const float f =
+          weighted ? parameter<P>(a.gate, (int64_t)(p / sh.parts_per_group) * a.ld_gate + i, 1.f) : 1.f;
       if (ws.a != nullptr) v[0] = fmaf(f, ws.a[at], v[0]);
       if (ws.b != nullptr) v[1] = fmaf(f, ws.b[at], v[1]);
-      if (g < 0) {
-        if (ws.c != nullptr) v[2] += ws.c[at];
-        if (ws.e != nullptr) v[3] += ws.e[at];
-      }
+      if (g < 0 && ws.c != nullptr) v[2] += ws.c[at];
+      if (g < 0 && ws.e != nullptr) v[3] += ws.e[at];
     }
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sums[k][l][c] = v[k];
-  __syncthreads();
-  // warp l adds the 32 lanes of sum l & 3 for 4 columns
-  const int k = l & 3;
-  for (int j = 0; j < 4; ++j) {
-    const int col = (l >> 2) * 4 + j;
-    float s = sums[k][c][col];
+  for (int o = COLS; o < 32; o *= 2)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    __syncwarp();
-    if (c == 0) sums[k][0][col] = s;
+    for (int k = 0; k < 4; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  const int lane = (int)lane_idx(), warp = (int)(threadIdx.x >> 5);
+  if (lane < COLS) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sums[warp][lane * 4 + k] = v[k];
   }
   __syncthreads();
-  if (l != 0 || i >= D) return;
-  const float A = sums[0][0][c] * a.branch_scale, B = sums[1][0][c] * a.branch_scale;
+  // a warp adds the warps' values of one column and sum at a time
+#pragma unroll 1
+  for (int q = warp; q < COLS * 4; q += warps) {
+    float s[1] = {lane < warps ? sums[lane][q] : 0.f};
+    warp_sums(s);
+    __syncwarp();
+    if (lane == 0) sums[0][q] = s[0];
+  }
+  __syncthreads();
+  if (threadIdx.x >= COLS || i >= D) return;
+  const float A = sums[0][c * 4] * a.branch_scale, B = sums[0][c * 4 + 1] * a.branch_scale;
   if (a.dgate != nullptr && !sh.many && (g >= 0 || a.groups == 1))
     a.dgate[(int64_t)max(g, 0) * D + i] = parameter<P>(a.post_weight, i, 1.f) * A +
                                           (ws.b != nullptr ? parameter<P>(a.post_bias, i, 0.f) * B : 0.f);
@@ -738,8 +760,8 @@ __global__ void __launch_bounds__(1024) k_norm_column_sums(const __grid_constant
   const float f = !sh.many && a.groups == 1 ? parameter<P>(a.gate, i, 1.f) : 1.f;
   if (a.dpost_weight != nullptr) a.dpost_weight[i] = f * A;
   if (a.dpost_bias != nullptr) a.dpost_bias[i] = f * B;
-  if (a.dpre_weight != nullptr) a.dpre_weight[i] = sums[2][0][c];
-  if (a.dpre_bias != nullptr) a.dpre_bias[i] = sums[3][0][c];
+  if (a.dpre_weight != nullptr) a.dpre_weight[i] = sums[0][c * 4 + 2];
+  if (a.dpre_bias != nullptr) a.dpre_bias[i] = sums[0][c * 4 + 3];
 }
 
 }  // namespace

@@ -78,6 +78,7 @@ cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& direct, const Nor
     const int64_t unit = sh.warp_rows ? 1 : sh.period, groups = sh.warp_rows ? sh.threads / 32 : 1;
     sh.grid = std::max<int64_t>(unit, (int64_t)per_sm * dev.num_sms / unit * unit);
     if (a.M >= 2 * sh.grid * groups) {
+      sh.share = NormShare::of((a.M + sh.period - 1) / sh.period, sh.grid * groups / sh.period);
       void* args[] = {&args_a, &sh, &status};
       return launch_dependent(k, dim3((unsigned)sh.grid), sh.threads, 1, sh.smem, args, st);
     }
@@ -110,9 +111,17 @@ cudaError_t norm_backward(const ffn_norm_grad_t& a, const NormGradShape& sh, con
   const bool totals = a.dpost_weight || a.dpost_bias || a.dpre_weight || a.dpre_bias;
   const bool gates = a.dgate != nullptr && !sh.many;
   if (!totals && !gates) return cudaSuccess;
-  // one gate for all rows: its sum is the total; else a layer of CTAs per group
-  const dim3 sums((unsigned)((a.D + 31) / 32), 1u + (gates && a.groups > 1 ? (unsigned)a.groups : 0u));
-  return launch_dependent((const void*)k_norm_column_sums<P>, sums, 1024, 1, 0, args, st);
+  // one gate for all rows: its sum is the total; else a layer of CTAs per group.  Short
+  // rows take 8 columns per CTA, so that there are CTAs for the parts
+  const bool narrow = a.D <= 1024;
+  const dim3 sums((unsigned)(narrow ? (a.D + 7) / 8 : (a.D + 31) / 32),
+                  1u + (gates && a.groups > 1 ? (unsigned)a.groups : 0u));
+  // four parts per lane where there are few
+  const int threads = sh.parts <= 128 ? 256 : sh.parts <= 256 ? 512 : 1024;
+  int element_bytes = (int)sizeof(T);
+  void* sums_args[] = {&args_a, &args_sh, &args_ws, &element_bytes};
+  return launch_dependent(narrow ? (const void*)k_norm_column_sums<P, 8> : (const void*)k_norm_column_sums<P, 32>, sums,
+                          threads, 1, 0, sums_args, st);
 }
 
 }  // namespace

@@ -89,6 +89,7 @@ struct RowCopies {
       n -= 16u;
       T* to = reinterpret_cast<T*>(slot);
       const int first = (int)(n / sizeof(T));
+#pragma unroll 1
       for (int e = first; e < first + (int)tail; ++e)
         if (e >= shift) to[e] = row[e - shift];
     }
@@ -126,20 +127,28 @@ __device__ __forceinline__ void clean_slot(uint8_t* slot, int piece, const Place
   fence_proxy_async_smem();
 }
 
-// A group's E elements to a row that starts at the shift its places were made for.
+// A group's E elements to a row that starts at the shift its places were made for; a
+// group that is not whole 16-byte pieces there goes by element.
 template <typename T, int E>
 __device__ __forceinline__ void to_row(T* row, const float (&f)[E], const Places& at, bool whole) {
-  if (!whole) {
+  const Pack<T, E> p = packed<T>(f);
+  row += at.first;
+  if (whole) {
+#pragma unroll
+    for (int k = 0; k < Pack<T, E>::W / 4; ++k)
+      reinterpret_cast<uint4*>(row)[k] = make_uint4(p.w[4 * k], p.w[4 * k + 1], p.w[4 * k + 2], p.w[4 * k + 3]);
+  } else if (at.first < at.end) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (at.inside(e)) row[at.first + e] = from_f32<T>(f[e]);
-    return;
+      if (at.inside(e)) {
+        const uint32_t w = p.w[e * (int)sizeof(T) / 4];
+        if constexpr (sizeof(T) == 4) {
+          reinterpret_cast<uint32_t*>(row)[e] = w;
+        } else {
+          reinterpret_cast<uint16_t*>(row)[e] = (uint16_t)((e & 1) ? w >> 16 : w);
+        }
+      }
   }
-  const Pack<T, E> p = packed<T>(f);
-#pragma unroll
-  for (int k = 0; k < Pack<T, E>::W / 4; ++k)
-    reinterpret_cast<uint4*>(row + at.first)[k] =
-        make_uint4(p.w[4 * k], p.w[4 * k + 1], p.w[4 * k + 2], p.w[4 * k + 3]);
 }
 
 // ------------------------------------------------------------------- forward
@@ -178,7 +187,7 @@ struct RowFactors {
   }
 };
 
-// An RMS norm with biases reads them for every row.
+// (An RMS norm with biases takes the direct form.)
 template <typename T, typename P, bool LAYER, bool WARP, int NV>
 __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) ? 2 : 1)
     k_norm_ring(const __grid_constant__ ffn_norm_t a, const __grid_constant__ NormShape sh, uint32_t* status) {
@@ -208,12 +217,11 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // this group's rows: a slice, and in it the rows of one class (see norm_walk)
-  const int64_t part = (int64_t)blockIdx.x * groups + lane_group, slices = (int64_t)gridDim.x * groups / sh.period;
-  const int64_t slice = part / sh.period, blocks = (a.M + sh.period - 1) / sh.period, step = sh.period;
-  if (slice >= slices) return;  // (whole groups: only a CTA of warps has any left over)
-  const int64_t r0 = blocks * slice / slices * step + part % step;
-  const int64_t r1 = min(a.M, blocks * (slice + 1) / slices * step);
-  if (r0 >= r1) return;
+  const int part = (int)blockIdx.x * groups + lane_group, slice = part / sh.period;
+  const int64_t step = sh.period;
+  const int64_t r0 = (int64_t)sh.share.begin(slice) * step + (part - slice * sh.period);
+  const int64_t r1 = min(a.M, (int64_t)sh.share.begin(slice + 1) * step);
+  if (r0 >= r1) return;  // (a whole group)
   const int shift = row_shift(static_cast<const T*>(a.y) + r0 * a.ld_y);
   // the first lanes fill, an array each, so that the rows' copies cost one array's code
   const bool fills = tid < (int)ring.arrays;
@@ -230,8 +238,10 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
     ahead += step;
     ++in_flight;
   };
-  if (fills)
+  if (fills) {
+#pragma unroll 1
     for (uint32_t s = 0; s < ring.stages; ++s) issue();
+  }
 
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   Places at[NV];
@@ -243,12 +253,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   }
   const float n_w = LAYER ? warp_elements<NV, E>(at) : 0.f;
   RowFactors<P, LAYER, NV, E> f(a, at);
-  const int64_t per = a.M / a.groups;
+  const uint32_t per = (uint32_t)a.M / (uint32_t)(a.gate != nullptr ? a.groups : 1);
   int64_t gate_end = 0;  // the first row with another gate
   for (int64_t r = r0; r < r1; r += step) {
     if (r >= gate_end) {
       const P* gate = gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r);
-      gate_end = a.gate == nullptr ? a.M : (r / per + 1) * per;
+      gate_end = (int64_t)((uint32_t)r / per + 1u) * per;
       f.for_gate(a, gate, at);
     }
     if (!ring.wait(in_flight)) return;
@@ -274,12 +284,6 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
       if constexpr (LAYER) {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[j][e] += f.branch_bias[j][e];
-      } else if (a.post_bias != nullptr) {
-        float b[E], g[E];
-        parameters<P>(b, a.post_bias, 0.f, at[j]);
-        parameters<P>(g, gate_row<P>(a.gate, a.ld_gate, a.M, a.groups, r), 1.f, at[j]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = fmaf(b[e], a.branch_scale * g[e], v[j][e]);
       }
       if (a.residual != nullptr) {
         float q[E];
@@ -314,11 +318,6 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
         if constexpr (LAYER) {
 #pragma unroll
           for (int e = 0; e < E; ++e) v[j][e] += f.pre_bias[j][e];
-        } else if (a.pre_bias != nullptr) {
-          float b[E];
-          parameters<P>(b, a.pre_bias, 0.f, at[j]);
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] += b[e];
         }
         to_row(static_cast<T*>(a.n) + r * a.ld_n, v[j], at[j], whole[j]);
       }
@@ -344,7 +343,7 @@ struct RowsRing {
   uint32_t y_at, ds_at;
   uint32_t slow;   // bits of the arrays off the walk's shift: s, dn, y, ds, dresidual, dy
   float* factors;  // [pre_weight, branch][2] groups of 8, `stride` floats apart
-  int stride, col0, piece[2];
+  int stride, col0, piece[2], clusters, rank, threads, tid;
   const T* in;     // (the lanes that fill, an array each) its row 0 here, null where it is slow
   int64_t in_ld;
   bool whole[2], fills, alone, first_row;
@@ -361,8 +360,10 @@ struct RowsRing {
     end = w.end;
     step = w.step;
     first_row = true;
-    if (fills)
+    if (fills) {
+#pragma unroll 1
       for (uint32_t s = 0; s < ring.stages; ++s) issue();
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float f[8];
@@ -382,14 +383,13 @@ struct RowsRing {
     }
   }
   __device__ __forceinline__ void fetch(const void* p, int64_t ld, int64_t r, uint32_t array) {
+    const T* row = static_cast<const T*>(p) + r * ld + col0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      Pack<T, 8> q;
-      load(q, static_cast<const T*>(p) + r * ld + col0, at[j]);
-      uint4* to = reinterpret_cast<uint4*>(ring.slot(ring.stage, array)) + piece[j];
-#pragma unroll
-      for (int k = 0; k < Pack<T, 8>::W / 4; ++k)
-        to[k] = make_uint4(q.w[4 * k], q.w[4 * k + 1], q.w[4 * k + 2], q.w[4 * k + 3]);
+      T* to = reinterpret_cast<T*>(ring.slot(ring.stage, array) + (size_t)piece[j] * 16);
+#pragma unroll 4
+      for (int e = 0; e < 8; ++e)
+        if (at[j].inside(e)) to[e] = row[at[j].first + e];
     }
   }
   __device__ __forceinline__ bool next(int64_t r) {
@@ -403,6 +403,7 @@ struct RowsRing {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (!whole[j]) {
+#pragma unroll 1
         for (uint32_t k = 0; k < ring.arrays; ++k) clean_slot<T, 8>(ring.slot(ring.stage, k), piece[j], at[j]);
       }
     return true;
@@ -439,6 +440,10 @@ struct RowsRing {
   }
   __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const { scale(v, j); }
   __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const { scale(v, 2 + j); }
+  // where the part's sums of this thread's first group go in a sums array
+  __device__ __forceinline__ int64_t sums_at(int part) const {
+    return ((int64_t)part * clusters + rank) * threads * 16 + tid * 8;
+  }
   // output 0: dresidual, 1: dy
   template <int OUTPUT>
   __device__ __forceinline__ void put(T* row, const float (&v)[8], int j) const {
@@ -464,8 +469,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   // bits, depend on the sizes alone.
   const NormWalk walk = norm_walk<MANY>(a, sh, min(part, sh.parts - 1));
   const int col0 = (int)(rank * sh.columns), cols = min((int)a.D - col0, (int)sh.columns);
-  const int shift =
-      sh.period > 1 ? (int)(((uint32_t)walk.first * (uint32_t)a.D * (uint32_t)sizeof(T)) & 15u) / (int)sizeof(T) : 0;
+  const int shift = norm_part_shift(a, sh, min(part, sh.parts - 1), sizeof(T));
   Places at[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
@@ -474,6 +478,10 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
   rows.alone = sum.warps == 1 && sum.cluster == 1;
   rows.col0 = col0;
+  rows.clusters = sh.cluster;
+  rows.rank = rank;
+  rows.threads = sh.threads;
+  rows.tid = tid;
   rows.slow = sh.slow;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {

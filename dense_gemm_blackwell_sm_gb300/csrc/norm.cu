@@ -63,6 +63,7 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
   ring.threads = ring.warp_rows ? 256 : round32((vectors + ring.nv - 1) / ring.nv);
   ring.smem = (size_t)kNormStages * (a.residual ? 2 : 1) * (size_t)(ring.nv * ring.threads * 16);
   const bool ring_ok = alike(a.residual, a.ld_residual) && alike(a.s, a.ld_s) && alike(a.n, a.ld_n) &&
+                       (layer || (!a.post_bias && !a.pre_bias)) &&
                        ring.threads <= 512 && ring.smem <= kNormRingBytes;
   const NormShape* maybe_ring = ring_ok ? &ring : nullptr;
   switch (a.dtype) {
@@ -104,13 +105,16 @@ NormGradShape grad_shape(const ffn_norm_grad_t& a) {
     parts = sh.parts_per_group * groups;
   }
   sh.parts = (int)parts;
+  sh.per = (int)(a.M / groups);
+  sh.share = sh.many ? NormShare::of(groups, parts)
+                     : NormShare::of((sh.per + sh.period - 1) / sh.period, sh.parts_per_group / sh.period);
   sh.bias = a.dpost_bias != nullptr || a.dpre_bias != nullptr || (a.dgate != nullptr && a.post_bias != nullptr);
   return sh;
 }
 
 int sums_of(const ffn_norm_grad_t& a, const NormGradShape& sh, NormSums* ws, float* base) {
   int n = 0;
-  const int64_t each = (int64_t)sh.parts * a.D;
+  const int64_t each = (int64_t)sh.parts * sh.cluster * sh.threads * 16;
   auto next = [&](bool need, float** p) {
     *p = nullptr;
     if (need) *p = base ? base + each * n : nullptr, ++n;
@@ -128,7 +132,7 @@ int sums_of(const ffn_norm_grad_t& a, const NormGradShape& sh, NormSums* ws, flo
 size_t norm_backward_workspace(const ffn_norm_grad_t& a) {
   const NormGradShape sh = grad_shape(a);
   NormSums ws{};
-  return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)a.D * 4;
+  return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)(sh.cluster * sh.threads * 16) * 4;
 }
 
 cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& dev, cudaStream_t st) {

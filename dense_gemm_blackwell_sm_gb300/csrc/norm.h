@@ -10,6 +10,19 @@
 
 namespace dgb {
 
+// `n` things dealt to `parts` parts in order, the first ones one more.
+struct NormShare {
+  int each, more;
+  static NormShare of(int64_t n, int64_t parts) { return {(int)(n / parts), (int)(n % parts)}; }
+#if defined(__CUDACC__)
+  __device__
+#endif
+      int
+      begin(int part) const {
+    return part * each + (part < more ? part : more);
+  }
+};
+
 // Forward, direct: one row per warp (warp_rows) or per CTA.  Ring: warps or CTAs walk
 // rows of one class each (rows `period` apart start alike, see norm_walk).
 struct NormShape {
@@ -19,6 +32,7 @@ struct NormShape {
   int64_t grid;    // (ring: settled with the kernel's residency)
   size_t smem;
   int period;
+  NormShare share; // blocks of `period` rows to slices of the grid
 };
 
 // 16-byte vectors a thread can hold of a row: 32 elements
@@ -35,6 +49,8 @@ struct NormGradShape {
   int parts;               // grid = ceil(parts / lanes) * cluster
   int parts_per_group;     // > 0: a part is in one group; 0: several whole groups
   int period;              // rows this far apart belong to one part
+  int per;                 // rows of a gate's group
+  NormShare share;         // blocks of `period` rows to the slices of a group; groups to parts (many)
   uint32_t slow;           // arrays off the walk's shift: s, dn, y, ds, dresidual, dy
   int64_t columns;         // per CTA
   bool many;               // several whole groups per part (parts_per_group == 0)
