@@ -79,6 +79,9 @@ class NormGradArgs(ctypes.Structure):
 NormGrads = collections.namedtuple("NormGrads", ["dresidual", "dy", "dgate", "dpost_weight", "dpost_bias",
                                                  "dpre_weight", "dpre_bias"])
 
+# the current stream's handle without a Stream object (torch's generated code uses it too)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 _lib = None
 
 
@@ -90,7 +93,7 @@ def load():
         for name, args in (("ffn_gated", GatedArgs), ("ffn_gated_backward", GatedGradArgs), ("ffn_norm", NormArgs),
                            ("ffn_norm_backward", NormGradArgs)):
             f = getattr(lib, name)
-            f.argtypes, f.restype = [ctypes.POINTER(args), _p], ctypes.c_int
+            f.argtypes, f.restype = [ctypes.POINTER(args), _p], ctypes.c_int  # (a structure is passed by reference)
         lib.ffn_norm_backward_workspace.argtypes = [ctypes.POINTER(NormGradArgs)]
         lib.ffn_norm_backward_workspace.restype = _i64
         lib.ffn_check.argtypes, lib.ffn_check.restype = [_p], ctypes.c_int
@@ -98,20 +101,18 @@ def load():
     return _lib
 
 
-def _matrix(name, t, rows, cols, like):
-    """Checks a (rows x cols) tensor of `like`'s type and device with dense rows."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s must be (%d, %d), not %s" % (name, rows, cols, tuple(t.shape)))
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError("%s must be %s on %s" % (name, like.dtype, like.device))
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+def _rows(name, t, shape, dtype, device):
+    """Checks a tensor of dense rows and returns their pitch."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError("%s must be %s of %s on %s, not %s of %s on %s"
+                         % (name, tuple(shape), dtype, device, tuple(t.shape), t.dtype, t.device))
+    rows, cols = shape
+    if t.is_contiguous():
+        return cols
+    pitch, step = t.stride()
+    if cols > 1 and step != 1 or rows > 1 and pitch < cols:
         raise ValueError("%s must have dense, non-overlapping rows" % name)
-    return t
-
-
-def _pitch(t):
-    """The row pitch of a checked matrix (its length where there is no second row)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return pitch if rows > 1 else cols
 
 
 def _code(table, value, what):
@@ -121,38 +122,35 @@ def _code(table, value, what):
     return code
 
 
-class _On:
-    """The stream a call runs on.  Memory allocated for the call belongs to the
-    current stream, so where the call goes to another one the allocator is told."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        self.stream = stream
-        self.other = stream is not None and stream != torch.cuda.current_stream(device)
-        self.ptr = gemm._stream_ptr(stream if stream is not None else torch.cuda.current_stream(device))
-
-    def empty(self, shape, dtype, device):
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if self.other:
-            self._order(t)
-        return t
-
-    def _order(self, t):
-        # the memory may still be in use on the current stream
-        current = torch.cuda.current_stream(t.device)
-        stream = self.stream if hasattr(self.stream, "cuda_stream") else torch.cuda.ExternalStream(int(self.stream))
-        stream.wait_stream(current)
-        t.record_stream(stream)
+def _share(stream, device, tensors):
+    """Memory allocated for a call belongs to the current stream: where the call goes
+    to another one, that stream first waits for what may still use the memory, and the
+    allocator is told of the use."""
+    current = torch.cuda.current_stream(device)
+    other = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+    if other == current:
+        return
+    other.wait_stream(current)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(other)
 
 
-def _call(name, args, device, on):
-    fn = getattr(load(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(ctypes.byref(args), on.ptr)
+def _call(name, args, device, stream, made):
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    fn = getattr(_lib or load(), name)
+    index = device.index
+    if stream is None:
+        ptr = _current_raw_stream(index)
+    else:
+        _share(stream, device, made)
+        ptr = gemm._stream_ptr(stream)
+    if index == torch._C._cuda_getDevice():
+        status = fn(args, ptr)
     else:
         with torch.cuda.device(device):
-            status = fn(ctypes.byref(args), on.ptr)
+            status = fn(args, ptr)
     if status != gemm.OK:
         raise GemmError(status, name)
 
@@ -160,13 +158,11 @@ def _call(name, args, device, on):
 def _gated_inputs(x, w):
     if x.dim() != 2 or w.dim() != 2 or w.shape[0] % 2 or x.shape[1] != w.shape[1]:
         raise ValueError("x must be (M, K) and w (2F, K), not %s and %s" % (tuple(x.shape), tuple(w.shape)))
-    M, K = x.shape
-    F = w.shape[0] // 2
-    _matrix("x", x, M, K, x)
-    _matrix("w", w, 2 * F, K, x)
-    if x.dtype not in (torch.float16, torch.bfloat16):
-        raise ValueError("x must be float16 or bfloat16, not %s" % x.dtype)
-    return M, F, K, _DTYPES[x.dtype]
+    dtype, device = x.dtype, x.device
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise ValueError("x must be float16 or bfloat16, not %s" % dtype)
+    return (*x.shape, w.shape[0] // 2, dtype, device, _rows("x", x, x.shape, dtype, device),
+            _rows("w", w, w.shape, dtype, device))
 
 
 def gated(x, w, act="silu", save=False, out=None, gu=None, stream=None, timeout_ns=0, debug_flags=0):
@@ -176,17 +172,21 @@ def gated(x, w, act="silu", save=False, out=None, gu=None, stream=None, timeout_
     ``act``: "none", "relu", "silu", "gelu_tanh", "gelu_erf" or a gemm.ACT_* code.
     With ``save`` the pre-activations (M, 2F) are kept for gated_backward and the
     answer is (h, gu).  ``out`` and ``gu`` may be given, as (M, F) and (M, 2F)."""
-    M, F, K, dtype = _gated_inputs(x, w)
-    on = _On(x.device, stream)
-    h = on.empty((M, F), x.dtype, x.device) if out is None else _matrix("out", out, M, F, x)
+    M, K, F, dtype, device, ld_x, ld_w = _gated_inputs(x, w)
+    ld_h, ld_gu = F, 2 * F
+    h = out
+    if h is None:
+        h = torch.empty((M, F), dtype=dtype, device=device)
+    else:
+        ld_h = _rows("out", h, (M, F), dtype, device)
     if gu is not None:
-        _matrix("gu", gu, M, 2 * F, x)
+        ld_gu = _rows("gu", gu, (M, 2 * F), dtype, device)
     elif save:
-        gu = on.empty((M, 2 * F), x.dtype, x.device)
-    args = GatedArgs(M, F, K, dtype, _code(ACTIVATIONS, act, "act"), x.data_ptr(), w.data_ptr(), h.data_ptr(),
-                     gu.data_ptr() if gu is not None else None, _pitch(x), _pitch(w), _pitch(h),
-                     _pitch(gu) if gu is not None else 0, timeout_ns, debug_flags)
-    _call("ffn_gated", args, x.device, on)
+        gu = torch.empty((M, 2 * F), dtype=dtype, device=device)
+    args = GatedArgs(M, F, K, _DTYPES[dtype], _code(ACTIVATIONS, act, "act"), x.data_ptr(), w.data_ptr(),
+                     h.data_ptr(), gu.data_ptr() if gu is not None else None, ld_x, ld_w, ld_h, ld_gu, timeout_ns,
+                     debug_flags)
+    _call("ffn_gated", args, device, stream, (h, gu))
     return (h, gu) if save else h
 
 
@@ -195,65 +195,58 @@ def gated_backward(dh, x, w, gu=None, act="silu", need_dx=True, need_dw=True, st
     """(dx, dw) of gated(x, w, act) for dh = dL/dh (M, F).  ``gu`` is what gated
     kept; without it the pre-activations are computed again from x and w.  dx
     (M, K) and dw (2F, K) have the inputs' type; either is None when not needed."""
-    M, F, K, dtype = _gated_inputs(x, w)
-    _matrix("dh", dh, M, F, x)
-    if gu is not None:
-        _matrix("gu", gu, M, 2 * F, x)
-    on = _On(x.device, stream)
+    M, K, F, dtype, device, ld_x, ld_w = _gated_inputs(x, w)
+    ld_dh = _rows("dh", dh, (M, F), dtype, device)
+    ld_gu = _rows("gu", gu, (M, 2 * F), dtype, device) if gu is not None else 0
     ld_dgu = (2 * F + 7) // 8 * 8
-    dgu = on.empty((M, ld_dgu), x.dtype, x.device)
-    dx = on.empty((M, K), x.dtype, x.device) if need_dx else None
-    dw = on.empty((2 * F, K), x.dtype, x.device) if need_dw else None
-    args = GatedGradArgs(M, F, K, dtype, _code(ACTIVATIONS, act, "act"), x.data_ptr(), w.data_ptr(),
+    dgu = torch.empty((M, ld_dgu), dtype=dtype, device=device)
+    dx = torch.empty((M, K), dtype=dtype, device=device) if need_dx else None
+    dw = torch.empty((2 * F, K), dtype=dtype, device=device) if need_dw else None
+    args = GatedGradArgs(M, F, K, _DTYPES[dtype], _code(ACTIVATIONS, act, "act"), x.data_ptr(), w.data_ptr(),
                          gu.data_ptr() if gu is not None else None, dh.data_ptr(), dgu.data_ptr(),
                          dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
-                         _pitch(x), _pitch(w), _pitch(gu) if gu is not None else 0, _pitch(dh), ld_dgu, K, K,
-                         timeout_ns, debug_flags)
-    _call("ffn_gated_backward", args, x.device, on)
+                         ld_x, ld_w, ld_gu, ld_dh, ld_dgu, K, K, timeout_ns, debug_flags)
+    _call("ffn_gated_backward", args, device, stream, (dgu, dx, dw))
     return dx, dw
 
 
-class _Norm:
-    """The arguments block_norm and block_norm_backward share, checked."""
-
-    def __init__(self, like, gate, vectors, kind, flags):
-        if like.dim() != 2:
-            raise ValueError("rows must be a 2-D tensor, not %s" % (tuple(like.shape),))
-        self.M, self.D = like.shape
-        self.dtype = _DTYPES.get(like.dtype)
-        if self.dtype is None:
-            raise ValueError("rows must be float16, bfloat16 or float32, not %s" % like.dtype)
-        self.kind, self.flags = _code(NORM_KINDS, kind, "kind"), flags
-        param = None
-        for name, v in vectors:
-            if v is not None:
-                if v.dim() != 1 or v.shape[0] != self.D or (self.D > 1 and v.stride(0) != 1):
-                    raise ValueError("%s must be %d dense values" % (name, self.D))
-                param = self._param(name, v, param, like)
-        self.gate, self.groups, self.ld_gate = None, 1, 0
-        if gate is not None:
-            g = gate.unsqueeze(0) if gate.dim() == 1 else gate
-            param = self._param("gate", g, param, like)
-            if g.dim() != 2 or g.shape[0] < 1 or self.M % g.shape[0]:
-                raise ValueError("gate must be (D) or (groups, D) with the rows a multiple of the groups")
-            _matrix("gate", g, g.shape[0], self.D, g)
-            self.gate, self.groups, self.ld_gate = g.data_ptr(), g.shape[0], _pitch(g)
-        self.param = _DTYPES[param] if param is not None else self.dtype
-
-    @staticmethod
-    def _param(name, v, param, like):
-        if v.device != like.device or v.dtype not in (like.dtype, torch.float32) or param not in (None, v.dtype):
-            raise ValueError("%s must be on %s, and weights, biases and gate all %s or all float32"
-                             % (name, like.device, like.dtype))
-        return v.dtype
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
-
-
-def _ld(t):
-    return _pitch(t) if t is not None else 0
+def _norm_parameters(like, gate, post_weight, post_bias, pre_weight, pre_bias, post_norm, pre_norm):
+    """Checks what block_norm and its gradient share: (M, D, type, parameter type,
+    the gate's pointer, groups and pitch, the vectors' pointers)."""
+    if like.dim() != 2:
+        raise ValueError("rows must be a 2-D tensor, not %s" % (tuple(like.shape),))
+    M, D = like.shape
+    dtype, device, param = like.dtype, like.device, None
+    if dtype not in _DTYPES:
+        raise ValueError("rows must be float16, bfloat16 or float32, not %s" % dtype)
+    if not post_norm and (post_weight is not None or post_bias is not None):
+        raise ValueError("post_weight and post_bias need post_norm")
+    if not pre_norm and (pre_weight is not None or pre_bias is not None):
+        raise ValueError("pre_weight and pre_bias need pre_norm")
+    gate_ptr, groups, ld_gate = None, 1, D
+    if gate is not None:
+        param = gate.dtype
+        g = gate.unsqueeze(0) if gate.dim() == 1 else gate
+        groups = g.shape[0]
+        if g.dim() != 2 or groups < 1 or M % groups:
+            raise ValueError("gate must be (D) or (groups, D) with the rows a multiple of the groups")
+        ld_gate = _rows("gate", g, (groups, D), param, device)
+        gate_ptr = g.data_ptr()
+    ptrs = []
+    for v in (post_weight, post_bias, pre_weight, pre_bias):
+        if v is None:
+            ptrs.append(None)
+            continue
+        if param is None:
+            param = v.dtype
+        if v.shape != (D,) or v.dtype is not param or v.device != device or not v.is_contiguous():
+            raise ValueError("weights and biases must be %d dense values of %s on %s" % (D, param, device))
+        ptrs.append(v.data_ptr())
+    if param is None:
+        param = dtype
+    elif param is not dtype and param is not torch.float32:
+        raise ValueError("weights, biases and gate must be %s or float32, not %s" % (dtype, param))
+    return M, D, dtype, device, _DTYPES[dtype], _DTYPES[param], gate_ptr, groups, ld_gate, ptrs
 
 
 def block_norm(y, residual=None, *, post_norm=False, post_weight=None, post_bias=None, gate=None, pre_norm=True,
@@ -270,29 +263,34 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, post_bias
     (kind "rms") or the layer norm ("layer").  gate is (D), or (groups, D) with
     consecutive runs of M / groups rows sharing one.  s may be the residual and n
     may be y (in place).  Weights, biases and gate share one type, y's or float32."""
-    P = _Norm(y, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                        ("pre_bias", pre_bias)), kind, (_POST if post_norm else 0) | (_PRE if pre_norm else 0))
-    M, D = P.M, P.D
-    _matrix("y", y, M, D, y)
+    M, D, dtype, device, code, param, gate_ptr, groups, ld_gate, p = _norm_parameters(
+        y, gate, post_weight, post_bias, pre_weight, pre_bias, post_norm, pre_norm)
+    shape = (M, D)
+    ld_y = _rows("y", y, shape, dtype, device)
+    res_ptr = s_ptr = n_ptr = None
+    ld_res = ld_s = ld_n = D
     if residual is not None:
-        _matrix("residual", residual, M, D, y)
-    if not post_norm and (post_weight is not None or post_bias is not None):
-        raise ValueError("post_weight and post_bias need post_norm")
-    if not pre_norm and (pre_weight is not None or pre_bias is not None or n is not None):
-        raise ValueError("pre_weight, pre_bias and n need pre_norm")
-    on = _On(y.device, stream)
+        ld_res = _rows("residual", residual, shape, dtype, device)
+        res_ptr = residual.data_ptr()
     if s is not None:
-        _matrix("s", s, M, D, y)
+        ld_s = _rows("s", s, shape, dtype, device)
     elif need_s:
-        s = on.empty((M, D), y.dtype, y.device)
+        s = torch.empty(shape, dtype=dtype, device=device)
     if n is not None:
-        _matrix("n", n, M, D, y)
+        if not pre_norm:
+            raise ValueError("n needs pre_norm")
+        ld_n = _rows("n", n, shape, dtype, device)
     elif pre_norm:
-        n = on.empty((M, D), y.dtype, y.device)
-    args = NormArgs(M, D, P.groups, P.dtype, P.param, P.kind, P.flags, eps, residual_scale, branch_scale, 0,
-                    y.data_ptr(), _ptr(residual), P.gate, _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight),
-                    _ptr(pre_bias), _ptr(s), _ptr(n), _pitch(y), _ld(residual), P.ld_gate, _ld(s), _ld(n))
-    _call("ffn_norm", args, y.device, on)
+        n = torch.empty(shape, dtype=dtype, device=device)
+    if s is not None:
+        s_ptr = s.data_ptr()
+    if n is not None:
+        n_ptr = n.data_ptr()
+    args = NormArgs(M, D, groups, code, param, _code(NORM_KINDS, kind, "kind"),
+                    (_POST if post_norm else 0) | (_PRE if pre_norm else 0), eps, residual_scale, branch_scale, 0,
+                    y.data_ptr(), res_ptr, gate_ptr, p[0], p[1], p[2], p[3], s_ptr, n_ptr, ld_y, ld_res, ld_gate,
+                    ld_s, ld_n)
+    _call("ffn_norm", args, device, stream, (s, n))
     return s, n
 
 
@@ -305,36 +303,33 @@ def block_norm_backward(ds, dn, y, s, *, post_norm=False, post_weight=None, post
     like = dn if dn is not None else ds
     if like is None:
         raise ValueError("ds or dn must be given")
-    P = _Norm(like, gate, (("post_weight", post_weight), ("post_bias", post_bias), ("pre_weight", pre_weight),
-                           ("pre_bias", pre_bias)), kind, (_POST if post_norm else 0) | (_PRE if pre_norm else 0))
-    M, D = P.M, P.D
     if pre_norm and (dn is None or s is None) or not pre_norm and dn is not None:
         raise ValueError("dn and s are needed with pre_norm, and dn only then")
     if y is None and (post_norm or gate is not None and need_dparams):
         raise ValueError("y is needed with post_norm or a gate")
-    if not post_norm and (post_weight is not None or post_bias is not None):
-        raise ValueError("post_weight and post_bias need post_norm")
-    if not pre_norm and (pre_weight is not None or pre_bias is not None):
-        raise ValueError("pre_weight and pre_bias need pre_norm")
+    M, D, dtype, device, code, param, gate_ptr, groups, ld_gate, p = _norm_parameters(
+        like, gate, post_weight, post_bias, pre_weight, pre_bias, post_norm, pre_norm)
+    shape = (M, D)
+    ins, lds = [], []
     for name, t in (("ds", ds), ("dn", dn), ("y", y), ("s", s)):
-        if t is not None:
-            _matrix(name, t, M, D, like)
-    on = _On(like.device, stream)
-    rows = lambda need: on.empty((M, D), like.dtype, like.device) if need else None  # noqa: E731
-    sums = lambda p: (on.empty(p.shape, torch.float32, like.device)  # noqa: E731
-                      if p is not None and need_dparams else None)
-    g = NormGrads(rows(need_dresidual), rows(need_dy), sums(gate), sums(post_weight), sums(post_bias),
-                  sums(pre_weight), sums(pre_bias))
-    args = NormGradArgs(M, D, P.groups, P.dtype, P.param, P.kind, P.flags, eps, residual_scale, branch_scale, 0,
-                        _ptr(ds), _ptr(dn), _ptr(y), _ptr(s), P.gate, _ptr(post_weight), _ptr(post_bias),
-                        _ptr(pre_weight), *map(_ptr, g), None, _ld(ds), _ld(dn), _ld(y), _ld(s), P.ld_gate,
-                        _ld(g.dresidual), _ld(g.dy))
-    size = load().ffn_norm_backward_workspace(ctypes.byref(args))
+        lds.append(_rows(name, t, shape, dtype, device) if t is not None else D)
+        ins.append(t.data_ptr() if t is not None else None)
+    empty = torch.empty
+    g = [empty(shape, dtype=dtype, device=device) if need_dresidual else None,
+         empty(shape, dtype=dtype, device=device) if need_dy else None]
+    for t in (gate, post_weight, post_bias, pre_weight, pre_bias):
+        g.append(empty(t.shape, dtype=torch.float32, device=device) if t is not None and need_dparams else None)
+    outs = [t.data_ptr() if t is not None else None for t in g]
+    args = NormGradArgs(M, D, groups, code, param, _code(NORM_KINDS, kind, "kind"),
+                        (_POST if post_norm else 0) | (_PRE if pre_norm else 0), eps, residual_scale, branch_scale, 0,
+                        *ins, gate_ptr, p[0], p[1], p[2], *outs, None, *lds, ld_gate, D, D)
+    workspace = None
+    size = (_lib or load()).ffn_norm_backward_workspace(args)
     if size > 0:
-        workspace = on.empty((size,), torch.uint8, like.device)
+        workspace = empty(size, dtype=torch.uint8, device=device)
         args.workspace = workspace.data_ptr()
-    _call("ffn_norm_backward", args, like.device, on)
-    return g
+    _call("ffn_norm_backward", args, device, stream, (*g, workspace))
+    return NormGrads(*g)
 
 
 def check(stream=None):
