@@ -49,8 +49,6 @@ Tiling gated_tiling(int64_t M, int64_t F, int64_t kb, int clusters) {
   return best;
 }
 
-constexpr int stages_of(int consumers) { return consumers == 2 ? 4 : 6; }
-
 void fill_task(GatedTask* t, int64_t rows, int64_t cols, int64_t kb, int tile_m, int tile_n, bool bf16, int mma_n,
                uint32_t major, void* out, int64_t ld) {
   t->rows = (int32_t)rows;
@@ -68,8 +66,9 @@ void fill_task(GatedTask* t, int64_t rows, int64_t cols, int64_t kb, int tile_m,
 
 cudaError_t launch_tiles(const void* func, int consumers, int64_t tiles, const FfnDevice& dev, CUtensorMap (&maps)[4],
                          GatedParams& p, cudaStream_t st) {
-  const size_t smem = gated_smem_bytes(consumers, p.stages);
-  const cudaError_t e = allow_smem_once(func, smem);
+  p.stages = gated_stages(consumers, p.a_rows, p.hw);
+  const size_t smem = gated_smem_bytes(consumers, p.a_rows, p.hw, p.stages);
+  const cudaError_t e = allow_smem_once(func, 232448);
   if (e != cudaSuccess) return e;
   LaunchSpec s;
   s.func = func;
@@ -102,9 +101,11 @@ cudaError_t launch_pair(const A& a, const FfnDevice& dev, GatedParams& p, void* 
   fill_task(&p.task[0], a.M, a.F, kb, 256 * t.consumers, t.hw, bf16, 2 * t.hw, 0, out, ld);
   p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
   p.hw = t.hw;
-  p.stages = stages_of(t.consumers);
+  // few tokens: only their rows come to shared memory, which leaves it to the weights
+  p.a_rows = a.M <= 120 ? (int)((a.M + 7) / 8 * 8) : 128;
   CUtensorMap maps[4];
-  if (!encode_rows16(&maps[0], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64, 128) ||
+  if (!encode_rows16(&maps[0], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64,
+                     (uint32_t)p.a_rows) ||
       !encode_rows16(&maps[1], bf16, a.w, (uint64_t)a.K, (uint64_t)(2 * a.F), (uint64_t)a.ld_w, 64, (uint32_t)t.hw))
     return cudaErrorInvalidValue;
   maps[2] = maps[0];
@@ -140,7 +141,7 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
     }
   GatedParams p = common_params(a, dev);
   p.hw = best.hw;
-  p.stages = stages_of(best.consumers);
+  p.a_rows = 128;
   const int tile_m = 256 * best.consumers, tile_n = 2 * best.hw;
   const bool dx_first = a.dx && (!a.dw || kb_dx >= kb_dw);
   CUtensorMap maps[4];

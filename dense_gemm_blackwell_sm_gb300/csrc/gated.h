@@ -39,6 +39,7 @@ struct GatedParams {
   int32_t n0, n1;             // tiles of the two tasks (n1 = 0: one task)
   int32_t fill;               // tiles of task 1 about as long as one of task 0
   int32_t hw;                 // MMA columns per CTA: half the tile's N
+  int32_t a_rows;             // rows of the first operand a CTA brings per consumer (128, or fewer for few tokens)
   int32_t stages;
   uint32_t debug_flags;
   uint32_t* status;
@@ -79,7 +80,9 @@ DGB_BOTH inline bool gated_tile(const GatedParams& p, int32_t cid, int32_t clust
 const void* gated_forward_kernel(bool bf16, int consumers, int act);
 const void* gated_slopes_kernel(bool bf16, int consumers, int act);
 const void* gated_products_kernel(bool bf16, int consumers);
-size_t gated_smem_bytes(int consumers, int stages);
+// stages that fit shared memory, and the bytes a CTA then takes
+int gated_stages(int consumers, int a_rows, int hw);
+size_t gated_smem_bytes(int consumers, int a_rows, int hw, int stages);
 constexpr int kGatedThreads = 384;
 
 // the gated projections for at most 16 tokens (kernel_gated_few.cu)

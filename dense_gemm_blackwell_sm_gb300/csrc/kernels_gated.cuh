@@ -36,10 +36,10 @@ namespace {
 
 constexpr int GT_THREADS = 384;
 constexpr uint32_t GT_A_BYTES = 128u * 128u;  // 128 rows of 64 16-bit elements
-constexpr uint32_t GT_B_BYTES = 128u * 128u;
 constexpr int GT_STAGE_ROW = 34;              // 16-bit elements of a staged epilogue row (32 + 2: no bank conflicts)
 constexpr uint32_t GT_STAGING = 8u * 32u * GT_STAGE_ROW * 2u;
-constexpr uint32_t GT_CTRL = 256;
+constexpr uint32_t GT_CTRL = 384;
+constexpr int GT_MAX_STAGES = 16;
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -138,20 +138,24 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     k_gated(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
             const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
             const __grid_constant__ GatedParams p) {
-  constexpr uint32_t STAGE = NCONS * GT_A_BYTES + GT_B_BYTES;
   constexpr int TILE_M = 256 * NCONS;
   constexpr uint32_t EPI_WARPS = NCONS == 2 ? 4 : 8;  // per accumulator and CTA
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
   const uint32_t S = (uint32_t)p.stages;
+  // A stage holds a_rows rows of the first operand per consumer and hw of the second.
+  // With fewer rows than the MMA's 128 (few tokens) the MMA reads on into what follows;
+  // those rows of the accumulator are never stored.
+  const uint32_t A_BYTES = NCONS == 2 ? GT_A_BYTES : (uint32_t)p.a_rows * 128u;
+  const uint32_t STAGE = NCONS * A_BYTES + (uint32_t)p.hw * 128u;
   uint16_t* staging = reinterpret_cast<uint16_t*>(ring + (size_t)S * STAGE);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(staging) + GT_STAGING);
-  uint64_t* full = bars;             // [8] TMA -> MMA
-  uint64_t* empty = bars + 8;        // [8] MMA -> TMA
-  uint64_t* acc_full = bars + 16;    // [2] MMA -> epilogue
-  uint64_t* acc_empty = bars + 18;   // [2] epilogue -> MMA
-  uint64_t* drain_bar = bars + 20;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  uint64_t* full = bars;                         // [16] TMA -> MMA
+  uint64_t* empty = bars + GT_MAX_STAGES;        // [16] MMA -> TMA
+  uint64_t* acc_full = bars + 2 * GT_MAX_STAGES;  // [2] MMA -> epilogue
+  uint64_t* acc_empty = acc_full + 2;            // [2] epilogue -> MMA
+  uint64_t* drain_bar = acc_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 5);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* zero_word = tmem_slot + 2;
 
@@ -207,16 +211,15 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         int32_t tm, tn;
         raster_tile(tile, t.tiles_m, t.tiles_n, t.raster_group, tm, tn);
         const int32_t row0 = tm * TILE_M + (int32_t)rank * 128;
-        const uint32_t b_bytes = (uint32_t)p.hw * 128u;
         for (int32_t it = 0; it < t.kb; ++it) {
           const int32_t k0 = it * 64;
           if (!mbar_wait(smem_u32(empty + stage), sphase ^ 1u, w, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
           const uint32_t own = smem_u32(full + stage);
           const uint32_t fb = mapa_shared(own, 0);
-          if (leader) mbar_arrive_expect_tx(own, 2u * (NCONS * GT_A_BYTES + b_bytes));
+          if (leader) mbar_arrive_expect_tx(own, 2u * STAGE);
           uint8_t* st = ring + (size_t)stage * STAGE;
           for (int c = 0; c < NCONS; ++c) {
-            const uint32_t dst = smem_u32(st + c * GT_A_BYTES);
+            const uint32_t dst = smem_u32(st + c * A_BYTES);
             const int32_t row = row0 + c * 256;
             if (MODE == GATED_PRODUCTS && t.a_mn) {
               tma_load_2d_pair(dst, tmA, fb, row, k0);
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
               tma_load_2d_pair(dst, tmA, fb, k0, row);
             }
           }
-          const uint32_t dst = smem_u32(st + NCONS * GT_A_BYTES);
+          const uint32_t dst = smem_u32(st + NCONS * A_BYTES);
           if (skip) {
             skip = false;  // test hook: this stage's bytes never all arrive
           } else if constexpr (MODE == GATED_PRODUCTS) {
@@ -276,8 +279,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         for (int32_t it = 0; it < t.kb; ++it) {
           if (!mbar_wait(smem_u32(full + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(ring + (size_t)stage * STAGE + cons * GT_A_BYTES);
-          const uint32_t sb = smem_u32(ring + (size_t)stage * STAGE + NCONS * GT_A_BYTES);
+          const uint32_t sa = smem_u32(ring + (size_t)stage * STAGE + cons * A_BYTES);
+          const uint32_t sb = smem_u32(ring + (size_t)stage * STAGE + NCONS * A_BYTES);
           const uint64_t ad = a_mn ? sdesc_mn_sw128(sa, 8192) : sdesc_k_sw128(sa);
           const uint64_t bd = MODE == GATED_PRODUCTS ? sdesc_mn_sw128(sb, 8192) : sdesc_k_sw128(sb);
           const uint64_t astep = a_mn ? 128 : 2, bstep = MODE == GATED_PRODUCTS ? 128 : 2;
