@@ -22,13 +22,39 @@ struct Tiling {
   int consumers, hw;
 };
 
-// Clocks of a launch whose clusters take `tiles` tiles in waves: per 64-wide block
-// of the reduction the MMAs of a tile (4 hw clocks per consumer), at least what its
-// copies and hand-offs take, and a fixed part per tile.
-double launch_clocks(int64_t tiles, int clusters, int64_t kb, int consumers, int hw) {
-  const double mma = 4.0 * consumers * hw * (consumers == 1 ? 1.12 : 1.0);
-  const double block = std::max(mma, 160.0);
-  return (double)ceil_div64(tiles, clusters) * ((double)kb * block + 2500.0 + 20.0 * hw * consumers);
+// One consumer's MMAs are issued by two threads (see kernels_gated.cuh) where TMEM
+// holds the accumulators: hw <= 64, or one tile per cluster.
+bool split_of(int consumers, int hw, int64_t tiles, int clusters) {
+  return consumers == 1 && (hw <= 64 || tiles <= clusters);
+}
+
+// Microseconds of x w^T for both projections on tiles of `consumers` x 256 rows and hw
+// columns: a launch, and per wave of clusters the 64-wide blocks of the reduction and
+// what a tile's end costs.  Fitted on 152 SMs to 14 shapes (M 40 - 8192, F 700 - 14336,
+// K 464 - 4096) timed with every tile; wide tiles take the MMAs' own time (4.2 ns per
+// block and column of h), narrow ones what issuing them costs, and two consumers have
+// no second accumulator to fill while the first is read.
+double pair_time(int64_t tiles, int clusters, int64_t kb, int consumers, int hw) {
+  double block, end;
+  if (consumers == 2) {
+    block = std::max(0.32, 0.06 + 0.0039 * hw);
+    end = 3.7;
+  } else if (split_of(consumers, hw, tiles, clusters)) {
+    block = std::max(0.21 + 0.0002 * hw, 0.0021 * hw);
+    end = 0.7;
+  } else {
+    block = 0.27 + 0.0003 * hw;
+    end = 0.7;
+  }
+  const double waves = (double)ceil_div64(tiles, clusters);
+  return 6.0 + waves * (double)kb * block + (waves - 1) * end;
+}
+
+// The same for one tile of a product of the backward pass (its operands' rows run along
+// the reduction), hw = 64 or 128 columns per CTA; fitted to eight shapes.
+double product_tile_time(int64_t kb, int consumers, int hw) {
+  const double block = consumers == 2 ? (hw == 128 ? 0.63 : 0.48) : (hw == 128 ? 0.42 : 0.36);
+  return (double)kb * block + (consumers == 2 ? 3.0 : 0.7);
 }
 
 // The tile that finishes soonest: one or two consumers (256 or 512 rows), hw = 16
@@ -40,7 +66,7 @@ Tiling gated_tiling(int64_t M, int64_t F, int64_t kb, int clusters) {
   for (int consumers = 2; consumers >= 1; --consumers)
     for (int hw = 128; hw >= 16; hw -= 16) {
       const int64_t tiles = ceil_div64(M, 256 * consumers) * ceil_div64(F, hw);
-      const double t = launch_clocks(tiles, clusters, kb, consumers, hw);
+      const double t = pair_time(tiles, clusters, kb, consumers, hw);
       if (least == 0 || t < least) {
         least = t;
         best = {consumers, hw};
@@ -101,6 +127,9 @@ cudaError_t launch_pair(const A& a, const FfnDevice& dev, GatedParams& p, void* 
   fill_task(&p.task[0], a.M, a.F, kb, 256 * t.consumers, t.hw, bf16, 2 * t.hw, 0, out, ld);
   p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
   p.hw = t.hw;
+  p.split = split_of(t.consumers, t.hw, p.n0, clusters) ? 2 : 1;
+  p.part_cols = t.hw <= 64 ? 128 : 256;
+  p.two_slots = p.split == 1 || t.hw <= 64;
   // few tokens: only their rows come to shared memory, which leaves it to the weights
   p.a_rows = a.M <= 120 ? (int)((a.M + 7) / 8 * 8) : 128;
   CUtensorMap maps[4];
@@ -119,21 +148,16 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
   const bool bf16 = a.dtype == FFN_BF16;
   const int clusters = std::max(1, dev.num_sms / 2);
   const int64_t kb_dx = ceil_div64(2 * a.F, 64), kb_dw = ceil_div64(a.M, 64);
-  // the tile with the least time for both products' work spread over the clusters
+  // The tile with the least time for both products' work spread over the clusters,
+  // whichever are wanted: a product's bits do not depend on the other's being asked for.
   Tiling best{1, 128};
   double least = 0;
   for (int consumers = 2; consumers >= 1; --consumers)
     for (int hw = 128; hw >= 64; hw -= 64) {
-      double total = 0, longest = 0;
-      auto add = [&](int64_t rows, int64_t kb) {
-        const int64_t tiles = ceil_div64(rows, 256 * consumers) * ceil_div64(a.K, 2 * hw);
-        const double one = launch_clocks(1, 1, kb, consumers, hw);
-        total += one * (double)tiles;
-        longest = std::max(longest, one);
-      };
-      if (a.dx) add(a.M, kb_dx);
-      if (a.dw) add(2 * a.F, kb_dw);
-      const double t = std::max(total / clusters, longest);
+      const int64_t tiles_k = ceil_div64(a.K, 2 * hw);
+      const int64_t n_dx = ceil_div64(a.M, 256 * consumers) * tiles_k, n_dw = ceil_div64(2 * a.F, 256 * consumers) * tiles_k;
+      const double dx = product_tile_time(kb_dx, consumers, hw), dw = product_tile_time(kb_dw, consumers, hw);
+      const double t = std::max((dx * (double)n_dx + dw * (double)n_dw) / clusters, std::max(dx, dw));
       if (least == 0 || t < least) {
         least = t;
         best = {consumers, hw};
@@ -142,6 +166,8 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
   GatedParams p = common_params(a, dev);
   p.hw = best.hw;
   p.a_rows = 128;
+  p.split = 1;  // (their operands' copies bound these, not the MMAs' issue)
+  p.two_slots = 1;
   const int tile_m = 256 * best.consumers, tile_n = 2 * best.hw;
   const bool dx_first = a.dx && (!a.dw || kb_dx >= kb_dw);
   CUtensorMap maps[4];
@@ -168,8 +194,8 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
   p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
   if (n == 2) {
     p.n1 = p.task[1].tiles_m * p.task[1].tiles_n;
-    p.fill = (int32_t)(launch_clocks(1, 1, p.task[0].kb, best.consumers, best.hw) /
-                           launch_clocks(1, 1, p.task[1].kb, best.consumers, best.hw) +
+    p.fill = (int32_t)(product_tile_time(p.task[0].kb, best.consumers, best.hw) /
+                           product_tile_time(p.task[1].kb, best.consumers, best.hw) +
                        0.5);
   } else {
     maps[2] = maps[0];

@@ -40,6 +40,9 @@ struct GatedParams {
   int32_t fill;               // tiles of task 1 about as long as one of task 0
   int32_t hw;                 // MMA columns per CTA: half the tile's N
   int32_t a_rows;             // rows of the first operand a CTA brings per consumer (128, or fewer for few tokens)
+  int32_t split;              // one consumer: threads that issue its MMAs (2: even and odd blocks)
+  int32_t part_cols;          // TMEM columns between their accumulators
+  int32_t two_slots;          // one consumer: accumulators for two tiles in turn
   int32_t stages;
   uint32_t debug_flags;
   uint32_t* status;
