@@ -432,11 +432,18 @@ __device__ __forceinline__ int norm_part_shift(const ffn_norm_grad_t& a, const N
   return (int)((row * (uint32_t)a.D * (uint32_t)element_bytes) & 15u) / element_bytes;
 }
 
-// The arithmetic of a row's elements.
-__device__ __forceinline__ float unit_value(float v, float mean, float r) { return __fmul_rn(v - mean, r); }
-// r (a - u mean(a u) - mean(a)), added to t
-__device__ __forceinline__ float unit_slope(float t, float r, float a, float u, float mean_au, float mean_a) {
-  return fmaf(r, __fsub_rn(fmaf(-u, mean_au, a), mean_a), t);
+// v - mean for the layer norm; elements outside the row stay 0
+template <bool LAYER, int E>
+__device__ __forceinline__ void centre(float (&v)[E], float mean, const Places& at, bool whole) {
+  if constexpr (LAYER) {
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] -= mean;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] -= at.inside(e) ? mean : 0.f;
+    }
+  }
 }
 
 // With u = unit(s), v = unit(y), a = dn * pre_weight, t = ds + r_s (a - u mean(a u)
@@ -459,6 +466,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
   constexpr int E = 8, G = 2;
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
   const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
+  const float inv_w = n_w > 0.f ? 1.f / n_w : 0.f;
   const int64_t per = sh.per;
   int64_t g = walk.group, group_end = (g + 1) * per;
   const bool whole[G] = {at[0].template whole<E>(), at[1].template whole<E>()};
@@ -492,8 +500,8 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         }
       }
       warp_sums(k);
-      mean_s = n_w > 0.f ? k[0] / n_w : 0.f;  // the warp's own for now
-      mean_y = n_w > 0.f ? k[1] / n_w : 0.f;
+      mean_s = k[0] * inv_w;  // the warp's own for now
+      mean_y = k[1] * inv_w;
       mean_a = k[2];
     }
     k[0] = k[1] = k[2] = k[3] = 0.f;
@@ -504,21 +512,19 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         rows.s(s, j);
         rows.dn(dn, j);
         rows.scale_pre(dn, j);
+        centre<LAYER>(s, mean_s, at[j], whole[j]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          const float c = s[e] - (LAYER ? (whole[j] || at[j].inside(e) ? mean_s : 0.f) : 0.f);
-          k[0] = fmaf(c, c, k[0]);
-          k[1] = fmaf(c, dn[e], k[1]);
+          k[0] = fmaf(s[e], s[e], k[0]);
+          k[1] = fmaf(s[e], dn[e], k[1]);
         }
       }
       if (post) {
         float y[E];
         rows.y(y, j);
+        centre<LAYER>(y, mean_y, at[j], whole[j]);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float c = y[e] - (LAYER ? (whole[j] || at[j].inside(e) ? mean_y : 0.f) : 0.f);
-          k[2] = fmaf(c, c, k[2]);
-        }
+        for (int e = 0; e < E; ++e) k[2] = fmaf(y[e], y[e], k[2]);
       }
     }
     if constexpr (!LAYER) {
@@ -554,7 +560,11 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
       mean_a *= inv;
     }
     rows.met();
-    const float r_s = rsqrtf(k[0] * inv + a.eps), mean_au = k[1] * inv * r_s;
+    // With c = s - mean_s and d = y - mean_y, u = c r_s and v = d r_y, in as few
+    // operations per element (the kernel is bound by their number):
+    //   t  = ds - r_s mean(a) + c (-r_s^3 mean(a c)) + (dn r_s) pre_weight
+    //   dy = b r_y - r_y mean(b) + d (-r_y^3 mean(b d))
+    const float r_s = rsqrtf(k[0] * inv + a.eps), k_c = -(k[1] * inv) * r_s * r_s * r_s, k_s = r_s * mean_a;
     const float r_y = post ? rsqrtf(k[2] * inv + a.eps) : 1.f;
     float t[G][E];
     float two[2] = {0.f, 0.f};
@@ -567,18 +577,24 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         for (int e = 0; e < E; ++e) t[j][e] = 0.f;
       }
       if (pre) {
-        float s[E], dn[E];
+        float s[E], dn[E], w[E];
         rows.s(s, j);
         rows.dn(dn, j);
+        rows.pre_factors(w, j);
+        if constexpr (LAYER) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            s[e] -= mean_s;
+            t[j][e] -= k_s;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          s[e] = unit_value(s[e], mean_s, r_s);
-          C[j][e] = fmaf(dn[e], s[e], C[j][e]);
           if constexpr (BIAS) Eo[j][e] += dn[e];
+          dn[e] *= r_s;
+          C[j][e] = fmaf(dn[e], s[e], C[j][e]);
+          t[j][e] = fmaf(dn[e], w[e], fmaf(s[e], k_c, t[j][e]));
         }
-        rows.scale_pre(dn, j);
-#pragma unroll
-        for (int e = 0; e < E; ++e) t[j][e] = unit_slope(t[j][e], r_s, dn[e], s[e], mean_au, mean_a);
       }
       if (LAYER && !whole[j]) {
 #pragma unroll
@@ -586,18 +602,23 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           if (!at[j].inside(e)) t[j][e] = 0.f;  // (0 - mean)
       }
       if (a.dresidual != nullptr) {
-        float o[E];
+        T* to = static_cast<T*>(a.dresidual) + r * a.ld_dresidual + col0;
+        if (a.residual_scale == 1.f) {
+          rows.template put<0>(to, t[j], j);
+        } else {
+          float o[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[j][e];
-        rows.template put<0>(static_cast<T*>(a.dresidual) + r * a.ld_dresidual + col0, o, j);
+          for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[j][e];
+          rows.template put<0>(to, o, j);
+        }
       }
       float y[E];
       if (a.y != nullptr) {
         rows.y(y, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          y[e] = unit_value(y[e], mean_y, r_y);
-          A[j][e] = fmaf(t[j][e], y[e], A[j][e]);
+          if constexpr (LAYER) y[e] -= mean_y;
+          A[j][e] = fmaf(t[j][e] * r_y, y[e], A[j][e]);
           if constexpr (BIAS) B[j][e] += t[j][e];
         }
       }
@@ -621,14 +642,19 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           sum(one);
           two[0] = one[0];
         }
-        const float mean_bv = two[0] * inv, mean_b = two[1] * inv;
+        const float k_d = -(two[0] * inv) * r_y * r_y * r_y, k_b = two[1] * inv * r_y;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
           float y[E];
           rows.y(y, j);
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            t[j][e] = unit_slope(0.f, r_y, t[j][e], unit_value(y[e], mean_y, r_y), mean_bv, mean_b);
+          for (int e = 0; e < E; ++e) {
+            if constexpr (LAYER) {
+              t[j][e] = fmaf(y[e] - mean_y, k_d, fmaf(t[j][e], r_y, -k_b));
+            } else {
+              t[j][e] = fmaf(y[e], k_d, t[j][e] * r_y);
+            }
+          }
         }
       }
 #pragma unroll

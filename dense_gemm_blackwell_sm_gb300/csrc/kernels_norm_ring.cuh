@@ -431,15 +431,25 @@ struct RowsRing {
     to[0] = make_float4(v[0], v[1], v[2], v[3]);
     to[stride / 8] = make_float4(v[4], v[5], v[6], v[7]);
   }
-  __device__ __forceinline__ void scale(float (&v)[8], int k) const {
+  __device__ __forceinline__ void factors_of(float (&f)[8], int k) const {
     const float4* from = reinterpret_cast<const float4*>(factors + k * stride);
     const float4 lo = from[0], hi = from[stride / 8];
-    const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w;
+    f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
+  }
+  __device__ __forceinline__ void pre_factors(float (&f)[8], int j) const { factors_of(f, j); }
+  __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const {
+    float f[8];
+    factors_of(f, j);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f[e];
   }
-  __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const { scale(v, j); }
-  __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const { scale(v, 2 + j); }
+  __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const {
+    float f[8];
+    factors_of(f, 2 + j);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f[e];
+  }
   // where the part's sums of this thread's first group go in a sums array
   __device__ __forceinline__ int64_t sums_at(int part) const {
     return ((int64_t)part * clusters + rank) * threads * 16 + tid * 8;
