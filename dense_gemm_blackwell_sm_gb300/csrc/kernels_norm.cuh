@@ -458,13 +458,16 @@ __device__ __forceinline__ void centre(float (&v)[E], float mean, const Places& 
 // A row takes two rounds of sums over its columns (RMS: of s^2, a s and y^2; of
 // b v).
 //
-// Rows come through RowsIn, a ring in shared memory (kernels_norm_ring.cuh).
-template <bool LAYER, bool BIAS, bool MANY, typename T, typename P, typename RowsIn>
+// Rows come through RowsIn, a ring in shared memory (kernels_norm_ring.cuh).  FULL:
+// both norms and every array are there, known to the compiler.
+template <bool FULL, bool LAYER, bool BIAS, bool MANY, typename T, typename P, typename RowsIn>
 __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
                                                RowsIn& rows, RowSums& sum, int part, const NormWalk& walk,
                                                const Places (&at)[2], int col0) {
   constexpr int E = 8, G = 2;
-  const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
+  const bool post = FULL || (a.flags & FFN_NORM_POST) != 0, pre = FULL || (a.flags & FFN_NORM_PRE) != 0;
+  const bool has_ds = FULL || a.ds != nullptr, has_y = FULL || a.y != nullptr;
+  const bool has_dres = FULL || a.dresidual != nullptr, has_dy = FULL || a.dy != nullptr;
   const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
   const float inv_w = n_w > 0.f ? 1.f / n_w : 0.f;
   const int64_t per = sh.per;
@@ -570,7 +573,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
     float two[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < G; ++j) {
-      if (a.ds != nullptr) {
+      if (has_ds) {
         rows.ds(t[j], j);
       } else {
 #pragma unroll
@@ -601,7 +604,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         for (int e = 0; e < E; ++e)
           if (!at[j].inside(e)) t[j][e] = 0.f;  // (0 - mean)
       }
-      if (a.dresidual != nullptr) {
+      if (has_dres) {
         T* to = static_cast<T*>(a.dresidual) + r * a.ld_dresidual + col0;
         if (a.residual_scale == 1.f) {
           rows.template put<0>(to, t[j], j);
@@ -613,7 +616,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         }
       }
       float y[E];
-      if (a.y != nullptr) {
+      if (has_y) {
         rows.y(y, j);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -622,7 +625,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           if constexpr (BIAS) B[j][e] += t[j][e];
         }
       }
-      if (a.dy != nullptr) {
+      if (has_dy) {
         rows.scale_branch(t[j], j);
         if (post) {
 #pragma unroll
@@ -633,7 +636,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         }
       }
     }
-    if (a.dy != nullptr) {
+    if (has_dy) {
       if (post) {
         if constexpr (LAYER) {
           sum(two);

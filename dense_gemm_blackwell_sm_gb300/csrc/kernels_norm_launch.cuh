@@ -90,8 +90,9 @@ cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& direct, const Nor
 
 template <typename T, typename P, bool LAYER, bool BIAS>
 const void* norm_grad_kernel(const NormGradShape& sh) {
-  return sh.many ? (const void*)k_norm_grad<T, P, LAYER, BIAS, true>
-                 : (const void*)k_norm_grad<T, P, LAYER, BIAS, false>;
+  if (sh.many) return (const void*)k_norm_grad<T, P, false, LAYER, BIAS, true>;
+  return sh.full ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false>
+                 : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false>;
 }
 
 template <typename T, typename P>

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
 // The factors of a thread's columns stay in shared memory too, in places only that
 // thread reads and writes: from global memory they came from L2 for every row, since
 // the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us).
-template <typename T, typename P>
+template <typename T, typename P, bool FULL>
 struct RowsRing {
   const ffn_norm_grad_t& a;
   const Places (&at)[2];
@@ -420,12 +420,12 @@ struct RowsRing {
     if (fills) issue();
   }
   __device__ __forceinline__ void values(float (&v)[8], uint32_t array, int j) const {
-    from_slot<T>(v, ring.slot(ring.stage, array), piece[j]);
+    from_slot<T>(v, ring.slots + ((FULL ? 4u : ring.arrays) * ring.stage + array) * ring.pitch, piece[j]);
   }
   __device__ __forceinline__ void s(float (&v)[8], int j) const { values(v, 0, j); }
   __device__ __forceinline__ void dn(float (&v)[8], int j) const { values(v, 1, j); }
-  __device__ __forceinline__ void y(float (&v)[8], int j) const { values(v, y_at, j); }
-  __device__ __forceinline__ void ds(float (&v)[8], int j) const { values(v, ds_at, j); }
+  __device__ __forceinline__ void y(float (&v)[8], int j) const { values(v, FULL ? 2u : y_at, j); }
+  __device__ __forceinline__ void ds(float (&v)[8], int j) const { values(v, FULL ? 3u : ds_at, j); }
   __device__ __forceinline__ void keep(const float (&v)[8], int k) {
     float4* to = reinterpret_cast<float4*>(factors + k * stride);
     to[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -461,7 +461,7 @@ struct RowsRing {
   }
 };
 
-template <typename T, typename P, bool LAYER, bool BIAS, bool MANY>
+template <typename T, typename P, bool FULL, bool LAYER, bool BIAS, bool MANY>
 __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 : 2)
     k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
                 const __grid_constant__ NormSums ws, uint32_t* status) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   Places at[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
-  RowsRing<T, P> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
+  RowsRing<T, P, FULL> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
   rows.y_at = a.dn != nullptr ? 2u : 0u;
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
   rows.alone = sum.warps == 1 && sum.cluster == 1;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (part >= sh.parts) return;  // (whole warps only)
   // from here on columns count from the slice's first, in every array
-  norm_grad_rows<LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
+  norm_grad_rows<FULL, LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
 }
 
 }  // namespace

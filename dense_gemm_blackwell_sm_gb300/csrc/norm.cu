@@ -149,6 +149,7 @@ cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& d
     const int64_t off = (sh.period > 1 ? arrays[i].ld - a.D : arrays[i].ld) * b;
     if (arrays[i].p != nullptr && (!aligned16(arrays[i].p) || off % 16 != 0)) sh.slow |= 1u << i;
   }
+  sh.full = a.dn && a.ds && a.y && a.dresidual && a.dy && (a.flags & FFN_NORM_POST) != 0;
   const int rows = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
   // three rows ahead where two CTAs still share an SM, else two
   auto bytes = [&](int stages) {

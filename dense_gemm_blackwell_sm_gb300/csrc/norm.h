@@ -54,6 +54,7 @@ struct NormGradShape {
   uint32_t slow;           // arrays off the walk's shift: s, dn, y, ds, dresidual, dy
   int64_t columns;         // per CTA
   bool many;               // several whole groups per part (parts_per_group == 0)
+  bool full;               // both norms, and every row array given or asked for
   bool bias;               // sums of t and of dn are needed beside those with the unit rows
 };
 
