@@ -27,35 +27,34 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 gemm_status_t current_ffn_device(FfnDevice* out) {
   static std::mutex mu;
   static FfnDevice known[kMaxDevices] = {};
-  int dev = 0, n = 0;
+  int dev = 0, major = 0, minor = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
     return GEMM_ERR_NO_DEVICE;
   }
-  std::lock_guard<std::mutex> lock(mu);
-  FfnDevice& d = known[dev];
-  if (d.status == nullptr) {
-    if (cudaGetDeviceCount(&n) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      return GEMM_ERR_NO_DEVICE;
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    FfnDevice& d = known[dev];
+    if (d.status == nullptr) {
+      void* p = nullptr;
+      if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+      }
+      if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
+      if (cudaGetSymbolAddress(&p, g_ffn_status) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+      }
+      d.status = static_cast<uint32_t*>(p);
     }
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_CUDA;
-    }
-    if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_ffn_status) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_CUDA;
-    }
-    d.status = static_cast<uint32_t*>(p);
+    *out = d;
+    return GEMM_OK;
+  } catch (...) {
+    return GEMM_ERR_OOM;
   }
-  *out = d;
-  return GEMM_OK;
 }
 
 gemm_status_t launched(cudaError_t e) {

@@ -273,6 +273,40 @@ def test_large_offsets():
     del h, gu, dh, dx, dw
 
 
+@pytest.mark.parametrize("M,F,K", [(17, 1, 8), (40, 3, 64), (130, 17, 72), (256, 16, 8), (600, 5, 136)])
+def test_gated_narrow(M, F, K):
+    """Fewer features than a tile's columns, and reductions of one block, in the tiled kernel."""
+    gen, x, w = gated_inputs(M, F, K, "f16", F)
+    want_h, want_gu = ref.gated(f64(x), f64(w), "silu", "f16")
+    h, gu = ffn.gated(x, w, save=True)
+    assert_within(h, want_h, "h")
+    assert_within(gu, want_gu, "gu")
+    dh = randn(gen, M, F, dtype="f16")
+    for kept in (gu, None):
+        want = ref.gated_backward(f64(dh), f64(x), f64(w), f64(kept), "silu", "f16")
+        for got, b in zip(ffn.gated_backward(dh, x, w, gu=kept), want):
+            assert_within(got, b, "gradient")
+
+
+@pytest.mark.parametrize("M,F,K", [(100, 300, 512), (300, 4000, 128), (2000, 4000, 256)])
+def test_a_copy_that_never_comes_ends_in_a_status(M, F, K):
+    """One operand copy left out: the bounded waits run out, the call's kernels return,
+    ffn.check reports it once, and the next call is whole."""
+    gen, x, w = gated_inputs(M, F, K, "bf16", 1)
+    dh = randn(gen, M, F, dtype="bf16")
+    want = ffn.gated(x, w)
+    grads = ffn.gated_backward(dh, x, w)
+    assert ffn.check() == gemm.OK
+    ffn.gated(x, w, timeout_ns=50_000_000, debug_flags=ffn.DEBUG_SKIP_ONE_LOAD)
+    assert ffn.check() == gemm.ERR_DEVICE_TIMEOUT
+    assert ffn.check() == gemm.OK
+    ffn.gated_backward(dh, x, w, timeout_ns=50_000_000, debug_flags=ffn.DEBUG_SKIP_ONE_LOAD)
+    assert ffn.check() == gemm.ERR_DEVICE_TIMEOUT
+    assert torch.equal(ffn.gated(x, w), want)
+    assert all(torch.equal(a, b) for a, b in zip(ffn.gated_backward(dh, x, w), grads))
+    assert ffn.check() == gemm.OK
+
+
 def test_gated_refusals_on_the_gpu():
     _, x, w = gated_inputs(4, 16, 64, "bf16", 0)
     with pytest.raises(ValueError):
