@@ -447,9 +447,8 @@ __device__ __forceinline__ void centre(float (&v)[E], float mean, const Places& 
 }
 
 // With u = unit(s), v = unit(y), a = dn * pre_weight, t = ds + r_s (a - u mean(a u)
-// [- mean a]) and b = branch_scale * gate * t * post_weight, a thread holds 16
-// columns (two groups of 8) of each of the rows its part takes, and over those rows
-// the sums
+// [- mean a]) and b = branch_scale * gate * t * post_weight, a thread holds G
+// groups of 8 columns of each of the rows its part takes, and over those rows the sums
 //   A = sum t v,  B = sum t,  C = sum dn u,  Eo = sum dn,
 // from which every parameter's gradient follows, since gate and post_weight are
 // constant over a group's rows:
@@ -460,19 +459,21 @@ __device__ __forceinline__ void centre(float (&v)[E], float mean, const Places& 
 //
 // Rows come through RowsIn, a ring in shared memory (kernels_norm_ring.cuh).  FULL:
 // both norms and every array are there, known to the compiler.
-template <bool FULL, bool LAYER, bool BIAS, bool MANY, typename T, typename P, typename RowsIn>
+template <bool FULL, bool LAYER, bool BIAS, bool MANY, int G, typename T, typename P, typename RowsIn>
 __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
                                                RowsIn& rows, RowSums& sum, int part, const NormWalk& walk,
-                                               const Places (&at)[2], int col0) {
-  constexpr int E = 8, G = 2;
+                                               const Places (&at)[G], int col0) {
+  constexpr int E = 8;
   const bool post = FULL || (a.flags & FFN_NORM_POST) != 0, pre = FULL || (a.flags & FFN_NORM_PRE) != 0;
   const bool has_ds = FULL || a.ds != nullptr, has_y = FULL || a.y != nullptr;
   const bool has_dres = FULL || a.dresidual != nullptr, has_dy = FULL || a.dy != nullptr;
-  const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<2, E>(at) : 0.f;
+  const float inv = 1.f / (float)a.D, n_w = LAYER ? warp_elements<G, E>(at) : 0.f;
   const float inv_w = n_w > 0.f ? 1.f / n_w : 0.f;
   const int64_t per = sh.per;
   int64_t g = walk.group, group_end = (g + 1) * per;
-  const bool whole[G] = {at[0].template whole<E>(), at[1].template whole<E>()};
+  bool whole[G];
+#pragma unroll
+  for (int j = 0; j < G; ++j) whole[j] = at[j].template whole<E>();
   float A[G][E] = {}, C[G][E] = {}, B[G][BIAS ? E : 1] = {}, Eo[G][BIAS ? E : 1] = {};
   float GA[G][MANY ? E : 1] = {}, GB[G][(MANY && BIAS) ? E : 1] = {};
   rows.set_group(g);
@@ -747,8 +748,8 @@ __global__ void __launch_bounds__(1024)
   const bool weighted = g < 0 && !sh.many && a.groups > 1;  // sums over groups: each part with its gate
   if (i < D) {
     // the column's place: its slice's, and in it the part's shift
-    const int rank = i / (int)sh.columns, place = rank * sh.threads * 16 + i - rank * (int)sh.columns;
-    const int64_t pitch = (int64_t)sh.cluster * sh.threads * 16;
+    const int rank = i / (int)sh.columns, place = rank * sh.threads * sh.each + i - rank * (int)sh.columns;
+    const int64_t pitch = (int64_t)sh.cluster * sh.threads * sh.each;
     const int p0 = g < 0 ? 0 : g * sh.parts_per_group, p1 = g < 0 ? sh.parts : p0 + sh.parts_per_group;
 #pragma unroll 4
     for (int p = p0 + l; p < p1; p += LANES) {

@@ -90,9 +90,12 @@ cudaError_t norm_forward(const ffn_norm_t& a, const NormShape& direct, const Nor
 
 template <typename T, typename P, bool LAYER, bool BIAS>
 const void* norm_grad_kernel(const NormGradShape& sh) {
-  if (sh.many) return (const void*)k_norm_grad<T, P, false, LAYER, BIAS, true>;
-  return sh.full ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false>
-                 : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false>;
+  if (sh.many) return (const void*)k_norm_grad<T, P, false, LAYER, BIAS, true, 2>;
+  if (sh.each == 8)
+    return sh.full ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false, 1>
+                   : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false, 1>;
+  return sh.full ? (const void*)k_norm_grad<T, P, true, LAYER, BIAS, false, 2>
+                 : (const void*)k_norm_grad<T, P, false, LAYER, BIAS, false, 2>;
 }
 
 template <typename T, typename P>

@@ -333,20 +333,20 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
 // The factors of a thread's columns stay in shared memory too, in places only that
 // thread reads and writes: from global memory they came from L2 for every row, since
 // the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us).
-template <typename T, typename P, bool FULL>
+template <typename T, typename P, bool FULL, int G>
 struct RowsRing {
   const ffn_norm_grad_t& a;
-  const Places (&at)[2];
+  const Places (&at)[G];
   const RowCopies<T> copies;
   Ring ring;
   int64_t ahead, end, step;
   uint32_t y_at, ds_at;
   uint32_t slow;   // bits of the arrays off the walk's shift: s, dn, y, ds, dresidual, dy
-  float* factors;  // [pre_weight, branch][2] groups of 8, `stride` floats apart
-  int stride, col0, piece[2], clusters, rank, threads, tid;
+  float* factors;  // [pre_weight, branch][G] groups of 8, `stride` floats apart
+  int stride, col0, piece[G], clusters, rank, threads, tid;
   const T* in;     // (the lanes that fill, an array each) its row 0 here, null where it is slow
   int64_t in_ld;
-  bool whole[2], fills, alone, first_row;
+  bool whole[G], fills, alone, first_row;
 
   __device__ __forceinline__ void issue() {
     if (ahead >= end) return;
@@ -365,7 +365,7 @@ struct RowsRing {
       for (uint32_t s = 0; s < ring.stages; ++s) issue();
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < G; ++j) {
       float f[8];
       parameters<P>(f, from_column<P>(a.pre_weight, col0), 1.f, at[j]);
       keep(f, j);
@@ -373,19 +373,19 @@ struct RowsRing {
   }
   __device__ __forceinline__ void set_group(int64_t g) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < G; ++j) {
       float f[8], w[8];
       parameters<P>(f, from_column<P>(a.gate, g * a.ld_gate + col0), 1.f, at[j]);
       parameters<P>(w, from_column<P>(a.post_weight, col0), 1.f, at[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= a.branch_scale * w[e];
-      keep(f, 2 + j);
+      keep(f, G + j);
     }
   }
   __device__ __forceinline__ void fetch(const void* p, int64_t ld, int64_t r, uint32_t array) {
     const T* row = static_cast<const T*>(p) + r * ld + col0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < G; ++j) {
       T* to = reinterpret_cast<T*>(ring.slot(ring.stage, array) + (size_t)piece[j] * 16);
 #pragma unroll 4
       for (int e = 0; e < 8; ++e)
@@ -401,7 +401,7 @@ struct RowsRing {
       if (a.ds != nullptr && (slow & 8u)) fetch(a.ds, a.ld_ds, r, ds_at);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < G; ++j)
       if (!whole[j]) {
 #pragma unroll 1
         for (uint32_t k = 0; k < ring.arrays; ++k) clean_slot<T, 8>(ring.slot(ring.stage, k), piece[j], at[j]);
@@ -446,13 +446,13 @@ struct RowsRing {
   }
   __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const {
     float f[8];
-    factors_of(f, 2 + j);
+    factors_of(f, G + j);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= f[e];
   }
   // where the part's sums of this thread's first group go in a sums array
   __device__ __forceinline__ int64_t sums_at(int part) const {
-    return ((int64_t)part * clusters + rank) * threads * 16 + tid * 8;
+    return ((int64_t)part * clusters + rank) * threads * 8 * G + tid * 8;
   }
   // output 0: dresidual, 1: dy
   template <int OUTPUT>
@@ -461,8 +461,8 @@ struct RowsRing {
   }
 };
 
-template <typename T, typename P, bool FULL, bool LAYER, bool BIAS, bool MANY>
-__global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 : 2)
+template <typename T, typename P, bool FULL, bool LAYER, bool BIAS, bool MANY, int G>
+__global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G == 2) ? 1 : 2)
     k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
                 const __grid_constant__ NormSums ws, uint32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -480,10 +480,10 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   const NormWalk walk = norm_walk<MANY>(a, sh, min(part, sh.parts - 1));
   const int col0 = (int)(rank * sh.columns), cols = min((int)a.D - col0, (int)sh.columns);
   const int shift = norm_part_shift(a, sh, min(part, sh.parts - 1), sizeof(T));
-  Places at[2];
+  Places at[G];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
-  RowsRing<T, P, FULL> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
+  for (int j = 0; j < G; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
+  RowsRing<T, P, FULL, G> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
   rows.y_at = a.dn != nullptr ? 2u : 0u;
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
   rows.alone = sum.warps == 1 && sum.cluster == 1;
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   rows.tid = tid;
   rows.slow = sh.slow;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < G; ++j) {
     rows.piece[j] = (j * sh.threads + tid) * (int)sizeof(T) / 2;
     rows.whole[j] = at[j].template whole<8>();
   }
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   rows.factors = reinterpret_cast<float*>(smem) + 4 * threadIdx.x;
   rows.ring.stages = (uint32_t)sh.stages;
   rows.ring.arrays = rows.ds_at + (a.ds != nullptr ? 1u : 0u);
-  rows.ring.pitch = (uint32_t)(16 * sh.threads * (int)sizeof(T));
+  rows.ring.pitch = (uint32_t)(8 * G * sh.threads * (int)sizeof(T));
   rows.fills = tid < (int)rows.ring.arrays;
   {
     // lane k fills the k-th array given: s and dn, then y, then ds
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
     const uint32_t bit = s ? 1u : dn ? 2u : y ? 4u : 8u;
     rows.in = (p == nullptr || (sh.slow & bit)) ? nullptr : static_cast<const T*>(p) + col0;
   }
-  rows.ring.slots = smem + (size_t)4 * rows.stride * sizeof(float) +
+  rows.ring.slots = smem + (size_t)2 * G * rows.stride * sizeof(float) +
                     (size_t)lane_group * sh.stages * rows.ring.arrays * rows.ring.pitch;
   rows.ring.full = bars + lane_group * kNormStages;
   rows.ring.abort_flag = &abort_flag;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || sizeof(T) == 4 ? 1 :
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (part >= sh.parts) return;  // (whole warps only)
   // from here on columns count from the slice's first, in every array
-  norm_grad_rows<FULL, LAYER, BIAS, MANY, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
+  norm_grad_rows<FULL, LAYER, BIAS, MANY, G, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
 }
 
 }  // namespace

@@ -78,35 +78,51 @@ namespace {
 // The split of the backward pass; it depends on the sizes alone, so that the
 // workspace can be sized without a device and sums are the same on every call.
 NormGradShape grad_shape(const ffn_norm_grad_t& a) {
-  constexpr int kResident = 304;  // CTAs of 256 threads: two on each of 152 SMs
-  NormGradShape sh{};
-  sh.period = row_period(a.D * elem_bytes(a.dtype));
-  const int spare = sh.period > 1 ? 8 : 0;  // columns a shifted row may need more
-  for (sh.cluster = 1;; ++sh.cluster) {
-    sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + kNormGradEach - 1) / kNormGradEach * kNormGradEach;
-    sh.threads = round32((sh.columns + spare + kNormGradEach - 1) / kNormGradEach);
-    if (sh.threads <= kNormGradThreads || sh.cluster == 8) break;
-  }
-  sh.lanes = sh.threads == 32 ? 8 : 1;
+  constexpr int kNumSms = 152;  // each takes 512 threads of this kernel
   const bool gates = a.gate != nullptr || a.dgate != nullptr;
   const int64_t groups = gates ? a.groups : 1;
-  int64_t parts = (int64_t)kResident * (kNormGradThreads / (sh.threads * sh.lanes)) * sh.lanes / sh.cluster;
-  // two rows at least per part: a part's sums cost about what a row does
-  parts = std::max<int64_t>(1, std::min(parts, (a.M + 1) / 2));
-  if (groups >= parts && groups > 1) {
-    sh.many = true;
-    sh.parts_per_group = 0;
-    sh.period = 1;
-    parts = std::min(groups, parts);
-  } else {
-    sh.parts_per_group = (int)std::max<int64_t>(1, std::min(parts / groups, a.M / groups));
-    if (sh.parts_per_group < sh.period) sh.period = 1;
-    sh.parts_per_group = sh.parts_per_group / sh.period * sh.period;
-    parts = sh.parts_per_group * groups;
+  auto split = [&](int each) {
+    NormGradShape sh{};
+    sh.each = each;
+    sh.period = row_period(a.D * elem_bytes(a.dtype));
+    const int spare = sh.period > 1 ? 8 : 0;  // columns a shifted row may need more
+    for (sh.cluster = 1;; ++sh.cluster) {
+      sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + 15) / 16 * 16;
+      sh.threads = round32((sh.columns + spare + each - 1) / each);
+      if (sh.threads <= kNormGradThreads || sh.cluster == 8) break;
+    }
+    sh.lanes = sh.threads == 32 ? 8 : 1;
+    sh.per_sm = 2 * kNormGradThreads / (sh.threads * sh.lanes);
+    int64_t parts = (int64_t)kNumSms * sh.per_sm * sh.lanes / sh.cluster;
+    // two rows at least per part: a part's sums cost about what a row does
+    parts = std::max<int64_t>(1, std::min(parts, (a.M + 1) / 2));
+    if (groups >= parts && groups > 1) {
+      sh.many = true;
+      sh.parts_per_group = 0;
+      sh.period = 1;
+      parts = std::min(groups, parts);
+    } else {
+      sh.parts_per_group = (int)std::max<int64_t>(1, std::min(parts / groups, a.M / groups));
+      if (sh.parts_per_group < sh.period) sh.period = 1;
+      sh.parts_per_group = sh.parts_per_group / sh.period * sh.period;
+      parts = sh.parts_per_group * groups;
+    }
+    sh.parts = (int)parts;
+    return sh;
+  };
+  // 8 columns per thread where one CTA of that many threads takes the row with room to
+  // spare, else 16: a row's chain of sums and barriers is shorter then and more rows are
+  // under way, until a row needs a cluster (us with 8 and with 16 columns, bf16:
+  // 8192 x 1024 32.5 and 40.1, LayerNorm 45.7 and 79.9; 8192 x 64 18.9 and 28.8;
+  // 8192 x 2048 58.4 and 51.6; 8192 x 4096 in CTAs of 512 threads 123, in clusters of two
+  // 175, with 16 columns 85)
+  NormGradShape sh = split(16);
+  if (!sh.many && a.D < 8 * kNormGradThreads) {
+    const NormGradShape fine = split(8);
+    if (!fine.many && fine.cluster == 1) sh = fine;
   }
-  sh.parts = (int)parts;
   sh.per = (int)(a.M / groups);
-  sh.share = sh.many ? NormShare::of(groups, parts)
+  sh.share = sh.many ? NormShare::of(groups, sh.parts)
                      : NormShare::of((sh.per + sh.period - 1) / sh.period, sh.parts_per_group / sh.period);
   sh.bias = a.dpost_bias != nullptr || a.dpre_bias != nullptr || (a.dgate != nullptr && a.post_bias != nullptr);
   return sh;
@@ -114,7 +130,7 @@ NormGradShape grad_shape(const ffn_norm_grad_t& a) {
 
 int sums_of(const ffn_norm_grad_t& a, const NormGradShape& sh, NormSums* ws, float* base) {
   int n = 0;
-  const int64_t each = (int64_t)sh.parts * sh.cluster * sh.threads * 16;
+  const int64_t each = (int64_t)sh.parts * sh.cluster * sh.threads * sh.each;
   auto next = [&](bool need, float** p) {
     *p = nullptr;
     if (need) *p = base ? base + each * n : nullptr, ++n;
@@ -132,7 +148,7 @@ int sums_of(const ffn_norm_grad_t& a, const NormGradShape& sh, NormSums* ws, flo
 size_t norm_backward_workspace(const ffn_norm_grad_t& a) {
   const NormGradShape sh = grad_shape(a);
   NormSums ws{};
-  return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)(sh.cluster * sh.threads * 16) * 4;
+  return (size_t)sums_of(a, sh, &ws, nullptr) * (size_t)sh.parts * (size_t)(sh.cluster * sh.threads * sh.each) * 4;
 }
 
 cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& dev, cudaStream_t st) {
@@ -151,11 +167,12 @@ cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& d
   }
   sh.full = a.dn && a.ds && a.y && a.dresidual && a.dy && (a.flags & FFN_NORM_POST) != 0;
   const int rows = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
-  // three rows ahead where two CTAs still share an SM, else two
+  // three rows ahead where the SM holds that for all its CTAs, else two
   auto bytes = [&](int stages) {
-    return (size_t)sh.threads * sh.lanes * 32 * 4 + (size_t)sh.lanes * stages * rows * (size_t)(16 * sh.threads * b);
+    return (size_t)sh.threads * sh.lanes * sh.each * 2 * 4 +
+           (size_t)sh.lanes * stages * rows * (size_t)(sh.each * sh.threads * b);
   };
-  sh.stages = bytes(kNormStages) <= 108 * 1024 ? kNormStages : 2;
+  sh.stages = bytes(kNormStages) * (size_t)sh.per_sm <= 216 * 1024 ? kNormStages : 2;
   sh.smem = bytes(sh.stages);
   NormSums ws{};
   sums_of(a, sh, &ws, static_cast<float*>(a.workspace));

@@ -44,8 +44,10 @@ struct NormGradShape {
   int stages;              // rows of the ring
   size_t smem;
   int cluster;             // CTAs that share a row's columns
+  int each;                // columns per thread: 16, or 8
   int threads;             // per row and CTA
-  int lanes;               // rows a CTA takes at once (warps; 1 above 512 columns)
+  int per_sm;              // CTAs that an SM is meant to hold
+  int lanes;               // rows a CTA takes at once (warps; 1 where a row takes several)
   int parts;               // grid = ceil(parts / lanes) * cluster
   int parts_per_group;     // > 0: a part is in one group; 0: several whole groups
   int period;              // rows this far apart belong to one part
@@ -79,8 +81,7 @@ cudaError_t norm_backward_bf16(const ffn_norm_grad_t& a, const NormGradShape& sh
 cudaError_t norm_backward_f32(const ffn_norm_grad_t& a, const NormGradShape& sh, const NormSums& ws,
                               const FfnDevice& dev, cudaStream_t st);
 
-constexpr int kNormGradThreads = 256;  // most per CTA, 16 columns each
-constexpr int kNormGradEach = 16;
+constexpr int kNormGradThreads = 256;  // most per CTA
 constexpr int kNormStages = 3;                     // most rows of a ring
 constexpr size_t kNormRingBytes = 200 * 1024;      // most of one CTA
 

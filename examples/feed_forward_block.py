@@ -5,7 +5,8 @@ token, with this library's operators alone:
     h    = gated(n, w_in)                 both projections, activation and product in one kernel
     y    = matmul(h, w_out)               down projection
 
-and the same backwards.  The blocks learn to reproduce a fixed random stack's output.
+and the same backwards (tokens, width and hidden width are multiples of 8, since each is
+a reduction of `matmul` there).  The blocks learn to reproduce a fixed random stack's output.
 
     python examples/feed_forward_block.py [--layers 4 --width 1024 --hidden 2752 --tokens 2048 --steps 20]
 """
