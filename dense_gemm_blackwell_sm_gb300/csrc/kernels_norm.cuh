@@ -159,20 +159,67 @@ __device__ __forceinline__ const P* from_column(const void* p, int64_t i) {
   return p == nullptr ? nullptr : static_cast<const P*>(p) + i;
 }
 
-// Sums of N values (1, 2 or 4) over a warp, in every lane.  The values are added by
-// halves: each exchange step adds one half of the values in one half of the lanes,
-// so four values take 6 shuffles instead of 20; N more bring them to every lane.
+// Arithmetic on a thread's elements in pairs: one instruction for two fp32 operations,
+// each rounded as by itself.  An operand is an array or one value for all elements.
+template <typename V>
+__device__ __forceinline__ float2 pair_of(const V& v, int i) {
+  if constexpr (std::is_array<V>::value) {
+    return make_float2(v[2 * i], v[2 * i + 1]);
+  } else {
+    return make_float2(v, v);
+  }
+}
+template <int E, typename A, typename B, typename C>
+__device__ __forceinline__ void fma_to(float (&to)[E], const A& a, const B& b, const C& c) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 r = __ffma2_rn(pair_of(a, i), pair_of(b, i), pair_of(c, i));
+    to[2 * i] = r.x;
+    to[2 * i + 1] = r.y;
+  }
+}
+template <int E, typename A, typename B>
+__device__ __forceinline__ void mul_to(float (&to)[E], const A& a, const B& b) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 r = __fmul2_rn(pair_of(a, i), pair_of(b, i));
+    to[2 * i] = r.x;
+    to[2 * i + 1] = r.y;
+  }
+}
+template <int E, typename A, typename B>
+__device__ __forceinline__ void add_to(float (&to)[E], const A& a, const B& b) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 r = __fadd2_rn(pair_of(a, i), pair_of(b, i));
+    to[2 * i] = r.x;
+    to[2 * i + 1] = r.y;
+  }
+}
+template <int E>
+__device__ __forceinline__ void dot_to(float2& sum, const float (&a)[E], const float (&b)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) sum = __ffma2_rn(pair_of(a, i), pair_of(b, i), sum);
+}
+template <int E>
+__device__ __forceinline__ void sum_to(float2& sum, const float (&a)[E]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) sum = __fadd2_rn(pair_of(a, i), sum);
+}
+
+// Sums of N values (1 to 4) over a warp: lanes 32 / N k (8 k for three) and the next
+// hold value k's.  The values are added by halves: each exchange step adds one half of
+// the values in one half of the lanes, so four values take 6 shuffles instead of 20.
 template <int N>
-__device__ __forceinline__ void warp_sums(float (&v)[N]) {
-  static_assert(N == 1 || N == 2 || N == 4, "values per sum");
+__device__ __forceinline__ float warp_sums_apart(const float (&v)[N]) {
   const uint32_t lane = lane_idx();
-  constexpr int SPAN = 32 / N;  // lanes that share a value
   float x;
-  if constexpr (N == 4) {
+  if constexpr (N > 2) {
     const bool hi = (lane & 16u) != 0, odd = (lane & 8u) != 0;
-    float k0 = hi ? v[2] : v[0], k1 = hi ? v[3] : v[1];
+    const float v3 = N == 4 ? v[N - 1] : 0.f;
+    float k0 = hi ? v[2] : v[0], k1 = hi ? v3 : v[1];
     k0 += __shfl_xor_sync(0xffffffffu, hi ? v[0] : v[2], 16);
-    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v[3], 16);
+    k1 += __shfl_xor_sync(0xffffffffu, hi ? v[1] : v3, 16);
     x = (odd ? k1 : k0) + __shfl_xor_sync(0xffffffffu, odd ? k0 : k1, 8);
   } else if constexpr (N == 2) {
     const bool hi = (lane & 16u) != 0;
@@ -181,9 +228,18 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
     x = v[0];
   }
 #pragma unroll
-  for (int o = SPAN / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = (N > 2 ? 4 : 16 / N); o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+template <int N>
+constexpr int kLanesPerSum = N > 2 ? 8 : 32 / N;
+
+// the same in every lane
+template <int N>
+__device__ __forceinline__ void warp_sums(float (&v)[N]) {
+  const float x = warp_sums_apart(v);
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xffffffffu, x, k * SPAN);
+  for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xffffffffu, x, k * kLanesPerSum<N>);
 }
 
 // What the warps of a row tell one another: one warp; a CTA's warps; or, in a
@@ -191,14 +247,23 @@ __device__ __forceinline__ void warp_sums(float (&v)[N]) {
 // exchange suffices: a buffer is written again only after the barrier of the
 // exchange in between.
 struct RowSums {
-  float* parts;  // [2][kFloats] in shared memory
+  float* parts;  // [2][8 values][kMost warps] in shared memory
   int warps;     // per row and CTA
   int cluster, rank, turn;
-  static constexpr int kFloats = 64 * 8;
+  static constexpr int kMost = 64, kFloats = 8 * kMost;
 
   __device__ __forceinline__ bool alone() const { return warps * cluster == 1; }
 
-  // every warp's N values (the same in all its lanes), at [warp * N + k] of the answer
+  // Before the first sums: places behind the warps that are read with theirs.
+  __device__ __forceinline__ void clear() {
+    for (int i = (int)threadIdx.x; i < 64; i += (int)blockDim.x) {
+      const int w = (warps & ~3) + (i & 3);
+      if (w >= warps) parts[(i >> 2) * kMost + w] = 0.f;
+    }
+  }
+
+  // every warp's N values (the same in all its lanes), value k of warp w at
+  // [k * kMost + w] of the answer
   template <int N>
   __device__ __forceinline__ const float* exchange(const float (&v)[N]) {
     float* buf = parts + turn * kFloats;
@@ -207,33 +272,53 @@ struct RowSums {
     if (cluster == 1) {
       if (lane == 0) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) buf[warp * N + k] = v[k];
+        for (int k = 0; k < N; ++k) buf[k * kMost + warp] = v[k];
       }
       __syncthreads();
     } else {
       if (lane < (uint32_t)cluster) {
-        const uint32_t to = mapa_shared(smem_u32(buf + (rank * warps + warp) * N), lane);
+        const uint32_t to = mapa_shared(smem_u32(buf + rank * warps + warp), lane);
 #pragma unroll
-        for (int k = 0; k < N; ++k) st_cluster_u32(to + 4u * k, __float_as_uint(v[k]));
+        for (int k = 0; k < N; ++k) st_cluster_u32(to + 4u * kMost * k, __float_as_uint(v[k]));
       }
       cluster_sync_all();
     }
     return buf;
   }
 
-  // sums over all the row's threads, in every thread
+  // Sums over all the row's threads, in every thread.  A CTA's warps' sums are read
+  // four at a time by every thread, which takes less than a second round of shuffles.
   template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
-    warp_sums(v);
-    if (alone()) return;
-    const float* buf = exchange(v);
+    if (alone()) {
+      warp_sums(v);
+    } else if (cluster == 1) {
+      const float x = warp_sums_apart(v);
+      float* buf = parts + turn * kFloats;
+      turn ^= 1;
+      const int lane = (int)lane_idx(), k = lane / kLanesPerSum<N>;
+      if (lane % kLanesPerSum<N> == 0 && k < N) buf[k * kMost + (int)(threadIdx.x >> 5)] = x;
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = 0.f;
-    for (int w = (int)lane_idx(); w < warps * cluster; w += 32) {
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+      for (int w = 0; w < warps; w += 4) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] += buf[w * N + k];
+        for (int i = 0; i < N; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(buf + i * kMost + w);
+          v[i] += (q.x + q.y) + (q.z + q.w);
+        }
+      }
+    } else {
+      warp_sums(v);
+      const float* buf = exchange(v);
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = 0.f;
+      for (int w = (int)lane_idx(); w < warps * cluster; w += 32) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] += buf[k * kMost + w];
+      }
+      warp_sums(v);
     }
-    warp_sums(v);
   }
 };
 
@@ -299,13 +384,14 @@ __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places 
       const float* all = sum.exchange(mine);
       float total[1] = {0.f};
       const int l = (int)lane_idx(), n = sum.warps * sum.cluster;
-      for (int w = l; w < n; w += 32) total[0] = fmaf(all[3 * w], all[3 * w + 1], total[0]);
+      constexpr int M = RowSums::kMost;
+      for (int w = l; w < n; w += 32) total[0] = fmaf(all[w], all[M + w], total[0]);
       warp_sums(total);
       mean = total[0] * inv;
       s[0] = 0.f;
       for (int w = l; w < n; w += 32) {
-        const float c = all[3 * w + 1] - mean;
-        s[0] += fmaf(all[3 * w] * c, c, all[3 * w + 2]);
+        const float c = all[M + w] - mean;
+        s[0] += fmaf(all[w] * c, c, all[2 * M + w]);
       }
       warp_sums(s);
     }
@@ -326,11 +412,12 @@ __device__ __forceinline__ float warp_elements(const Places (&at)[NV]) {
 template <typename T, typename P, bool LAYER, bool WARP, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_norm_t a) {
   constexpr int E = 16 / (int)sizeof(T);
-  __shared__ float parts[2 * RowSums::kFloats];
+  __shared__ __align__(16) float parts[2 * RowSums::kFloats];
   const int tid = WARP ? (int)lane_idx() : (int)threadIdx.x, per_row = WARP ? 32 : (int)blockDim.x;
   const int64_t r = WARP ? (int64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
   const int D = (int)a.D;
   RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
+  if constexpr (!WARP) sum.clear();
   Places at[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -437,8 +524,7 @@ template <bool LAYER, int E>
 __device__ __forceinline__ void centre(float (&v)[E], float mean, const Places& at, bool whole) {
   if constexpr (LAYER) {
     if (whole) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] -= mean;
+      add_to(v, v, -mean);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] -= at.inside(e) ? mean : 0.f;
@@ -480,9 +566,15 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
   rows.begin(walk);
   for (int64_t r = walk.first; r < walk.end; r += walk.step) {
     if (!rows.next(r)) break;
-    float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[4];
+    float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[3];
+    float2 k2[3];  // sums of the even and of the odd elements
+    auto zero = [&] { k2[0] = k2[1] = k2[2] = make_float2(0.f, 0.f); };
+    auto join = [&] {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) k[i] = k2[i].x + k2[i].y;
+    };
+    zero();
     if constexpr (LAYER) {
-      k[0] = k[1] = k[2] = k[3] = 0.f;
 #pragma unroll
       for (int j = 0; j < G; ++j) {
         if (pre) {
@@ -490,25 +582,22 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           rows.s(s, j);
           rows.dn(dn, j);
           rows.scale_pre(dn, j);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            k[0] += s[e];
-            k[2] += dn[e];
-          }
+          sum_to(k2[0], s);
+          sum_to(k2[2], dn);
         }
         if (post) {
           float y[E];
           rows.y(y, j);
-#pragma unroll
-          for (int e = 0; e < E; ++e) k[1] += y[e];
+          sum_to(k2[1], y);
         }
       }
+      join();
+      zero();
       warp_sums(k);
       mean_s = k[0] * inv_w;  // the warp's own for now
       mean_y = k[1] * inv_w;
       mean_a = k[2];
     }
-    k[0] = k[1] = k[2] = k[3] = 0.f;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if (pre) {
@@ -517,20 +606,17 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         rows.dn(dn, j);
         rows.scale_pre(dn, j);
         centre<LAYER>(s, mean_s, at[j], whole[j]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          k[0] = fmaf(s[e], s[e], k[0]);
-          k[1] = fmaf(s[e], dn[e], k[1]);
-        }
+        dot_to(k2[0], s, s);
+        dot_to(k2[1], s, dn);
       }
       if (post) {
         float y[E];
         rows.y(y, j);
         centre<LAYER>(y, mean_y, at[j], whole[j]);
-#pragma unroll
-        for (int e = 0; e < E; ++e) k[2] = fmaf(y[e], y[e], k[2]);
+        dot_to(k2[2], y, y);
       }
     }
+    join();
     if constexpr (!LAYER) {
       sum(k);
     } else {
@@ -540,12 +626,13 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         const float mine[7] = {n_w, mean_s, mean_y, mean_a, k[0], k[1], k[2]};
         const float* all = sum.exchange(mine);
         const int l = (int)lane_idx(), n = sum.warps * sum.cluster;
-        k[0] = k[1] = k[2] = k[3] = 0.f;
+        constexpr int M = RowSums::kMost;
+        k[0] = k[1] = k[2] = 0.f;
         for (int w = l; w < n; w += 32) {
-          const float* q = all + 7 * w;
-          k[0] = fmaf(q[0], q[1], k[0]);
-          k[1] = fmaf(q[0], q[2], k[1]);
-          k[2] += q[3];
+          const float* q = all + w;
+          k[0] = fmaf(q[0], q[M], k[0]);
+          k[1] = fmaf(q[0], q[2 * M], k[1]);
+          k[2] += q[3 * M];
         }
         warp_sums(k);
         mean_s = k[0] * inv;
@@ -553,11 +640,11 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         mean_a = k[2];
         k[0] = k[1] = k[2] = 0.f;
         for (int w = l; w < n; w += 32) {
-          const float* q = all + 7 * w;
-          const float cs = q[1] - mean_s, cy = q[2] - mean_y;
-          k[0] += fmaf(q[0] * cs, cs, q[4]);
-          k[1] += fmaf(q[3], cs, q[5]);
-          k[2] += fmaf(q[0] * cy, cy, q[6]);
+          const float* q = all + w;
+          const float cs = q[M] - mean_s, cy = q[2 * M] - mean_y;
+          k[0] += fmaf(q[0] * cs, cs, q[4 * M]);
+          k[1] += fmaf(q[3 * M], cs, q[5 * M]);
+          k[2] += fmaf(q[0] * cy, cy, q[6 * M]);
         }
         warp_sums(k);
       }
@@ -571,7 +658,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
     const float r_s = rsqrtf(k[0] * inv + a.eps), k_c = -(k[1] * inv) * r_s * r_s * r_s, k_s = r_s * mean_a;
     const float r_y = post ? rsqrtf(k[2] * inv + a.eps) : 1.f;
     float t[G][E];
-    float two[2] = {0.f, 0.f};
+    float2 two2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int j = 0; j < G; ++j) {
       if (has_ds) {
@@ -586,19 +673,14 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         rows.dn(dn, j);
         rows.pre_factors(w, j);
         if constexpr (LAYER) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            s[e] -= mean_s;
-            t[j][e] -= k_s;
-          }
+          add_to(s, s, -mean_s);
+          add_to(t[j], t[j], -k_s);
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if constexpr (BIAS) Eo[j][e] += dn[e];
-          dn[e] *= r_s;
-          C[j][e] = fmaf(dn[e], s[e], C[j][e]);
-          t[j][e] = fmaf(dn[e], w[e], fmaf(s[e], k_c, t[j][e]));
-        }
+        if constexpr (BIAS) add_to(Eo[j], Eo[j], dn);
+        mul_to(dn, dn, r_s);
+        fma_to(C[j], dn, s, C[j]);
+        fma_to(t[j], s, k_c, t[j]);
+        fma_to(t[j], dn, w, t[j]);
       }
       if (LAYER && !whole[j]) {
 #pragma unroll
@@ -611,34 +693,30 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           rows.template put<0>(to, t[j], j);
         } else {
           float o[E];
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = a.residual_scale * t[j][e];
+          mul_to(o, t[j], a.residual_scale);
           rows.template put<0>(to, o, j);
         }
       }
       float y[E];
       if (has_y) {
         rows.y(y, j);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          if constexpr (LAYER) y[e] -= mean_y;
-          A[j][e] = fmaf(t[j][e] * r_y, y[e], A[j][e]);
-          if constexpr (BIAS) B[j][e] += t[j][e];
-        }
+        if constexpr (LAYER) add_to(y, y, -mean_y);
+        float tr[E];
+        mul_to(tr, t[j], r_y);
+        fma_to(A[j], tr, y, A[j]);
+        if constexpr (BIAS) add_to(B[j], B[j], t[j]);
       }
       if (has_dy) {
         rows.scale_branch(t[j], j);
         if (post) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            two[0] = fmaf(t[j][e], y[e], two[0]);
-            if constexpr (LAYER) two[1] += t[j][e];
-          }
+          dot_to(two2[0], t[j], y);
+          if constexpr (LAYER) sum_to(two2[1], t[j]);
         }
       }
     }
     if (has_dy) {
       if (post) {
+        float two[2] = {two2[0].x + two2[0].y, two2[1].x + two2[1].y};
         if constexpr (LAYER) {
           sum(two);
         } else {
@@ -651,14 +729,13 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
         for (int j = 0; j < G; ++j) {
           float y[E];
           rows.y(y, j);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if constexpr (LAYER) {
-              t[j][e] = fmaf(y[e] - mean_y, k_d, fmaf(t[j][e], r_y, -k_b));
-            } else {
-              t[j][e] = fmaf(y[e], k_d, t[j][e] * r_y);
-            }
+          if constexpr (LAYER) {
+            add_to(y, y, -mean_y);
+            fma_to(t[j], t[j], r_y, -k_b);
+          } else {
+            mul_to(t[j], t[j], r_y);
           }
+          fma_to(t[j], y, k_d, t[j]);
         }
       }
 #pragma unroll

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   constexpr int E = 16 / (int)sizeof(T);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[8 * kNormStages];
-  __shared__ float parts[2 * RowSums::kFloats];
+  __shared__ __align__(16) float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
   const int tid = WARP ? (int)lane_idx() : (int)threadIdx.x, per_row = WARP ? 32 : (int)blockDim.x;
   const int lane_group = WARP ? (int)(threadIdx.x >> 5) : 0, groups = WARP ? (int)(blockDim.x / 32) : 1;
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   ring.abort_flag = &abort_flag;
   ring.status = status;
   RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
+  if constexpr (!WARP) sum.clear();
   if (tid == 0) {
     for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), ring.arrays);
     fence_mbar_init();
@@ -441,14 +442,12 @@ struct RowsRing {
   __device__ __forceinline__ void scale_pre(float (&v)[8], int j) const {
     float f[8];
     factors_of(f, j);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f[e];
+    mul_to(v, v, f);
   }
   __device__ __forceinline__ void scale_branch(float (&v)[8], int j) const {
     float f[8];
     factors_of(f, G + j);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f[e];
+    mul_to(v, v, f);
   }
   // where the part's sums of this thread's first group go in a sums array
   __device__ __forceinline__ int64_t sums_at(int part) const {
@@ -467,13 +466,14 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G
                 const __grid_constant__ NormSums ws, uint32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[8 * kNormStages];
-  __shared__ float parts[2 * RowSums::kFloats];
+  __shared__ __align__(16) float parts[2 * RowSums::kFloats];
   __shared__ volatile uint32_t abort_flag;
   const int rank = sh.cluster > 1 ? (int)cluster_ctarank() : 0;
   const int tid = sh.lanes > 1 ? (int)lane_idx() : (int)threadIdx.x;
   const int lane_group = sh.lanes > 1 ? (int)(threadIdx.x >> 5) : 0;
   const int part = sh.lanes > 1 ? (int)blockIdx.x * sh.lanes + lane_group : (int)blockIdx.x / sh.cluster;
   RowSums sum{parts, sh.threads / 32, sh.cluster, rank, 0};
+  if (sh.cluster == 1) sum.clear();
   // The walk's shift is that of rows without gaps from a 16-byte boundary on, whatever
   // the arrays' pitches: which elements a thread adds up, and so the results' last
   // bits, depend on the sizes alone.
