@@ -346,54 +346,53 @@ template <bool LAYER, int NV, int E>
 __device__ __forceinline__ float2 unit_of(const float (&v)[NV][E], const Places (&at)[NV], int D, float n_w, float eps,
                                           RowSums& sum) {
   const float inv = 1.f / (float)D;
-  float s[1] = {0.f};
+  float2 pairs = make_float2(0.f, 0.f);
+  float s[1];
   if constexpr (!LAYER) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e) s[0] = fmaf(v[j][e], v[j][e], s[0]);
+    for (int j = 0; j < NV; ++j) dot_to(pairs, v[j], v[j]);
+    s[0] = pairs.x + pairs.y;
     sum(s);
     return make_float2(0.f, rsqrtf(s[0] * inv + eps));
   } else {
+    const float inv_w = n_w > 0.f ? 1.f / n_w : 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < E; ++e) s[0] += v[j][e];
+    for (int j = 0; j < NV; ++j) sum_to(pairs, v[j]);
+    s[0] = pairs.x + pairs.y;
     warp_sums(s);
-    float mean = n_w > 0.f ? s[0] / n_w : 0.f;
-    s[0] = 0.f;
+    float mean = s[0] * inv_w;
+    pairs = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (at[j].template whole<E>()) {
+      float c[E];
+      add_to(c, v[j], -mean);
+      if (!at[j].template whole<E>()) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float c = v[j][e] - mean;
-            s[0] = fmaf(c, c, s[0]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float c = at[j].inside(e) ? v[j][e] - mean : 0.f;
-            s[0] = fmaf(c, c, s[0]);
-          }
-        }
+        for (int e = 0; e < E; ++e)
+          if (!at[j].inside(e)) c[e] = 0.f;
       }
+      dot_to(pairs, c, c);
+    }
+    s[0] = pairs.x + pairs.y;
     warp_sums(s);
-    if (!sum.alone()) {
+    if (!sum.alone()) {  // (one CTA per row here)
       const float mine[3] = {n_w, mean, s[0]};
       const float* all = sum.exchange(mine);
-      float total[1] = {0.f};
-      const int l = (int)lane_idx(), n = sum.warps * sum.cluster;
       constexpr int M = RowSums::kMost;
-      for (int w = l; w < n; w += 32) total[0] = fmaf(all[w], all[M + w], total[0]);
-      warp_sums(total);
-      mean = total[0] * inv;
-      s[0] = 0.f;
-      for (int w = l; w < n; w += 32) {
-        const float c = all[M + w] - mean;
-        s[0] += fmaf(all[w] * c, c, all[2 * M + w]);
+      auto four = [&](int i) { return *reinterpret_cast<const float4*>(all + i); };
+      mean = 0.f;
+      for (int w = 0; w < sum.warps; w += 4) {
+        const float4 n = four(w), m = four(M + w);
+        mean += fmaf(n.x, m.x, n.y * m.y) + fmaf(n.z, m.z, n.w * m.w);
       }
-      warp_sums(s);
+      mean *= inv;
+      s[0] = 0.f;
+      for (int w = 0; w < sum.warps; w += 4) {
+        const float4 n = four(w), m = four(M + w), q = four(2 * M + w);
+        const float4 c = make_float4(m.x - mean, m.y - mean, m.z - mean, m.w - mean);
+        s[0] += (fmaf(n.x * c.x, c.x, q.x) + fmaf(n.y * c.y, c.y, q.y)) +
+                (fmaf(n.z * c.z, c.z, q.z) + fmaf(n.w * c.w, c.w, q.w));
+      }
     }
     return make_float2(mean, rsqrtf(s[0] * inv + eps));
   }

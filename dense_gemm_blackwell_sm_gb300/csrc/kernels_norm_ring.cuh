@@ -277,20 +277,18 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (post) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y;
+        if constexpr (LAYER) add_to(v[j], v[j], -st.x);
+        mul_to(v[j], v[j], st.y);
       }
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[j][e] *= f.branch[j][e];
       if constexpr (LAYER) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] += f.branch_bias[j][e];
+        fma_to(v[j], v[j], f.branch[j], f.branch_bias[j]);
+      } else {
+        mul_to(v[j], v[j], f.branch[j]);
       }
       if (a.residual != nullptr) {
         float q[E];
         from_slot<T>(q, ring.slot(ring.stage, 1), j * per_row + tid);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = fmaf(a.residual_scale, q[e], v[j][e]);
+        fma_to(v[j], q, a.residual_scale, v[j]);
       }
       if (LAYER && !whole[j]) {  // (past the row: a mean)
 #pragma unroll
@@ -314,11 +312,12 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
     if (pre) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = (v[j][e] - st.x) * st.y * f.pre[j][e];
+        if constexpr (LAYER) add_to(v[j], v[j], -st.x);
+        mul_to(v[j], v[j], st.y);
         if constexpr (LAYER) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] += f.pre_bias[j][e];
+          fma_to(v[j], v[j], f.pre[j], f.pre_bias[j]);
+        } else {
+          mul_to(v[j], v[j], f.pre[j]);
         }
         to_row(static_cast<T*>(a.n) + r * a.ld_n, v[j], at[j], whole[j]);
       }
