@@ -414,6 +414,42 @@ def test_sums_over_rows(M, groups, D):
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("M,D", [(5000, 33), (4000, 255), (2000, 1031), (1300, 2032), (1301, 2039), (1300, 2047),
+                                 (1300, 2048), (1300, 2049), (900, 4095), (900, 4096), (901, 4097), (700, 5001),
+                                 (500, 9003)])
+@pytest.mark.parametrize("dtype,kind", [("bf16", "rms"), ("f16", "layer"), ("f32", "rms")])
+def test_many_rows(M, D, dtype, kind):
+    """More rows than a device holds at once, around the widths where a row's split changes."""
+    t, p = norm_inputs(M, D, dtype, "f32", kind, 1, M + D)
+    check_norm(t, p, dtype, kind)
+
+
+def test_norm_large_offsets():
+    """Rows past 2^31 elements: the last rows' values, and sums over rows that are zero but there."""
+    M, D = 131080, 16392
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    t = {k: torch.zeros((M, D), dtype=torch.bfloat16, device=DEV) for k in ("y", "residual", "ds", "dn")}
+    assert t["y"].numel() > 2 ** 31
+    last = slice(M - 3, M)
+    for v in t.values():
+        v[last] = torch.randn((3, D), generator=gen, device=DEV).bfloat16()
+    p = dict(post_weight=torch.randn(D, generator=gen, device=DEV), post_bias=None, pre_bias=None,
+             pre_weight=torch.randn(D, generator=gen, device=DEV), gate=torch.randn(D, generator=gen, device=DEV))
+    s, n = ffn.block_norm(t["y"], t["residual"], post_norm=True, **p)
+    got = ffn.block_norm_backward(t["ds"], t["dn"], t["y"], s, post_norm=True, **p)
+    few = {k: v[last] for k, v in t.items()}
+    one = {**p, "gate": p["gate"][None]}
+    kw = dict(post=True, pre=True, kind="rms", eps=1e-6)
+    want_s, want_n = ref_norm(few, one, "bf16", **kw)
+    want = ref_norm_grad(few, one, s[last], "bf16", **kw)
+    assert_within(s[last], want_s, "s")
+    assert_within(n[last], want_n, "n")
+    for name, g, b in zip(got._fields, got, want):
+        if g is not None:
+            assert_within(g[last] if g.shape == (M, D) else g.reshape(b[0].shape), b, name)
+    assert not s[:M - 3].any() and not n[:M - 3].any() and not got.dy[:M - 3].any()
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_rows_of_zeros_and_constants(kind):
     """A padding row of zeros and a constant row: eps alone is under the root."""
