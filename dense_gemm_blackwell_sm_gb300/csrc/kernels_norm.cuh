@@ -408,6 +408,8 @@ __device__ __forceinline__ float warp_elements(const Places (&at)[NV]) {
   return n[0];
 }
 
+// A row per warp or CTA straight from global memory, for calls with too few rows to
+// keep a ring busy: bound by the launch and one row's latency (1 x 4096 bf16 2.7 us).
 template <typename T, typename P, bool LAYER, bool WARP, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_norm_t a) {
   constexpr int E = 16 / (int)sizeof(T);
@@ -723,6 +725,7 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
           sum(one);
           two[0] = one[0];
         }
+        if constexpr (!LAYER) rows.met_again();
         const float k_d = -(two[0] * inv) * r_y * r_y * r_y, k_b = two[1] * inv * r_y;
 #pragma unroll
         for (int j = 0; j < G; ++j) {

@@ -155,7 +155,8 @@ __device__ __forceinline__ void to_row(T* row, const float (&f)[E], const Places
 
 // A thread keeps its columns' factors in registers where it can (HOLD): with 32-bit
 // parameters they are more bytes than a 16-bit row, and with most of the SM's memory
-// given to the ring they would come from L2 for every row (8192 x 4096: 63 us so).
+// given to the ring they would come from L2 for every row (8192 x 4096: 63 us so, 45
+// held).
 //   z -> s:  post_weight * gate * branch_scale, post_bias * gate * branch_scale
 //   s -> n:  pre_weight, pre_bias
 template <typename P, bool LAYER, int NV, int E>
@@ -187,7 +188,9 @@ struct RowFactors {
   }
 };
 
-// (An RMS norm with biases takes the direct form.)
+// Bound by memory: 8192 x 4096 bf16, RMS twice, 44.8 us (6.0 TB/s of the four arrays'
+// bytes); as a layer norm 72, where the sums around the warps' means and their joining
+// take as long as the copies.  (An RMS norm with biases takes the direct form.)
 template <typename T, typename P, bool LAYER, bool WARP, int NV>
 __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) ? 2 : 1)
     k_norm_ring(const __grid_constant__ ffn_norm_t a, const __grid_constant__ NormShape sh, uint32_t* status) {
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
 // groups) are brought to their slots by the threads that read them.
 // The factors of a thread's columns stay in shared memory too, in places only that
 // thread reads and writes: from global memory they came from L2 for every row, since
-// the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us).
+// the ring leaves little of the SM's memory to L1 (8192 x 4096: 238 us so, 78 now).
 template <typename T, typename P, bool FULL, int G>
 struct RowsRing {
   const ffn_norm_grad_t& a;
@@ -346,7 +349,9 @@ struct RowsRing {
   int stride, col0, piece[G], clusters, rank, threads, tid;
   const T* in;     // (the lanes that fill, an array each) its row 0 here, null where it is slow
   int64_t in_ld;
-  bool whole[G], fills, alone, first_row;
+  // (the lanes that fill) where a row's slot is free again: at the barrier of its second
+  // round of sums, or, where it is read after that, at the next row's first barrier
+  bool whole[G], fills, alone, first_row, early, late;
 
   __device__ __forceinline__ void issue() {
     if (ahead >= end) return;
@@ -410,8 +415,12 @@ struct RowsRing {
   }
   // every thread of the group has come to this row: the slots of the one before are free
   __device__ __forceinline__ void met() {
-    if (fills && !alone && !first_row) issue();
+    if (late && !first_row) issue();
     first_row = false;
+  }
+  // every thread has this row's second sums: all but y has been read
+  __device__ __forceinline__ void met_again() {
+    if (early) issue();
   }
   __device__ __forceinline__ void done() {
     ring.advance();
@@ -459,6 +468,10 @@ struct RowsRing {
   }
 };
 
+// 8192 x 4096 bf16, RMS twice: 78 us with the columns' sums, 5.1 TB/s of the six arrays'
+// bytes.  128 registers hold a thread's parameter sums and one row's values, so 16 warps
+// share an SM, and what a row's two rounds of sums leave idle is what is missing: about
+// half the issue slots are used.  As a layer norm 141 us: one more pass over the row.
 template <typename T, typename P, bool FULL, bool LAYER, bool BIAS, bool MANY, int G>
 __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G == 2) ? 1 : 2)
     k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,
@@ -512,6 +525,11 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G
     rows.in_ld = s ? a.ld_s : dn ? a.ld_dn : y ? a.ld_y : a.ld_ds;
     const uint32_t bit = s ? 1u : dn ? 2u : y ? 4u : 8u;
     rows.in = (p == nullptr || (sh.slow & bit)) ? nullptr : static_cast<const T*>(p) + col0;
+    // (8192 x 4096 82.4 -> 78.0 us; the layer norm's kernel has no registers left for it:
+    // 142 -> 149)
+    const bool again = !LAYER && (FULL || (a.dy != nullptr && (a.flags & FFN_NORM_POST) != 0));
+    rows.early = rows.fills && !rows.alone && again && !y;
+    rows.late = rows.fills && !rows.alone && !rows.early;
   }
   rows.ring.slots = smem + (size_t)2 * G * rows.stride * sizeof(float) +
                     (size_t)lane_group * sh.stages * rows.ring.arrays * rows.ring.pitch;
