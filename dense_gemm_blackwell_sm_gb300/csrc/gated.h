@@ -88,7 +88,8 @@ int gated_stages(int consumers, int a_rows, int hw);
 size_t gated_smem_bytes(int consumers, int a_rows, int hw, int stages);
 constexpr int kGatedThreads = 384;
 
-// the gated projections for at most 16 tokens (kernel_gated_few.cu)
+// the gated projections for few tokens (kernel_gated_few.cu)
+constexpr int64_t kGatedFewTokens = 32;
 cudaError_t launch_gated_few(const ffn_gated_t& a, cudaStream_t st);
 
 // the pre-activations' gradient from kept ones (kernel_gated_slopes.cu)

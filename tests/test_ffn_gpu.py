@@ -48,7 +48,8 @@ def assert_within(got, want, what):
 # one token, decode batches, the edges of 16 / 32 / 128 / 256 / 512-row tiles, widths and depths
 # around tiles of 64 and 128, odd F, a K of one 16-byte chunk and one past a stage
 GATED = [(1, 256, 128), (1, 1, 8), (2, 77, 1000), (3, 128, 64), (5, 33, 2056), (8, 300, 512), (9, 64, 72),
-         (15, 129, 264), (16, 1000, 640), (17, 96, 136), (33, 257, 520), (64, 1543, 200), (127, 128, 64),
+         (15, 129, 264), (16, 1000, 640), (17, 96, 136), (20, 100, 72),
+         (24, 513, 264), (25, 9, 8), (29, 1541, 2056), (32, 300, 4104), (33, 257, 520), (64, 1543, 200), (127, 128, 64),
          (128, 256, 1032), (129, 130, 192), (255, 511, 328), (256, 127, 64), (257, 640, 72), (300, 1541, 520),
          (511, 88, 136), (513, 260, 256), (1100, 1031, 392)]
 
@@ -74,7 +75,7 @@ def test_gated(M, F, K, dtype):
 
 
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("M", [4, 150, 520])
+@pytest.mark.parametrize("M", [4, 28, 150, 520])
 def test_gated_activations(act, M):
     """Each activation in each kernel, gates from deep saturation to zero."""
     F, K = 200, 64
@@ -87,7 +88,7 @@ def test_gated_activations(act, M):
         assert_within(got, want, act)
 
 
-@pytest.mark.parametrize("M", [1, 7, 13, 40, 300, 700])
+@pytest.mark.parametrize("M", [1, 7, 13, 22, 32, 40, 300, 700])
 def test_integers_are_exact(M):
     """Small integers: every fp32 sum and product is exact, so the outputs must be too."""
     F, K = 130, 256
@@ -151,7 +152,7 @@ def test_gated_gradient_against_differences():
     assert abs(got - want) <= 8 * (np.sqrt(((bx * vx) ** 2).sum()) + np.sqrt(((bw * vw) ** 2).sum()))
 
 
-@pytest.mark.parametrize("M", [3, 12, 100, 600])
+@pytest.mark.parametrize("M", [3, 12, 31, 100, 600])
 def test_gated_pitched_rows(M):
     """Rows wider than their use (and odd pitches of h, gu and dh), with NaN in between:
     nothing outside the arrays is read into a result or written."""
@@ -170,7 +171,7 @@ def test_gated_pitched_rows(M):
         assert_within(got, b, "gradient")
 
 
-@pytest.mark.parametrize("M", [1, 6, 20, 300])
+@pytest.mark.parametrize("M", [1, 6, 20, 30, 300])
 def test_unaligned_output(M):
     """An output that starts 2 bytes off a 16-byte boundary."""
     F, K = 128, 128
@@ -181,7 +182,7 @@ def test_unaligned_output(M):
     assert flat[0] == 7 and flat[-1] == 7
 
 
-@pytest.mark.parametrize("M", [2, 40, 700])
+@pytest.mark.parametrize("M", [2, 18, 40, 700])
 def test_values_that_are_not_finite_stay_in_their_row_and_column(M):
     F, K = 150, 136
     gen, x, w = gated_inputs(M, F, K, "bf16", 5)
@@ -197,7 +198,7 @@ def test_values_that_are_not_finite_stay_in_their_row_and_column(M):
     assert not bool(h[:, 7].isfinite().any())
 
 
-@pytest.mark.parametrize("M", [5, 12, 90, 530])
+@pytest.mark.parametrize("M", [5, 12, 27, 90, 530])
 def test_gated_is_reproducible(M):
     F, K = 260, 328
     gen, x, w = gated_inputs(M, F, K, "bf16", 9)
@@ -273,7 +274,7 @@ def test_large_offsets():
     del h, gu, dh, dx, dw
 
 
-@pytest.mark.parametrize("M,F,K", [(17, 1, 8), (40, 3, 64), (130, 17, 72), (256, 16, 8), (600, 5, 136)])
+@pytest.mark.parametrize("M,F,K", [(33, 1, 8), (40, 3, 64), (130, 17, 72), (256, 16, 8), (600, 5, 136)])
 def test_gated_narrow(M, F, K):
     """Fewer features than a tile's columns, and reductions of one block, in the tiled kernel."""
     gen, x, w = gated_inputs(M, F, K, "f16", F)
