@@ -178,3 +178,12 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
         ffn.block_norm_backward(None, None, x, x)
     with pytest.raises(ValueError):
         ffn.block_norm_backward(x, None, x, x)
+
+
+def test_binding_refuses_what_is_no_tensor():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for call in (lambda: ffn.gated(x, [1.0]), lambda: ffn.gated(None, x), lambda: ffn.gated_backward(1, x, x),
+                 lambda: ffn.block_norm("y"), lambda: ffn.block_norm(x, 3), lambda: ffn.block_norm(x, gate=1.0),
+                 lambda: ffn.block_norm_backward(x, x, x, 0), lambda: ffn.block_norm(x, eps="small")):
+        with pytest.raises((TypeError, ValueError)):
+            call()

@@ -326,6 +326,37 @@ def test_gated_refusals_on_the_gpu():
         ffn.gated(x, w, out=torch.zeros(4, 15, dtype=torch.bfloat16, device=DEV))
 
 
+def test_calls_keep_nothing():
+    """Outputs, temporaries and refused calls leave no memory and no references behind."""
+    import sys
+    _, x, w = gated_inputs(40, 24, 64, "bf16", 3)
+    gate = torch.ones(64, device=DEV)
+    dh = torch.ones(40, 24, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+
+    def calls():
+        h, gu = ffn.gated(x, w, save=True)
+        ffn.gated_backward(dh, x, w, gu=gu)
+        ffn.gated(x, w, out=h, gu=gu, stream=side)
+        s, n = ffn.block_norm(x, gate=gate, post_norm=True, pre_weight=gate)
+        ffn.block_norm_backward(n, s, x, s, gate=gate, post_norm=True, pre_weight=gate, stream=side.cuda_stream)
+        for bad in (lambda: ffn.gated(x, w[:7]), lambda: ffn.gated(x, w, act=9), lambda: ffn.block_norm(x, x[:2]),
+                    lambda: ffn.block_norm(x, gate=gate[:3])):
+            with pytest.raises((ValueError, gemm.GemmError)):
+                bad()
+        torch.cuda.synchronize()
+        return h, gu
+
+    h, gu = calls()
+    assert ffn.gated(x, w, out=h) is h
+    held = torch.cuda.memory_allocated()
+    counts = [sys.getrefcount(t) for t in (x, w, gate, dh, h, None)][:-1]
+    for _ in range(20):
+        calls()
+    assert torch.cuda.memory_allocated() <= held  # (what another stream used is freed some calls later)
+    assert [sys.getrefcount(t) for t in (x, w, gate, dh, h, None)][:-1] == counts
+
+
 # ------------------------------------------------------------------------ norms
 
 # rows of one element, around warps and 8-element accesses, powers of two, odd lengths, the longest
