@@ -563,8 +563,8 @@ __device__ __forceinline__ void norm_grad_rows(const ffn_norm_grad_t& a, const N
   for (int j = 0; j < G; ++j) whole[j] = at[j].template whole<E>();
   float A[G][E] = {}, C[G][E] = {}, B[G][BIAS ? E : 1] = {}, Eo[G][BIAS ? E : 1] = {};
   float GA[G][MANY ? E : 1] = {}, GB[G][(MANY && BIAS) ? E : 1] = {};
-  rows.set_group(g);
   rows.begin(walk);
+  rows.set_group(g);
   for (int64_t r = walk.first; r < walk.end; r += walk.step) {
     if (!rows.next(r)) break;
     float mean_s = 0.f, mean_y = 0.f, mean_a = 0.f, k[3];
@@ -830,11 +830,17 @@ __global__ void __launch_bounds__(1024)
     const int rank = i / (int)sh.columns, place = rank * sh.threads * sh.each + i - rank * (int)sh.columns;
     const int64_t pitch = (int64_t)sh.cluster * sh.threads * sh.each;
     const int p0 = g < 0 ? 0 : g * sh.parts_per_group, p1 = g < 0 ? sh.parts : p0 + sh.parts_per_group;
+    // (parts come in whole periods and so do lanes: a lane's parts are of one kind)
+    const uint32_t row_bytes = (uint32_t)D * (uint32_t)element_bytes;
+    const uint32_t kind_bytes = sh.period > 1 ? (uint32_t)(l % sh.period) * row_bytes : 0u;
+    const float per_group = sh.many ? 0.f : 1.f / (float)sh.parts_per_group;
 #pragma unroll 4
     for (int p = p0 + l; p < p1; p += LANES) {
-      const int64_t at = p * pitch + place + norm_part_shift(a, sh, p, element_bytes);
-      const float f =
-          weighted ? parameter<P>(a.gate, (int64_t)(p / sh.parts_per_group) * a.ld_gate + i, 1.f) : 1.f;
+      const int pg = (int)(((float)p + 0.5f) * per_group);  // the part's group: exact below 2^22
+      const uint32_t off =
+          sh.period > 1 ? (((uint32_t)pg * (uint32_t)sh.per * row_bytes + kind_bytes) & 15u) / (uint32_t)element_bytes : 0u;
+      const int64_t at = p * pitch + place + off;
+      const float f = weighted ? parameter<P>(a.gate, (int64_t)pg * a.ld_gate + i, 1.f) : 1.f;
       if (ws.a != nullptr) v[0] = fmaf(f, ws.a[at], v[0]);
       if (ws.b != nullptr) v[1] = fmaf(f, ws.b[at], v[1]);
       if (g < 0 && ws.c != nullptr) v[2] += ws.c[at];
