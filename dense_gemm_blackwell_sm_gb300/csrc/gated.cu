@@ -208,7 +208,7 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
 }  // namespace
 
 cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_t st) {
-  if (a.M <= kGatedFewTokens) return launch_gated_few(a, st);
+  if (a.M <= kGatedFewTokens) return launch_gated_few(a, dev.num_sms, st);
   GatedParams p = common_params(a, dev);
   p.gu = a.gu;
   p.ld_gu = a.ld_gu;

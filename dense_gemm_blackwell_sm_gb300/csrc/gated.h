@@ -90,7 +90,7 @@ constexpr int kGatedThreads = 384;
 
 // the gated projections for few tokens (kernel_gated_few.cu)
 constexpr int64_t kGatedFewTokens = 32;
-cudaError_t launch_gated_few(const ffn_gated_t& a, cudaStream_t st);
+cudaError_t launch_gated_few(const ffn_gated_t& a, int num_sms, cudaStream_t st);
 
 // the pre-activations' gradient from kept ones (kernel_gated_slopes.cu)
 cudaError_t launch_gated_slopes(const ffn_gated_grad_t& a, int num_sms, cudaStream_t st);

@@ -12,16 +12,19 @@
 // A CTA owns 8 hidden features; its 8 warps split K and add their sums in shared
 // memory, where one thread per feature and token joins g and u.  Above 8 tokens, x
 // (which comes through L1, a piece per 8 tokens) would be as many loads as the weights,
-// so a CTA owns 16 features and each piece of x serves four weight rows.  The launch is
-// a programmatic dependent of the previous kernel; while it waits, L2 fetches the first
-// weights (a prefetch returns no data, so it may run ahead of the wait even if the
-// previous kernel writes them).
+// so a CTA owns 16 features and each piece of x serves four weight rows.  Where that
+// leaves the SMs half empty, 16 warps split K (up to 16 tokens: their sums fit shared
+// memory).  The launch is a programmatic dependent of the previous kernel; while it
+// waits, L2 fetches the first weights (a prefetch returns no data, so it may run ahead
+// of the wait even if the previous kernel writes them).
 //
 // us for F x K = 14336 x 4096, 4096 x 4096 and 1024 x 1024 (bf16):
-//    1 token    33.4 (7.0 TB/s)  10.9   1.9     the weights are read exactly once
-//   16 tokens   37.9             13.2   2.8     with 8 features per CTA 45.4, 15.2, 3.2
+//    1 token    33.4 (7.0 TB/s)  10.9   1.6     the weights are read exactly once
+//   16 tokens   37.9             13.2   2.4     with 8 features per CTA 45.4, 15.2, 3.2
 //   32 tokens   45.0             15.8   3.7     on tensor-memory tiles 46.2, 20.3, 8.1
 //   48 tokens   76.7             28.3   6.9     the same, 46.6, 20.3, 8.1: hence the limit
+// 16 and 8 warps at one token: 2048 x 4096 5.9 and 8.2, 700 x 4096 4.3 and 6.9,
+// 4096 x 4096 (512 CTAs) 12.8 and 11.0.
 #include <type_traits>
 
 #include "ffn_common.cuh"
@@ -32,7 +35,6 @@ namespace dgb {
 
 namespace {
 
-constexpr int GF_THREADS = 256;
 constexpr int GF_ROWS = 8;  // hidden features of a fragment
 
 __device__ __forceinline__ uint4 load_once(const void* p) {
@@ -62,11 +64,11 @@ __device__ __forceinline__ void mma_rows16(float (&d)[4], uint32_t a0, uint32_t 
 }
 
 // NT: token tiles of 8.  FR: fragments of 8 features (with their gate and up rows) a warp
-// takes at once, which share the tokens' pieces.
-template <typename T, int NT, int FR, int ACT>
-__global__ void __launch_bounds__(GF_THREADS, FR == 1 ? 4 : 2)
+// takes at once, which share the tokens' pieces.  W: warps that split K.
+template <typename T, int NT, int FR, int W, int ACT>
+__global__ void __launch_bounds__(32 * W, (FR == 1 ? 32 : 16) / W)
     k_gated_few(const __grid_constant__ ffn_gated_t a) {
-  constexpr int W = GF_THREADS / 32, ROWS = GF_ROWS * FR;
+  constexpr int ROWS = GF_ROWS * FR;
   constexpr int PIECES = 3 - FR;  // 16-byte pieces of each row in a group
   constexpr int GROUPS = 2;       // groups on their way
   __shared__ float red[W][2 * ROWS][8 * NT + 1];
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(GF_THREADS, FR == 1 ? 4 : 2)
   __syncthreads();
   // neighbouring threads store neighbouring features
 #pragma unroll
-  for (int i = (int)threadIdx.x; i < 8 * NT * ROWS; i += GF_THREADS) {
+  for (int i = (int)threadIdx.x; i < 8 * NT * ROWS; i += 32 * W) {
     const int r = i % ROWS, m = i / ROWS;
     const int64_t fo = (int64_t)blockIdx.x * ROWS + r;
     if (m >= a.M || fo >= a.F) continue;
@@ -168,31 +170,35 @@ __global__ void __launch_bounds__(GF_THREADS, FR == 1 ? 4 : 2)
   }
 }
 
-template <typename T, int NT, int FR>
+template <typename T, int NT, int FR, int W>
 const void* few_kernel(int act) {
   switch (act) {
-    case EPI_ACT_RELU: return (const void*)k_gated_few<T, NT, FR, EPI_ACT_RELU>;
-    case EPI_ACT_SILU: return (const void*)k_gated_few<T, NT, FR, EPI_ACT_SILU>;
-    case EPI_ACT_GELU_TANH: return (const void*)k_gated_few<T, NT, FR, EPI_ACT_GELU_TANH>;
-    case EPI_ACT_GELU_ERF: return (const void*)k_gated_few<T, NT, FR, EPI_ACT_GELU_ERF>;
-    default: return (const void*)k_gated_few<T, NT, FR, EPI_ACT_NONE>;
+    case EPI_ACT_RELU: return (const void*)k_gated_few<T, NT, FR, W, EPI_ACT_RELU>;
+    case EPI_ACT_SILU: return (const void*)k_gated_few<T, NT, FR, W, EPI_ACT_SILU>;
+    case EPI_ACT_GELU_TANH: return (const void*)k_gated_few<T, NT, FR, W, EPI_ACT_GELU_TANH>;
+    case EPI_ACT_GELU_ERF: return (const void*)k_gated_few<T, NT, FR, W, EPI_ACT_GELU_ERF>;
+    default: return (const void*)k_gated_few<T, NT, FR, W, EPI_ACT_NONE>;
   }
 }
 
 template <typename T>
-const void* few_kernel(int64_t M, int act) {
-  if (M <= 8) return few_kernel<T, 1, 1>(act);
-  return M <= 16 ? few_kernel<T, 2, 2>(act) : M <= 24 ? few_kernel<T, 3, 2>(act) : few_kernel<T, 4, 2>(act);
+const void* few_kernel(int64_t M, int act, bool wide) {
+  if (M <= 8) return wide ? few_kernel<T, 1, 1, 16>(act) : few_kernel<T, 1, 1, 8>(act);
+  if (M <= 16) return wide ? few_kernel<T, 2, 2, 16>(act) : few_kernel<T, 2, 2, 8>(act);
+  return M <= 24 ? few_kernel<T, 3, 2, 8>(act) : few_kernel<T, 4, 2, 8>(act);
 }
 
 }  // namespace
 
-cudaError_t launch_gated_few(const ffn_gated_t& a, cudaStream_t st) {
+cudaError_t launch_gated_few(const ffn_gated_t& a, int num_sms, cudaStream_t st) {
   const int rows = a.M <= 8 ? GF_ROWS : 2 * GF_ROWS;
+  const int64_t ctas = (a.F + rows - 1) / rows;
+  const bool wide = a.M <= 16 && ctas <= (a.M <= 8 ? 2 : 1) * (int64_t)num_sms;
   LaunchSpec s;
-  s.func = a.dtype == FFN_BF16 ? few_kernel<__nv_bfloat16>(a.M, a.activation) : few_kernel<__half>(a.M, a.activation);
-  s.grid = dim3((unsigned)((a.F + rows - 1) / rows), 1, 1);
-  s.block = dim3(GF_THREADS, 1, 1);
+  s.func = a.dtype == FFN_BF16 ? few_kernel<__nv_bfloat16>(a.M, a.activation, wide)
+                               : few_kernel<__half>(a.M, a.activation, wide);
+  s.grid = dim3((unsigned)ctas, 1, 1);
+  s.block = dim3(wide ? 512 : 256, 1, 1);
   s.pdl = true;
   ffn_gated_t copy = a;
   void* args[] = {&copy};

@@ -326,6 +326,17 @@ def test_gated_refusals_on_the_gpu():
         ffn.gated(x, w, out=torch.zeros(4, 15, dtype=torch.bfloat16, device=DEV))
 
 
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 17, 25])
+@pytest.mark.parametrize("F,K", [(2440, 264), (1208, 72), (2424, 8), (1217, 4096)])
+def test_few_tokens_over_the_device(M, F, K):
+    """As many CTAs as SMs, twice as many and a few more; K of fewer pieces than warps."""
+    gen, x, w = gated_inputs(M, F, K, "bf16", F)
+    want_h, want_gu = ref.gated(f64(x), f64(w), "gelu_erf", "bf16")
+    h, gu = ffn.gated(x, w, act="gelu_erf", save=True)
+    assert_within(h, want_h, "h")
+    assert_within(gu, want_gu, "gu")
+
+
 def test_calls_keep_nothing():
     """Outputs, temporaries and refused calls leave no memory and no references behind."""
     import sys
