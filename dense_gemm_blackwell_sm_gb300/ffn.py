@@ -103,7 +103,7 @@ def load():
 _calls = None
 
 
-def _load_calls():
+def load_calls():
     """The extension (raises if it is not built)."""
     global _calls
     if _calls is None:
@@ -143,7 +143,7 @@ def gated(x, w, act="silu", save=False, out=None, gu=None, stream=None, timeout_
     ``act``: "none", "relu", "silu", "gelu_tanh", "gelu_erf" or a gemm.ACT_* code.
     With ``save`` the pre-activations (M, 2F) are kept for gated_backward and the
     answer is (h, gu).  ``out`` and ``gu`` may be given, as (M, F) and (M, 2F)."""
-    h, gu = (_calls or _load_calls()).gated(x, w, _code(ACTIVATIONS, act, "act"), save, out, gu, stream, timeout_ns,
+    h, gu = (_calls or load_calls()).gated(x, w, _code(ACTIVATIONS, act, "act"), save, out, gu, stream, timeout_ns,
                                             debug_flags)
     return (h, gu) if save else h
 
@@ -153,7 +153,7 @@ def gated_backward(dh, x, w, gu=None, act="silu", need_dx=True, need_dw=True, st
     """(dx, dw) of gated(x, w, act) for dh = dL/dh (M, F).  ``gu`` is what gated
     kept; without it the pre-activations are computed again from x and w.  dx
     (M, K) and dw (2F, K) have the inputs' type; either is None when not needed."""
-    return (_calls or _load_calls()).gated_backward(dh, x, w, gu, _code(ACTIVATIONS, act, "act"), need_dx, need_dw,
+    return (_calls or load_calls()).gated_backward(dh, x, w, gu, _code(ACTIVATIONS, act, "act"), need_dx, need_dw,
                                                     stream, timeout_ns, debug_flags)
 
 
@@ -171,7 +171,7 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, post_bias
     (kind "rms") or the layer norm ("layer").  gate is (D), or (groups, D) with
     consecutive runs of M / groups rows sharing one.  s may be the residual and n
     may be y (in place).  Weights, biases and gate share one type, y's or float32."""
-    return (_calls or _load_calls()).block_norm(
+    return (_calls or load_calls()).block_norm(
         y, residual, post_norm, post_weight, post_bias, gate, pre_norm, pre_weight, pre_bias,
         _code(NORM_KINDS, kind, "kind"), eps, residual_scale, branch_scale, need_s, s, n, stream)
 
@@ -182,7 +182,7 @@ def block_norm_backward(ds, dn, y, s, *, post_norm=False, post_weight=None, post
     """NormGrads of block_norm for ds = dL/ds (None: zero) and dn = dL/dn, from its y
     and the s it returned.  A parameter's gradient (fp32) is computed where the
     parameter is given; dgate has the gate's shape."""
-    return NormGrads._make((_calls or _load_calls()).block_norm_backward(
+    return NormGrads._make((_calls or load_calls()).block_norm_backward(
         ds, dn, y, s, post_norm, post_weight, post_bias, gate, pre_norm, pre_weight, pre_bias,
         _code(NORM_KINDS, kind, "kind"), eps, residual_scale, branch_scale, need_dresidual, need_dy, need_dparams,
         stream))
