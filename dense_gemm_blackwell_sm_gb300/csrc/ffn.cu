@@ -159,6 +159,12 @@ gemm_status_t ffn_gated(const ffn_gated_t* args, gemm_stream_t stream) {
   return launched(launch_gated(a, dev, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int64_t ffn_gated_backward_workspace(const ffn_gated_grad_t* args) {
+  if (!args || gated_sizes(args->M, args->F, args->K, args->dtype, args->activation, args->timeout_ns) != GEMM_OK)
+    return -1;
+  return (int64_t)gated_backward_workspace(*args);
+}
+
 gemm_status_t ffn_gated_backward(const ffn_gated_grad_t* args, gemm_stream_t stream) {
   if (!args) return GEMM_ERR_INVALID_ARG;
   ffn_gated_grad_t a = *args;
@@ -169,7 +175,8 @@ gemm_status_t ffn_gated_backward(const ffn_gated_grad_t* args, gemm_stream_t str
       !pitch(&a.ld_dgu, 2 * a.F) || !pitch(&a.ld_dx, a.K) || !pitch(&a.ld_dw, a.K))
     return GEMM_ERR_INVALID_ARG;
   if (a.ld_x % 8 != 0 || a.ld_w % 8 != 0 || a.ld_dgu % 8 != 0 || !aligned(a.x, 16) || !aligned(a.w, 16) ||
-      !aligned(a.dgu, 16) || !aligned(a.gu, 2) || !aligned(a.dh, 2) || !aligned(a.dx, 2) || !aligned(a.dw, 2))
+      !aligned(a.dgu, 16) || !aligned(a.gu, 2) || !aligned(a.dh, 2) || !aligned(a.dx, 2) || !aligned(a.dw, 2) ||
+      !aligned(a.workspace, 32))
     return GEMM_ERR_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   FfnDevice dev;
@@ -182,6 +189,7 @@ gemm_status_t ffn_gated_backward(const ffn_gated_grad_t* args, gemm_stream_t str
   }
   if (!a.dh || !a.dgu) return GEMM_ERR_INVALID_ARG;
   if (!a.x && (a.dw || !a.gu)) return GEMM_ERR_INVALID_ARG;
+  if (!a.workspace && gated_backward_workspace(a) > 0) return GEMM_ERR_INVALID_ARG;
   if (!a.w && (a.dx || !a.gu)) return GEMM_ERR_INVALID_ARG;
   const gemm_status_t ds = current_ffn_device(&dev);
   if (ds != GEMM_OK) return ds;

@@ -24,6 +24,7 @@ cudaError_t resident_ctas(const void* func, int threads, size_t smem, size_t mos
 
 // The pitches below are resolved (never 0).
 cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_t st);
+size_t gated_backward_workspace(const ffn_gated_grad_t& a);
 cudaError_t launch_gated_backward(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st);
 
 cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st);

@@ -82,6 +82,12 @@ Tensor empty_rows(int64_t M, int64_t N, at::ScalarType dtype, int index) {
   return at::empty({M, N}, at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)index));
 }
 
+// (a refused call asks for -1 bytes and is refused when it is made)
+Tensor workspace_of(int64_t bytes, int index) {
+  if (bytes <= 0) return Tensor();
+  return at::empty({bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, (c10::DeviceIndex)index));
+}
+
 // The call on the given stream, or the current one.  `made`: memory of this call, which
 // another stream has to know of.
 template <typename Args>
@@ -209,7 +215,9 @@ PyObject* gated_backward(PyObject*, PyObject* const* p, Py_ssize_t n) {
   a.dw = dw.defined() ? dw.data_ptr() : nullptr;
   a.timeout_ns = int_of(p[8]);
   a.debug_flags = (int32_t)int_of(p[9]);
-  call(ffn_gated_backward, "ffn_gated_backward", a, index, p[7], {&dgu, &dx, &dw});
+  const Tensor workspace = workspace_of(ffn_gated_backward_workspace(&a), index);
+  a.workspace = workspace.defined() ? workspace.data_ptr() : nullptr;
+  call(ffn_gated_backward, "ffn_gated_backward", a, index, p[7], {&dgu, &dx, &dw, &workspace});
   return tuple_of({&dx, &dw});
   END_HANDLE_TH_ERRORS
 }
@@ -351,11 +359,8 @@ PyObject* block_norm_backward(PyObject*, PyObject* const* p, Py_ssize_t nargs) {
   a.dpost_bias = gradient(v.post_bias, dpost_bias);
   a.dpre_weight = gradient(v.pre_weight, dpre_weight);
   a.dpre_bias = gradient(v.pre_bias, dpre_bias);
-  const int64_t bytes = ffn_norm_backward_workspace(&a);
-  if (bytes > 0) {
-    workspace = at::empty({bytes}, f32.dtype(at::kByte));
-    a.workspace = workspace.data_ptr();
-  }
+  workspace = workspace_of(ffn_norm_backward_workspace(&a), index);
+  a.workspace = workspace.defined() ? workspace.data_ptr() : nullptr;
   call(ffn_norm_backward, "ffn_norm_backward", a, index, p[18],
        {&dresidual, &dy, &dgate, &dpost_weight, &dpost_bias, &dpre_weight, &dpre_bias, &workspace});
   return tuple_of({&dresidual, &dy, &dgate, &dpost_weight, &dpost_bias, &dpre_weight, &dpre_bias});

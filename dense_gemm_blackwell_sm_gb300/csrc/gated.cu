@@ -80,6 +80,7 @@ void fill_task(GatedTask* t, int64_t rows, int64_t cols, int64_t kb, int tile_m,
   t->rows = (int32_t)rows;
   t->cols = (int32_t)cols;
   t->kb = (int32_t)kb;
+  t->kb_slice = (int32_t)kb;
   t->tiles_m = (int32_t)ceil_div64(rows, tile_m);
   t->tiles_n = (int32_t)ceil_div64(cols, tile_n);
   t->raster_group = std::min(8, t->tiles_m);
@@ -142,39 +143,66 @@ cudaError_t launch_pair(const A& a, const FfnDevice& dev, GatedParams& p, void* 
   return launch_tiles(func_of(bf16, t.consumers, a.activation), t.consumers, p.n0, dev, maps, p, st);
 }
 
+// How the products of the backward pass are cut: consumers and columns of a tile, and
+// slices of dx's reduction.
+struct ProductPlan {
+  int consumers, hw, slices;
+  int64_t kb_slice;
+};
+
+// The cut with the least time for both products' work spread over the clusters, whichever
+// are wanted: a product's bits do not depend on the other's being asked for.  It takes
+// the SM pairs of the device the library is for, so that it is known without a device.
+// With few tokens and wide layers dx is a few tiles with a long reduction each; slices of
+// it keep the other clusters busy, for a pass over their sums (a launch, and each sum
+// written and read).
+ProductPlan plan_products(int64_t M, int64_t F, int64_t K) {
+  constexpr double kClusters = 76;
+  const int64_t kb_dx = ceil_div64(2 * F, 64), kb_dw = ceil_div64(M, 64);
+  ProductPlan best{1, 128, 1, kb_dx};
+  double least = 0;
+  for (int consumers = 2; consumers >= 1; --consumers)
+    for (int hw = 128; hw >= 64; hw -= 64) {
+      const int64_t tiles_k = ceil_div64(K, 2 * hw);
+      const int64_t n_dx = ceil_div64(M, 256 * consumers) * tiles_k, n_dw = ceil_div64(2 * F, 256 * consumers) * tiles_k;
+      for (const int64_t want : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        const int64_t kb_slice = ceil_div64(kb_dx, want), slices = ceil_div64(kb_dx, kb_slice);
+        const double sums = slices > 1 ? (double)slices * (double)M * (double)K * 4.0 : 0.0;
+        if (want > 1 && (slices != want || kb_slice < 4 || sums > 64e6)) continue;
+        const double dx = product_tile_time(kb_slice, consumers, hw), dw = product_tile_time(kb_dw, consumers, hw);
+        const double t = std::max((dx * (double)(n_dx * slices) + dw * (double)n_dw) / kClusters, std::max(dx, dw)) +
+                         (slices > 1 ? 3.0 + sums * 2 / 4e6 : 0.0);
+        if (least == 0 || t < least) {
+          least = t;
+          best = {consumers, hw, (int)slices, kb_slice};
+        }
+      }
+    }
+  return best;
+}
+
 // dx = dgu w and dw = dgu^T x in one launch, the product with the longer reduction first
 cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st) {
   if (!a.dx && !a.dw) return cudaSuccess;
   const bool bf16 = a.dtype == FFN_BF16;
-  const int clusters = std::max(1, dev.num_sms / 2);
   const int64_t kb_dx = ceil_div64(2 * a.F, 64), kb_dw = ceil_div64(a.M, 64);
-  // The tile with the least time for both products' work spread over the clusters,
-  // whichever are wanted: a product's bits do not depend on the other's being asked for.
-  Tiling best{1, 128};
-  double least = 0;
-  for (int consumers = 2; consumers >= 1; --consumers)
-    for (int hw = 128; hw >= 64; hw -= 64) {
-      const int64_t tiles_k = ceil_div64(a.K, 2 * hw);
-      const int64_t n_dx = ceil_div64(a.M, 256 * consumers) * tiles_k, n_dw = ceil_div64(2 * a.F, 256 * consumers) * tiles_k;
-      const double dx = product_tile_time(kb_dx, consumers, hw), dw = product_tile_time(kb_dw, consumers, hw);
-      const double t = std::max((dx * (double)n_dx + dw * (double)n_dw) / clusters, std::max(dx, dw));
-      if (least == 0 || t < least) {
-        least = t;
-        best = {consumers, hw};
-      }
-    }
+  const ProductPlan best = plan_products(a.M, a.F, a.K);
   GatedParams p = common_params(a, dev);
   p.hw = best.hw;
   p.a_rows = 128;
   p.split = 1;  // (their operands' copies bound these, not the MMAs' issue)
   p.two_slots = 1;
   const int tile_m = 256 * best.consumers, tile_n = 2 * best.hw;
-  const bool dx_first = a.dx && (!a.dw || kb_dx >= kb_dw);
+  const bool dx_first = a.dx && (!a.dw || best.kb_slice >= kb_dw);
   CUtensorMap maps[4];
+  int32_t tiles[2] = {0, 0};
   int n = 0;
   bool ok = true;
   auto add_dx = [&] {
     fill_task(&p.task[n], a.M, a.K, kb_dx, tile_m, tile_n, bf16, tile_n, IDESC_B_MN_MAJOR, a.dx, a.ld_dx);
+    p.task[n].kb_slice = (int32_t)best.kb_slice;
+    if (best.slices > 1) p.task[n].partial = static_cast<float*>(a.workspace);
+    tiles[n] = p.task[n].tiles_m * p.task[n].tiles_n * best.slices;
     ok = ok &&
          encode_rows16(&maps[2 * n], bf16, a.dgu, (uint64_t)(2 * a.F), (uint64_t)a.M, (uint64_t)a.ld_dgu, 64, 128) &&
          encode_rows16(&maps[2 * n + 1], bf16, a.w, (uint64_t)a.K, (uint64_t)(2 * a.F), (uint64_t)a.ld_w, 64, 64);
@@ -184,6 +212,7 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
   if (a.dw) {
     fill_task(&p.task[n], 2 * a.F, a.K, kb_dw, tile_m, tile_n, bf16, tile_n, IDESC_A_MN_MAJOR | IDESC_B_MN_MAJOR, a.dw,
               a.ld_dw);
+    tiles[n] = p.task[n].tiles_m * p.task[n].tiles_n;
     ok = ok &&
          encode_rows16(&maps[2 * n], bf16, a.dgu, (uint64_t)(2 * a.F), (uint64_t)a.M, (uint64_t)a.ld_dgu, 64, 64) &&
          encode_rows16(&maps[2 * n + 1], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64, 64);
@@ -191,18 +220,20 @@ cudaError_t launch_products(const ffn_gated_grad_t& a, const FfnDevice& dev, cud
   }
   if (a.dx && !dx_first) add_dx();
   if (!ok) return cudaErrorInvalidValue;
-  p.n0 = p.task[0].tiles_m * p.task[0].tiles_n;
+  p.n0 = tiles[0];
+  p.n1 = tiles[1];
   if (n == 2) {
-    p.n1 = p.task[1].tiles_m * p.task[1].tiles_n;
-    p.fill = (int32_t)(product_tile_time(p.task[0].kb, best.consumers, best.hw) /
-                           product_tile_time(p.task[1].kb, best.consumers, best.hw) +
+    p.fill = (int32_t)(product_tile_time(p.task[0].kb_slice, best.consumers, best.hw) /
+                           product_tile_time(p.task[1].kb_slice, best.consumers, best.hw) +
                        0.5);
   } else {
     maps[2] = maps[0];
     maps[3] = maps[1];
   }
-  return launch_tiles(gated_products_kernel(bf16, best.consumers), best.consumers, (int64_t)p.n0 + p.n1, dev, maps, p,
-                      st);
+  const cudaError_t e = launch_tiles(gated_products_kernel(bf16, best.consumers), best.consumers,
+                                     (int64_t)p.n0 + p.n1, dev, maps, p, st);
+  if (e != cudaSuccess || !a.dx || best.slices == 1) return e;
+  return launch_gated_join(a, best.slices, dev.num_sms, st);
 }
 
 }  // namespace
@@ -215,6 +246,12 @@ cudaError_t launch_gated(const ffn_gated_t& a, const FfnDevice& dev, cudaStream_
   p.vec_gate = alignment_of(a.gu, a.ld_gu);
   p.vec_up = alignment_of(static_cast<const char*>(a.gu) + 2 * a.F, a.ld_gu);
   return launch_pair(a, dev, p, a.h, a.ld_h, gated_forward_kernel, st);
+}
+
+size_t gated_backward_workspace(const ffn_gated_grad_t& a) {
+  if (a.dx == nullptr || a.M == 0) return 0;
+  const int slices = plan_products(a.M, a.F, a.K).slices;
+  return slices > 1 ? (size_t)slices * (size_t)a.M * (size_t)a.K * 4 : 0;
 }
 
 cudaError_t launch_gated_backward(const ffn_gated_grad_t& a, const FfnDevice& dev, cudaStream_t st) {

@@ -26,12 +26,14 @@ enum GatedMode {
 struct GatedTask {
   int32_t rows, cols;         // of the output (cols = F for the gated modes)
   int32_t kb;                 // 64-wide blocks of the reduction
+  int32_t kb_slice;           // of one slice of it, where tiles take a slice each
   int32_t tiles_m, tiles_n, raster_group;
   int32_t a_mn;               // the first operand's rows run along the reduction
   uint32_t idesc;
   int32_t vec_out;            // alignment of the output's rows: 2 = 32 bytes, 1 = 16 bytes, 0 = neither
   void* out;
   int64_t ld_out;
+  float* partial;             // slices x rows x cols, or null: the tiles' sums go to `out`
 };
 
 struct GatedParams {
@@ -91,6 +93,9 @@ constexpr int kGatedThreads = 384;
 // the gated projections for few tokens (kernel_gated_few.cu)
 constexpr int64_t kGatedFewTokens = 32;
 cudaError_t launch_gated_few(const ffn_gated_t& a, int num_sms, cudaStream_t st);
+
+// adds the slices of dx
+cudaError_t launch_gated_join(const ffn_gated_grad_t& a, int slices, int num_sms, cudaStream_t st);
 
 // the pre-activations' gradient from kept ones (kernel_gated_slopes.cu)
 cudaError_t launch_gated_slopes(const ffn_gated_grad_t& a, int num_sms, cudaStream_t st);

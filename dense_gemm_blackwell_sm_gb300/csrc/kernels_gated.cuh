@@ -212,6 +212,18 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   const WaitCtl w{abort_flag, p.status, p.timeout_ns, mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u)};
   const int32_t cid = (int32_t)(blockIdx.x / 2), clusters = (int32_t)(gridDim.x / 2);
 
+  // the slice of the reduction a tile takes (products; `tile` is then the tile in it), and
+  // its blocks
+  auto slice_of = [&](const GatedTask& t, int32_t& tile) {
+    if (MODE != GATED_PRODUCTS || t.partial == nullptr) return 0;
+    const int32_t tiles = t.tiles_m * t.tiles_n, slice = tile / tiles;
+    tile -= slice * tiles;
+    return slice;
+  };
+  auto blocks_of = [&](const GatedTask& t, int32_t slice) {
+    return MODE == GATED_PRODUCTS ? min(t.kb_slice, t.kb - slice * t.kb_slice) : t.kb;
+  };
+
   // the accumulator of a cluster's i-th tile: two take turns where TMEM holds them
   auto slot_of = [&](int32_t i, uint32_t cons) {
     return NCONS == 2 ? cons : p.two_slots ? (uint32_t)(i & 1) : 0u;
@@ -232,10 +244,12 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         const CUtensorMap* tmA = (MODE == GATED_PRODUCTS && task) ? &tmA1 : &tmA0;
         const CUtensorMap* tmB = (MODE == GATED_PRODUCTS && task) ? &tmB1 : &tmB0;
         int32_t tm, tn;
+        const int32_t slice = slice_of(t, tile);
         raster_tile(tile, t.tiles_m, t.tiles_n, t.raster_group, tm, tn);
         const int32_t row0 = tm * TILE_M + (int32_t)rank * 128;
-        for (int32_t it = 0; it < t.kb; ++it) {
-          const int32_t k0 = it * 64;
+        const int32_t first = slice * t.kb_slice, blocks = blocks_of(t, slice);
+        for (int32_t it = 0; it < blocks; ++it) {
+          const int32_t k0 = (first + it) * 64;
           if (!mbar_wait(smem_u32(empty + stage), sphase ^ 1u, w, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
           const uint32_t own = smem_u32(full + stage);
           const uint32_t fb = mapa_shared(own, 0);
@@ -297,6 +311,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
       bool ok = true;
       for (int32_t i = 0; ok && gated_tile(p, cid, clusters, i, task, tile); ++i) {
         const GatedTask& t = p.task[task];
+        const int32_t blocks = blocks_of(t, slice_of(t, tile));
         const uint32_t slot = slot_of(i, cons), apar = parity_of(i);
         if (!mbar_wait<true>(smem_u32(acc_empty + slot), apar ^ 1u, w, WAIT_MMA_ACC_EMPTY)) break;
         tc_fence_after();
@@ -308,7 +323,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
         };
         advance(first);
         int32_t it = (int32_t)first;
-        for (; it < t.kb; it += (int32_t)step) {
+        for (; it < blocks; it += (int32_t)step) {
           if (!mbar_wait(smem_u32(full + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
           tc_fence_after();
           const uint32_t sa = smem_u32(ring + (size_t)stage * STAGE + cons * A_BYTES);
@@ -323,8 +338,8 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           advance(step);
         }
         if (!ok) break;
-        // (the ring goes on at block kb: step back where this thread went past it)
-        if (it > t.kb) {
+        // (the ring goes on behind the last block: step back where this thread went past it)
+        if (it > blocks) {
           if (stage == 0) { stage = S - 1u; sphase ^= 1u; } else { --stage; }
         }
         mma_commit_pair(smem_u32(acc_full + slot), 3u);
@@ -344,6 +359,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     for (int32_t i = 0; gated_tile(p, cid, clusters, i, task, tile); ++i) {
       const GatedTask& t = p.task[task];
       int32_t tm, tn;
+      const int32_t slice = slice_of(t, tile);
       raster_tile(tile, t.tiles_m, t.tiles_n, t.raster_group, tm, tn);
       const uint32_t slot = slot_of(i, grp), apar = parity_of(i);
       const int32_t row0 =
@@ -386,6 +402,13 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
           uint32_t v[32];
           load_sums(tbase + 32u * (uint32_t)s, v);
           if (s + dstep >= steps) hand_back();
+          if (t.partial != nullptr) {  // (rows of cols fp32: a multiple of 32 bytes)
+            float* dst = t.partial + ((int64_t)slice * t.rows + row0 + (int32_t)lane) * t.cols + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if ((int)lane < rows && 8 * j + 8 <= n) st_global_v8(dst + 8 * j, v + 8 * j);
+            continue;
+          }
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = pack2<T>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));

@@ -51,7 +51,7 @@ class GatedArgs(ctypes.Structure):
 class GatedGradArgs(ctypes.Structure):
     _fields_ = [("M", _i64), ("F", _i64), ("K", _i64), ("dtype", _i32), ("activation", _i32),
                 ("x", _p), ("w", _p), ("gu", _p), ("dh", _p), ("dgu", _p), ("dx", _p), ("dw", _p),
-                ("ld_x", _i64), ("ld_w", _i64), ("ld_gu", _i64), ("ld_dh", _i64), ("ld_dgu", _i64),
+                ("workspace", _p), ("ld_x", _i64), ("ld_w", _i64), ("ld_gu", _i64), ("ld_dh", _i64), ("ld_dgu", _i64),
                 ("ld_dx", _i64), ("ld_dw", _i64),
                 ("timeout_ns", _i64), ("debug_flags", _i32), ("reserved", _i32 * 3)]
 
@@ -93,8 +93,9 @@ def load():
                            ("ffn_norm_backward", NormGradArgs)):
             f = getattr(lib, name)
             f.argtypes, f.restype = [ctypes.POINTER(args), _p], ctypes.c_int  # (a structure is passed by reference)
-        lib.ffn_norm_backward_workspace.argtypes = [ctypes.POINTER(NormGradArgs)]
-        lib.ffn_norm_backward_workspace.restype = _i64
+        for name, args in (("ffn_gated_backward_workspace", GatedGradArgs), ("ffn_norm_backward_workspace", NormGradArgs)):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = [ctypes.POINTER(args)], _i64
         lib.ffn_check.argtypes, lib.ffn_check.restype = [_p], ctypes.c_int
         _lib = lib
     return _lib

@@ -78,11 +78,17 @@ typedef struct {
                            2F rounded up to a multiple of 8) */
   void* dx;             /* M x K, output, or NULL */
   void* dw;             /* 2F x K, output, or NULL */
+  void* workspace;      /* 32-byte aligned, ffn_gated_backward_workspace bytes; may be NULL if those are 0 */
   int64_t ld_x, ld_w, ld_gu, ld_dh, ld_dgu, ld_dx, ld_dw;
   int64_t timeout_ns;
   int32_t debug_flags;
   int32_t reserved[3];
 } ffn_gated_grad_t;
+
+/* Bytes of workspace that ffn_gated_backward needs for these sizes and this dx (0 for
+ * dx NULL and where dx is summed in one piece), or -1 for arguments it refuses.  It
+ * depends on M, F, K and on whether dx is NULL alone. */
+GEMM_API int64_t ffn_gated_backward_workspace(const ffn_gated_grad_t* args);
 
 GEMM_API gemm_status_t ffn_gated_backward(const ffn_gated_grad_t* args, gemm_stream_t stream);
 

@@ -132,6 +132,18 @@ def test_norm_backward_refusals(lib, change, status):
     assert lib.ffn_norm_backward(ctypes.byref(norm_grad_args(**change)), None) == status
 
 
+def test_gated_backward_workspace(lib):
+    """Asked for where few tokens meet a long reduction; then it has to be there."""
+    size = lambda **kw: lib.ffn_gated_backward_workspace(ctypes.byref(grad_args(**kw)))  # noqa: E731
+    assert lib.ffn_gated_backward_workspace(None) == -1
+    assert size(K=12) == -1 and size() == 0 and size(M=0) == 0 and size(M=8192, F=14336, K=4096) == 0
+    wide = dict(M=64, F=14336, K=512)
+    n = size(**wide)
+    assert n > 0 and n % (64 * 512 * 4) == 0 and size(**wide, dx=0) == 0
+    assert lib.ffn_gated_backward(ctypes.byref(grad_args(**wide)), None) == gemm.ERR_INVALID_ARG
+    assert lib.ffn_gated_backward(ctypes.byref(grad_args(**wide, workspace=P + 16)), None) == gemm.ERR_MISALIGNED
+
+
 def test_null_arguments_and_workspace(lib):
     for f in (lib.ffn_gated, lib.ffn_gated_backward, lib.ffn_norm, lib.ffn_norm_backward):
         assert f(None, None) == gemm.ERR_INVALID_ARG

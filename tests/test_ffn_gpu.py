@@ -130,6 +130,21 @@ def test_gated_backward(M, F, K, dtype, kept):
     assert none is None and torch.equal(only_w, dw)
 
 
+@pytest.mark.parametrize("M,F,K", [(1, 2000, 64), (20, 5003, 264), (100, 7001, 520), (130, 14336, 128), (300, 1541, 520),
+                                   (777, 1097, 1032), (513, 3000, 72)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gated_backward_long_reductions(M, F, K, dtype):
+    """dx of few tokens through wide layers: slices of its reduction, joined."""
+    gen, x, w = gated_inputs(M, F, K, dtype, F)
+    dh, gu = randn(gen, M, F, dtype=dtype), randn(gen, M, 2 * F, dtype=dtype)
+    dx, dw = ffn.gated_backward(dh, x, w, gu=gu)
+    want = ref.gated_backward(f64(dh), f64(x), f64(w), f64(gu), "silu", dtype)
+    assert_within(dx, want[0], "dx")
+    assert_within(dw, want[1], "dw")
+    assert torch.equal(dx, ffn.gated_backward(dh, x, w, gu=gu, need_dw=False)[0])
+    assert torch.equal(dw, ffn.gated_backward(dh, x, w, gu=gu, need_dx=False)[1])
+
+
 def test_gated_gradient_against_differences():
     """The kernel's gradient along a direction is the 64-bit loss's central difference."""
     M, F, K, act = 70, 90, 128, "silu"
