@@ -51,10 +51,13 @@ double pair_time(int64_t tiles, int clusters, int64_t kb, int consumers, int hw)
 }
 
 // The same for one tile of a product of the backward pass (its operands' rows run along
-// the reduction), hw = 64 or 128 columns per CTA; fitted to eight shapes.
+// the reduction), hw = 64 or 128 columns per CTA; fitted to eight shapes with long
+// reductions, and to four with 1 to 10 blocks, where storing the tile takes longer than
+// making the next one.
 double product_tile_time(int64_t kb, int consumers, int hw) {
-  const double block = consumers == 2 ? (hw == 128 ? 0.63 : 0.48) : (hw == 128 ? 0.42 : 0.36);
-  return (double)kb * block + (consumers == 2 ? 3.0 : 0.7);
+  const double n = (double)kb;
+  if (consumers == 2) return hw == 128 ? std::max(0.63 * n + 3.0, 0.58 * n + 4.7) : 0.48 * n + 3.0;
+  return hw == 128 ? std::max(0.42 * n + 0.7, 0.2 * n + 2.6) : std::max(0.36 * n + 0.7, 0.1 * n + 2.0);
 }
 
 // The tile that finishes soonest: one or two consumers (256 or 512 rows), hw = 16
