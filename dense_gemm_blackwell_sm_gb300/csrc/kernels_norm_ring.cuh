@@ -67,36 +67,46 @@ struct Ring {
   }
 };
 
-// Brings row slices that start `shift` elements past a 16-byte boundary to slots, which
-// keep that offset: `pieces` bytes from the boundary on.  In an array's last row the
-// last piece may reach past the array; its elements are then copied one by one, so
-// nothing outside an array is read.
+// Brings row slices to slots, which keep their offset to a boundary (see RowPieces).
 template <typename T>
 struct RowCopies {
-  uint32_t pieces, tail;  // bytes copied per row; elements of a partial last piece
+  static constexpr int N = 16 / (int)sizeof(T);
+  RowPieces pieces;
   int shift;
-  __device__ __forceinline__ RowCopies(int shift_, int cols, bool ends_row) : shift(shift_) {
-    constexpr uint32_t N = 16 / sizeof(T);
-    const uint32_t n = (uint32_t)(shift + cols);
-    pieces = (n + N - 1) / N * 16u;
-    tail = ends_row ? n % N : 0u;
+  __device__ __forceinline__ RowCopies(int shift_, int cols, bool ends_row)
+      : pieces(RowPieces::of(shift_, cols, N, ends_row)), shift(shift_) {}
+  __device__ __forceinline__ static void by_element(const T* row, uint8_t* slot, int shift, int begin, int end) {
+    T* to = reinterpret_cast<T*>(slot);
+#pragma unroll 1
+    for (int e = begin; e < end; ++e)
+      if (e >= shift) to[e] = row[e - shift];
   }
   // One array's row: one arrival on the stage's barrier (which counts the arrays).  A
   // null row (an array that its readers fetch themselves) only arrives.
-  __device__ __forceinline__ void issue(const T* row, uint8_t* slot, uint32_t bar, bool last_row) const {
-    uint32_t n = row != nullptr ? pieces : 0u;
-    if (last_row && tail != 0 && n != 0) {
+  __device__ __forceinline__ void issue(const T* row, uint8_t* slot, uint32_t bar, bool tail) const {
+    uint32_t n = row != nullptr ? (uint32_t)pieces.bytes : 0u;
+    if (tail && pieces.rest != 0 && n != 0u) {
       n -= 16u;
-      T* to = reinterpret_cast<T*>(slot);
       const int first = (int)(n / sizeof(T));
-#pragma unroll 1
-      for (int e = first; e < first + (int)tail; ++e)
-        if (e >= shift) to[e] = row[e - shift];
+      by_element(row, slot, shift, first, first + pieces.rest);
     }
     mbar_arrive_expect_tx(bar, n);  // (after the elements copied one by one)
-    if (n != 0) bulk_load(smem_u32(slot), row - shift, n, bar);
+    if (n != 0u) bulk_load(smem_u32(slot), row - shift, n, bar);
   }
 };
+
+// The same for one of the first rows of an array that starts off a boundary.
+template <typename T>
+static __device__ __noinline__ void issue_head(const T* row, uint8_t* slot, uint32_t bar, int shift, int cols, bool tail) {
+  constexpr int N = 16 / (int)sizeof(T);
+  const RowPieces p = RowPieces::of(shift, cols, N, true);
+  const int begin = p.begin(true), end = p.end(tail);
+  RowCopies<T>::by_element(row, slot, shift, 0, min(N, shift + cols));
+  RowCopies<T>::by_element(row, slot, shift, max(N, end / (int)sizeof(T)), shift + cols);
+  const uint32_t n = begin < end ? (uint32_t)(end - begin) : 0u;
+  mbar_arrive_expect_tx(bar, n);
+  if (n != 0u) bulk_load(smem_u32(slot) + (uint32_t)begin, row - shift + N, n, bar);
+}
 
 // A group's E elements from a slot; `piece` is the thread's first 16-byte piece there.
 template <typename T, int E>
@@ -234,17 +244,24 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   int64_t ahead = r0;  // (the lanes that fill) the row to fetch next
   uint32_t in_flight = 0;
   const RowCopies<T> copies(shift, D, true);
-  auto issue = [&]() {
-    if (ahead >= r1) return;
-    copies.issue(in + ahead * in_ld, ring.slot(ring.filled, (uint32_t)tid), smem_u32(ring.full + ring.filled),
-                 ahead == a.M - 1);
+  auto next_stage = [&]() {
     if (++ring.filled == ring.stages) ring.filled = 0;
     ahead += step;
     ++in_flight;
   };
+  auto issue = [&]() {
+    if (ahead >= r1) return;
+    copies.issue(in + ahead * in_ld, ring.slot(ring.filled, (uint32_t)tid), smem_u32(ring.full + ring.filled),
+                 ahead >= sh.tail);
+    next_stage();
+  };
   if (fills) {
+    if (r0 < sh.head && shift != 0) {
+      issue_head(in + r0 * in_ld, ring.slot(0, (uint32_t)tid), smem_u32(ring.full), shift, D, r0 >= sh.tail);
+      next_stage();
+    }
 #pragma unroll 1
-    for (uint32_t s = 0; s < ring.stages; ++s) issue();
+    while (in_flight < ring.stages && ahead < r1) issue();
   }
 
   const bool post = (a.flags & FFN_NORM_POST) != 0, pre = (a.flags & FFN_NORM_PRE) != 0;
@@ -339,6 +356,7 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
 template <typename T, typename P, bool FULL, int G>
 struct RowsRing {
   const ffn_norm_grad_t& a;
+  const NormGradShape& sh;
   const Places (&at)[G];
   const RowCopies<T> copies;
   Ring ring;
@@ -355,8 +373,9 @@ struct RowsRing {
 
   __device__ __forceinline__ void issue() {
     if (ahead >= end) return;
+    // (arrays that come this way start on a boundary)
     copies.issue(in != nullptr ? in + ahead * in_ld : nullptr, ring.slot(ring.filled, (uint32_t)lane_idx()),
-                 smem_u32(ring.full + ring.filled), ahead == a.M - 1);
+                 smem_u32(ring.full + ring.filled), ahead >= sh.tail);
     if (++ring.filled == ring.stages) ring.filled = 0;
     ahead += step;
   }
@@ -495,7 +514,7 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G
   Places at[G];
 #pragma unroll
   for (int j = 0; j < G; ++j) at[j] = Places{(j * sh.threads + tid) * 8 - shift, cols};
-  RowsRing<T, P, FULL, G> rows{a, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
+  RowsRing<T, P, FULL, G> rows{a, sh, at, RowCopies<T>(shift, cols, rank == sh.cluster - 1)};
   rows.y_at = a.dn != nullptr ? 2u : 0u;
   rows.ds_at = rows.y_at + (a.y != nullptr ? 1u : 0u);
   rows.alone = sum.warps == 1 && sum.cluster == 1;

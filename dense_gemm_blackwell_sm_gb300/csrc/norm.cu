@@ -65,6 +65,9 @@ cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t 
   const bool ring_ok = alike(a.residual, a.ld_residual) && alike(a.s, a.ld_s) && alike(a.n, a.ld_n) &&
                        (layer || (!a.post_bias && !a.pre_bias)) &&
                        ring.threads <= 512 && ring.smem <= kNormRingBytes;
+  const int64_t ld = a.residual ? std::min(a.ld_y, a.ld_residual) : a.ld_y;
+  ring.head = aligned16(a.y) ? 0 : rows_at_an_end(ld, E);
+  ring.tail = a.M - rows_at_an_end(ld, E);
   const NormShape* maybe_ring = ring_ok ? &ring : nullptr;
   switch (a.dtype) {
     case FFN_F16: return norm_forward_f16(a, direct, maybe_ring, dev, st);
@@ -165,6 +168,10 @@ cudaError_t launch_norm_backward(const ffn_norm_grad_t& args, const FfnDevice& d
     const int64_t off = (sh.period > 1 ? arrays[i].ld - a.D : arrays[i].ld) * b;
     if (arrays[i].p != nullptr && (!aligned16(arrays[i].p) || off % 16 != 0)) sh.slow |= 1u << i;
   }
+  int64_t ld = a.dn ? std::min(a.ld_s, a.ld_dn) : a.ld_ds;
+  if (a.y) ld = std::min(ld, a.ld_y);
+  if (a.ds) ld = std::min(ld, a.ld_ds);
+  sh.tail = a.M - rows_at_an_end(ld, 16 / b);
   sh.full = a.dn && a.ds && a.y && a.dresidual && a.dy && (a.flags & FFN_NORM_POST) != 0;
   const int rows = (a.dn ? 2 : 0) + (a.y ? 1 : 0) + (a.ds ? 1 : 0);
   // three rows ahead where the SM holds that for all its CTAs, else two
