@@ -426,6 +426,8 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_no
     // (shifted as rows without gaps from a 16-byte boundary on: which elements a thread
     // adds up depends on the sizes alone)
     at[j].first = (j * per_row + tid) * E - (int)(((uint32_t)r * (uint32_t)D * (uint32_t)sizeof(T)) & 15u) / (int)sizeof(T);
+    // the widest rows leave no thread for the shift
+    if (THREADS == 1024 && NV * per_row * E < D + E - 1) at[j].first = (j * per_row + tid) * E;
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

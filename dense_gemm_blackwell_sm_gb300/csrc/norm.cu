@@ -27,10 +27,12 @@ int row_period(int64_t pitch_bytes) {
 
 cudaError_t launch_norm(const ffn_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int b = elem_bytes(a.dtype), E = 16 / b;
-  // a row that may start off a boundary takes one vector more
+  // a row that may start off a boundary takes one vector more, if the largest CTA holds that
+  // (else k_norm splits it from its start: D > 32761 in 16 bits, D > 32765 in 32)
   const bool aligned = a.D * b % 16 == 0 && aligned16(a.y) && a.ld_y * b % 16 == 0;
-  const int64_t vectors = (a.D + E - 1 + (aligned ? 0 : E - 1)) / E;
   const int most = norm_most_vectors(b);
+  const int64_t shifted = (a.D + E - 1 + (aligned ? 0 : E - 1)) / E;
+  const int64_t vectors = shifted <= 1024 * most ? shifted : (a.D + E - 1) / E;
   NormShape direct{};
   if (vectors <= 32 * 4 && a.M > 2 * (int64_t)dev.num_sms) {
     // short rows: a warp each, no barrier
