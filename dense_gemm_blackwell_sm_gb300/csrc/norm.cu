@@ -90,11 +90,21 @@ NormGradShape grad_shape(const ffn_norm_grad_t& a) {
     NormGradShape sh{};
     sh.each = each;
     sh.period = row_period(a.D * elem_bytes(a.dtype));
-    const int spare = sh.period > 1 ? 8 : 0;  // columns a shifted row may need more
-    for (sh.cluster = 1;; ++sh.cluster) {
-      sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + 15) / 16 * 16;
-      sh.threads = round32((sh.columns + spare + each - 1) / each);
-      if (sh.threads <= kNormGradThreads || sh.cluster == 8) break;
+    // columns and threads of a CTA, with room for `spare` columns more; whether the largest
+    // cluster holds the row so
+    auto cut = [&](int spare) {
+      for (sh.cluster = 1;; ++sh.cluster) {
+        sh.columns = ((a.D + sh.cluster - 1) / sh.cluster + 15) / 16 * 16;
+        sh.threads = round32((sh.columns + spare + each - 1) / each);
+        if (sh.threads <= kNormGradThreads) return true;
+        if (sh.cluster == 8) return false;
+      }
+    };
+    // a shifted row may need 8 columns more; where they do not fit (D > 32640) rows are split
+    // from their starts, and the threads bring those that are off a boundary
+    if (!cut(sh.period > 1 ? 8 : 0)) {
+      sh.period = 1;
+      cut(0);
     }
     sh.lanes = sh.threads == 32 ? 8 : 1;
     sh.per_sm = 2 * kNormGradThreads / (sh.threads * sh.lanes);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from dense_gemm_blackwell_sm_gb300 import ffn, gemm
-from test_ffn_gpu import DEV, assert_within, norm_inputs, ref_norm
+from test_ffn_gpu import DEV, assert_within, norm_inputs, ref_norm, ref_norm_grad
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,38 @@ def test_widest_rows_off_their_boundary(D, dtype, off, gap):
 def test_widest_rows_for_a_prompt():
     t, p = norm_inputs(400, 32767, "bf16", "bf16", "layer", 4, 5)
     check_forward(t, p, "bf16", "layer")
+
+
+def check_gradient(t, p, dtype, kind):
+    s, _ = ffn.block_norm(t["y"], t["residual"], post_norm=True, kind=kind, **p)
+    got = ffn.block_norm_backward(t["ds"], t["dn"], t["y"], s, post_norm=True, kind=kind, **p)
+    want = ref_norm_grad(t, p, s, dtype, post=True, pre=True, kind=kind, eps=1e-6)
+    for name, g, b in zip(got._fields, got, want):
+        assert (g is None) == (b is None), name
+        if g is not None:
+            assert_within(g, b, name)
+
+
+@pytest.mark.parametrize("D", WIDE)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_widest_gradients(D, dtype, kind):
+    t, p = norm_inputs(3, D, dtype, "f32", kind, 1, D)
+    check_gradient(t, p, dtype, kind)
+
+
+@pytest.mark.parametrize("D", [32641, 32767, 32768])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("off,gap", OFF)
+def test_widest_gradients_off_their_boundary(D, dtype, off, gap):
+    t, p = norm_inputs(3, D, dtype, "f32", "rms", 1, D)
+    check_gradient({k: rows_at(v, off, D + gap) for k, v in t.items()}, p, dtype, "rms")
+
+
+@pytest.mark.parametrize("D", [32641, 32767])
+def test_widest_gradients_with_gates(D):
+    """A gate for few rows (whole groups per part), and few gates over many rows."""
+    t, p = norm_inputs(6, D, "bf16", "f32", "layer", 3, D)
+    check_gradient(t, p, "bf16", "layer")
+    t, p = norm_inputs(600, D, "bf16", "bf16", "rms", 2, D)
+    check_gradient(t, p, "bf16", "rms")
