@@ -11,6 +11,19 @@
 
 namespace dgb {
 
+// These kernels launch as programmatic dependents.  Each waits for the kernel before it
+// ahead of its first access to global memory, and lets the next one be placed only after
+// that wait, those that fill the SMs for long (tiles, the slopes' pass) when their own
+// work is done: so at most two of them are on the device at once, and none stands beside
+// a long one for its whole run.  (While every kernel let the next one start at its own
+// start, a row of gradient calls queued behind other work could stop: erf GeLU, kept
+// pre-activations, 4096 x 14336 x 4096.  No kernel here waits for a later one, and what
+// stopped was not found by reading; with this order the same calls run.)
+__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -46,7 +59,7 @@ __device__ __forceinline__ void act_and_slope(float g, float& a, float& d) {
     a = g * s;
     d = fmaf(gc * s * (1.f - s), k2 * fmaf(3.f * 0.044715f * gc, gc, 1.f), s);
   } else if constexpr (ACT == EPI_ACT_GELU_ERF) {
-    const float p = 0.5f * (1.f + erff(g * 0.7071067811865476f));
+    const float p = 0.5f * erfcf(g * -0.7071067811865476f);
     a = g * p;
     d = fmaf(g * 0.3989422804014327f, exp2f(-0.7213475204444817f * g * g), p);  // density e^(-g^2/2) / sqrt(2 pi)
   } else {

@@ -106,14 +106,14 @@ __global__ void __launch_bounds__(32 * W, (FR == 1 ? 32 : 16) / W)
       }
     }
   };
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
   for (int r = 0; r < FR; ++r)
     if (row_in[r] && c < 2 && k0 + 8 * c < k1) {
       prefetch_l2_line(row[r][0] + k0 + 8 * c);
       prefetch_l2_line(row[r][1] + k0 + 8 * c);
     }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
 #pragma unroll
   for (int i = 0; i < GROUPS; ++i) load_group(i, bw[i]);
   float d[FR][NT][4] = {};

@@ -16,8 +16,8 @@ constexpr int GJ_THREADS = 256;
 // A thread takes 8 columns of a row at a time (K is a multiple of 8).
 template <typename T>
 __global__ void __launch_bounds__(GJ_THREADS) k_gated_join(const __grid_constant__ ffn_gated_grad_t a, int slices) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
   const int64_t groups = a.M * (a.K / 8), step = (int64_t)gridDim.x * GJ_THREADS;
   const float4* sums = static_cast<const float4*>(a.workspace);
   for (int64_t i = (int64_t)blockIdx.x * GJ_THREADS + threadIdx.x; i < groups; i += step) {

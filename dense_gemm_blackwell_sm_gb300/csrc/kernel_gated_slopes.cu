@@ -66,8 +66,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n) {
 
 template <typename T, int ACT>
 __global__ void __launch_bounds__(GS_THREADS) k_gated_slopes(const __grid_constant__ ffn_gated_grad_t a) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
   const int F = (int)a.F, c = ((int)blockIdx.x * GS_THREADS + (int)threadIdx.x) * 8, n = F - c;
   if (n <= 0) return;
   for (int64_t r = blockIdx.y; r < a.M; r += gridDim.y) {
@@ -87,6 +86,7 @@ __global__ void __launch_bounds__(GS_THREADS) k_gated_slopes(const __grid_consta
     store8(dgu, dg, n);
     store8(dgu + F, u, n);
   }
+  let_next_kernel_start();
 }
 
 template <typename T>

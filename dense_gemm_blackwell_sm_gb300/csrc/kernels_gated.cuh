@@ -36,7 +36,8 @@
 //
 // Every wait is bounded (ptx.cuh).  The kernels launch as programmatic dependents:
 // barriers, TMEM and the cluster are set up while the previous kernel drains, and
-// every thread waits for that kernel before it touches global memory.
+// every thread waits for that kernel before it touches global memory.  The next kernel
+// may be placed when a CTA's tiles are done (ffn_common.cuh).
 #pragma once
 
 #include <type_traits>
@@ -207,8 +208,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
   const WaitCtl w{abort_flag, p.status, p.timeout_ns, mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u)};
   const int32_t cid = (int32_t)(blockIdx.x / 2), clusters = (int32_t)(gridDim.x / 2);
 
@@ -471,6 +471,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  let_next_kernel_start();
   cluster_sync_all();
   if (warp == 2) {
     tc_fence_after();

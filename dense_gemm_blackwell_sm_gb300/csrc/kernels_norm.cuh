@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(THREADS) k_norm(const __grid_constant__ ffn_no
     // the widest rows leave no thread for the shift
     if (THREADS == 1024 && NV * per_row * E < D + E - 1) at[j].first = (j * per_row + tid) * E;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
   if (r >= a.M) return;  // (whole warps only: with a CTA per row every r is a row)
   const float n_w = LAYER ? warp_elements<NV, E>(at) : 0.f;
   Pack<T, E> y[NV], res[NV];
@@ -823,8 +823,8 @@ __global__ void __launch_bounds__(1024)
   const int c = (int)threadIdx.x % COLS, l = (int)threadIdx.x / COLS, D = (int)a.D;
   const int i = (int)blockIdx.x * COLS + c;
   const int g = (int)blockIdx.y - 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
   float v[4] = {0.f, 0.f, 0.f, 0.f};
   const bool weighted = g < 0 && !sh.many && a.groups > 1;  // sums over groups: each part with its gate
   if (i < D) {

@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   }
   if (threadIdx.x == 0) abort_flag = 0u;
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
   // this group's rows: a slice, and in it the rows of one class (see norm_walk)
   const int part = (int)blockIdx.x * groups + lane_group, slice = part / sh.period;
   const int64_t step = sh.period;
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G
   } else {
     __syncthreads();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_prior_kernel();
+  let_next_kernel_start();
   if (part >= sh.parts) return;  // (whole warps only)
   // from here on columns count from the slice's first, in every array
   norm_grad_rows<FULL, LAYER, BIAS, MANY, G, T, P>(a, sh, ws, rows, sum, part, walk, at, col0);
