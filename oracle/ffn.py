@@ -19,7 +19,7 @@ sums alone:
 from __future__ import annotations
 
 import numpy as np
-from scipy.special import erf
+from scipy.special import erfc
 
 E = 2.0 ** -24
 FORMATS = {"bf16": (7, -126), "f16": (10, -14), "f32": (23, -126)}  # stored mantissa bits, smallest normal exponent
@@ -48,7 +48,7 @@ def activation(name, g):
         k = np.sqrt(2.0 / np.pi)
         t = np.tanh(k * (g + 0.044715 * g ** 3))
         return 0.5 * g * (1.0 + t), 0.5 * (1.0 + t) + 0.5 * g * (1.0 - t * t) * k * (1.0 + 3 * 0.044715 * g ** 2)
-    p = 0.5 * (1.0 + erf(g / np.sqrt(2.0)))
+    p = 0.5 * erfc(-g / np.sqrt(2.0))
     return g * p, p + g * np.exp(-0.5 * g * g) / np.sqrt(2.0 * np.pi)
 
 
