@@ -153,6 +153,16 @@ __device__ __forceinline__ void parameters(float (&v)[E], const void* p, float a
   }
 }
 
+// Zeros at the places outside the row: a factor that meets a 0 there and is
+// infinite would make it a NaN, which a sum over the row takes in.
+template <int E>
+__device__ __forceinline__ void zero_outside(float (&v)[E], const Places& at) {
+  if (at.template whole<E>()) return;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (!at.inside(e)) v[e] = 0.f;
+}
+
 // a parameter array from element i on, or null
 template <typename P>
 __device__ __forceinline__ const P* from_column(const void* p, int64_t i) {

@@ -182,10 +182,13 @@ struct RowFactors {
       parameters<P>(branch[j], a.post_weight, 1.f, at[j]);
 #pragma unroll
       for (int e = 0; e < E; ++e) branch[j][e] *= a.branch_scale * g[e];
+      zero_outside(branch[j], at[j]);
       if constexpr (LAYER) {
         parameters<P>(branch_bias[j], a.post_bias, 0.f, at[j]);
+        if (a.post_bias != nullptr) {  // (an absent bias stays 0 whatever the gate)
 #pragma unroll
-        for (int e = 0; e < E; ++e) branch_bias[j][e] *= a.branch_scale * g[e];
+          for (int e = 0; e < E; ++e) branch_bias[j][e] *= a.branch_scale * g[e];
+        }
       }
     }
   }
@@ -392,6 +395,7 @@ struct RowsRing {
     for (int j = 0; j < G; ++j) {
       float f[8];
       parameters<P>(f, from_column<P>(a.pre_weight, col0), 1.f, at[j]);
+      zero_outside(f, at[j]);
       keep(f, j);
     }
   }
@@ -403,6 +407,7 @@ struct RowsRing {
       parameters<P>(w, from_column<P>(a.post_weight, col0), 1.f, at[j]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] *= a.branch_scale * w[e];
+      zero_outside(f, at[j]);
       keep(f, G + j);
     }
   }
