@@ -134,8 +134,7 @@ cudaError_t launch_pair(const A& a, const FfnDevice& dev, GatedParams& p, void* 
   p.split = split_of(t.consumers, t.hw, p.n0, clusters) ? 2 : 1;
   p.part_cols = t.hw <= 64 ? 128 : 256;
   p.two_slots = p.split == 1 || t.hw <= 64;
-  // few tokens: only their rows come to shared memory, which leaves it to the weights
-  p.a_rows = a.M <= 120 ? (int)((a.M + 7) / 8 * 8) : 128;
+  p.a_rows = gated_a_rows(t.consumers, a.M);
   CUtensorMap maps[4];
   if (!encode_rows16(&maps[0], bf16, a.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)a.ld_x, 64,
                      (uint32_t)p.a_rows) ||

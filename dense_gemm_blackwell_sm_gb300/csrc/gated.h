@@ -41,7 +41,7 @@ struct GatedParams {
   int32_t n0, n1;             // tiles of the two tasks (n1 = 0: one task)
   int32_t fill;               // tiles of task 1 about as long as one of task 0
   int32_t hw;                 // MMA columns per CTA: half the tile's N
-  int32_t a_rows;             // rows of the first operand a CTA brings per consumer (128, or fewer for few tokens)
+  int32_t a_rows;             // rows of the first operand a CTA brings per consumer (gated_a_rows)
   int32_t split;              // one consumer: threads that issue its MMAs (2: even and odd blocks)
   int32_t part_cols;          // TMEM columns between their accumulators
   int32_t two_slots;          // one consumer: accumulators for two tiles in turn
@@ -80,6 +80,13 @@ DGB_BOTH inline bool gated_tile(const GatedParams& p, int32_t cid, int32_t clust
   const int32_t base = p.fill * idle < p.n1 ? p.fill * idle : p.n1;
   tile = base + cid + i * clusters;
   return tile < p.n1;
+}
+
+// Rows of the first operand that a CTA brings per consumer.  With few tokens only their
+// rows come to shared memory, which leaves it to the weights; two consumers' kernels count
+// on whole operands, whatever the number of tokens.
+inline int gated_a_rows(int consumers, int64_t tokens) {
+  return consumers == 1 && tokens <= 120 ? (int)((tokens + 7) / 8 * 8) : 128;
 }
 
 const void* gated_forward_kernel(bool bf16, int consumers, int act);
