@@ -39,6 +39,11 @@ static __device__ __noinline__ bool ring_wait_slow(uint32_t full, uint32_t stage
   return false;
 }
 
+// Test hook: one arrival more than will come, on the first stage of the first group.
+__device__ __forceinline__ uint32_t missing_arrival(int32_t debug_flags, int group, uint32_t stage) {
+  return (debug_flags & FFN_DEBUG_SKIP_ONE_LOAD) != 0 && blockIdx.x == 0 && group == 0 && stage == 0 ? 1u : 0u;
+}
+
 // The ring of one group: `arrays` rows (or column slices of rows) per stage.
 struct Ring {
   uint8_t* slots;      // [stages][arrays][pitch]
@@ -226,7 +231,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) 
   RowSums sum{parts, WARP ? 1 : (int)(blockDim.x / 32), 1, 0, 0};
   if constexpr (!WARP) sum.clear();
   if (tid == 0) {
-    for (uint32_t s = 0; s < ring.stages; ++s) mbar_init(smem_u32(ring.full + s), ring.arrays);
+    for (uint32_t s = 0; s < ring.stages; ++s)
+      mbar_init(smem_u32(ring.full + s), ring.arrays + missing_arrival(a.debug_flags, lane_group, s));
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = 0u;
@@ -421,8 +427,15 @@ struct RowsRing {
         if (at[j].inside(e)) to[e] = row[at[j].first + e];
     }
   }
+  static constexpr int64_t kStopped = INT64_MAX;
+  // The row's values are there; false where the wait for them ran out.  A CTA of a cluster
+  // goes on then, on values that are void and without fetching more: its peers meet it at
+  // every sum and write to its shared memory there.
   __device__ __forceinline__ bool next(int64_t r) {
-    if (!ring.wait(fills ? ring.stages : 0u)) return false;
+    if (!ring.wait(fills && ahead != kStopped ? ring.stages : 0u)) {
+      if (clusters == 1) return false;
+      ahead = kStopped;
+    }
     if (slow & 15u) {  // (a thread's own places: no one else reads them)
       if (a.dn != nullptr && (slow & 1u)) fetch(a.s, a.ld_s, r, 0);
       if (a.dn != nullptr && (slow & 2u)) fetch(a.dn, a.ld_dn, r, 1);
@@ -561,7 +574,8 @@ __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G
   rows.ring.abort_flag = &abort_flag;
   rows.ring.status = status;
   if (tid == 0) {
-    for (int s = 0; s < sh.stages; ++s) mbar_init(smem_u32(rows.ring.full + s), rows.ring.arrays);
+    for (int s = 0; s < sh.stages; ++s)
+      mbar_init(smem_u32(rows.ring.full + s), rows.ring.arrays + missing_arrival(a.debug_flags, lane_group, (uint32_t)s));
     fence_mbar_init();
   }
   if (threadIdx.x == 0) abort_flag = 0u;

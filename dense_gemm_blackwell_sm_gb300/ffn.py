@@ -59,7 +59,7 @@ class GatedGradArgs(ctypes.Structure):
 class NormArgs(ctypes.Structure):
     _fields_ = [("M", _i64), ("D", _i64), ("groups", _i64), ("dtype", _i32), ("param_dtype", _i32),
                 ("kind", _i32), ("flags", _i32), ("eps", _f32), ("residual_scale", _f32), ("branch_scale", _f32),
-                ("reserved", _i32),
+                ("debug_flags", _i32),
                 ("y", _p), ("residual", _p), ("gate", _p), ("post_weight", _p), ("post_bias", _p),
                 ("pre_weight", _p), ("pre_bias", _p), ("s", _p), ("n", _p),
                 ("ld_y", _i64), ("ld_residual", _i64), ("ld_gate", _i64), ("ld_s", _i64), ("ld_n", _i64)]
@@ -68,7 +68,7 @@ class NormArgs(ctypes.Structure):
 class NormGradArgs(ctypes.Structure):
     _fields_ = [("M", _i64), ("D", _i64), ("groups", _i64), ("dtype", _i32), ("param_dtype", _i32),
                 ("kind", _i32), ("flags", _i32), ("eps", _f32), ("residual_scale", _f32), ("branch_scale", _f32),
-                ("reserved", _i32),
+                ("debug_flags", _i32),
                 ("ds", _p), ("dn", _p), ("y", _p), ("s", _p), ("gate", _p), ("post_weight", _p),
                 ("post_bias", _p), ("pre_weight", _p),
                 ("dresidual", _p), ("dy", _p), ("dgate", _p), ("dpost_weight", _p), ("dpost_bias", _p),

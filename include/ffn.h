@@ -32,8 +32,10 @@ extern "C" {
 
 typedef enum { FFN_F16 = 0, FFN_BF16 = 1, FFN_F32 = 2 } ffn_dtype_t;
 
-/* Test hook of the tensor-core kernels: leave out one copy into shared memory,
- * so that a bounded wait runs out and ffn_check reports it. */
+/* Test hook of the tensor-core kernels and of the norms' kernels that bring rows
+ * through shared memory (every gradient, and many rows forward): one copy is left
+ * out, or waited for in vain, so that a bounded wait runs out and ffn_check reports
+ * it.  The call's outputs are then void. */
 #define FFN_DEBUG_SKIP_ONE_LOAD 1
 
 /* h = act(x Wg^T) * (x Wu^T): M tokens, K input features, F hidden features.
@@ -116,7 +118,7 @@ typedef struct {
   int32_t kind;           /* ffn_norm_kind_t, of both norms */
   int32_t flags;          /* FFN_NORM_* */
   float eps, residual_scale, branch_scale;
-  int32_t reserved;
+  int32_t debug_flags;    /* FFN_DEBUG_* (their waits are bound by 2 s) */
   const void* y;          /* M x D */
   const void* residual;   /* M x D, or NULL */
   const void* gate;       /* groups x D, or NULL */
@@ -144,7 +146,7 @@ typedef struct {
   int64_t M, D, groups;
   int32_t dtype, param_dtype, kind, flags;
   float eps, residual_scale, branch_scale;
-  int32_t reserved;
+  int32_t debug_flags;
   const void* ds;         /* M x D, or NULL (zero) */
   const void* dn;         /* M x D; given exactly when FFN_NORM_PRE is set */
   const void* y;          /* M x D (may be NULL without FFN_NORM_POST and dgate) */
