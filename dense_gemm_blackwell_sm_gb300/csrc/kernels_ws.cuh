@@ -332,9 +332,11 @@ __device__ __forceinline__ void ws_body(const CUtensorMap* tmA, const CUtensorMa
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // everything above touched only this CTA's (or cluster's) shared memory and TMEM;
-  // from here on global memory is read and written
-  grid_launch_dependents();
+  // from here on global memory is read and written.  The next kernel may be placed only
+  // now, so that a chain has two kernels on the device at most (ffn_common.cuh); at nine
+  // sizes from 1024 x 1024 x 4096 to 8192^3 the order makes no difference in time.
   grid_wait_prior();
+  grid_launch_dependents();
   const uint32_t peer_abort = (CG == 2) ? mapa_shared(smem_u32((const void*)abort_flag), crank ^ 1u) : 0u;
   const WaitCtl w{abort_flag, p.status, p.timeout_ns, peer_abort};
   // K elements per stage: one 128-byte swizzle row of A / B (64 x 16-bit or 128 x 8-bit)

@@ -82,3 +82,28 @@ def test_blocks_in_a_row(M):
     ended()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("M,K,F", [(4096, 4096, 14336), (512, 1024, 4096), (40, 4096, 4096)])
+def test_blocks_with_matmul_in_a_row(M, K, F):
+    """A stack's forward pass: norm, projections, the library's GEMM, norm, and so on."""
+    x, w, _, _ = inputs(M, F, K, 5)
+    down = inputs(M, K, F, 6)[1][:K]
+    weight = torch.ones(K, device=DEV)
+
+    def stack():
+        s, n = ffn.block_norm(x, pre_weight=weight)
+        for _ in range(4):
+            y = gemm.matmul(ffn.gated(n, w, act="gelu_erf"), down, out_dtype=torch.bfloat16)
+            s, n = ffn.block_norm(y, s, post_norm=True, gate=weight, pre_weight=weight)
+        return s, n
+
+    ended()
+    want = stack()
+    ended()
+    inputs(M, F, K, 7)
+    got = [stack() for _ in range(3)]
+    ended()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    assert gemm.gemm_check() == gemm.OK
