@@ -1,6 +1,9 @@
 // kernel_gated_slopes.cu -- the gradient of the gated projections' pre-activations
 // from kept ones: dgu = [dh * u * act'(g), dh * act(g)].
 //
+// dgu is rounded once to the inputs' type: it is the Tensor Core's operand next (see
+// kernels_gated.cuh for what that costs in exactness).
+//
 // A pass over memory: 3 values read and 2 written per hidden feature and token.  A
 // CTA takes a run of a row's columns, a thread 8 of them, with 16-byte accesses where
 // they start on a boundary, else by element (a warp's elements are neighbours' then

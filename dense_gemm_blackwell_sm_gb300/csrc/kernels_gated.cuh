@@ -24,12 +24,20 @@
 // one.
 //
 // Bound by the tensor pipe once there are tiles for every SM pair: 8192 x 14336 x 4096
-// bf16 takes 977 us (1970 TFLOP/s; 1102 when the pre-activations are written too), the
+// bf16 takes 960 to 980 us (1960 to 2000 TFLOP/s; 1050 to 1150 when the pre-activations
+// are written too; replayed in a graph: under the power cap of longer runs 1120), the
 // pipe is active 89% of 2048 x 14336 x 4096.  Two consumers share a weight stage, so
 // that a 512-row tile reads 3/4 of the bytes of two 256-row ones; the price is that
-// nothing hides the end of a tile (3.7 us).  The backward products take 1074 us with
-// the pass that makes their operand at 4096 x 14336 x 4096 (1792 TFLOP/s): their
+// nothing hides the end of a tile (3.7 us).  The backward products take 1065 to 1095 us
+// with the pass that makes their operand at 4096 x 14336 x 4096 (1760 to 1810 TFLOP/s): their
 // operands' rows run along the reduction, so a stage is more and smaller copies.
+//
+// The gradient of the pre-activations is rounded to the inputs' 16 bits, since it is an
+// operand of the two products (one type for both operands): dx and dw are sqrt 2 as far
+// from the exact values as one rounding.  Two 16-bit parts would double the products' time.
+//
+// Where F is no multiple of 8 the epilogue's rows go through shared memory and 2-byte
+// stores: 8192 x 14335 x 4096 takes 1056 us, 1218 with the pre-activations.
 //
 // Every cluster walks its own list of tiles (no scheduler, no atomics): which
 // tiles a cluster takes depends on the sizes alone, so results do too.

@@ -206,8 +206,8 @@ struct RowFactors {
   }
 };
 
-// Bound by memory: 8192 x 4096 bf16, RMS twice, 44.8 us (6.0 TB/s of the four arrays'
-// bytes); as a layer norm 72, where the sums around the warps' means and their joining
+// Bound by memory: 8192 x 4096 bf16, RMS twice, 45 us (6.0 TB/s of the four arrays'
+// bytes); as a layer norm 73, where the sums around the warps' means and their joining
 // take as long as the copies.  (An RMS norm with biases takes the direct form.)
 template <typename T, typename P, bool LAYER, bool WARP, int NV>
 __global__ void __launch_bounds__(WARP ? 256 : 512, WARP && !(LAYER && NV == 4) ? 2 : 1)
@@ -508,7 +508,7 @@ struct RowsRing {
 // 8192 x 4096 bf16, RMS twice: 78 us with the columns' sums, 5.1 TB/s of the six arrays'
 // bytes.  128 registers hold a thread's parameter sums and one row's values, so 16 warps
 // share an SM, and what a row's two rounds of sums leave idle is what is missing: about
-// half the issue slots are used.  As a layer norm 141 us: one more pass over the row.
+// half the issue slots are used.  As a layer norm 136 us: one more pass over the row.
 template <typename T, typename P, bool FULL, bool LAYER, bool BIAS, bool MANY, int G>
 __global__ void __launch_bounds__(kNormGradThreads, MANY || (sizeof(T) == 4 && G == 2) ? 1 : 2)
     k_norm_grad(const __grid_constant__ ffn_norm_grad_t a, const __grid_constant__ NormGradShape sh,

@@ -101,7 +101,8 @@ NormGradShape grad_shape(const ffn_norm_grad_t& a) {
       }
     };
     // a shifted row may need 8 columns more; where they do not fit (D > 32640) rows are split
-    // from their starts, and the threads bring those that are off a boundary
+    // from their starts, and the threads bring those that are off a boundary (2000 x 32640
+    // bf16 415 us, 2000 x 32641 1350)
     if (!cut(sh.period > 1 ? 8 : 0)) {
       sh.period = 1;
       cut(0);
@@ -127,10 +128,10 @@ NormGradShape grad_shape(const ffn_norm_grad_t& a) {
   };
   // 8 columns per thread where one CTA of that many threads takes the row with room to
   // spare, else 16: a row's chain of sums and barriers is shorter then and more rows are
-  // under way, until a row needs a cluster (us with 8 and with 16 columns, bf16:
-  // 8192 x 1024 32.5 and 40.1, LayerNorm 45.7 and 79.9; 8192 x 64 18.9 and 28.8;
-  // 8192 x 2048 58.4 and 51.6; 8192 x 4096 in CTAs of 512 threads 123, in clusters of two
-  // 175, with 16 columns 85)
+  // under way, until a row needs a cluster (us with 8 and with 16 columns when the rule was
+  // made, bf16: 8192 x 1024 32.5 and 40.1 (29.9 today), LayerNorm 45.7 and 79.9 (43.3 today);
+  // 8192 x 64 18.9 and 28.8; 8192 x 2048 58.4 and 51.6; 8192 x 4096 in CTAs of 512 threads
+  // 123, in clusters of two 175, with 16 columns 85 (78 today))
   NormGradShape sh = split(16);
   if (!sh.many && a.D < 8 * kNormGradThreads) {
     const NormGradShape fine = split(8);
