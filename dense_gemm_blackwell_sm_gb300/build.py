@@ -1,11 +1,11 @@
 """Build the CUDA library libdgbgemm.so in-tree (sm_103a only), and the Python
-extension that calls include/ffn.h of it.
+extensions that call include/ffn.h and include/quant.h of it.
 
 Each translation unit under csrc/ is compiled by nvcc in parallel, then the
 objects are linked into one shared library next to this file.  The CUDA
 runtime is linked statically and the driver's tensor-map encoder is looked up
-at run time, so loading the library needs no GPU.  The extension (one C++ file
-against the installed torch's headers) lies next to it and loads it from there.
+at run time, so loading the library needs no GPU.  The extensions (a C++ file each
+against the installed torch's headers) lie next to it and load it from there.
 """
 from __future__ import annotations
 
@@ -22,7 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdgbgemm.so")
-CALLS = os.path.join(HERE, "_ffn_calls.so")
+CALLS = {"ffn_python.cpp": os.path.join(HERE, "_ffn_calls.so"),
+         "quant_python.cpp": os.path.join(HERE, "_quant_calls.so")}
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -42,7 +43,7 @@ def _sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hs += [os.path.join(INCLUDE, f) for f in ("gemm.h", "ffn.h")]
+    hs += [os.path.join(INCLUDE, f) for f in ("gemm.h", "ffn.h", "quant.h")]
     return hs
 
 
@@ -71,8 +72,8 @@ def _torch_root() -> str:
     return spec.submodule_search_locations[0]
 
 
-def _compile_calls() -> str:
-    src, obj = os.path.join(CSRC, "ffn_python.cpp"), os.path.join(BUILD, "ffn_python.o")
+def _compile_calls(name: str) -> str:
+    src, obj = os.path.join(CSRC, name), os.path.join(BUILD, name[:-4] + ".o")
     torch = _torch_root()
     if _stale(obj, [src, os.path.join(torch, "version.py")] + _headers()):
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -87,26 +88,26 @@ def _compile_calls() -> str:
     return obj
 
 
-def _link_calls(obj: str) -> None:
-    tmp, lib = CALLS + ".tmp.%d" % os.getpid(), os.path.join(_torch_root(), "lib")
+def _link_calls(name: str, obj: str) -> None:
+    tmp, lib = CALLS[name] + ".tmp.%d" % os.getpid(), os.path.join(_torch_root(), "lib")
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L", lib,
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
-    os.replace(tmp, CALLS)
+    os.replace(tmp, CALLS[name])
 
 
 def build(force: bool = False, jobs: int | None = None, extra_flags=()) -> str:
-    """Compile and link libdgbgemm.so and _ffn_calls.so; returns the former's path."""
+    """Compile and link libdgbgemm.so and the extensions; returns the former's path."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     if force:
         for f in os.listdir(BUILD):
             os.remove(os.path.join(BUILD, f))
-    jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
+    jobs = jobs or min(len(srcs) + len(CALLS), os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        calls = ex.submit(_compile_calls)
+        calls = {name: ex.submit(_compile_calls, name) for name in CALLS}
         objs = list(ex.map(lambda s: _compile(s, extra_flags), srcs))
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp.%d" % os.getpid()
@@ -115,8 +116,9 @@ def build(force: bool = False, jobs: int | None = None, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
-    if force or _stale(CALLS, [calls.result()]):
-        _link_calls(calls.result())
+    for name, obj in calls.items():
+        if force or _stale(CALLS[name], [obj.result()]):
+            _link_calls(name, obj.result())
     return LIB
 
 

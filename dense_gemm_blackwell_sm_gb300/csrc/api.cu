@@ -1027,6 +1027,24 @@ bool dgb::encode_rows16(CUtensorMap* m, bool bf16, const void* ptr, uint64_t inn
                    box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_128B, pitch);
 }
 
+bool dgb::encode_byte_rows(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
+                           uint32_t box_rows) {
+  return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, row_bytes, rows, 128, box_rows,
+                   CU_TENSOR_MAP_SWIZZLE_128B, pitch);
+}
+
+bool dgb::encode_scale_blocks(CUtensorMap* m, const void* ptr, uint64_t k_blocks, uint64_t row_blocks, uint32_t box_k,
+                              uint32_t box_rows) {
+  if (!encode_fn_ready()) return false;
+  cuuint64_t dims[3] = {128, 4 * k_blocks, row_blocks};
+  cuuint64_t strides[2] = {128, 512 * k_blocks};
+  cuuint32_t box[3] = {128, 4 * box_k, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 extern "C" {
 
 gemm_status_t gemm_auto_variant(int64_t M, int64_t N, int64_t K, gemm_dtype_t dtype, int32_t num_sms,

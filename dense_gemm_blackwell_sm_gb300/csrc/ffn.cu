@@ -18,44 +18,10 @@ constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxNormD = 32768;
 constexpr int kMaxDevices = 64;
 
-// the status word of the bounded waits, one per device that loads the library
+// the status words of the bounded waits (device_of_call's), per device that loads the library
 __device__ uint32_t g_ffn_status[4];
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// The current device, checked once per device to be one this library has code for.
-gemm_status_t current_ffn_device(FfnDevice* out) {
-  static std::mutex mu;
-  static FfnDevice known[kMaxDevices] = {};
-  int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-    cudaGetLastError();
-    return GEMM_ERR_NO_DEVICE;
-  }
-  try {
-    std::lock_guard<std::mutex> lock(mu);
-    FfnDevice& d = known[dev];
-    if (d.status == nullptr) {
-      void* p = nullptr;
-      if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-          cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-          cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_NO_DEVICE;
-      }
-      if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
-      if (cudaGetSymbolAddress(&p, g_ffn_status) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_CUDA;
-      }
-      d.status = static_cast<uint32_t*>(p);
-    }
-    *out = d;
-    return GEMM_OK;
-  } catch (...) {
-    return GEMM_ERR_OOM;
-  }
-}
 
 gemm_status_t launched(cudaError_t e) {
   if (e == cudaSuccess) return GEMM_OK;
@@ -96,7 +62,59 @@ gemm_status_t norm_grad_sizes(const ffn_norm_grad_t& a) {
                     a.gate != nullptr || a.dgate != nullptr);
 }
 
+// the feed-forward operators' device
+gemm_status_t current_ffn_device(FfnDevice* out) { return device_of_call(0, out); }
+
 }  // namespace
+
+// The current device, checked once per device to be one this library has code for.
+gemm_status_t dgb::device_of_call(int word, FfnDevice* out) {
+  static std::mutex mu;
+  static FfnDevice known[kMaxDevices] = {};
+  int dev = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+    cudaGetLastError();
+    return GEMM_ERR_NO_DEVICE;
+  }
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    FfnDevice& d = known[dev];
+    if (d.status == nullptr) {
+      void* p = nullptr;
+      if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+          cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+      }
+      if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
+      if (cudaGetSymbolAddress(&p, g_ffn_status) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+      }
+      d.status = static_cast<uint32_t*>(p);
+    }
+    *out = d;
+    out->status += word;
+    return GEMM_OK;
+  } catch (...) {
+    return GEMM_ERR_OOM;
+  }
+}
+
+gemm_status_t dgb::check_word(int word, cudaStream_t st) {
+  FfnDevice dev;
+  const gemm_status_t ds = device_of_call(word, &dev);
+  if (ds != GEMM_OK) return ds;
+  uint32_t found = 0;
+  if (cudaStreamSynchronize(st) != cudaSuccess ||
+      cudaMemcpy(&found, dev.status, sizeof(found), cudaMemcpyDeviceToHost) != cudaSuccess ||
+      (found != 0 && cudaMemset(dev.status, 0, sizeof(found)) != cudaSuccess)) {
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+  }
+  return found != 0 ? GEMM_ERR_DEVICE_TIMEOUT : GEMM_OK;
+}
 
 // A kernel's shared-memory limit is raised once per device.
 cudaError_t dgb::allow_smem_once(const void* func, size_t bytes) {
@@ -261,18 +279,6 @@ gemm_status_t ffn_norm_backward(const ffn_norm_grad_t* args, gemm_stream_t strea
   return launched(launch_norm_backward(a, dev, s));
 }
 
-gemm_status_t ffn_check(gemm_stream_t stream) {
-  FfnDevice dev;
-  const gemm_status_t ds = current_ffn_device(&dev);
-  if (ds != GEMM_OK) return ds;
-  uint32_t word = 0;
-  if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess ||
-      cudaMemcpy(&word, dev.status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      (word != 0 && cudaMemset(dev.status, 0, sizeof(word)) != cudaSuccess)) {
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
-  }
-  return word != 0 ? GEMM_ERR_DEVICE_TIMEOUT : GEMM_OK;
-}
+gemm_status_t ffn_check(gemm_stream_t stream) { return check_word(0, reinterpret_cast<cudaStream_t>(stream)); }
 
 }  // extern "C"

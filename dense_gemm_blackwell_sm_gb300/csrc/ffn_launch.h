@@ -15,6 +15,12 @@ struct FfnDevice {
   uint32_t* status;  // device status word of the bounded waits
 };
 
+// The current device, checked once to be one this library has code for; `word` 0: the
+// feed-forward operators' status word, 1: that of quant.h's.
+gemm_status_t device_of_call(int word, FfnDevice* out);
+// synchronises the stream, then reports and clears that word
+gemm_status_t check_word(int word, cudaStream_t st);
+
 // raise a kernel's dynamic shared-memory limit, once per device
 cudaError_t allow_smem_once(const void* func, size_t bytes);
 

@@ -4,7 +4,7 @@
 // The descriptor tells tcgen05.mma the accumulator format, the A / B element
 // formats, whether A or B is stored MN-major, and the MMA shape (N / 8 and
 // M / 16).  Bit positions follow the PTX ISA's table of the instruction
-// descriptor for kind::f16, kind::f8f6f4 and kind::mxf8f6f4.
+// descriptor for kind::f16, kind::f8f6f4, kind::mxf8f6f4, kind::mxf4 and kind::mxf4nvf4.
 #pragma once
 
 #include <cstdint>
@@ -43,6 +43,13 @@ inline uint32_t idesc_f8(bool e5m2, int M, int N) {
 inline uint32_t idesc_mx(bool e5m2, int M, int N) {
   const uint32_t f = e5m2 ? 1u : 0u;
   return (f << 7) | (f << 10) | IDESC_SCALE_UE8M0 | idesc_shape(M, N);
+}
+
+// kind::mxf4 and kind::mxf4nvf4: E2M1 operands (format 1), 64 K-elements per instruction, with
+// UE8M0 or UE4M3 block scales; the scale selectors of UE8M0 (B: bits 4-5, A: bits 29-30, 0 or 2)
+// are added per MMA by the kernel
+inline uint32_t idesc_fp4(bool ue8m0, int M, int N) {
+  return (1u << 7) | (1u << 10) | (ue8m0 ? IDESC_SCALE_UE8M0 : 0u) | idesc_shape(M, N);
 }
 
 // the same descriptor with another N

@@ -1,0 +1,10 @@
+// kernels_quant_rows_bf16.cu -- the kernels of kernels_quant_rows.cuh for bf16 inputs
+#include "kernels_quant_rows.cuh"
+
+namespace dgb {
+
+const void* quant_rows_bf16(int format, bool norm, int nv) {
+  return norm ? rows_kernel_of<__nv_bfloat16, true>(format, nv) : rows_kernel_of<__nv_bfloat16, false>(format, nv);
+}
+
+}  // namespace dgb

@@ -43,6 +43,14 @@ cudaError_t allow_dynamic_smem(const void* func, size_t bytes);
 bool encode_rows16(CUtensorMap* m, bool bf16, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
                    uint32_t box_inner, uint32_t box_outer);
 
+// TMA map of rows of bytes (`pitch` bytes apart, a multiple of 16), as encode_rows16
+bool encode_byte_rows(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
+                      uint32_t box_rows);
+// TMA map of an array of tiled block scales (include/quant.h): `k_blocks` 512-byte blocks across,
+// `row_blocks` down, boxes of box_k x box_rows of them; coordinates (0, 4 * K block, row block)
+bool encode_scale_blocks(CUtensorMap* m, const void* ptr, uint64_t k_blocks, uint64_t row_blocks, uint32_t box_k,
+                         uint32_t box_rows);
+
 // steps 1-3 (thread copies), 4-5 (TMA ring), 6 (persistent + scheduler)
 cudaError_t spec_step123(int M, int N, bool out_f32, LaunchSpec* out);
 cudaError_t spec_step45(int M, int N, int stages, bool out_f32, LaunchSpec* out);

@@ -1,0 +1,141 @@
+// quant.cu -- the C ABI of the low-precision operands (include/quant.h): argument
+// validation, launches and status checks.
+#include "quant_launch.h"
+
+#include "launch.h"
+
+using namespace dgb;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxNormD = 32768;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+gemm_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return GEMM_OK;
+  cudaGetLastError();
+  return e == cudaErrorMemoryAllocation ? GEMM_ERR_OOM : GEMM_ERR_CUDA;
+}
+
+// A row pitch: 0 means dense.  False where it is shorter than a row.
+bool pitch(int64_t* ld, int64_t row) {
+  if (*ld == 0) *ld = row;
+  return *ld >= row && *ld < kMaxDim;
+}
+
+bool is_format(int32_t f) { return f >= QUANT_E4M3 && f <= QUANT_NVFP4; }
+bool is_dtype(int32_t t) { return t >= FFN_F16 && t <= FFN_F32; }
+uintptr_t elem(int32_t dtype) { return dtype == FFN_F32 ? 4 : 2; }
+
+// The arrays of a quantised operand: each given exactly where its format has it.
+gemm_status_t operand(const void* data, const void* scales, const float* row_scale, int32_t format) {
+  const bool block = format != QUANT_E4M3, row = format == QUANT_E4M3 || format == QUANT_NVFP4;
+  if (!data || (scales != nullptr) != block || (row_scale != nullptr) != row) return GEMM_ERR_INVALID_ARG;
+  if (!aligned(data, 16) || !aligned(scales, 16) || !aligned(row_scale, 4)) return GEMM_ERR_MISALIGNED;
+  return GEMM_OK;
+}
+
+gemm_status_t rows_sizes(const quant_rows_t& a) {
+  if (!is_dtype(a.dtype) || !is_format(a.format)) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.transpose != 0 && a.transpose != 1) return GEMM_ERR_INVALID_ARG;
+  if (a.rows < 0 || a.cols < 0 || a.rows >= kMaxDim - 32 || a.cols >= kMaxDim - 32) return GEMM_ERR_INVALID_ARG;
+  // (one CTA per tile of 256 x 64, in one dimension of the grid)
+  if (a.transpose && ((a.rows + 287) / 256) * ((a.cols + 127) / 64) >= kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t quant_width(int64_t cols) { return cols < 0 || cols >= kMaxDim - 32 ? -1 : width_of(cols); }
+
+int64_t quant_row_bytes(int64_t cols, int32_t format) {
+  if (quant_width(cols) < 0 || !is_format(format)) return -1;
+  return bytes_of(width_of(cols), format);
+}
+
+int64_t quant_scale_bytes(int64_t rows, int64_t cols, int32_t format) {
+  if (quant_width(cols) < 0 || !is_format(format) || rows < 0 || rows >= kMaxDim) return -1;
+  return (rows + 127) / 128 * ((scales_of(width_of(cols), format) + 3) / 4) * 512;
+}
+
+int64_t quant_rows_workspace(const quant_rows_t* args) {
+  if (!args || rows_sizes(*args) != GEMM_OK) return -1;
+  return args->transpose && args->cols > 0 ? (int64_t)quant_columns_workspace(*args) : 0;
+}
+
+gemm_status_t quant_rows(const quant_rows_t* args, gemm_stream_t stream) {
+  if (!args) return GEMM_ERR_INVALID_ARG;
+  quant_rows_t a = *args;
+  gemm_status_t st = rows_sizes(a);
+  if (st != GEMM_OK) return st;
+  if (!pitch(&a.ld_x, a.cols) || !pitch(&a.ld_data, bytes_of(width_of(a.transpose ? a.rows : a.cols), a.format)))
+    return GEMM_ERR_INVALID_ARG;
+  if ((a.transpose ? a.cols : a.rows) == 0) return GEMM_OK;
+  if (!a.x && a.rows > 0 && a.cols > 0) return GEMM_ERR_INVALID_ARG;
+  st = operand(a.data, a.scales, a.row_scale, a.format);
+  if (st != GEMM_OK) return st;
+  if (!aligned(a.x, elem(a.dtype)) || a.ld_data % 16 != 0 || !aligned(a.workspace, 16)) return GEMM_ERR_MISALIGNED;
+  if (a.transpose && quant_columns_workspace(a) > 0 && !a.workspace) return GEMM_ERR_INVALID_ARG;
+  FfnDevice dev;
+  st = device_of_call(1, &dev);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return launched(a.transpose ? launch_quant_columns(a, dev, s) : launch_quant_rows(a, dev, s));
+}
+
+gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream) {
+  if (!args) return GEMM_ERR_INVALID_ARG;
+  quant_norm_t a = *args;
+  if (!is_dtype(a.dtype) || !is_format(a.format) || (a.param_dtype != a.dtype && a.param_dtype != FFN_F32))
+    return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.M < 0 || a.D < 1 || a.M >= kMaxDim || a.D >= kMaxDim) return GEMM_ERR_INVALID_ARG;
+  if (a.D > kMaxNormD) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (!pitch(&a.ld_y, a.D) || !pitch(&a.ld_residual, a.D) || !pitch(&a.ld_s, a.D) ||
+      !pitch(&a.ld_data, bytes_of(width_of(a.D), a.format)))
+    return GEMM_ERR_INVALID_ARG;
+  if (a.M == 0) return GEMM_OK;
+  if (!a.y) return GEMM_ERR_INVALID_ARG;
+  gemm_status_t st = operand(a.data, a.scales, a.row_scale, a.format);
+  if (st != GEMM_OK) return st;
+  const uintptr_t e = elem(a.dtype);
+  if (!aligned(a.y, e) || !aligned(a.residual, e) || !aligned(a.s, e) || !aligned(a.weight, elem(a.param_dtype)) ||
+      a.ld_data % 16 != 0)
+    return GEMM_ERR_MISALIGNED;
+  FfnDevice dev;
+  st = device_of_call(1, &dev);
+  if (st != GEMM_OK) return st;
+  return launched(launch_quant_norm(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t stream) {
+  if (!args) return GEMM_ERR_INVALID_ARG;
+  quant_product_t a = *args;
+  if (a.format != QUANT_MXFP4 && a.format != QUANT_NVFP4) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.out_dtype != FFN_BF16 && a.out_dtype != FFN_F32) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.M < 0 || a.N < 0 || a.K < 32 || a.M >= kMaxDim || a.N >= kMaxDim || a.K >= kMaxDim || a.timeout_ns < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (a.activation < GEMM_ACT_NONE || a.activation > GEMM_ACT_GELU_ERF || (a.flags & ~QUANT_STATIC_B) != 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (a.K % 32 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (!pitch(&a.ld_a, a.K / 2) || !pitch(&a.ld_b, a.K / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N))
+    return GEMM_ERR_INVALID_ARG;
+  if (a.M == 0 || a.N == 0) return GEMM_OK;
+  if (!a.a || !a.b || !a.scales_a || !a.scales_b || !a.c) return GEMM_ERR_INVALID_ARG;
+  const uintptr_t e = elem(a.out_dtype);
+  if (!aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales_a, 16) || !aligned(a.scales_b, 16) ||
+      a.ld_a % 16 != 0 || a.ld_b % 16 != 0 || !aligned(a.row_scale_a, 4) || !aligned(a.row_scale_b, 4) ||
+      !aligned(a.bias, 4) || !aligned(a.residual, e) || !aligned(a.c, e))
+    return GEMM_ERR_MISALIGNED;
+  FfnDevice dev;
+  const gemm_status_t st = device_of_call(1, &dev);
+  if (st != GEMM_OK) return st;
+  return launched(launch_fp4_product(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gemm_status_t quant_check(gemm_stream_t stream) { return check_word(1, reinterpret_cast<cudaStream_t>(stream)); }
+
+}  // extern "C"

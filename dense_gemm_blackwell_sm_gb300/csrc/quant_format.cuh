@@ -1,0 +1,154 @@
+// quant_format.cuh -- how values become codes and scales, for every kernel that writes a
+// quantised operand.  The formats are described in include/quant.h.
+#pragma once
+
+#include "ffn_common.cuh"
+#include "quant.h"
+
+namespace dgb {
+
+template <int F>
+inline constexpr bool kFourBit = F == QUANT_MXFP4 || F == QUANT_NVFP4;
+template <int F>
+inline constexpr bool kRowScaled = F == QUANT_E4M3 || F == QUANT_NVFP4;
+// elements per block scale (0: none)
+template <int F>
+inline constexpr int kBlock = F == QUANT_E4M3 ? 0 : F == QUANT_NVFP4 ? 16 : 32;
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The larger magnitude; a NaN wins.  (Magnitudes are kept as floats: a NaN or an infinity
+// among the values shows in the largest.)
+__device__ __forceinline__ float larger(float most, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(most), "f"(fabsf(v)));
+  return r;
+}
+__device__ __forceinline__ bool finite(float magnitude) { return __float_as_uint(magnitude) < kInfBits; }
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // -126 <= e <= 127
+
+// The smallest e with m <= top * 2^e, for top = (1 + over / 2^23) * 2^shift.  (A subnormal m
+// gives a larger e; every user clamps e above it.)
+__device__ __forceinline__ int covering(float m, int shift, uint32_t over) {
+  const uint32_t bits = __float_as_uint(m);
+  return (int)(bits >> 23) - 127 - shift + ((bits & 0x7fffffu) > over ? 1 : 0);
+}
+
+// ---------------------------------------------------------------- 16 elements
+
+// codes of values already in units of their scale, the first one lowest
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ uint32_t e2m1x8(const float* t) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
+  return r;
+}
+
+// What a row's scale is and what multiplies its values.
+struct RowUnit {
+  float scale;  // as written to row_scale
+  float inv;    // E4M3: 1 / scale; NVFP4: 1 / row_scale, a power of two (0 where the row has no finite scale)
+};
+template <int F>
+__device__ __forceinline__ RowUnit row_unit(float most) {
+  RowUnit u{1.f, 1.f};
+  if constexpr (F == QUANT_E4M3) {
+    u.scale = fmaxf(__fdiv_rn(most, 448.f), 1.17549435e-38f);
+    u.inv = __frcp_rn(u.scale);
+  } else if constexpr (F == QUANT_NVFP4) {
+    // 2688 = 1.3125 * 2^11
+    const int k = most == 0.f ? 0 : max(covering(most, 11, 0x280000u), -100);
+    u.scale = pow2(k);
+    u.inv = pow2(-k);
+  }
+  if (kRowScaled<F> && !finite(most)) {
+    u.scale = __uint_as_float(0x7fffffffu);
+    u.inv = 0.f;
+  }
+  return u;
+}
+
+// A block's scale: the byte kept, and what multiplies the block's values.
+struct BlockUnit {
+  uint32_t byte;
+  float inv;    // 0 where the values are to be 0
+  float scale;  // NVFP4 in 32 bits: the scale, to divide by
+};
+template <int F>
+__device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) {
+  BlockUnit b{0u, row.inv, 1.f};
+  if constexpr (F == QUANT_MXE4M3 || F == QUANT_MXFP4) {
+    // 448 = 1.75 * 2^8, 6 = 1.5 * 2^2
+    const int e = most == 0.f ? -127
+                              : max(F == QUANT_MXE4M3 ? covering(most, 8, 0x600000u) : covering(most, 2, 0x400000u), -127);
+    b.byte = (uint32_t)(e + 127);
+    b.inv = pow2(-e);
+    if (!finite(most)) b = {255u, 0.f, 1.f};
+  } else if constexpr (F == QUANT_NVFP4) {
+    const float q = __fdiv_rn(most * row.inv, 6.f);
+    uint32_t byte, half;
+    asm("{\n\t.reg .b16 r;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 r, %2, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, r;\n\t"
+        "cvt.u32.u16 %0, r;\n\t}"
+        : "=r"(byte), "=r"(half)
+        : "f"(q));
+    b.byte = byte & 0xffu;
+    b.scale = __half2float(__ushort_as_half((unsigned short)half));
+    // The reciprocal rounded up and the products rounded towards zero: a value that lies on
+    // the middle between two codes stays there (b * s * r is at least b and below b's
+    // neighbour for every scale s and midpoint b), so that ties go to even as for the exact
+    // quotient.  16-bit values that are no ties are 2^-11 from them at least.
+    b.inv = b.byte == 0u ? 0.f : __frcp_ru(b.scale) * row.inv;
+    if (row.inv == 0.f) b = {0x7fu, 0.f, 1.f};
+  }
+  return b;
+}
+
+// 16 values to codes: 16 bytes (E4M3) or 8 (E2M1) at `dst`.  EXACT: values that may lie
+// nearer to a tie than the reciprocal is exact (32-bit inputs) are divided.
+template <int F, bool EXACT>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
+  float t[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if constexpr (F == QUANT_NVFP4) {
+      t[j] = EXACT ? __fdiv_rn(v[j] * row.inv, b.scale) : __fmul_rz(v[j], b.inv);
+    } else {
+      t[j] = v[j] * b.inv;
+    }
+  }
+  const bool zero = b.inv == 0.f;  // (an infinity times 0 is no 0)
+  if constexpr (kFourBit<F>) {
+    *reinterpret_cast<uint2*>(dst) = zero ? make_uint2(0u, 0u) : make_uint2(e2m1x8(t), e2m1x8(t + 8));
+  } else {
+    *reinterpret_cast<uint4*>(dst) =
+        zero ? make_uint4(0u, 0u, 0u, 0u)
+             : make_uint4(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]),
+                          e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
+  }
+}
+
+// byte offset of the tiled scale of row r, scale column c, of an array with `cb` blocks a row
+__device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t c, int64_t cb) {
+  return ((r >> 7) * cb + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
+}
+
+}  // namespace dgb

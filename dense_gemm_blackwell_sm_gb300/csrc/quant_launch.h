@@ -1,0 +1,29 @@
+// quant_launch.h -- internal interface between the C entry points of the low-precision
+// operands (quant.cu) and their kernels.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ffn_launch.h"
+#include "quant.h"
+
+namespace dgb {
+
+// The pitches below are resolved (never 0).
+cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaStream_t st);
+size_t quant_columns_workspace(const quant_rows_t& a);
+cudaError_t launch_quant_columns(const quant_rows_t& a, const FfnDevice& dev, cudaStream_t st);
+cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaStream_t st);
+cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, cudaStream_t st);
+
+// elements, scale columns and bytes of a quantised row
+inline int64_t width_of(int64_t cols) { return cols < 32 ? 32 : (cols + 31) / 32 * 32; }
+inline int64_t scales_of(int64_t width, int32_t format) {
+  return format == QUANT_E4M3 ? 0 : format == QUANT_NVFP4 ? width / 16 : width / 32;
+}
+inline int64_t bytes_of(int64_t width, int32_t format) {
+  return format == QUANT_MXFP4 || format == QUANT_NVFP4 ? width / 2 : width;
+}
+
+}  // namespace dgb

@@ -1,0 +1,288 @@
+// quant_python.cpp -- what quant.py calls: checks of the tensors, allocation of the outputs and
+// the calls of include/quant.h, as a Python extension (see ffn_python.cpp for the reason).
+//
+// A quantised operand travels as five values: data, scales or None, row_scale or None, format
+// code, columns.
+#include "python_calls.h"
+#include "quant.h"
+
+namespace {
+
+struct Operand {
+  Tensor data, scales, row_scale;
+  int64_t rows = 0, cols = 0, ld = 0;
+  int32_t format = 0;
+  int index = 0;
+};
+
+at::ScalarType data_type(int32_t format) {
+  return format == QUANT_E4M3 || format == QUANT_MXE4M3 ? at::kFloat8_e4m3fn : at::kByte;
+}
+
+Tensor empty_flat(int64_t n, at::ScalarType dtype, int index) {
+  return at::empty({n}, at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)index));
+}
+
+// the operand of `rows` rows of `cols` values, allocated
+Operand empty_operand(int64_t rows, int64_t cols, int32_t format, int index) {
+  Operand o;
+  o.rows = rows;
+  o.cols = cols;
+  o.format = format;
+  o.index = index;
+  const int64_t bytes = quant_row_bytes(cols, format), scales = quant_scale_bytes(rows, cols, format);
+  TORCH_CHECK_VALUE(bytes >= 0 && scales >= 0, "rows of ", cols, " values are too long");
+  o.ld = bytes;
+  o.data = empty_rows(rows, bytes, data_type(format), index);
+  if (format != QUANT_E4M3) o.scales = empty_flat(scales, at::kByte, index);
+  if (format == QUANT_E4M3 || format == QUANT_NVFP4) o.row_scale = empty_flat(rows, at::kFloat, index);
+  return o;
+}
+
+// a given operand: p points at its five values
+Operand operand_of(const char* name, PyObject* const* p) {
+  Operand o;
+  o.data = tensor_of(p[0], name);
+  const Tensor *scales = optional_of(p[1], name), *row_scale = optional_of(p[2], name);
+  o.format = (int32_t)int_of(p[3]);
+  o.cols = int_of(p[4]);
+  TORCH_CHECK_VALUE(o.format == QUANT_MXFP4 || o.format == QUANT_NVFP4, name, " must be a 4-bit operand (mxfp4 or nvfp4)");
+  o.index = index_of(o.data);
+  TORCH_CHECK_VALUE(o.data.dim() == 2, name, "'s data must be a 2-D tensor, not ", o.data.sizes());
+  o.rows = o.data.size(0);
+  const int64_t bytes = quant_row_bytes(o.cols, o.format);
+  TORCH_CHECK_VALUE(bytes >= 0, name, " has ", o.cols, " columns");
+  o.ld = rows_of(name, o.data, o.rows, bytes, at::kByte, o.index);
+  const int64_t want = quant_scale_bytes(o.rows, o.cols, o.format);
+  TORCH_CHECK_VALUE(scales != nullptr && scales->scalar_type() == at::kByte && scales->is_contiguous() &&
+                        scales->numel() == want && scales->is_cuda() && scales->get_device() == o.index,
+                    name, "'s scales must be ", want, " dense bytes on cuda:", o.index);
+  o.scales = *scales;
+  if (row_scale != nullptr) {
+    TORCH_CHECK_VALUE(row_scale->scalar_type() == at::kFloat && row_scale->is_contiguous() && row_scale->dim() == 1 &&
+                          row_scale->size(0) == o.rows && row_scale->is_cuda() && row_scale->get_device() == o.index,
+                      name, "'s row scales must be ", o.rows, " dense values of float32 on cuda:", o.index);
+    o.row_scale = *row_scale;
+  }
+  return o;
+}
+
+void* pointer(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+
+PyObject* operand_tuple(const Operand& o) { return tuple_of({&o.data, &o.scales, &o.row_scale}); }
+
+int32_t format_of(PyObject* o) {
+  const int64_t f = int_of(o);
+  TORCH_CHECK_VALUE(f >= QUANT_E4M3 && f <= QUANT_NVFP4, "unknown format ", f);
+  return (int32_t)f;
+}
+
+// x's rows or columns, quantised
+Operand quantised(const char* name, const Tensor& x, int32_t format, bool transpose, PyObject* stream) {
+  TORCH_CHECK_VALUE(x.dim() == 2, name, " must be a 2-D tensor, not ", x.sizes());
+  quant_rows_t a{};
+  const int index = index_of(x);
+  const at::ScalarType dtype = x.scalar_type();
+  a.rows = x.size(0);
+  a.cols = x.size(1);
+  a.dtype = code_of(dtype);
+  TORCH_CHECK_VALUE(a.dtype >= 0, name, " must be float16, bfloat16 or float32, not ", dtype);
+  a.format = format;
+  a.transpose = transpose;
+  a.ld_x = rows_of(name, x, a.rows, a.cols, dtype, index);
+  Operand o = empty_operand(transpose ? a.cols : a.rows, transpose ? a.rows : a.cols, format, index);
+  a.x = x.data_ptr();
+  a.data = pointer(o.data);
+  a.scales = pointer(o.scales);
+  a.row_scale = static_cast<float*>(pointer(o.row_scale));
+  const Tensor workspace = workspace_of(quant_rows_workspace(&a), index);
+  a.workspace = pointer(workspace);
+  call(quant_rows, "quant_rows", a, index, stream, {&o.data, &o.scales, &o.row_scale, &workspace});
+  return o;
+}
+
+struct Finish {
+  const Tensor *bias, *residual, *out;
+  int32_t activation, flags, debug_flags;
+  at::ScalarType dtype;
+  int64_t timeout_ns;
+};
+
+Tensor multiplied(const Operand& a, const Operand& b, const Finish& f, PyObject* stream) {
+  TORCH_CHECK_VALUE(a.format == b.format && a.cols == b.cols, "operands must have one format and as many columns, not ",
+                    a.cols, " and ", b.cols);
+  TORCH_CHECK_VALUE(a.index == b.index, "operands must be on one device");
+  TORCH_CHECK_VALUE(f.dtype == at::kBFloat16 || f.dtype == at::kFloat, "the output must be bfloat16 or float32, not ",
+                    f.dtype);
+  quant_product_t p{};
+  p.M = a.rows;
+  p.N = b.rows;
+  p.K = quant_width(a.cols);
+  p.format = a.format;
+  p.out_dtype = code_of(f.dtype);
+  p.activation = f.activation;
+  p.flags = f.flags;
+  p.a = pointer(a.data);
+  p.b = pointer(b.data);
+  p.scales_a = pointer(a.scales);
+  p.scales_b = pointer(b.scales);
+  p.row_scale_a = static_cast<const float*>(pointer(a.row_scale));
+  p.row_scale_b = static_cast<const float*>(pointer(b.row_scale));
+  if (f.bias != nullptr) {
+    TORCH_CHECK_VALUE(f.bias->dim() == 1 && f.bias->size(0) == p.N && f.bias->scalar_type() == at::kFloat &&
+                          f.bias->is_contiguous() && f.bias->is_cuda() && f.bias->get_device() == a.index,
+                      "bias must be ", p.N, " dense values of float32 on cuda:", a.index);
+    p.bias = static_cast<const float*>(f.bias->data_ptr());
+  }
+  if (f.residual != nullptr) {
+    p.ld_residual = rows_of("residual", *f.residual, p.M, p.N, f.dtype, a.index);
+    p.residual = f.residual->data_ptr();
+  }
+  Tensor c;
+  if (f.out != nullptr) {
+    p.ld_c = rows_of("out", *f.out, p.M, p.N, f.dtype, a.index);
+    c = *f.out;
+  } else {
+    c = empty_rows(p.M, p.N, f.dtype, a.index);
+  }
+  p.c = c.data_ptr();
+  p.ld_a = a.ld;
+  p.ld_b = b.ld;
+  p.timeout_ns = f.timeout_ns;
+  p.debug_flags = f.debug_flags;
+  call(quant_product, "quant_product", p, a.index, stream, {&c});
+  return c;
+}
+
+// p: out dtype code, bias, act, residual, out, static_b, stream, timeout_ns, debug_flags
+Finish finish_of(PyObject* const* p) {
+  Finish f{};
+  const int64_t code = int_of(p[0]);
+  TORCH_CHECK_VALUE(code == FFN_BF16 || code == FFN_F32, "the output must be bfloat16 or float32");
+  f.dtype = code == FFN_F32 ? at::kFloat : at::kBFloat16;
+  f.bias = optional_of(p[1], "bias");
+  f.activation = (int32_t)int_of(p[2]);
+  f.residual = optional_of(p[3], "residual");
+  f.out = optional_of(p[4], "out");
+  f.flags = flag_of(p[5]) ? QUANT_STATIC_B : 0;
+  f.timeout_ns = int_of(p[7]);
+  f.debug_flags = (int32_t)int_of(p[8]);
+  return f;
+}
+
+// (x, format, transpose, stream) -> (data, scales, row_scale)
+PyObject* quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 4);
+  return operand_tuple(quantised("x", tensor_of(p[0], "x"), format_of(p[1]), flag_of(p[2]), p[3]));
+  END_HANDLE_TH_ERRORS
+}
+
+// (y, residual, weight, format, eps, residual_scale, branch_scale, need_s, s, stream)
+// -> (s or None, data, scales, row_scale)
+PyObject* norm_quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 10);
+  const Tensor &y = tensor_of(p[0], "y"), *residual = optional_of(p[1], "residual"), *weight = optional_of(p[2], "weight"),
+               *s_given = optional_of(p[8], "s");
+  TORCH_CHECK_VALUE(y.dim() == 2, "y must be a 2-D tensor, not ", y.sizes());
+  quant_norm_t a{};
+  const int index = index_of(y);
+  const at::ScalarType dtype = y.scalar_type();
+  a.M = y.size(0);
+  a.D = y.size(1);
+  a.dtype = a.param_dtype = code_of(dtype);
+  TORCH_CHECK_VALUE(a.dtype >= 0, "y must be float16, bfloat16 or float32, not ", dtype);
+  a.format = format_of(p[3]);
+  a.eps = float_of(p[4]);
+  a.residual_scale = float_of(p[5]);
+  a.branch_scale = float_of(p[6]);
+  a.ld_y = rows_of("y", y, a.M, a.D, dtype, index);
+  if (residual != nullptr) a.ld_residual = rows_of("residual", *residual, a.M, a.D, dtype, index);
+  if (weight != nullptr) {
+    TORCH_CHECK_VALUE(weight->dim() == 1 && weight->size(0) == a.D && weight->is_contiguous() && weight->is_cuda() &&
+                          weight->get_device() == index &&
+                          (weight->scalar_type() == dtype || weight->scalar_type() == at::kFloat),
+                      "weight must be ", a.D, " dense values of ", dtype, " or float32 on cuda:", index);
+    a.param_dtype = code_of(weight->scalar_type());
+  }
+  Tensor s;
+  a.ld_s = a.D;
+  if (s_given != nullptr) {
+    a.ld_s = rows_of("s", *s_given, a.M, a.D, dtype, index);
+    s = *s_given;
+  } else if (flag_of(p[7])) {
+    s = empty_rows(a.M, a.D, dtype, index);
+  }
+  Operand o = empty_operand(a.M, a.D, a.format, index);
+  a.y = y.data_ptr();
+  a.residual = data_of(residual);
+  a.weight = data_of(weight);
+  a.s = pointer(s);
+  a.data = pointer(o.data);
+  a.scales = pointer(o.scales);
+  a.row_scale = static_cast<float*>(pointer(o.row_scale));
+  call(quant_norm, "quant_norm", a, index, p[9], {&s, &o.data, &o.scales, &o.row_scale});
+  return tuple_of({&s, &o.data, &o.scales, &o.row_scale});
+  END_HANDLE_TH_ERRORS
+}
+
+// (a's five values, b's five, out dtype, bias, act, residual, out, static_b, stream, timeout_ns,
+//  debug_flags) -> c
+PyObject* product(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 19);
+  return wrapped(multiplied(operand_of("a", p), operand_of("b", p + 5), finish_of(p + 10), p[16]));
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, w's five values, and as product from out dtype on) -> y.  The operand made on the way
+// is read by a later call on the same stream, so the first call tells the allocator enough.
+PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 15);
+  const Tensor& x = tensor_of(p[0], "x");
+  const Operand w = operand_of("w", p + 1);
+  const Finish f = finish_of(p + 6);
+  TORCH_CHECK_VALUE(x.dim() == 2 && x.size(1) == w.cols, "x must be (M, ", w.cols, "), not ", x.sizes());
+  TORCH_CHECK_VALUE(index_of(x) == w.index, "x and w must be on one device");
+  return wrapped(multiplied(quantised("x", x, w.format, false, p[12]), w, f, p[12]));
+  END_HANDLE_TH_ERRORS
+}
+
+// (dy, x, w, format, need_dx, need_dw, out dtype, stream, timeout_ns) -> (dx or None, dw or None)
+PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 9);
+  const Tensor &dy = tensor_of(p[0], "dy"), *x = optional_of(p[1], "x"), *w = optional_of(p[2], "w");
+  const int32_t format = format_of(p[3]);
+  const bool need_dx = flag_of(p[4]), need_dw = flag_of(p[5]);
+  TORCH_CHECK_VALUE(format == QUANT_MXFP4 || format == QUANT_NVFP4, "the format must be a 4-bit one (mxfp4 or nvfp4)");
+  TORCH_CHECK_VALUE((!need_dx || w != nullptr) && (!need_dw || x != nullptr), "dx needs w, dw needs x");
+  TORCH_CHECK_VALUE(dy.dim() == 2 && (!need_dw || (x->dim() == 2 && x->size(0) == dy.size(0))) &&
+                        (!need_dx || (w->dim() == 2 && w->size(0) == dy.size(1))),
+                    "dy must be (M, N), x (M, K) and w (N, K)");
+  const int index = index_of(dy);
+  TORCH_CHECK_VALUE((!need_dw || index_of(*x) == index) && (!need_dx || index_of(*w) == index),
+                    "tensors must be on one device");
+  Finish f{};
+  const int64_t code = int_of(p[6]);
+  TORCH_CHECK_VALUE(code == FFN_BF16 || code == FFN_F32, "the output must be bfloat16 or float32");
+  f.dtype = code == FFN_F32 ? at::kFloat : at::kBFloat16;
+  f.activation = GEMM_ACT_NONE;
+  f.timeout_ns = int_of(p[8]);
+  Tensor dx, dw;
+  if (need_dx) dx = multiplied(quantised("dy", dy, format, false, p[7]), quantised("w", *w, format, true, p[7]), f, p[7]);
+  if (need_dw) dw = multiplied(quantised("dy", dy, format, true, p[7]), quantised("x", *x, format, true, p[7]), f, p[7]);
+  return tuple_of({&dx, &dw});
+  END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {method<bind>("bind"),       method<quantise>("quantise"), method<norm_quantise>("norm_quantise"),
+                         method<product>("product"), method<linear>("linear"),     method<linear_backward>("linear_backward"),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quant_calls", nullptr, -1, methods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__quant_calls() { return PyModule_Create(&module); }
