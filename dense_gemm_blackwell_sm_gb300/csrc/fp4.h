@@ -46,6 +46,6 @@ constexpr int kFp4PairThreads = 384;
 const void* fp4_few_kernel(bool nv, bool out_f32);
 size_t fp4_few_smem(bool nv, int tokens, int stages);
 int fp4_few_stages(bool nv, int tokens);
-constexpr int kFp4FewThreads = 128;
+constexpr int kFp4FewThreads = 256;
 
 }  // namespace dgb

@@ -44,9 +44,6 @@ __device__ __forceinline__ void fp4_act(float (&x)[N], int32_t act) {
   }
 }
 
-template <typename OutT>
-__device__ __forceinline__ OutT fp4_out(float v) { return from_f32<OutT>(v); }
-
 // 32 sums of row `row`, columns col .. col + 31 (fewer at the matrix' edge), to c.  A lane has a
 // row; where rows are not aligned the values go through `staging` (32 x 33 floats of the
 // warp's) so that lanes write neighbours.  Every lane of the warp calls it; rows past M are
@@ -129,7 +126,7 @@ __device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const uint32_t
     for (int32_t r = 0; r < rows; ++r) {
       float y = staging[r * 33 + lane];
       if (src != nullptr) y += to_f32(src[(int64_t)r * e.ld_residual]);
-      dst[(int64_t)r * e.ld_c] = fp4_out<OutT>(y);
+      dst[(int64_t)r * e.ld_c] = from_f32<OutT>(y);
     }
   }
   __syncwarp();

@@ -8,8 +8,9 @@
 // Two CTAs fit an SM, so that one's copies run while the other ends.
 //
 // Warp 0 is the TMA producer, warp 1 copies the scales into TMEM and issues the MMAs, and all
-// four warps then add, scale and store.
+// eight warps then add, scale and store.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4_common.cuh"
 
@@ -29,6 +30,98 @@ static_assert(kScaleCol + kMostStages * kSlot<true> <= kTmemColumns, "scales fit
 
 __host__ __device__ inline uint32_t stage_bytes(int blocks, int tokens) {
   return kOperand + (uint32_t)tokens * 128u + 2u * 512u * (uint32_t)blocks;
+}
+
+// Sums [begin, end) of a tile's [token][feature] from the cluster's SPLIT CTAs, in the order of
+// their ranks, to c: V neighbours a time.  What a thread reads from the CTAs is under way
+// together (8 groups of 4 or 8 single values): one after the other, eight reads of distributed
+// shared memory took 2 us.
+template <int V, int SPLIT, typename OutT>
+__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* partial, int32_t begin, int32_t end,
+                                           int32_t row0, int32_t col0) {
+  constexpr int U = 8 / SPLIT;
+  constexpr int kStep = kFp4FewThreads * V;
+  const Fp4Epilogue& e = p.e;
+  uint32_t from[SPLIT];
+#pragma unroll
+  for (int r = 0; r < SPLIT; ++r) from[r] = SPLIT == 1 ? smem_u32(partial) : mapa_shared(smem_u32(partial), (uint32_t)r);
+#pragma unroll 1
+  for (int32_t i0 = begin + (int32_t)threadIdx.x * V; i0 < end; i0 += kStep * U) {
+    float y[U][SPLIT][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t i = min(i0 + u * kStep, end - V);  // (a multiple of V)
+#pragma unroll
+      for (int r = 0; r < SPLIT; ++r) {
+        if constexpr (SPLIT == 1) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) y[u][r][j] = partial[i + j];
+        } else if constexpr (V == 4) {
+          const float4 f = ld_cluster_f32x4(from[r] + 4u * (uint32_t)i);
+          y[u][r][0] = f.x;
+          y[u][r][1] = f.y;
+          y[u][r][2] = f.z;
+          y[u][r][3] = f.w;
+        } else {
+          y[u][r][0] = __uint_as_float(ld_cluster_u32(from[r] + 4u * (uint32_t)i));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int32_t i = i0 + u * kStep;
+      const int32_t row = row0 + i / 128, col = col0 + i % 128;
+      if (i >= end || col >= e.N) continue;
+      // (a group that the matrix' edge cuts goes by single values)
+      const bool whole = col + V <= e.N;
+      const float sa = e.row_scale_a != nullptr ? __ldg(e.row_scale_a + row) : 1.f;
+      float x[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        x[j] = y[u][0][j];
+#pragma unroll
+        for (int r = 1; r < SPLIT; ++r) x[j] += y[u][r][j];
+        x[j] *= sa;
+        const int32_t c = min(col + j, e.N - 1);
+        if (e.row_scale_b != nullptr) x[j] *= __ldg(e.row_scale_b + c);
+        if (e.bias != nullptr) x[j] += __ldg(e.bias + c);
+      }
+      fp4_act(x, e.act);
+      const OutT* res = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
+      OutT* dst = reinterpret_cast<OutT*>(e.c) + (int64_t)row * e.ld_c + col;
+      if (V == 4 && whole) {
+        using Word = typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type;
+        Word word;
+        OutT* t = reinterpret_cast<OutT*>(&word);
+        if (e.residual != nullptr) {
+          word = *reinterpret_cast<const Word*>(res);
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[j] += to_f32(t[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) t[j] = from_f32<OutT>(x[j]);
+        *reinterpret_cast<Word*>(dst) = word;
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if (col + j >= e.N) break;
+          if (e.residual != nullptr) x[j] += to_f32(res[j]);
+          dst[j] = from_f32<OutT>(x[j]);
+        }
+      }
+    }
+  }
+}
+
+template <int V, typename OutT>
+__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* partial, int32_t begin, int32_t end,
+                                           int32_t row0, int32_t col0) {
+  switch (p.split) {
+    case 1: return few_finish<V, 1, OutT>(p, partial, begin, end, row0, col0);
+    case 2: return few_finish<V, 2, OutT>(p, partial, begin, end, row0, col0);
+    case 4: return few_finish<V, 4, OutT>(p, partial, begin, end, row0, col0);
+    default: return few_finish<V, 8, OutT>(p, partial, begin, end, row0, col0);
+  }
 }
 
 template <bool NV, typename OutT>
@@ -145,14 +238,15 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   const int32_t tokens = min((int32_t)T, p.e.M - tm * 128);
   if (ok) {
     tc_fence_after();
-    const uint32_t feature = warp * 32u + lane;
+    // (warps 4-7 take every other 16 tokens)
+    const uint32_t feature = (warp & 3u) * 32u + lane;
 #pragma unroll 1
-    for (int32_t t0 = 0; t0 < tokens; t0 += 16) {
+    for (int32_t t0 = 16 * (int32_t)(warp >> 2); t0 < tokens; t0 += 32) {
       uint32_t v[16];
-      tmem_ld_32x32b_x16(tmem + ((warp * 32u) << 16) + (uint32_t)t0, v);
+      tmem_ld_32x32b_x16(tmem + (((warp & 3u) * 32u) << 16) + (uint32_t)t0, v);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) partial[(t0 + j) * 128 + feature] = nkb > 0 ? __uint_as_float(v[j]) : 0.f;
+      for (int j = 0; j < 16; ++j) partial[(t0 + j) * 128 + feature] = __uint_as_float(v[j]);
     }
   }
   if (p.split > 1) {
@@ -161,28 +255,15 @@ __global__ void __launch_bounds__(kFp4FewThreads)
     __syncthreads();
   }
   if (ok) {
+    // (features of a tile that the matrix has; groups of four, or single ones where rows are not
+    // aligned to groups)
     const int32_t total = tokens * 128;
-    const int32_t share = ((total + p.split - 1) / p.split + 31) / 32 * 32;
-    const int32_t end = min(total, (rank + 1) * share);
-    const uint32_t base = smem_u32(partial);
-    for (int32_t i = rank * share + (int32_t)threadIdx.x; i < end; i += kFp4FewThreads) {
-      float sum = 0.f;
-      if (p.split > 1) {
-        for (int32_t r = 0; r < p.split; ++r)
-          sum += __uint_as_float(ld_cluster_u32(mapa_shared(base + 4u * (uint32_t)i, (uint32_t)r)));
-      } else {
-        sum = partial[i];
-      }
-      const int32_t row = tm * 128 + i / 128, col = tn * 128 + i % 128;
-      if (col >= p.e.N) continue;
-      if (p.e.row_scale_a != nullptr) sum *= __ldg(p.e.row_scale_a + row);
-      if (p.e.row_scale_b != nullptr) sum *= __ldg(p.e.row_scale_b + col);
-      if (p.e.bias != nullptr) sum += __ldg(p.e.bias + col);
-      float x[1] = {sum};
-      fp4_act(x, p.e.act);
-      if (p.e.residual != nullptr)
-        x[0] += to_f32(reinterpret_cast<const OutT*>(p.e.residual)[(int64_t)row * p.e.ld_residual + col]);
-      reinterpret_cast<OutT*>(p.e.c)[(int64_t)row * p.e.ld_c + col] = fp4_out<OutT>(x[0]);
+    const int32_t share = ((total + p.split - 1) / p.split + 127) / 128 * 128;
+    const int32_t begin = rank * share, end = min(total, begin + share);
+    if (p.e.vec != 0) {
+      few_finish<4, OutT>(p, partial, begin, end, tm * 128, tn * 128);
+    } else {
+      few_finish<1, OutT>(p, partial, begin, end, tm * 128, tn * 128);
     }
   }
   if (!ok && threadIdx.x == 0) {

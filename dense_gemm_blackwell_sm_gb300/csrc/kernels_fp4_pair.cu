@@ -70,12 +70,12 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     for (uint32_t s = 0; s < S; ++s) {
       mbar_init(smem_u32(full + s), 1);
       mbar_init(smem_u32(empty + s), 1);
-      mbar_init(smem_u32(ready + s), 1);
+      mbar_init(smem_u32(ready + s), 2);
     }
     mbar_init(smem_u32(acc_full), 1);
     mbar_init(smem_u32(acc_empty), 16);
     mbar_init(smem_u32(drain_bar), 1);
-    mbar_init(smem_u32(copy_drain), 1);
+    mbar_init(smem_u32(copy_drain), 2);
     *abort_flag = 0u;
     *zero_word = 0u;
     fence_mbar_init();
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
       const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
       mbar_wait(smem_u32(drain_bar), 0, wd, WAIT_DRAIN);
     }
-  } else if (warp == 3 && leader) {
+  } else if ((warp == 2 || warp == 3) && leader) {
     // ---------------------------------------------------------- scale copies
     if (lane == 0) {
       uint32_t stage = 0, sphase = 0;
@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
           tc_fence_after();
           const uint32_t from = smem_u32(ring + stage * kStage<NV> + kScalesAt);
           const uint32_t to = tmem + kScaleCol + stage * kSlot<NV>;
+          // each of the two threads takes half of the blocks
 #pragma unroll
-          for (uint32_t j = 0; j < NB; ++j) {
+          for (uint32_t i = 0; i < NB / 2; ++i) {
+            const uint32_t j = i + (warp - 2u) * (NB / 2);
             tmem_cp_32x128b_x4<2>(to + 4u * j, sdesc_rows16(from + 512u * j));
             tmem_cp_32x128b_x4<2>(to + 4u * NB + 8u * j, sdesc_rows16(from + 512u * (NB + j)));
             tmem_cp_32x128b_x4<2>(to + 4u * NB + 8u * j + 4u, sdesc_rows16(from + 512u * (2u * NB + j)));

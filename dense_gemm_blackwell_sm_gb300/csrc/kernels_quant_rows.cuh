@@ -6,7 +6,9 @@
 //   norm:  s = rs * residual + bs * y,  r = 1 / sqrt(sum s^2 / D + eps),  v = s r weight
 //   E4M3, NVFP4: the row's largest magnitude, from all its threads
 //   block scales: the block's largest magnitude, from one thread (16) or two (32)
-// and then the codes.  Rows longer than a group holds (no norm) are read twice.
+// and then the codes.  The grid is what the device holds at once: a group walks its rows and
+// loads the next one before it works on the one it has.  Rows longer than a group holds (no
+// norm) are read twice.
 //
 // Bound by memory: 2 bytes read and 0.56 to 1.03 written per element (norm: 4 and 3.03).
 #pragma once
@@ -22,7 +24,7 @@ struct QuantRowsParams {
   int32_t chunks;      // runs of 16 elements of a padded row
   int32_t all_chunks;  // and of the scale array's columns
   int32_t blocks;      // 512-byte scale blocks across a row
-  int32_t vec;         // rows start on 16-byte boundaries
+  int32_t vec;         // rows start on boundaries of: 2 = 32 bytes, 1 = 16, 0 = neither
   const void* x;       // norm: y
   const void* residual;
   const void* weight;
@@ -38,53 +40,84 @@ struct QuantRowsParams {
 
 namespace {
 
-// 16 columns from `col` on, zeros from column `cols` on (plain loads: s may be y or the residual)
+// 16 columns as they are in memory
 template <typename T>
-__device__ __forceinline__ void load16(float (&v)[16], const T* row, int32_t col, int32_t cols, bool vec) {
-  if (vec && col + 16 <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4* p = reinterpret_cast<const uint4*>(row + col);
-      const uint4 a = p[0], b = p[1];
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[2 * j] = to_f32(reinterpret_cast<const T*>(&w[j])[0]);
-        v[2 * j + 1] = to_f32(reinterpret_cast<const T*>(&w[j])[1]);
-      }
+struct Run {
+  uint32_t w[4 * sizeof(T)];
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(w[j]);
     } else {
-      const float4* p = reinterpret_cast<const float4*>(row + col);
+      return to_f32(reinterpret_cast<const T*>(w)[j]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 f = p[j];
-        v[4 * j] = f.x;
-        v[4 * j + 1] = f.y;
-        v[4 * j + 2] = f.z;
-        v[4 * j + 3] = f.w;
+    for (int j = 0; j < (int)(4 * sizeof(T)); ++j) w[j] = 0u;
+  }
+};
+
+// The columns from `col` on, zeros from column `cols` on (plain loads: s may be y or the residual).
+template <typename T>
+__device__ __forceinline__ void load16(Run<T>& v, const T* row, int32_t col, int32_t cols, int32_t vec) {
+  constexpr int words = 4 * (int)sizeof(T);
+  if (vec != 0 && col + 16 <= cols) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row + col);
+    if (vec == 2) {
+#pragma unroll
+      for (int j = 0; j < words; j += 8)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v.w[j]), "=r"(v.w[j + 1]), "=r"(v.w[j + 2]), "=r"(v.w[j + 3]), "=r"(v.w[j + 4]),
+                       "=r"(v.w[j + 5]), "=r"(v.w[j + 6]), "=r"(v.w[j + 7])
+                     : "l"(p + j)
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < words; j += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p + j);
+        v.w[j] = u.x;
+        v.w[j + 1] = u.y;
+        v.w[j + 2] = u.z;
+        v.w[j + 3] = u.w;
       }
     }
     return;
   }
+  T e[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = col + j < cols ? to_f32(row[col + j]) : 0.f;
+  for (int j = 0; j < 16; ++j) e[j] = col + j < cols ? row[col + j] : from_f32<T>(0.f);
+#pragma unroll
+  for (int j = 0; j < words; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      v.w[j] = __float_as_uint(e[j]);
+    } else {
+      v.w[j] = (uint32_t)reinterpret_cast<const uint16_t&>(e[2 * j]) |
+               (uint32_t)reinterpret_cast<const uint16_t&>(e[2 * j + 1]) << 16;
+    }
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ void store16(T* row, const float (&v)[16], int32_t col, int32_t cols, bool vec) {
-  if (vec && col + 16 <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[8];
+__device__ __forceinline__ void store16(T* row, const float (&v)[16], int32_t col, int32_t cols, int32_t vec) {
+  if (vec != 0 && col + 16 <= cols) {
+    constexpr int words = 4 * (int)sizeof(T);
+    uint32_t w[words];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < words; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        w[j] = __float_as_uint(v[j]);
+      } else {
         reinterpret_cast<T*>(&w[j])[0] = from_f32<T>(v[2 * j]);
         reinterpret_cast<T*>(&w[j])[1] = from_f32<T>(v[2 * j + 1]);
       }
-      uint4* p = reinterpret_cast<uint4*>(row + col);
-      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-      float4* p = reinterpret_cast<float4*>(row + col);
+    }
+    uint32_t* p = reinterpret_cast<uint32_t*>(row + col);
+    if (vec == 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      for (int j = 0; j < words; j += 8) st_global_v8(p + j, w + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < words; j += 4) *reinterpret_cast<uint4*>(p + j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
     }
     return;
   }
@@ -100,7 +133,8 @@ struct Largest {
   __device__ __forceinline__ float operator()(float a, float b) const { return larger(a, b); }
 };
 
-// Over the threads of a row, in a fixed order.  Every thread of the CTA calls it.
+// Over the threads of a row, in a fixed order.  Every thread of the CTA calls it; `shared` is
+// another one than in the call before.
 template <typename Op>
 __device__ __forceinline__ float over_row(float v, Op op, float* shared) {
 #pragma unroll
@@ -117,112 +151,137 @@ __device__ __forceinline__ float over_row(float v, Op op, float* shared) {
 
 template <typename T, int F, bool NORM, int NV>
 __global__ void __launch_bounds__(512) k_quant_rows(const QuantRowsParams p) {
-  __shared__ float shared[2][16];
+  constexpr bool AHEAD = NV <= 2;  // the next row's loads are under way while this one is worked on
+  __shared__ float shared[2][2][16];
   wait_for_prior_kernel();
   let_next_kernel_start();
-  const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const bool live = r < p.rows;
   const int32_t threads = (int32_t)blockDim.x, tx = (int32_t)threadIdx.x;
-  const T* x = reinterpret_cast<const T*>(p.x) + r * p.ld_x;
   const int32_t per = threads * NV;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
 
-  float v[NV][16];
-  auto load = [&](int32_t base) {
+  Run<T> raw[NV], raw_res[NORM ? NV : 1];
+  auto load = [&](int64_t r, int32_t base) {
+    const T* x = reinterpret_cast<const T*>(p.x) + r * p.ld_x;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int32_t c = base + i * threads + tx;
-      if (live && c < p.chunks) {
-        load16<T>(v[i], x, 16 * c, p.cols, p.vec != 0);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[i][j] = 0.f;
-      }
-    }
-  };
-  auto largest = [&](float most) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) most = larger(most, v[i][j]);
-    return most;
-  };
-
-  load(0);
-  if constexpr (NORM) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int32_t c = i * threads + tx;
-      if (!live || c >= p.chunks) continue;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[i][j] *= p.branch_scale;
-      if (p.residual != nullptr) {
-        float e[16];
-        load16<T>(e, reinterpret_cast<const T*>(p.residual) + r * p.ld_residual, 16 * c, p.cols, p.vec != 0);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[i][j] = fmaf(p.residual_scale, e[j], v[i][j]);
-      }
-      if (p.s != nullptr) store16<T>(reinterpret_cast<T*>(p.s) + r * p.ld_s, v[i], 16 * c, p.cols, p.vec != 0);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) sum = fmaf(v[i][j], v[i][j], sum);
-    }
-    sum = over_row(sum, Sum{}, shared[0]);
-    const float unit = __frsqrt_rn(sum / (float)p.cols + p.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int32_t c = i * threads + tx;
-      if (!live || c >= p.chunks) continue;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[i][j] *= unit;
-      if (p.weight != nullptr) {
-        float e[16];
-        if (p.weight_f32) {
-          load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec != 0);
+      const bool in = r < p.rows && c < p.chunks;
+      if (in) load16<T>(raw[i], x, 16 * c, p.cols, p.vec);
+      else raw[i].clear();
+      if constexpr (NORM) {
+        if (in && p.residual != nullptr) {
+          load16<T>(raw_res[i], reinterpret_cast<const T*>(p.residual) + r * p.ld_residual, 16 * c, p.cols, p.vec);
         } else {
-          load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec != 0);
+          raw_res[i].clear();
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[i][j] *= e[j];
       }
     }
-  }
+  };
 
-  RowUnit row = row_unit<F>(0.f);
-  if constexpr (kRowScaled<F>) {
-    float most = largest(0.f);
-    if constexpr (!NORM) {
-      for (int32_t base = per; base < p.chunks; base += per) {
-        load(base);
-        most = largest(most);
-      }
-    }
-    row = row_unit<F>(over_row(most, Largest{}, shared[1]));
-    if (live && tx == 0) p.row_scale[r] = row.scale;
-  }
-
-  for (int32_t base = 0; base < p.all_chunks; base += per) {
-    if (!NORM && (base > 0 || (kRowScaled<F> && per < p.chunks))) load(base);
+  uint32_t turn = 0;
+  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
+  if (AHEAD) load(row0 + threadIdx.y, 0);
+  for (int64_t r0 = row0; r0 < p.all_rows; r0 += step, turn ^= 1u) {
+    const int64_t r = r0 + threadIdx.y;
+    const bool live = r < p.rows;
+    if (!AHEAD) load(r, 0);
+    float v[NV][16];
+    auto take = [&]() {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int32_t c = base + i * threads + tx;
-      BlockUnit b{0u, row.inv, 1.f};
-      if constexpr (kBlock<F> != 0) {
-        float most = 0.f;
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[i][j] = raw[i][j];
+    };
+    auto largest = [&](float most) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) most = larger(most, v[i][j]);
-        if constexpr (kBlock<F> == 32) most = larger(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        b = block_unit<F>(most, row);
-        // four scales, of four or eight threads, are stored together
-        constexpr int lanes = 4 * kBlock<F> / 16;
-        uint32_t word = live && c < p.chunks ? b.byte << (8 * ((c * 16 / kBlock<F>) & 3)) : 0u;
+      return most;
+    };
+    take();
+    if constexpr (NORM) {
 #pragma unroll
-        for (int o = kBlock<F> / 16; o < lanes; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
-        if (c % lanes == 0 && c < p.all_chunks && r < p.all_rows)
-          *reinterpret_cast<uint32_t*>(p.scales + scale_offset(r, c * 16 / kBlock<F>, p.blocks)) = word;
-      }
-      if (live && c < p.chunks)
-        store_codes<F, sizeof(T) == 4 && !NORM>(p.data + r * p.ld_data + (int64_t)c * (kFourBit<F> ? 8 : 16), v[i], row, b);
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[i][j] = fmaf(p.residual_scale, raw_res[i][j], v[i][j] * p.branch_scale);
     }
+    if (AHEAD && (NORM || p.chunks <= per)) load(r + step, 0);
+    if constexpr (NORM) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int32_t c = i * threads + tx;
+        if (live && c < p.chunks && p.s != nullptr)
+          store16<T>(reinterpret_cast<T*>(p.s) + r * p.ld_s, v[i], 16 * c, p.cols, p.vec);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+      }
+      sum = over_row(sum, Sum{}, shared[0][turn]);
+      const float unit = __frsqrt_rn(sum / (float)p.cols + p.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int32_t c = i * threads + tx;
+        if (c >= p.chunks) continue;
+        if (p.weight == nullptr) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[i][j] *= unit;
+        } else if (p.weight_f32) {
+          Run<float> e;
+          load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * unit * e[j];
+        } else {
+          Run<T> e;
+          load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * unit * e[j];
+        }
+      }
+    }
+
+    RowUnit row = row_unit<F>(0.f);
+    if constexpr (kRowScaled<F>) {
+      float most = largest(0.f);
+      if constexpr (!NORM) {
+        for (int32_t base = per; base < p.chunks; base += per) {
+          load(r, base);
+          take();
+          most = largest(most);
+        }
+      }
+      row = row_unit<F>(over_row(most, Largest{}, shared[1][turn]));
+      if (live && tx == 0) p.row_scale[r] = row.scale;
+    }
+
+    for (int32_t base = 0; base < p.all_chunks; base += per) {
+      if (!NORM && (base > 0 || (kRowScaled<F> && per < p.chunks))) {
+        load(r, base);
+        take();
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int32_t c = base + i * threads + tx;
+        BlockUnit b{0u, row.inv, 1.f};
+        if constexpr (kBlock<F> != 0) {
+          float most = 0.f;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) most = larger(most, v[i][j]);
+          if constexpr (kBlock<F> == 32) most = larger(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          b = block_unit<F>(most, row);
+          // four scales, of four or eight threads, are stored together
+          constexpr int lanes = 4 * kBlock<F> / 16;
+          uint32_t word = live && c < p.chunks ? b.byte << (8 * ((c * 16 / kBlock<F>) & 3)) : 0u;
+#pragma unroll
+          for (int o = kBlock<F> / 16; o < lanes; o *= 2) word |= __shfl_xor_sync(0xffffffffu, word, o);
+          if (c % lanes == 0 && c < p.all_chunks && r < p.all_rows)
+            *reinterpret_cast<uint32_t*>(p.scales + scale_offset(r, c * 16 / kBlock<F>, p.blocks)) = word;
+        }
+        if (live && c < p.chunks)
+          store_codes<F, sizeof(T) == 4 && !NORM>(p.data + r * p.ld_data + (int64_t)c * (kFourBit<F> ? 8 : 16), v[i], row, b);
+      }
+    }
+    if (AHEAD && !NORM && p.chunks > per) load(r + step, 0);
   }
 }
 
@@ -247,7 +306,7 @@ const void* rows_kernel_of(int format, int nv) {
 
 }  // namespace
 
-// by the inputs' type (quant_rows_f16.cu and so on)
+// by the inputs' type (kernels_quant_rows_f16.cu and so on)
 const void* quant_rows_f16(int format, bool norm, int nv);
 const void* quant_rows_bf16(int format, bool norm, int nv);
 const void* quant_rows_f32(int format, bool norm, int nv);

@@ -11,8 +11,10 @@ namespace {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bool rows_aligned(const void* p, int64_t pitch_bytes) {
-  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && pitch_bytes % 16 == 0);
+// 2: rows start on 32-byte boundaries, 1: on 16-byte ones, 0: neither
+int alignment_of(const void* p, int64_t pitch_bytes) {
+  const uintptr_t bits = p == nullptr ? 0 : reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes;
+  return (bits & 31u) == 0 ? 2 : (bits & 15u) == 0 ? 1 : 0;
 }
 
 cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm, int num_sms, cudaStream_t st) {
@@ -21,19 +23,19 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
   p.blocks = (int32_t)up(scales, 4);
   p.all_chunks = scales == 0 ? p.chunks : (int32_t)(p.blocks * 4 * (format == QUANT_NVFP4 ? 1 : 2));
   p.all_rows = scales == 0 ? p.rows : up(p.rows, 128) * 128;
-  // Threads for a row: one run of 16 each while all rows together keep the device busy with
-  // more, then up to four.
+  // one run of 16 columns a thread up to 512 threads a row, then up to four
   int nv = 1;
-  while (nv < 4 && up(p.chunks, nv) > 32 &&
-         (up(p.chunks, nv) > 512 || up(p.chunks, nv) * p.rows > (int64_t)num_sms * 2048))
-    nv *= 2;
+  while (nv < 4 && up(p.chunks, nv) > 512) nv *= 2;
   const int threads = (int)std::min<int64_t>(512, up(up(p.chunks, nv), 32) * 32);
-  const int rows = std::max(1, 128 / threads);
+  const int rows = std::max(1, 256 / threads);
   LaunchSpec s;
   s.func = dtype == FFN_F32    ? quant_rows_f32(format, norm, nv)
            : dtype == FFN_BF16 ? quant_rows_bf16(format, norm, nv)
                                : quant_rows_f16(format, norm, nv);
-  s.grid = dim3((unsigned)up(p.all_rows, rows), 1, 1);
+  int resident = 0;
+  const cudaError_t e = resident_ctas(s.func, threads * rows, 0, 0, &resident);
+  if (e != cudaSuccess) return e;
+  s.grid = dim3((unsigned)std::min<int64_t>(up(p.all_rows, rows), (int64_t)num_sms * std::max(1, resident)), 1, 1);
   s.block = dim3((unsigned)threads, (unsigned)rows, 1);
   s.pdl = true;
   void* args[] = {&p};
@@ -47,7 +49,7 @@ cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaS
   QuantRowsParams p{};
   p.rows = a.rows;
   p.cols = (int32_t)a.cols;
-  p.vec = rows_aligned(a.x, a.ld_x * e);
+  p.vec = alignment_of(a.x, a.ld_x * e);
   p.x = a.x;
   p.data = static_cast<uint8_t*>(a.data);
   p.scales = static_cast<uint8_t*>(a.scales);
@@ -62,7 +64,8 @@ cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaS
   QuantRowsParams p{};
   p.rows = a.M;
   p.cols = (int32_t)a.D;
-  p.vec = rows_aligned(a.y, a.ld_y * e) && rows_aligned(a.residual, a.ld_residual * e) && rows_aligned(a.s, a.ld_s * e);
+  p.vec = std::min({alignment_of(a.y, a.ld_y * e), alignment_of(a.residual, a.ld_residual * e),
+                    alignment_of(a.s, a.ld_s * e)});
   p.x = a.y;
   p.residual = a.residual;
   p.weight = a.weight;
@@ -75,7 +78,7 @@ cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaS
   p.ld_s = a.ld_s;
   p.ld_data = a.ld_data;
   p.weight_f32 = a.param_dtype == FFN_F32;
-  p.weight_vec = rows_aligned(a.weight, 0);
+  p.weight_vec = alignment_of(a.weight, 0);
   p.eps = a.eps;
   p.residual_scale = a.residual_scale;
   p.branch_scale = a.branch_scale;
