@@ -21,6 +21,18 @@ __device__ __forceinline__ uint32_t fp4_idesc(uint32_t idesc, int k) {
   return idesc | (id << 4) | (id << 29);
 }
 
+// A bounded wait of a whole warp: one lane's answer for all.
+template <bool CLUSTER_ACQ = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, uint32_t code) {
+  if (__all_sync(0xffffffffu, CLUSTER_ACQ ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+  uint32_t ok = 1;
+  if (lane_idx() == 0) ok = mbar_wait_slow<CLUSTER_ACQ>(bar, parity, w, code) ? 1u : 0u;
+  // (every lane has to see the phase itself: the acquire is a thread's own)
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  if (ok) ok = CLUSTER_ACQ ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok != 0u);
+}
+
 template <int N>
 __device__ __forceinline__ void fp4_act(float (&x)[N], int32_t act) {
   switch (act) {

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // (the same in all lanes, for the compiler)
   const WaitCtl w{abort_flag, p.status, p.timeout_ns, 0};
 
   const int32_t rank = (int32_t)cluster_ctarank();
@@ -202,30 +202,31 @@ __global__ void __launch_bounds__(kFp4FewThreads)
       if (j >= first || !p.static_b) features(j, s);
       token_rows(j, s);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------------- scales and MMAs
+    const uint32_t issue = elect_lane();
     for (int32_t j = 0; j < nkb; ++j) {
       const uint32_t s = (uint32_t)j % S;
-      if (!mbar_wait(smem_u32(full + s), (uint32_t)j / S & 1u, w, WAIT_MMA_FULL)) break;
+      if (!warp_wait(smem_u32(full + s), (uint32_t)j / S & 1u, w, WAIT_MMA_FULL)) break;
       tc_fence_after();
       const uint32_t st = smem_u32(ring + s * STAGE);
       const uint32_t sf = tmem + kScaleCol + s * kSlot<NV>;
 #pragma unroll
       for (uint32_t i = 0; i < NB; ++i) {
-        tmem_cp_32x128b_x4<1>(sf + 4u * i, sdesc_rows16(st + fscales_at + 512u * i));
-        tmem_cp_32x128b_x4<1>(sf + 4u * NB + 4u * i, sdesc_rows16(st + tscales_at + 512u * i));
+        tmem_cp_32x128b_x4<1>(issue, sf + 4u * i, sdesc_rows16(st + fscales_at + 512u * i));
+        tmem_cp_32x128b_x4<1>(issue, sf + 4u * NB + 4u * i, sdesc_rows16(st + tscales_at + 512u * i));
       }
       const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(st + tokens_at);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t i = fp4_scale_block<NV>(k);
         if (4 * (kb0 + j) + k < p.steps)
-          mma_fp4<1, NV>(tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * i, sf + 4u * NB + 4u * i,
-                         (uint32_t)(j | k));
+          mma_fp4<1, NV>(issue, tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * i,
+                         sf + 4u * NB + 4u * i, (uint32_t)(j | k));
       }
-      mma_commit(smem_u32(empty + s));
+      if (issue) mma_commit(smem_u32(empty + s));
     }
-    mma_commit(smem_u32(done));
+    if (issue) mma_commit(smem_u32(done));
   }
   __syncwarp();
   wait_for_prior_kernel();

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // (the same in all lanes, for the compiler)
   wait_for_prior_kernel();
   const WaitCtl w{abort_flag, p.status, p.timeout_ns, mapa_shared(smem_u32((const void*)abort_flag), rank ^ 1u)};
   const int32_t cid = (int32_t)(blockIdx.x / 2), clusters = (int32_t)(gridDim.x / 2);
@@ -147,32 +147,34 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     }
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      uint32_t stage = 0, sphase = 0, apar = 0;
-      bool ok = true;
-      for (int32_t tile = cid; ok && tile < tiles; tile += clusters, apar ^= 1u) {
-        if (!mbar_wait<true>(smem_u32(acc_empty), apar ^ 1u, w, WAIT_MMA_ACC_EMPTY)) break;
+    // the whole warp walks the loop and one lane issues (see mma_fp4)
+    const uint32_t issue = elect_lane();
+    uint32_t stage = 0, sphase = 0, apar = 0;
+    bool ok = true;
+    for (int32_t tile = cid; ok && tile < tiles; tile += clusters, apar ^= 1u) {
+      if (!warp_wait<true>(smem_u32(acc_empty), apar ^ 1u, w, WAIT_MMA_ACC_EMPTY)) break;
+      tc_fence_after();
+      for (int32_t kb = 0; kb < p.blocks; ++kb) {
+        // (the copier saw the stage land, so this covers the operands too)
+        if (!warp_wait(smem_u32(ready + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
         tc_fence_after();
-        for (int32_t kb = 0; kb < p.blocks; ++kb) {
-          // (the copier saw the stage land, so this covers the operands too)
-          if (!mbar_wait(smem_u32(ready + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t st = smem_u32(ring + stage * kStage<NV>);
-          const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(st + kOperand);
-          const uint32_t sf = tmem + kScaleCol + stage * kSlot<NV>;
+        const uint32_t st = smem_u32(ring + stage * kStage<NV>);
+        const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(st + kOperand);
+        const uint32_t sf = tmem + kScaleCol + stage * kSlot<NV>;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t j = fp4_scale_block<NV>(k);
-            if (4 * kb + k < p.steps)
-              mma_fp4<2, NV>(tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * j,
-                             sf + 4u * NB + 8u * j, (uint32_t)(kb | k));
-          }
-          mma_commit_pair(smem_u32(empty + stage), 3u);
-          if (++stage == S) { stage = 0; sphase ^= 1u; }
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t j = fp4_scale_block<NV>(k);
+          if (4 * kb + k < p.steps)
+            mma_fp4<2, NV>(issue, tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * j,
+                           sf + 4u * NB + 8u * j, (uint32_t)(kb | k));
         }
-        if (!ok) break;
-        mma_commit_pair(smem_u32(acc_full), 3u);
+        if (issue) mma_commit_pair(smem_u32(empty + stage), 3u);
+        if (++stage == S) { stage = 0; sphase ^= 1u; }
       }
+      if (!ok) break;
+      if (issue) mma_commit_pair(smem_u32(acc_full), 3u);
+    }
+    if (issue) {
       // every MMA this thread issued must be complete before TMEM is released
       mma_commit_cg<2>(smem_u32(drain_bar));
       const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
@@ -180,29 +182,30 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     }
   } else if ((warp == 2 || warp == 3) && leader) {
     // ---------------------------------------------------------- scale copies
-    if (lane == 0) {
-      uint32_t stage = 0, sphase = 0;
-      bool ok = true;
-      for (int32_t tile = cid; ok && tile < tiles; tile += clusters) {
-        for (int32_t kb = 0; kb < p.blocks; ++kb) {
-          // the stage's slot was last read by MMAs that completed before the stage was
-          // refilled, so it is free once the stage has landed
-          if (!mbar_wait(smem_u32(full + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t from = smem_u32(ring + stage * kStage<NV> + kScalesAt);
-          const uint32_t to = tmem + kScaleCol + stage * kSlot<NV>;
-          // each of the two threads takes half of the blocks
+    const uint32_t issue = elect_lane();
+    const uint32_t part = warp - 2u;  // each of the two warps takes half of the blocks
+    uint32_t stage = 0, sphase = 0;
+    bool ok = true;
+    for (int32_t tile = cid; ok && tile < tiles; tile += clusters) {
+      for (int32_t kb = 0; kb < p.blocks; ++kb) {
+        // the stage's slot was last read by MMAs that completed before the stage was
+        // refilled, so it is free once the stage has landed
+        if (!warp_wait(smem_u32(full + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t from = smem_u32(ring + stage * kStage<NV> + kScalesAt);
+        const uint32_t to = tmem + kScaleCol + stage * kSlot<NV>;
 #pragma unroll
-          for (uint32_t i = 0; i < NB / 2; ++i) {
-            const uint32_t j = i + (warp - 2u) * (NB / 2);
-            tmem_cp_32x128b_x4<2>(to + 4u * j, sdesc_rows16(from + 512u * j));
-            tmem_cp_32x128b_x4<2>(to + 4u * NB + 8u * j, sdesc_rows16(from + 512u * (NB + j)));
-            tmem_cp_32x128b_x4<2>(to + 4u * NB + 8u * j + 4u, sdesc_rows16(from + 512u * (2u * NB + j)));
-          }
-          mma_commit_cg<2>(smem_u32(ready + stage));
-          if (++stage == S) { stage = 0; sphase ^= 1u; }
+        for (uint32_t i = 0; i < NB / 2; ++i) {
+          const uint32_t j = i + part * (NB / 2);
+          tmem_cp_32x128b_x4<2>(issue, to + 4u * j, sdesc_rows16(from + 512u * j));
+          tmem_cp_32x128b_x4<2>(issue, to + 4u * NB + 8u * j, sdesc_rows16(from + 512u * (NB + j)));
+          tmem_cp_32x128b_x4<2>(issue, to + 4u * NB + 8u * j + 4u, sdesc_rows16(from + 512u * (2u * NB + j)));
         }
+        if (issue) mma_commit_cg<2>(smem_u32(ready + stage));
+        if (++stage == S) { stage = 0; sphase ^= 1u; }
       }
+    }
+    if (issue) {
       // the copies this thread issued must be complete before TMEM is released
       mma_commit_cg<2>(smem_u32(copy_drain));
       const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};

@@ -499,37 +499,39 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, ui
 // The same for 4-bit (E2M1) operands, 64 K-elements per instruction: one UE8M0 scale per 32
 // of them (two scales a row, `NV` false: bytes 0 and 1 or 2 and 3 of the TMEM word, chosen by
 // the instruction descriptor), or one UE4M3 scale per 16 (four scales, the whole word).
+// All lanes of the warp call it with the same operands and the lane with `issue` != 0 hands it
+// over: in a branch of one lane every operand takes a move into a uniform register first.
 template <int CG, bool NV>
-__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+__device__ __forceinline__ void mma_fp4(uint32_t issue, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+#define DGB_MMA_FP4(group, kind)                                                                                       \
+  asm volatile(                                                                                                        \
+      "{\n\t.reg .pred p, q;\n\t"                                                                                      \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                                      \
+      "setp.ne.b32 q, %7, 0;\n\t"                                                                                      \
+      "@q tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),        \
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(issue)                    \
+      : "memory")
   if constexpr (CG == 1 && NV)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    DGB_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
   else if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    DGB_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
   else if constexpr (NV)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    DGB_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-        : "memory");
+    DGB_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+#undef DGB_MMA_FP4
+}
+
+// 1 in one lane of the (whole) warp, 0 in the others
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
 }
 
 // Copy 32 rows x 16 bytes of shared memory (described by `sdesc`) into TMEM
@@ -543,6 +545,23 @@ __device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t taddr, uint64_t sdes
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
   else
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// the same from the lane with `issue` != 0 of a warp that calls it together
+template <int CG>
+__device__ __forceinline__ void tmem_cp_32x128b_x4(uint32_t issue, uint32_t taddr, uint64_t sdesc) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(sdesc), "r"(issue)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(sdesc), "r"(issue)
+        : "memory");
 }
 
 // one arrival on `bar` once every tcgen05 op this thread issued so far is done
