@@ -1033,6 +1033,11 @@ bool dgb::encode_byte_rows(CUtensorMap* m, const void* ptr, uint64_t row_bytes, 
                    CU_TENSOR_MAP_SWIZZLE_128B, pitch);
 }
 
+bool dgb::encode_out_tiles(CUtensorMap* m, bool f32, const void* ptr, uint64_t cols, uint64_t rows, uint64_t pitch) {
+  return f32 ? encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, ptr, cols, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B, pitch)
+             : encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, cols, rows, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, pitch);
+}
+
 bool dgb::encode_scale_blocks(CUtensorMap* m, const void* ptr, uint64_t k_blocks, uint64_t row_blocks, uint32_t box_k,
                               uint32_t box_rows) {
   if (!encode_fn_ready()) return false;

@@ -13,9 +13,8 @@ namespace {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int alignment_of(const void* p, int64_t pitch_bytes) {
-  const uintptr_t bits = reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes;
-  return (bits & 31u) == 0 ? 2 : (bits & 15u) == 0 ? 1 : 0;
+bool aligned_rows(const void* p, int64_t pitch_bytes) {
+  return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)pitch_bytes) & 15u) == 0;
 }
 
 }  // namespace
@@ -27,8 +26,7 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
   p.e.M = (int32_t)a.M;
   p.e.N = (int32_t)a.N;
   p.e.act = a.activation;
-  p.e.vec = alignment_of(a.c, a.ld_c * e);
-  if (a.residual) p.e.vec = std::min(p.e.vec, alignment_of(a.residual, a.ld_residual * e));
+  p.e.vec = aligned_rows(a.c, a.ld_c * e) && aligned_rows(a.residual, a.ld_residual * e);
   p.e.row_scale_a = a.row_scale_a;
   p.e.row_scale_b = a.row_scale_b;
   p.e.bias = a.bias;
@@ -45,10 +43,12 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
 
   const uint32_t box_k = nv ? 4 : 2;  // scale blocks of a stage
   const uint64_t across = (uint64_t)up(scales_of(a.K, a.format), 4);
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   LaunchSpec s;
   s.pdl = true;
-  void* args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+  void* pair_args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &maps[4], &p};
+  void* few_args[] = {&maps[0], &maps[1], &maps[2], &maps[3], &p};
+  void** args = few_args;
   if (!encode_scale_blocks(&maps[2], a.scales_a, across, (uint64_t)up(a.M, 128), box_k, 1)) return cudaErrorInvalidValue;
 
   const int64_t pair_tiles = up(a.M, 256) * up(a.N, 256);
@@ -62,6 +62,10 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
         !encode_byte_rows(&maps[1], a.b, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.ld_b, 128) ||
         !encode_scale_blocks(&maps[3], a.scales_b, across, (uint64_t)up(a.N, 128), box_k, 2))
       return cudaErrorInvalidValue;
+    maps[4] = maps[0];  // (not used where c's rows are not aligned)
+    if (p.e.vec && !encode_out_tiles(&maps[4], f32, a.c, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ld_c))
+      return cudaErrorInvalidValue;
+    args = pair_args;
     s.func = fp4_pair_kernel(nv, f32);
     s.grid = dim3(2u * (unsigned)std::min<int64_t>(pair_tiles, std::max(1, dev.num_sms / 2)), 1, 1);
     s.block = dim3(kFp4PairThreads, 1, 1);

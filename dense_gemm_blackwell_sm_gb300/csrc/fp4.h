@@ -13,7 +13,7 @@ namespace dgb {
 // What happens to a sum: c = act(row_scale_a[i] row_scale_b[j] sum + bias[j]) + residual[i][j].
 struct Fp4Epilogue {
   int32_t M, N, act;
-  int32_t vec;              // c's and the residual's rows and starts: 2 = 32-byte aligned, 1 = 16, 0 = neither
+  int32_t vec;              // c's and the residual's rows start on 16-byte boundaries
   const float* row_scale_a; // or null, as the next three
   const float* row_scale_b;
   const float* bias;

@@ -21,16 +21,21 @@ __device__ __forceinline__ uint32_t fp4_idesc(uint32_t idesc, int k) {
   return idesc | (id << 4) | (id << 29);
 }
 
-// A bounded wait of a whole warp: one lane's answer for all.
+// A bounded wait of a whole warp: every lane looks for the phase itself (the acquire is a
+// thread's own) and all leave together.  It calls nothing and no lane runs ahead: what the warp's
+// loop keeps in uniform registers must not live across a call that one lane makes.
 template <bool CLUSTER_ACQ = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, uint32_t code) {
-  if (__all_sync(0xffffffffu, CLUSTER_ACQ ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
-  uint32_t ok = 1;
-  if (lane_idx() == 0) ok = mbar_wait_slow<CLUSTER_ACQ>(bar, parity, w, code) ? 1u : 0u;
-  // (every lane has to see the phase itself: the acquire is a thread's own)
-  ok = __shfl_sync(0xffffffffu, ok, 0);
-  if (ok) ok = CLUSTER_ACQ ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok != 0u);
+  uint64_t since = 0;
+  for (uint32_t spins = 1;; ++spins) {
+    if (__all_sync(0xffffffffu, CLUSTER_ACQ ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) return true;
+    if ((spins & 15u) != 0u) continue;
+    const uint64_t now = globaltimer_ns();
+    if (spins == 16u) since = now;
+    const bool late = now - since > w.timeout_ns && now > since;
+    if (late) raise_abort(w, code);  // (the first code stays)
+    if (__any_sync(0xffffffffu, late || *w.abort_flag != 0u)) return false;
+  }
 }
 
 template <int N>
@@ -56,92 +61,91 @@ __device__ __forceinline__ void fp4_act(float (&x)[N], int32_t act) {
   }
 }
 
-// 32 sums of row `row`, columns col .. col + 31 (fewer at the matrix' edge), to c.  A lane has a
-// row; where rows are not aligned the values go through `staging` (32 x 33 floats of the
-// warp's) so that lanes write neighbours.  Every lane of the warp calls it; rows past M are
-// left out.
+// 32 x 32 sums, a lane's row in v, of columns col .. col + 31, to c: scaled, finished, rounded
+// into `staging` (4096 bytes of the warp's, 1024-byte aligned) and stored from there, by a TMA
+// copy where c's rows are aligned to 16 bytes (tmC: boxes of 32 x 32, swizzled over 128 bytes for
+// fp32 and 64 for bf16), else by the lanes, each a column, so that they write neighbours.
+// `scale` and `bias`: the columns' values in shared memory.  Every lane of the warp calls it;
+// `buffer` counts the warp's copies: bf16 takes the halves of the staging space in turn.
 template <typename OutT>
-__device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const uint32_t (&v)[32], int32_t row0, int32_t col,
-                                            float sa, float* staging, uint32_t lane) {
+__device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const CUtensorMap* tmC, const uint32_t (&v)[32],
+                                            int32_t row0, int32_t col, float sa, const float* scale, const float* bias,
+                                            uint8_t* staging, uint32_t& buffer, uint32_t lane) {
+  if (row0 >= e.M || col >= e.N) return;
   const int32_t row = row0 + (int32_t)lane;
-  const int32_t n = min(32, e.N - col);
-  if (n <= 0 || row0 >= e.M) return;
   float x[32];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]) * sa;
-  const bool whole = n == 32;
-  auto columns = [&](const float* p, auto apply) {
-    if (p == nullptr) return;
-    if (whole && (reinterpret_cast<uintptr_t>(p + col) & 15u) == 0) {
-      const float4* q = reinterpret_cast<const float4*>(p + col);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 f = __ldg(q + j);
-        apply(x[4 * j], f.x);
-        apply(x[4 * j + 1], f.y);
-        apply(x[4 * j + 2], f.z);
-        apply(x[4 * j + 3], f.w);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) apply(x[j], __ldg(p + col + j));
-    }
-  };
-  columns(e.row_scale_b, [](float& a, float b) { a *= b; });
-  columns(e.bias, [](float& a, float b) { a += b; });
+  for (int j = 0; j < 8; ++j) {
+    const float4 s = reinterpret_cast<const float4*>(scale)[j], b = reinterpret_cast<const float4*>(bias)[j];
+    x[4 * j] = fmaf(__uint_as_float(v[4 * j]) * sa, s.x, b.x);
+    x[4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]) * sa, s.y, b.y);
+    x[4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]) * sa, s.z, b.z);
+    x[4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]) * sa, s.w, b.w);
+  }
   fp4_act(x, e.act);
-  constexpr int per16 = 16 / (int)sizeof(OutT);
-  if (e.vec != 0 && (whole || n % per16 == 0)) {
-    if (row >= e.M) return;
-    OutT* dst = reinterpret_cast<OutT*>(e.c) + (int64_t)row * e.ld_c + col;
-    if (e.residual != nullptr) {
+  if (e.vec != 0) {
+    constexpr int per16 = 16 / (int)sizeof(OutT);
+    if (e.residual != nullptr && row < e.M) {
       const OutT* src = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
 #pragma unroll
       for (int q = 0; q < 32 / per16; ++q) {
-        if (q * per16 >= n) break;
-        const uint4 u = *reinterpret_cast<const uint4*>(src + q * per16);
-        const OutT* w = reinterpret_cast<const OutT*>(&u);
+        if (col + q * per16 + per16 <= e.N) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + q * per16);
+          const OutT* w = reinterpret_cast<const OutT*>(&u);
 #pragma unroll
-        for (int j = 0; j < per16; ++j) x[q * per16 + j] += to_f32(w[j]);
+          for (int j = 0; j < per16; ++j) x[q * per16 + j] += to_f32(w[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < per16; ++j)
+            if (col + q * per16 + j < e.N) x[q * per16 + j] += to_f32(src[q * per16 + j]);
+        }
       }
     }
-    uint32_t o[8 * sizeof(OutT)];
+    uint8_t* buf = staging + (sizeof(OutT) == 2 ? (buffer++ & 1u) * 2048u : 0u);
+    // the copy issued from this buffer before has read it
+    if (lane == 0) bulk_wait_group_read<sizeof(OutT) == 2 ? 1 : 0>();
+    __syncwarp();
     if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(x[j]);
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<float4*>(buf + sw128_offset(lane, (uint32_t)j)) =
+            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__float_as_uint(x[2 * j]), __float_as_uint(x[2 * j + 1]));
+      for (uint32_t j = 0; j < 4; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = pack_bf16x2(__float_as_uint(x[8 * j + 2 * i]), __float_as_uint(x[8 * j + 2 * i + 1]));
+        // 64-byte rows swizzled: the 16-byte piece's index takes bits 1 and 2 of the row
+        *reinterpret_cast<uint4*>(buf + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
-    constexpr int words = (int)(8 * sizeof(OutT));
-    if (e.vec == 2 && whole) {
-#pragma unroll
-      for (int j = 0; j < words / 8; ++j) st_global_v8(reinterpret_cast<uint32_t*>(dst) + 8 * j, o + 8 * j);
-    } else {
-#pragma unroll
-      for (int j = 0; j < words / 4; ++j)
-        if (j * per16 < n)
-          reinterpret_cast<uint4*>(dst)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tmC, smem_u32(buf), col, row0);
+      bulk_commit_group();
     }
     return;
   }
+  float* rows = reinterpret_cast<float*>(staging);
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 32; ++j) staging[lane * 33 + j] = x[j];
+  for (uint32_t j = 0; j < 32; ++j) rows[lane * 32u + (j ^ lane)] = x[j];
   __syncwarp();
-  if ((int32_t)lane < n) {
-    const int32_t rows = min(32, e.M - row0);
+  if (col + (int32_t)lane < e.N) {
+    const int32_t n = min(32, e.M - row0);
     OutT* dst = reinterpret_cast<OutT*>(e.c) + (int64_t)row0 * e.ld_c + col + lane;
     const OutT* src = reinterpret_cast<const OutT*>(e.residual);
     if (src != nullptr) src += (int64_t)row0 * e.ld_residual + col + lane;
-    for (int32_t r = 0; r < rows; ++r) {
-      float y = staging[r * 33 + lane];
+#pragma unroll 4
+    for (int32_t r = 0; r < n; ++r) {
+      float y = rows[r * 32 + (int32_t)(lane ^ (uint32_t)r)];
       if (src != nullptr) y += to_f32(src[(int64_t)r * e.ld_residual]);
       dst[(int64_t)r * e.ld_c] = from_f32<OutT>(y);
     }
   }
-  __syncwarp();
 }
 
 }  // namespace dgb

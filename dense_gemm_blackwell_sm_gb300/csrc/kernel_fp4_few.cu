@@ -225,12 +225,13 @@ __global__ void __launch_bounds__(kFp4FewThreads)
                          sf + 4u * NB + 4u * i, (uint32_t)(j | k));
       }
       if (issue) mma_commit(smem_u32(empty + s));
+      __syncwarp();
     }
     if (issue) mma_commit(smem_u32(done));
   }
   __syncwarp();
   wait_for_prior_kernel();
-  bool ok = mbar_wait(smem_u32(done), 0, w, WAIT_LADDER_MMA);
+  bool ok = warp_wait(smem_u32(done), 0, w, WAIT_LADDER_MMA);
   ok = __syncthreads_and(ok && *abort_flag == 0u) != 0;
 
   // The partial sums, [token][feature], where the stages were; each CTA of the cluster then

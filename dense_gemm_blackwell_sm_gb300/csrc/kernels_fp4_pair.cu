@@ -3,13 +3,17 @@
 // A pair (cta_group::2) computes a tile of 256 x 256: each CTA brings 128 rows of A and 128 of
 // B, 256 K-elements a stage (128 bytes a row), and the block scales of its rows of A and of all
 // 256 of B.  tcgen05.mma kind::mxf4 / mxf4nvf4 takes 64 K-elements at a time, with scales that
-// tcgen05.cp has moved from shared memory into TMEM; the sums are one 256-column fp32
-// accumulator, the scales take the other TMEM columns, a slot a stage.
+// tcgen05.cp has moved from shared memory into TMEM, to one of a few slots in turn.
 //
-// Roles (384 threads): warp 0 TMA producer, warp 1 MMA, warp 2 allocates TMEM, warp 3 copies the
-// scales (one thread's issue rate bounds the MMAs, so the copies have a thread of their own),
-// warps 4-11 the epilogue: each takes its part of the accumulator into registers, hands it back
-// and then scales and stores it while the next tile's MMAs run.
+// The sums take 256 columns of TMEM, and the scales leave no room for two such accumulators.  So
+// consecutive tiles overlap: even ones lie at columns 0-255, odd ones at 96-351.  The epilogue
+// reads the 160 columns in common first and hands them back, and the next tile's MMAs start
+// while it reads the other 96 and stores the tile.
+//
+// Roles (384 threads): warp 0 TMA producer, warp 1 MMA, warps 2 (which allocates TMEM) and 3 copy
+// the scales, since one thread's issue rate bounds the MMAs (8192^3 NVFP4: 247 us with one copier,
+// 206 with two), warps 4-11 the epilogue.  Issuing warps walk their loops as a whole and one lane's
+// predicate lets an instruction go (8192^3: 176 us).
 //
 // Every cluster takes the tiles cid, cid + clusters, ...: results depend on the sizes alone.
 // Every wait is bounded (ptx.cuh); programmatic launches as in ffn_common.cuh.
@@ -22,10 +26,12 @@ namespace dgb {
 namespace {
 
 constexpr uint32_t kOperand = 128u * 128u;  // 128 rows of 256 4-bit elements
-constexpr uint32_t kStaging = 8u * 32u * 33u * 4u;
+constexpr uint32_t kStaging = 8u * 4096u;
+constexpr uint32_t kColumns = 2u * 256u * 4u;  // a tile's column scales and biases
 constexpr uint32_t kCtrl = 512;
 constexpr int kMostStages = 8;
-constexpr uint32_t kScaleCol = 256;  // first TMEM column of the scales
+constexpr int32_t kOwn = 96;          // columns of an accumulator that the next tile's does not take
+constexpr uint32_t kScaleCol = 256u + kOwn;  // first TMEM column of the scales
 
 template <bool NV>
 constexpr uint32_t kStage = 2u * kOperand + 3u * 512u * kScaleBlocks<NV>;
@@ -33,31 +39,43 @@ template <bool NV>
 constexpr uint32_t kSlot = 12u * kScaleBlocks<NV>;  // TMEM columns of a stage's scales
 
 template <bool NV>
+constexpr uint32_t kSlots = (512u - kScaleCol) / kSlot<NV>;  // 3 with a scale per 16, 6 with one per 32
+
+template <bool NV>
+__host__ __device__ constexpr size_t smem_of(int stages) {
+  return 1024u + (size_t)stages * kStage<NV> + kStaging + kColumns + kCtrl;
+}
+template <bool NV>
 __host__ __device__ constexpr int stages_of() {
   int s = kMostStages;
-  while (1024u + (uint32_t)s * kStage<NV> + kStaging + kCtrl > 232448u || (uint32_t)s * kSlot<NV> > 256u) --s;
+  while (smem_of<NV>(s) > 232448u) --s;
   return s;
 }
+
+// the eight warps of the epilogue
+__device__ __forceinline__ void epilogue_sync() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
 
 template <bool NV, typename OutT>
 __global__ void __launch_bounds__(kFp4PairThreads, 1)
     k_fp4_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-               const __grid_constant__ Fp4Params p) {
+               const __grid_constant__ CUtensorMap tmC, const __grid_constant__ Fp4Params p) {
   constexpr uint32_t S = (uint32_t)stages_of<NV>();
   constexpr uint32_t NB = (uint32_t)kScaleBlocks<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
-  float* staging = reinterpret_cast<float*>(ring + S * kStage<NV>);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(staging) + kStaging);
+  uint8_t* staging = ring + S * kStage<NV>;
+  float* columns = reinterpret_cast<float*>(staging + kStaging);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kStaging + kColumns);
   uint64_t* full = bars;                     // TMA -> scale copies
   uint64_t* empty = bars + kMostStages;      // MMA -> TMA
   uint64_t* ready = bars + 2 * kMostStages;  // scale copies -> MMA
   uint64_t* acc_full = bars + 3 * kMostStages;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain_bar = acc_full + 2;
-  uint64_t* copy_drain = acc_full + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 4);
+  uint64_t* acc_empty = acc_full + 1;  // the common columns are read
+  uint64_t* own_empty = acc_full + 2;  // the tile's own columns too
+  uint64_t* drain_bar = acc_full + 3;
+  uint64_t* copy_drain = acc_full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 5);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* zero_word = tmem_slot + 2;
   // (the stage's scales follow its operands: A's blocks, B's blocks of rows 0-127, of 128-255)
@@ -74,6 +92,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     }
     mbar_init(smem_u32(acc_full), 1);
     mbar_init(smem_u32(acc_empty), 16);
+    mbar_init(smem_u32(own_empty), 16);
     mbar_init(smem_u32(drain_bar), 1);
     mbar_init(smem_u32(copy_drain), 2);
     *abort_flag = 0u;
@@ -85,6 +104,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
+    if (p.e.vec != 0) tma_prefetch_desc(&tmC);
   }
   if (warp == 2) {
     tmem_alloc<2>(smem_u32(tmem_slot), 512);
@@ -149,51 +169,62 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     // ------------------------------------------------------------------ MMA
     // the whole warp walks the loop and one lane issues (see mma_fp4)
     const uint32_t issue = elect_lane();
-    uint32_t stage = 0, sphase = 0, apar = 0;
+    uint32_t stage = 0, sphase = 0, apar = 0, slot = 0;
     bool ok = true;
     for (int32_t tile = cid; ok && tile < tiles; tile += clusters, apar ^= 1u) {
+      // the tile before has handed the common columns back, the one before that its own
       if (!warp_wait<true>(smem_u32(acc_empty), apar ^ 1u, w, WAIT_MMA_ACC_EMPTY)) break;
+      if (tile >= cid + 2 * clusters && !warp_wait<true>(smem_u32(own_empty), apar, w, WAIT_MMA_ACC_EMPTY)) break;
       tc_fence_after();
+      const uint32_t d = tmem + (apar != 0u ? (uint32_t)kOwn : 0u);
       for (int32_t kb = 0; kb < p.blocks; ++kb) {
         // (the copier saw the stage land, so this covers the operands too)
         if (!warp_wait(smem_u32(ready + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
         tc_fence_after();
         const uint32_t st = smem_u32(ring + stage * kStage<NV>);
         const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(st + kOperand);
-        const uint32_t sf = tmem + kScaleCol + stage * kSlot<NV>;
+        const uint32_t sf = tmem + kScaleCol + slot * kSlot<NV>;
+        if (++slot == kSlots<NV>) slot = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t j = fp4_scale_block<NV>(k);
           if (4 * kb + k < p.steps)
-            mma_fp4<2, NV>(issue, tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * j,
+            mma_fp4<2, NV>(issue, d, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * j,
                            sf + 4u * NB + 8u * j, (uint32_t)(kb | k));
         }
         if (issue) mma_commit_pair(smem_u32(empty + stage), 3u);
+        __syncwarp();
         if (++stage == S) { stage = 0; sphase ^= 1u; }
       }
       if (!ok) break;
       if (issue) mma_commit_pair(smem_u32(acc_full), 3u);
+      __syncwarp();
     }
-    if (issue) {
-      // every MMA this thread issued must be complete before TMEM is released
-      mma_commit_cg<2>(smem_u32(drain_bar));
-      const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
-      mbar_wait(smem_u32(drain_bar), 0, wd, WAIT_DRAIN);
-    }
+    // every MMA this warp issued must be complete before TMEM is released
+    if (issue) mma_commit_cg<2>(smem_u32(drain_bar));
+    const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
+    warp_wait(smem_u32(drain_bar), 0, wd, WAIT_DRAIN);
   } else if ((warp == 2 || warp == 3) && leader) {
     // ---------------------------------------------------------- scale copies
     const uint32_t issue = elect_lane();
     const uint32_t part = warp - 2u;  // each of the two warps takes half of the blocks
-    uint32_t stage = 0, sphase = 0;
+    uint32_t stage = 0, sphase = 0, slot = 0, behind = 0, bphase = 0;
+    int64_t copied = 0;
     bool ok = true;
     for (int32_t tile = cid; ok && tile < tiles; tile += clusters) {
       for (int32_t kb = 0; kb < p.blocks; ++kb) {
-        // the stage's slot was last read by MMAs that completed before the stage was
-        // refilled, so it is free once the stage has landed
         if (!warp_wait(smem_u32(full + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
+        // The slot was last read by the MMAs of the stage kSlots before this one.  With more slots
+        // than stages those completed before this stage was refilled.
+        if (kSlots<NV> < S && copied >= (int64_t)kSlots<NV>) {
+          if (!warp_wait(smem_u32(empty + behind), bphase, w, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
+          if (++behind == S) { behind = 0; bphase ^= 1u; }
+        }
+        ++copied;
         tc_fence_after();
         const uint32_t from = smem_u32(ring + stage * kStage<NV> + kScalesAt);
-        const uint32_t to = tmem + kScaleCol + stage * kSlot<NV>;
+        const uint32_t to = tmem + kScaleCol + slot * kSlot<NV>;
+        if (++slot == kSlots<NV>) slot = 0;
 #pragma unroll
         for (uint32_t i = 0; i < NB / 2; ++i) {
           const uint32_t j = i + part * (NB / 2);
@@ -202,43 +233,70 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
           tmem_cp_32x128b_x4<2>(issue, to + 4u * NB + 8u * j + 4u, sdesc_rows16(from + 512u * (2u * NB + j)));
         }
         if (issue) mma_commit_cg<2>(smem_u32(ready + stage));
+        __syncwarp();
         if (++stage == S) { stage = 0; sphase ^= 1u; }
       }
     }
-    if (issue) {
-      // the copies this thread issued must be complete before TMEM is released
-      mma_commit_cg<2>(smem_u32(copy_drain));
-      const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
-      mbar_wait(smem_u32(copy_drain), 0, wd, WAIT_DRAIN);
-    }
+    // the copies both warps issued must be complete before TMEM is released
+    if (issue) mma_commit_cg<2>(smem_u32(copy_drain));
+    const WaitCtl wd{zero_word, p.status, p.timeout_ns, 0};
+    warp_wait(smem_u32(copy_drain), 0, wd, WAIT_DRAIN);
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const uint32_t q = warp & 3u;           // TMEM lane quarter
-    const uint32_t half = (warp - 4u) >> 2;  // columns 0-127 or 128-255
-    float* mine = staging + (warp - 4u) * 32u * 33u;
-    uint32_t apar = 0;
+    // Four of the eight runs of 32 columns a warp: of the five in common with the next tile (first
+    // `common`, which lie at the tile's end in even tiles, at its start in odd ones) group 0 takes
+    // three, of the three others one.
+    const uint32_t q = warp & 3u;  // TMEM lane quarter
+    const uint32_t group = (warp - 4u) >> 2;
+    uint8_t* mine = staging + (warp - 4u) * 4096u;
+    const int32_t thread = (int32_t)threadIdx.x - 128;
+    uint32_t apar = 0, buffer = 0;
+    bool dead = false;
     for (int32_t tile = cid; tile < tiles; tile += clusters, apar ^= 1u) {
       int32_t tm, tn;
       raster_tile(tile, p.tiles_m, p.tiles_n, p.raster_group, tm, tn);
       const int32_t row0 = tm * 256 + (int32_t)(rank * 128u + q * 32u), row = row0 + (int32_t)lane;
+      const int32_t col0 = tn * 256;
       const float sa = p.e.row_scale_a != nullptr && row < p.e.M ? __ldg(p.e.row_scale_a + row) : 1.f;
-      uint32_t got = 1;
-      if (lane == 0) got = mbar_wait(smem_u32(acc_full), apar, w, WAIT_EPI_ACC_FULL) ? 1u : 0u;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) break;
+      const bool in = col0 + thread < p.e.N;
+      const float cs = in && p.e.row_scale_b != nullptr ? __ldg(p.e.row_scale_b + col0 + thread) : 1.f;
+      const float cb = in && p.e.bias != nullptr ? __ldg(p.e.bias + col0 + thread) : 0.f;
+      epilogue_sync();  // (the tile before is done with the columns)
+      columns[thread] = cs;
+      columns[256 + thread] = cb;
+      epilogue_sync();
+      // (a warp that gave up still meets the others at every tile's barriers)
+      dead = dead || !warp_wait(smem_u32(acc_full), apar, w, WAIT_EPI_ACC_FULL);
+      if (dead) continue;
       tc_fence_after();
-      uint32_t v[4][32];
-      const uint32_t at = tmem + ((q * 32u) << 16) + half * 128u;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) tmem_ld_32x32b_x32(at + 32u * s, v[s]);
+      const uint32_t acc = tmem + ((q * 32u) << 16) + (apar != 0u ? (uint32_t)kOwn : 0u);
+      const int32_t common = (apar != 0u ? 0 : kOwn) + 96 * (int32_t)group;
+      const int32_t own = (apar != 0u ? 256 - kOwn : 0) + 32 * (int32_t)group;
+      auto hand_back = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(smem_u32(bar), 0));
+      };
+      auto store = [&](const uint32_t(&v)[32], int32_t c) {
+        fp4_store32<OutT>(p.e, &tmC, v, row0, col0 + c, sa, columns + c, columns + 256 + c, mine, buffer, lane);
+      };
+      uint32_t v0[32], v1[32], v2[32];
+      tmem_ld_32x32b_x32(acc + (uint32_t)common, v0);
+      tmem_ld_32x32b_x32(acc + (uint32_t)common + 32u, v1);
+      if (group == 0) tmem_ld_32x32b_x32(acc + (uint32_t)common + 64u, v2);
       tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(acc_empty), 0));
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        fp4_store32<OutT>(p.e, v[s], row0, tn * 256 + (int32_t)half * 128 + 32 * s, sa, mine, lane);
+      hand_back(acc_empty);
+      store(v0, common);
+      store(v1, common + 32);
+      if (group == 0) store(v2, common + 64);
+      tmem_ld_32x32b_x32(acc + (uint32_t)own, v0);
+      if (group != 0) tmem_ld_32x32b_x32(acc + (uint32_t)own + 32u, v1);
+      tmem_wait_ld();
+      hand_back(own_empty);
+      store(v0, own);
+      if (group != 0) store(v1, own + 32);
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
 
   // ---------------------------------------------------------------- teardown
@@ -265,7 +323,7 @@ const void* fp4_pair_kernel(bool nv, bool out_f32) {
 
 int fp4_pair_stages(bool nv) { return nv ? stages_of<true>() : stages_of<false>(); }
 size_t fp4_pair_smem(bool nv) {
-  return 1024 + (size_t)fp4_pair_stages(nv) * (nv ? kStage<true> : kStage<false>) + kStaging + kCtrl;
+  return nv ? smem_of<true>(stages_of<true>()) : smem_of<false>(stages_of<false>());
 }
 
 }  // namespace dgb

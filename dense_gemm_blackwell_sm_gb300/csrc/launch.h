@@ -51,6 +51,9 @@ bool encode_byte_rows(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint6
 bool encode_scale_blocks(CUtensorMap* m, const void* ptr, uint64_t k_blocks, uint64_t row_blocks, uint32_t box_k,
                          uint32_t box_rows);
 
+// TMA map of an output's tiles of 32 x 32 elements, fp32 (swizzled over 128 bytes) or bf16 (over 64)
+bool encode_out_tiles(CUtensorMap* m, bool f32, const void* ptr, uint64_t cols, uint64_t rows, uint64_t pitch);
+
 // steps 1-3 (thread copies), 4-5 (TMA ring), 6 (persistent + scheduler)
 cudaError_t spec_step123(int M, int N, bool out_f32, LaunchSpec* out);
 cudaError_t spec_step45(int M, int N, int stages, bool out_f32, LaunchSpec* out);

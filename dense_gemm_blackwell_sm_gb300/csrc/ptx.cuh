@@ -62,6 +62,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
+// The same for a hand-off that passes no memory, such as TMEM columns read with tcgen05.ld: the
+// release is of this CTA's scope (of the cluster's it waits for the thread's stores on their way,
+// about 2000 clocks behind a tile's stores).
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // arrive once and raise the expected transaction byte count of the phase
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile(
