@@ -8,6 +8,7 @@
 //
 // Bound by memory: 2 bytes read per element, 0.56 to 1.03 written.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "quant_format.cuh"
@@ -53,32 +54,83 @@ __device__ __forceinline__ uint4 load_piece(const QuantColumnsParams& p, int64_t
   return piece.u;
 }
 
+// Whether rows r0 .. r0 + n and columns c0 .. c0 + 63 are whole and aligned
+__device__ __forceinline__ bool inside(const QuantColumnsParams& p, int64_t r0, int64_t n, int64_t c0) {
+  return p.vec != 0 && r0 + n <= p.rows && c0 + kTileCols <= p.cols;
+}
+
+// largest magnitudes of 16 bytes of values, pairs at a time for 16-bit types
+template <typename T>
+struct Most {
+  static constexpr int n = 16 / (int)sizeof(T);
+  float v[n];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < n; ++j) v[j] = 0.f;
+  }
+  __device__ __forceinline__ void take(const uint4& u) {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int j = 0; j < n; ++j) v[j] = larger(v[j], to_f32(e[j]));
+  }
+  __device__ __forceinline__ float at(int j) const { return v[j]; }
+};
+template <typename T, typename T2>
+struct MostPairs {
+  static constexpr int n = 8;
+  T2 v[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t zero = 0u;
+      v[j] = *reinterpret_cast<const T2*>(&zero);
+    }
+  }
+  __device__ __forceinline__ void take(const uint4& u) {
+    const T2* e = reinterpret_cast<const T2*>(&u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __hmax2_nan(v[j], __habs2(e[j]));
+  }
+  __device__ __forceinline__ float at(int j) const { return to_f32(reinterpret_cast<const T*>(v)[j]); }
+};
+template <>
+struct Most<__half> : MostPairs<__half, __half2> {};
+template <>
+struct Most<__nv_bfloat16> : MostPairs<__nv_bfloat16, __nv_bfloat162> {};
+
 // the largest magnitudes of part blockIdx.y of 64 columns
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_quant_column_most(const QuantColumnsParams p) {
-  constexpr int n = 16 / (int)sizeof(T), across = kTileCols / n, down = kThreads / across;
+  constexpr int n = 16 / (int)sizeof(T), across = kTileCols / n, down = kThreads / across, U = 8;
   __shared__ float found[down][kTileCols + 1];
   wait_for_prior_kernel();
   let_next_kernel_start();
   const int tx = (int)threadIdx.x % across, ty = (int)threadIdx.x / across;
   const int64_t c0 = (int64_t)blockIdx.x * kTileCols;
   const int64_t r0 = blockIdx.y * p.part_rows, r1 = min(p.rows, r0 + p.part_rows);
-  float most[n];
+  Most<T> most;
+  most.clear();
+  int64_t r = r0 + ty;
+  if (inside(p, 0, 0, c0)) {
+    // eight rows of a thread on their way at once
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.x) + r * p.ld_x + c0 + tx * n);
+    const int64_t step = (int64_t)down * p.ld_x / n;
+    for (; r + (U - 1) * down < r1; r += U * down, from += U * step) {
+      uint4 u[U];
 #pragma unroll
-  for (int j = 0; j < n; ++j) most[j] = 0.f;
-#pragma unroll 4
-  for (int64_t r = r0 + ty; r < r1; r += down) {
-    const uint4 u = load_piece<T>(p, r, c0 + tx * n);
-    const T* e = reinterpret_cast<const T*>(&u);
+      for (int i = 0; i < U; ++i) u[i] = __ldg(from + i * step);
 #pragma unroll
-    for (int j = 0; j < n; ++j) most[j] = larger(most[j], to_f32(e[j]));
+      for (int i = 0; i < U; ++i) most.take(u[i]);
+    }
   }
+  for (; r < r1; r += down) most.take(load_piece<T>(p, r, c0 + tx * n));
 #pragma unroll
-  for (int j = 0; j < n; ++j) found[ty][tx * n + j] = most[j];
+  for (int j = 0; j < n; ++j) found[ty][tx * n + j] = most.at(j);
   __syncthreads();
   const int64_t c = c0 + threadIdx.x;
   if (threadIdx.x < kTileCols && c < p.cols) {
     float m = 0.f;
+#pragma unroll
     for (int i = 0; i < down; ++i) m = larger(m, found[i][threadIdx.x]);
     p.most[blockIdx.y * p.cols + c] = m;
   }
@@ -88,7 +140,7 @@ template <typename T>
 constexpr int kPitch = kTileCols + (sizeof(T) == 2 ? 8 : 4);  // elements: 16-byte pieces, lanes on different banks
 
 template <typename T, int F>
-__global__ void __launch_bounds__(kThreads) k_quant_columns(const QuantColumnsParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quant_columns(const QuantColumnsParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   T* tile = reinterpret_cast<T*>(smem);
   __shared__ uint8_t bytes[kTileCols][16];
@@ -100,15 +152,29 @@ __global__ void __launch_bounds__(kThreads) k_quant_columns(const QuantColumnsPa
   const int64_t c0 = strip * kTileCols, r0 = row_tile * kTileRows;
   {
     const int tx = (int)threadIdx.x % across, ty = (int)threadIdx.x / across;
-#pragma unroll 4
-    for (int r = ty; r < kTileRows; r += down)
-      *reinterpret_cast<uint4*>(tile + r * kPitch<T> + tx * n) = load_piece<T>(p, r0 + r, c0 + tx * n);
+    if (inside(p, r0, kTileRows, c0)) {
+      constexpr int U = 8;
+      const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.x) + (r0 + ty) * p.ld_x + c0 + tx * n);
+      const int64_t step = (int64_t)down * p.ld_x / n;
+#pragma unroll 1
+      for (int r = ty; r < kTileRows; r += U * down, from += U * step) {
+        uint4 u[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) u[i] = __ldg(from + i * step);
+#pragma unroll
+        for (int i = 0; i < U; ++i) *reinterpret_cast<uint4*>(tile + (r + i * down) * kPitch<T> + tx * n) = u[i];
+      }
+    } else {
+      for (int r = ty; r < kTileRows; r += down)
+        *reinterpret_cast<uint4*>(tile + r * kPitch<T> + tx * n) = load_piece<T>(p, r0 + r, c0 + tx * n);
+    }
   }
   if (threadIdx.x < kTileCols) {
     float most = 0.f;
     if constexpr (kRowScaled<F>) {
       const int64_t c = c0 + threadIdx.x;
       if (c < p.cols)
+#pragma unroll 8
         for (int i = 0; i < p.parts; ++i) most = larger(most, p.most[i * p.cols + c]);
       units[threadIdx.x] = row_unit<F>(most);
       if (row_tile == 0 && c < p.cols) p.row_scale[c] = units[threadIdx.x].scale;
@@ -119,29 +185,49 @@ __global__ void __launch_bounds__(kThreads) k_quant_columns(const QuantColumnsPa
   __syncthreads();
   const int warp = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
   const int64_t k0 = r0 + warp * 32;  // the operand's first column of this warp
-#pragma unroll 1
+  using Two = typename std::conditional<sizeof(T) == 2, uint32_t, float2>::type;
+  Two both[32];  // two columns of a lane
+#pragma unroll
+  for (int j = 0; j < 32; ++j) both[j] = *reinterpret_cast<const Two*>(tile + (warp * 32 + j) * kPitch<T> + 2 * lane);
+  float most[2][2];  // of either 16 rows, of either column
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      T2 m = __habs2(reinterpret_cast<const T2&>(both[16 * i]));
+#pragma unroll
+      for (int j = 1; j < 16; ++j) m = __hmax2_nan(m, __habs2(reinterpret_cast<const T2&>(both[16 * i + j])));
+      most[i][0] = to_f32(m.x);
+      most[i][1] = to_f32(m.y);
+    } else {
+      most[i][0] = most[i][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        most[i][0] = larger(most[i][0], both[16 * i + j].x);
+        most[i][1] = larger(most[i][1], both[16 * i + j].y);
+      }
+    }
+  }
+#pragma unroll
   for (int half = 0; half < 2; ++half) {
     const int col = 2 * lane + half;
     const int64_t c = c0 + col;
     const RowUnit row = units[col];
-    float v[2][16];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = to_f32(tile[(warp * 32 + j) * kPitch<T> + col]);
-    float most[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < 32; ++j) most[j / 16] = larger(most[j / 16], v[j / 16][j % 16]);
-    if constexpr (kBlock<F> == 32) most[0] = most[1] = larger(most[0], most[1]);
+    const bool in = c < p.cols && k0 < p.width;
+    if constexpr (kBlock<F> == 32) most[0][half] = most[1][half] = larger(most[0][half], most[1][half]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       BlockUnit b{0u, row.inv, 1.f};
       if constexpr (kBlock<F> != 0) {
-        b = block_unit<F>(most[i], row);
-        const bool in = c < p.cols && k0 < p.width;
+        b = block_unit<F>(most[i][half], row);
         if constexpr (kBlock<F> == 16) bytes[col][2 * warp + i] = (uint8_t)(in ? b.byte : 0u);
         if (kBlock<F> == 32 && i == 0) bytes[col][warp] = (uint8_t)(in ? b.byte : 0u);
       }
-      if (c < p.cols && k0 < p.width)
-        store_codes<F, sizeof(T) == 4>(p.data + c * p.ld_data + (kFourBit<F> ? (k0 + 16 * i) / 2 : k0 + 16 * i), v[i], row, b);
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = to_f32(reinterpret_cast<const T*>(&both[16 * i + j])[half]);
+      if (in)
+        store_codes<F, sizeof(T) == 4>(p.data + c * p.ld_data + (kFourBit<F> ? (k0 + 16 * i) / 2 : k0 + 16 * i), v, row, b);
     }
   }
   if constexpr (kBlock<F> != 0) {
