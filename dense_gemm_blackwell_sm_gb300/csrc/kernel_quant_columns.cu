@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_quant_colu
     for (int i = 0; i < 2; ++i) {
       BlockUnit b{0u, row.inv, 1.f};
       if constexpr (kBlock<F> != 0) {
-        b = block_unit<F>(most[i][half], row);
+        b = block_unit<F, sizeof(T) == 4>(most[i][half], row);
         if constexpr (kBlock<F> == 16) bytes[col][2 * warp + i] = (uint8_t)(in ? b.byte : 0u);
         if (kBlock<F> == 32 && i == 0) bytes[col][warp] = (uint8_t)(in ? b.byte : 0u);
       }

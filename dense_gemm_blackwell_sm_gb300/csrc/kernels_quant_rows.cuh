@@ -13,6 +13,8 @@
 // Bound by memory: 2 bytes read and 0.56 to 1.03 written per element (norm: 4 and 3.03).
 #pragma once
 
+#include <type_traits>
+
 #include "quant_format.cuh"
 
 namespace dgb {
@@ -47,8 +49,10 @@ struct Run {
   __device__ __forceinline__ float operator[](int j) const {
     if constexpr (sizeof(T) == 4) {
       return __uint_as_float(w[j]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+      return __uint_as_float((j & 1) ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
     } else {
-      return to_f32(reinterpret_cast<const T*>(w)[j]);
+      return __half2float(__ushort_as_half((unsigned short)((j & 1) ? w[j / 2] >> 16 : w[j / 2])));
     }
   }
   __device__ __forceinline__ void clear() {
@@ -106,9 +110,11 @@ __device__ __forceinline__ void store16(T* row, const float (&v)[16], int32_t co
     for (int j = 0; j < words; ++j) {
       if constexpr (sizeof(T) == 4) {
         w[j] = __float_as_uint(v[j]);
+      } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        w[j] = pack_bf16x2(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1]));
       } else {
-        reinterpret_cast<T*>(&w[j])[0] = from_f32<T>(v[2 * j]);
-        reinterpret_cast<T*>(&w[j])[1] = from_f32<T>(v[2 * j + 1]);
+        const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
     uint32_t* p = reinterpret_cast<uint32_t*>(row + col);
@@ -143,15 +149,15 @@ __device__ __forceinline__ float over_row(float v, Op op, float* shared) {
   const int warps = (int)blockDim.x / 32;
   float* mine = shared + threadIdx.y * warps;
   if ((threadIdx.x & 31u) == 0) mine[threadIdx.x / 32] = v;
-  __syncthreads();
+  asm volatile("barrier.sync %0, %1;" ::"r"(threadIdx.y + 1u), "r"(blockDim.x) : "memory");  // (the row's threads)
   v = mine[0];
   for (int i = 1; i < warps; ++i) v = op(v, mine[i]);
   return v;
 }
 
 template <typename T, int F, bool NORM, int NV>
-__global__ void __launch_bounds__(512) k_quant_rows(const QuantRowsParams p) {
-  constexpr bool AHEAD = NV <= 2;  // the next row's loads are under way while this one is worked on
+__global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 : 1) k_quant_rows(const QuantRowsParams p) {
+  constexpr bool AHEAD = NORM ? NV == 1 : NV <= 2;  // the next row's loads are under way while this one is worked on
   __shared__ float shared[2][2][16];
   wait_for_prior_kernel();
   let_next_kernel_start();
@@ -185,72 +191,84 @@ __global__ void __launch_bounds__(512) k_quant_rows(const QuantRowsParams p) {
     const int64_t r = r0 + threadIdx.y;
     const bool live = r < p.rows;
     if (!AHEAD) load(r, 0);
-    float v[NV][16];
+    float v[NV][16], most[NV];  // (and each run's largest magnitude)
     auto take = [&]() {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[i][j] = raw[i][j];
     };
-    auto largest = [&](float most) {
+    auto find = [&](float of_row) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) most = larger(most, v[i][j]);
-      return most;
+      for (int i = 0; i < NV; ++i) {
+        most[i] = largest16(v[i]);
+        of_row = larger(of_row, most[i]);
+      }
+      return of_row;
     };
     take();
     if constexpr (NORM) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[i][j] = fmaf(p.residual_scale, raw_res[i][j], v[i][j] * p.branch_scale);
+        for (int j = 0; j < 16; j += 2) {
+          mul2(v[i][j], v[i][j + 1], p.branch_scale, p.branch_scale);
+          fma2(v[i][j], v[i][j + 1], raw_res[i][j], raw_res[i][j + 1], p.residual_scale, p.residual_scale);
+        }
     }
     if (AHEAD && (NORM || p.chunks <= per)) load(r + step, 0);
     if constexpr (NORM) {
-      float sum = 0.f;
+      float sum = 0.f, sum1 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int32_t c = i * threads + tx;
         if (live && c < p.chunks && p.s != nullptr)
           store16<T>(reinterpret_cast<T*>(p.s) + r * p.ld_s, v[i], 16 * c, p.cols, p.vec);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+        for (int j = 0; j < 16; j += 2) fma2(sum, sum1, v[i][j], v[i][j + 1], v[i][j], v[i][j + 1]);
       }
-      sum = over_row(sum, Sum{}, shared[0][turn]);
+      auto weigh = [&]() {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int32_t c = i * threads + tx;
+          auto scale = [&](const auto& e) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) mul2(v[i][j], v[i][j + 1], e[j], e[j + 1]);
+          };
+          if (c >= p.chunks || p.weight == nullptr) continue;
+          if (p.weight_f32) {
+            Run<float> e;
+            load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec);
+            scale(e);
+          } else {
+            Run<T> e;
+            load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec);
+            scale(e);
+          }
+        }
+      };
+      // (the weight comes while the row's sum is found; 32-bit rows have no registers for that)
+      if (sizeof(T) == 2) weigh();
+      sum = over_row(sum + sum1, Sum{}, shared[0][turn]);
       const float unit = __frsqrt_rn(sum / (float)p.cols + p.eps);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int32_t c = i * threads + tx;
-        if (c >= p.chunks) continue;
-        if (p.weight == nullptr) {
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[i][j] *= unit;
-        } else if (p.weight_f32) {
-          Run<float> e;
-          load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * unit * e[j];
-        } else {
-          Run<T> e;
-          load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * unit * e[j];
-        }
-      }
+        for (int j = 0; j < 16; j += 2) mul2(v[i][j], v[i][j + 1], unit, unit);
+      if (sizeof(T) == 4) weigh();
     }
 
     RowUnit row = row_unit<F>(0.f);
     if constexpr (kRowScaled<F>) {
-      float most = largest(0.f);
+      float of_row = find(0.f);
       if constexpr (!NORM) {
         for (int32_t base = per; base < p.chunks; base += per) {
           load(r, base);
           take();
-          most = largest(most);
+          of_row = find(of_row);
         }
       }
-      row = row_unit<F>(over_row(most, Largest{}, shared[1][turn]));
+      row = row_unit<F>(over_row(of_row, Largest{}, shared[1][turn]));
       if (live && tx == 0) p.row_scale[r] = row.scale;
     }
 
@@ -258,17 +276,17 @@ __global__ void __launch_bounds__(512) k_quant_rows(const QuantRowsParams p) {
       if (!NORM && (base > 0 || (kRowScaled<F> && per < p.chunks))) {
         load(r, base);
         take();
+        if constexpr (kBlock<F> != 0) find(0.f);
+      } else if constexpr (kBlock<F> != 0 && !kRowScaled<F>) {
+        find(0.f);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int32_t c = base + i * threads + tx;
         BlockUnit b{0u, row.inv, 1.f};
         if constexpr (kBlock<F> != 0) {
-          float most = 0.f;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) most = larger(most, v[i][j]);
-          if constexpr (kBlock<F> == 32) most = larger(most, __shfl_xor_sync(0xffffffffu, most, 1));
-          b = block_unit<F>(most, row);
+          if constexpr (kBlock<F> == 32) most[i] = larger(most[i], __shfl_xor_sync(0xffffffffu, most[i], 1));
+          b = block_unit<F, sizeof(T) == 4 && !NORM>(most[i], row);
           // four scales, of four or eight threads, are stored together
           constexpr int lanes = 4 * kBlock<F> / 16;
           uint32_t word = live && c < p.chunks ? b.byte << (8 * ((c * 16 / kBlock<F>) & 3)) : 0u;

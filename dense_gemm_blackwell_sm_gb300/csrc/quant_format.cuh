@@ -17,12 +17,44 @@ inline constexpr int kBlock = F == QUANT_E4M3 ? 0 : F == QUANT_NVFP4 ? 16 : 32;
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// Two fp32 operations at once
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void mul2_rz(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+      "mul.rz.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+// (a, b) = (x, y) * (u, v) + (a, b)
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
+  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\tmov.b64 r, {%4, %5};\n\t"
+      "fma.rn.f32x2 p, q, r, p;\n\tmov.b64 {%0, %1}, p;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(u), "f"(v));
+}
+
 // The larger magnitude; a NaN wins.  (Magnitudes are kept as floats: a NaN or an infinity
 // among the values shows in the largest.)
 __device__ __forceinline__ float larger(float most, float v) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(most), "f"(fabsf(v)));
   return r;
+}
+__device__ __forceinline__ float larger(float most, float v, float w) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(most), "f"(v), "f"(w));
+  return r;
+}
+__device__ __forceinline__ float largest16(const float (&v)[16]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) m = larger(m, v[j], v[j + 1]);
+  return m;
 }
 __device__ __forceinline__ bool finite(float magnitude) { return __float_as_uint(magnitude) < kInfBits; }
 
@@ -91,7 +123,17 @@ struct BlockUnit {
   float inv;    // 0 where the values are to be 0
   float scale;  // NVFP4 in 32 bits: the scale, to divide by
 };
-template <int F>
+// The smallest float not below 1 / s, for s an E4M3 value above 0: one Newton step from the
+// approximate reciprocal (the nearest float to 1 / s), and up where that is below.
+__device__ __forceinline__ float reciprocal_up(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = fmaf(r, fmaf(-r, s, 1.f), r);
+  return fmaf(r, s, -1.f) < 0.f ? __uint_as_float(__float_as_uint(r) + 1u) : r;
+}
+
+// EXACT: for 32-bit inputs, whose quotients may lie nearer to a tie than a reciprocal is exact.
+template <int F, bool EXACT>
 __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) {
   BlockUnit b{0u, row.inv, 1.f};
   if constexpr (F == QUANT_MXE4M3 || F == QUANT_MXFP4) {
@@ -102,7 +144,9 @@ __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) 
     b.inv = pow2(-e);
     if (!finite(most)) b = {255u, 0.f, 1.f};
   } else if constexpr (F == QUANT_NVFP4) {
-    const float q = __fdiv_rn(most * row.inv, 6.f);
+    // (for 16-bit magnitudes a product with 1/6 rounded up, rounded towards zero, stays on a tie
+    // that the quotient is on: see below)
+    const float q = EXACT ? __fdiv_rn(most * row.inv, 6.f) : __fmul_rz(most * row.inv, 0.166666671633720397949f);
     uint32_t byte, half;
     asm("{\n\t.reg .b16 r;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 r, %2, %2;\n\t"
@@ -116,7 +160,7 @@ __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) 
     // the middle between two codes stays there (b * s * r is at least b and below b's
     // neighbour for every scale s and midpoint b), so that ties go to even as for the exact
     // quotient.  16-bit values that are no ties are 2^-11 from them at least.
-    b.inv = b.byte == 0u ? 0.f : __frcp_ru(b.scale) * row.inv;
+    b.inv = b.byte == 0u ? 0.f : reciprocal_up(b.scale) * row.inv;
     if (row.inv == 0.f) b = {0x7fu, 0.f, 1.f};
   }
   return b;
@@ -128,11 +172,16 @@ template <int F, bool EXACT>
 __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
   float t[16];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if constexpr (F == QUANT_NVFP4) {
-      t[j] = EXACT ? __fdiv_rn(v[j] * row.inv, b.scale) : __fmul_rz(v[j], b.inv);
+  for (int j = 0; j < 16; j += 2) {
+    t[j] = v[j];
+    t[j + 1] = v[j + 1];
+    if constexpr (F == QUANT_NVFP4 && EXACT) {
+      t[j] = __fdiv_rn(t[j] * row.inv, b.scale);
+      t[j + 1] = __fdiv_rn(t[j + 1] * row.inv, b.scale);
+    } else if constexpr (F == QUANT_NVFP4) {
+      mul2_rz(t[j], t[j + 1], b.inv, b.inv);
     } else {
-      t[j] = v[j] * b.inv;
+      mul2(t[j], t[j + 1], b.inv, b.inv);
     }
   }
   const bool zero = b.inv == 0.f;  // (an infinity times 0 is no 0)
