@@ -37,6 +37,9 @@ struct QuantRowsParams {
   int64_t ld_x, ld_residual, ld_s, ld_data;
   int32_t weight_f32;  // weight is fp32 (else the inputs' type)
   int32_t weight_vec;
+  const void* x_end;   // the first byte past the last element of x, of the residual, of the weight
+  const void* residual_end;
+  const void* weight_end;
   float eps, residual_scale, branch_scale;
 };
 
@@ -61,9 +64,13 @@ struct Run {
   }
 };
 
-// The columns from `col` on, zeros from column `cols` on (plain loads: s may be y or the residual).
+// The columns from `col` on, zeros from column `cols` on (plain loads: s may be y or the
+// residual).  Rows off a 16-byte boundary (vec 0) come as the 16-byte pieces that hold the run,
+// where those lie in the array [begin, end), and are shifted: 8192 x 4095 bf16 to MXFP8 takes
+// 37 us by single elements.
 template <typename T>
-__device__ __forceinline__ void load16(Run<T>& v, const T* row, int32_t col, int32_t cols, int32_t vec) {
+__device__ __forceinline__ void load16(Run<T>& v, const T* row, int32_t col, int32_t cols, int32_t vec,
+                                       const void* begin, const void* end) {
   constexpr int words = 4 * (int)sizeof(T);
   if (vec != 0 && col + 16 <= cols) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(row + col);
@@ -83,6 +90,34 @@ __device__ __forceinline__ void load16(Run<T>& v, const T* row, int32_t col, int
         v.w[j + 1] = u.y;
         v.w[j + 2] = u.z;
         v.w[j + 3] = u.w;
+      }
+    }
+    return;
+  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + col), first = at & ~(uintptr_t)15;
+  if (first >= reinterpret_cast<uintptr_t>(begin) && first + 16 * sizeof(T) + 16 <= reinterpret_cast<uintptr_t>(end)) {
+    uint32_t w[words + 4];
+#pragma unroll
+    for (int j = 0; j < words + 4; j += 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(first + 4 * j);
+      w[j] = u.x;
+      w[j + 1] = u.y;
+      w[j + 2] = u.z;
+      w[j + 3] = u.w;
+    }
+    const uint32_t off = (uint32_t)(at & 15u);
+#pragma unroll
+    for (int j = 0; j < words + 2; ++j) w[j] = (off & 8u) != 0u ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < words + 1; ++j) w[j] = (off & 4u) != 0u ? w[j + 1] : w[j];
+#pragma unroll
+    for (int j = 0; j < words; ++j) v.w[j] = sizeof(T) == 2 && (off & 2u) != 0u ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+    if (col + 16 > cols) {
+      constexpr int per = 4 / (int)sizeof(T);  // columns of a word
+#pragma unroll
+      for (int j = 0; j < words; ++j) {
+        if (col + per * j >= cols) v.w[j] = 0u;
+        else if (per == 2 && col + per * j + 1 >= cols) v.w[j] &= 0xffffu;
       }
     }
     return;
@@ -132,27 +167,32 @@ __device__ __forceinline__ void store16(T* row, const float (&v)[16], int32_t co
     if (col + j < cols) row[col + j] = from_f32<T>(v[j]);
 }
 
-struct Sum {
-  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-struct Largest {
-  __device__ __forceinline__ float operator()(float a, float b) const { return larger(a, b); }
-};
-
-// Over the threads of a row, in a fixed order.  Every thread of the CTA calls it; `shared` is
-// another one than in the call before.
-template <typename Op>
-__device__ __forceinline__ float over_row(float v, Op op, float* shared) {
+// A row's sum or largest magnitude from all its threads, in a fixed order.  Every thread of the
+// row calls it; `shared` (a float per warp of the CTA) is another one than in the call before.
+template <bool LARGEST>
+__device__ __forceinline__ float over_warp(float v, int lanes) {
+  if constexpr (LARGEST) {
+    // (magnitudes order as their bits do, a NaN above an infinity)
+    uint32_t r;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(__float_as_uint(v)));
+    return __uint_as_float(r);
+  } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1)
+      if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+}
+template <bool LARGEST>
+__device__ __forceinline__ float over_row(float v, float* shared) {
+  v = over_warp<LARGEST>(v, 32);
   if (blockDim.x == 32) return v;
-  const int warps = (int)blockDim.x / 32;
+  const uint32_t warps = blockDim.x / 32u, lane = threadIdx.x & 31u;
   float* mine = shared + threadIdx.y * warps;
-  if ((threadIdx.x & 31u) == 0) mine[threadIdx.x / 32] = v;
+  if (lane == 0) mine[threadIdx.x / 32u] = v;
   asm volatile("barrier.sync %0, %1;" ::"r"(threadIdx.y + 1u), "r"(blockDim.x) : "memory");  // (the row's threads)
-  v = mine[0];
-  for (int i = 1; i < warps; ++i) v = op(v, mine[i]);
-  return v;
+  // (at most 16 warps)
+  return over_warp<LARGEST>((lane & 15u) < warps ? mine[lane & 15u] : 0.f, 16);
 }
 
 template <typename T, int F, bool NORM, int NV>
@@ -172,11 +212,12 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
     for (int i = 0; i < NV; ++i) {
       const int32_t c = base + i * threads + tx;
       const bool in = r < p.rows && c < p.chunks;
-      if (in) load16<T>(raw[i], x, 16 * c, p.cols, p.vec);
+      if (in) load16<T>(raw[i], x, 16 * c, p.cols, p.vec, p.x, p.x_end);
       else raw[i].clear();
       if constexpr (NORM) {
         if (in && p.residual != nullptr) {
-          load16<T>(raw_res[i], reinterpret_cast<const T*>(p.residual) + r * p.ld_residual, 16 * c, p.cols, p.vec);
+          load16<T>(raw_res[i], reinterpret_cast<const T*>(p.residual) + r * p.ld_residual, 16 * c, p.cols, p.vec,
+                    p.residual, p.residual_end);
         } else {
           raw_res[i].clear();
         }
@@ -238,18 +279,18 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
           if (c >= p.chunks || p.weight == nullptr) continue;
           if (p.weight_f32) {
             Run<float> e;
-            load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec);
+            load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
             scale(e);
           } else {
             Run<T> e;
-            load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec);
+            load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
             scale(e);
           }
         }
       };
       // (the weight comes while the row's sum is found; 32-bit rows have no registers for that)
       if (sizeof(T) == 2) weigh();
-      sum = over_row(sum + sum1, Sum{}, shared[0][turn]);
+      sum = over_row<false>(sum + sum1, shared[0][turn]);
       const float unit = __frsqrt_rn(sum / (float)p.cols + p.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -268,7 +309,7 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
           of_row = find(of_row);
         }
       }
-      row = row_unit<F>(over_row(of_row, Largest{}, shared[1][turn]));
+      row = row_unit<F>(over_row<true>(of_row, shared[1][turn]));
       if (live && tx == 0) p.row_scale[r] = row.scale;
     }
 
