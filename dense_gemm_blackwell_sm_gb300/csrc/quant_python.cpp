@@ -1,80 +1,141 @@
 // quant_python.cpp -- what quant.py calls: checks of the tensors, allocation of the outputs and
 // the calls of include/quant.h, as a Python extension (see ffn_python.cpp for the reason).
 //
-// A quantised operand travels as five values: data, scales or None, row_scale or None, format
-// code, columns.
+// A quantised operand travels as five values: data, scales or None, row_scale or None, format,
+// columns.  Its arrays are one allocation: an allocation costs a third of a small call.
+#include <ATen/cuda/EmptyTensor.h>
+
 #include "python_calls.h"
 #include "quant.h"
 
 namespace {
 
+PyObject* format_codes = nullptr;  // {name: code}
+PyObject* format_names = nullptr;  // names by code
+
 struct Operand {
-  Tensor data, scales, row_scale;
-  int64_t rows = 0, cols = 0, ld = 0;
+  Tensor memory;  // of a new operand; a given one has its tensors'
+  Tensor data_tensor, scales_tensor, row_scale_tensor;
+  uint8_t* data = nullptr;
+  uint8_t* scales = nullptr;
+  float* row_scale = nullptr;
+  int64_t rows = 0, cols = 0, ld = 0, scale_bytes = 0;
   int32_t format = 0;
   int index = 0;
 };
 
-at::ScalarType data_type(int32_t format) {
-  return format == QUANT_E4M3 || format == QUANT_MXE4M3 ? at::kFloat8_e4m3fn : at::kByte;
+// a format's name, or its code
+int32_t format_of(PyObject* o) {
+  if (!PyLong_Check(o)) {
+    PyObject* code = PyDict_GetItemWithError(format_codes, o);
+    if (code == nullptr) {
+      if (PyErr_Occurred()) throw python_error();
+      TORCH_CHECK_VALUE(false, "format must be one of e4m3, mxe4m3, mxfp4, nvfp4");
+    }
+    o = code;
+  }
+  const int64_t f = int_of(o);
+  TORCH_CHECK_VALUE(f >= QUANT_E4M3 && f <= QUANT_NVFP4, "unknown format ", f);
+  return (int32_t)f;
 }
 
-Tensor empty_flat(int64_t n, at::ScalarType dtype, int index) {
-  return at::empty({n}, at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)index));
+bool has_scales(int32_t format) { return format != QUANT_E4M3; }
+bool has_row_scale(int32_t format) { return format == QUANT_E4M3 || format == QUANT_NVFP4; }
+
+Tensor new_tensor(at::IntArrayRef sizes, at::ScalarType dtype, int index) {
+  return Tensor(at::detail::empty_cuda(sizes, dtype, at::Device(at::kCUDA, (c10::DeviceIndex)index), std::nullopt));
+}
+Tensor new_rows(int64_t M, int64_t N, at::ScalarType dtype, int index) { return new_tensor({M, N}, dtype, index); }
+
+// `sizes` values of `memory` from byte `offset` on, as a tensor
+Tensor part_of(const Tensor& memory, int64_t offset, at::ScalarType dtype, at::IntArrayRef sizes) {
+  Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(memory.storage()), memory.key_set(),
+                                                      c10::scalarTypeToTypeMeta(dtype));
+  c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  impl->set_storage_offset(offset / (int64_t)c10::elementSize(dtype));
+  impl->set_sizes_contiguous(sizes);
+  return t;
 }
 
-// the operand of `rows` rows of `cols` values, allocated
-Operand empty_operand(int64_t rows, int64_t cols, int32_t format, int index) {
+int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
+
+// the operand of `rows` rows of `cols` values, allocated, with `more` bytes behind it
+Operand empty_operand(int64_t rows, int64_t cols, int32_t format, int index, int64_t more = 0) {
   Operand o;
   o.rows = rows;
   o.cols = cols;
   o.format = format;
   o.index = index;
-  const int64_t bytes = quant_row_bytes(cols, format), scales = quant_scale_bytes(rows, cols, format);
-  TORCH_CHECK_VALUE(bytes >= 0 && scales >= 0, "rows of ", cols, " values are too long");
+  const int64_t bytes = quant_row_bytes(cols, format);
+  o.scale_bytes = quant_scale_bytes(rows, cols, format);
+  TORCH_CHECK_VALUE(bytes >= 0 && o.scale_bytes >= 0, "rows of ", cols, " values are too long");
   o.ld = bytes;
-  o.data = empty_rows(rows, bytes, data_type(format), index);
-  if (format != QUANT_E4M3) o.scales = empty_flat(scales, at::kByte, index);
-  if (format == QUANT_E4M3 || format == QUANT_NVFP4) o.row_scale = empty_flat(rows, at::kFloat, index);
+  const int64_t scales_at = round_up(rows * bytes), row_scale_at = scales_at + round_up(o.scale_bytes);
+  const int64_t more_at = row_scale_at + (has_row_scale(format) ? round_up(4 * rows) : 0);
+  // (an array of no bytes has an address all the same)
+  o.memory = new_tensor({more_at + more + 16}, at::kByte, index);
+  uint8_t* base = static_cast<uint8_t*>(o.memory.data_ptr());
+  o.data = base;
+  if (has_scales(format)) o.scales = base + scales_at;
+  if (has_row_scale(format)) o.row_scale = reinterpret_cast<float*>(base + row_scale_at);
   return o;
+}
+void* behind(const Operand& o) {
+  const int64_t at = round_up(o.rows * o.ld) + round_up(o.scale_bytes) + (has_row_scale(o.format) ? round_up(4 * o.rows) : 0);
+  return static_cast<uint8_t*>(o.memory.data_ptr()) + at;
 }
 
 // a given operand: p points at its five values
 Operand operand_of(const char* name, PyObject* const* p) {
   Operand o;
-  o.data = tensor_of(p[0], name);
+  const Tensor& data = o.data_tensor = tensor_of(p[0], name);
   const Tensor *scales = optional_of(p[1], name), *row_scale = optional_of(p[2], name);
-  o.format = (int32_t)int_of(p[3]);
+  o.format = format_of(p[3]);
   o.cols = int_of(p[4]);
   TORCH_CHECK_VALUE(o.format == QUANT_MXFP4 || o.format == QUANT_NVFP4, name, " must be a 4-bit operand (mxfp4 or nvfp4)");
-  o.index = index_of(o.data);
-  TORCH_CHECK_VALUE(o.data.dim() == 2, name, "'s data must be a 2-D tensor, not ", o.data.sizes());
-  o.rows = o.data.size(0);
+  o.index = index_of(data);
+  TORCH_CHECK_VALUE(data.dim() == 2, name, "'s data must be a 2-D tensor, not ", data.sizes());
+  o.rows = data.size(0);
   const int64_t bytes = quant_row_bytes(o.cols, o.format);
   TORCH_CHECK_VALUE(bytes >= 0, name, " has ", o.cols, " columns");
-  o.ld = rows_of(name, o.data, o.rows, bytes, at::kByte, o.index);
+  o.ld = rows_of(name, data, o.rows, bytes, at::kByte, o.index);
   const int64_t want = quant_scale_bytes(o.rows, o.cols, o.format);
   TORCH_CHECK_VALUE(scales != nullptr && scales->scalar_type() == at::kByte && scales->is_contiguous() &&
                         scales->numel() == want && scales->is_cuda() && scales->get_device() == o.index,
                     name, "'s scales must be ", want, " dense bytes on cuda:", o.index);
-  o.scales = *scales;
+  o.scales_tensor = *scales;
+  o.data = static_cast<uint8_t*>(data.data_ptr());
+  o.scales = static_cast<uint8_t*>(scales->data_ptr());
   if (row_scale != nullptr) {
     TORCH_CHECK_VALUE(row_scale->scalar_type() == at::kFloat && row_scale->is_contiguous() && row_scale->dim() == 1 &&
                           row_scale->size(0) == o.rows && row_scale->is_cuda() && row_scale->get_device() == o.index,
                       name, "'s row scales must be ", o.rows, " dense values of float32 on cuda:", o.index);
-    o.row_scale = *row_scale;
+    o.row_scale_tensor = *row_scale;
+    o.row_scale = static_cast<float*>(row_scale->data_ptr());
   }
   return o;
 }
 
-void* pointer(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
-
-PyObject* operand_tuple(const Operand& o) { return tuple_of({&o.data, &o.scales, &o.row_scale}); }
-
-int32_t format_of(PyObject* o) {
-  const int64_t f = int_of(o);
-  TORCH_CHECK_VALUE(f >= QUANT_E4M3 && f <= QUANT_NVFP4, "unknown format ", f);
-  return (int32_t)f;
+// the five values of a new operand
+PyObject* operand_tuple(const Operand& o, const Tensor* first = nullptr) {
+  const bool four = o.format == QUANT_MXFP4 || o.format == QUANT_NVFP4;
+  const uint8_t* base = static_cast<const uint8_t*>(o.memory.data_ptr());
+  const Tensor data = part_of(o.memory, 0, four ? at::kByte : at::kFloat8_e4m3fn, {o.rows, o.ld});
+  Tensor scales, row_scale;
+  if (o.scales) scales = part_of(o.memory, o.scales - base, at::kByte, {o.scale_bytes});
+  if (o.row_scale) row_scale = part_of(o.memory, reinterpret_cast<const uint8_t*>(o.row_scale) - base, at::kFloat, {o.rows});
+  const Py_ssize_t n = first != nullptr ? 1 : 0;
+  THPObjectPtr out(PyTuple_New(5 + n));
+  if (!out) throw python_error();
+  if (first != nullptr) PyTuple_SET_ITEM(out.get(), 0, wrapped(*first));
+  PyTuple_SET_ITEM(out.get(), n, wrapped(data));
+  PyTuple_SET_ITEM(out.get(), n + 1, wrapped(scales));
+  PyTuple_SET_ITEM(out.get(), n + 2, wrapped(row_scale));
+  PyTuple_SET_ITEM(out.get(), n + 3, Py_NewRef(PyTuple_GET_ITEM(format_names, o.format)));
+  PyObject* cols = PyLong_FromLongLong(o.cols);
+  if (cols == nullptr) throw python_error();
+  PyTuple_SET_ITEM(out.get(), n + 4, cols);
+  return out.release();
 }
 
 // x's rows or columns, quantised
@@ -90,14 +151,15 @@ Operand quantised(const char* name, const Tensor& x, int32_t format, bool transp
   a.format = format;
   a.transpose = transpose;
   a.ld_x = rows_of(name, x, a.rows, a.cols, dtype, index);
-  Operand o = empty_operand(transpose ? a.cols : a.rows, transpose ? a.rows : a.cols, format, index);
+  // (a refused call asks for -1 bytes and is refused when it is made)
+  const int64_t workspace = std::max<int64_t>(0, quant_rows_workspace(&a));
+  Operand o = empty_operand(transpose ? a.cols : a.rows, transpose ? a.rows : a.cols, format, index, workspace);
   a.x = x.data_ptr();
-  a.data = pointer(o.data);
-  a.scales = pointer(o.scales);
-  a.row_scale = static_cast<float*>(pointer(o.row_scale));
-  const Tensor workspace = workspace_of(quant_rows_workspace(&a), index);
-  a.workspace = pointer(workspace);
-  call(quant_rows, "quant_rows", a, index, stream, {&o.data, &o.scales, &o.row_scale, &workspace});
+  a.data = o.data;
+  a.scales = o.scales;
+  a.row_scale = o.row_scale;
+  a.workspace = behind(o);
+  call(quant_rows, "quant_rows", a, index, stream, {&o.memory});
   return o;
 }
 
@@ -122,12 +184,12 @@ Tensor multiplied(const Operand& a, const Operand& b, const Finish& f, PyObject*
   p.out_dtype = code_of(f.dtype);
   p.activation = f.activation;
   p.flags = f.flags;
-  p.a = pointer(a.data);
-  p.b = pointer(b.data);
-  p.scales_a = pointer(a.scales);
-  p.scales_b = pointer(b.scales);
-  p.row_scale_a = static_cast<const float*>(pointer(a.row_scale));
-  p.row_scale_b = static_cast<const float*>(pointer(b.row_scale));
+  p.a = a.data;
+  p.b = b.data;
+  p.scales_a = a.scales;
+  p.scales_b = b.scales;
+  p.row_scale_a = a.row_scale;
+  p.row_scale_b = b.row_scale;
   if (f.bias != nullptr) {
     TORCH_CHECK_VALUE(f.bias->dim() == 1 && f.bias->size(0) == p.N && f.bias->scalar_type() == at::kFloat &&
                           f.bias->is_contiguous() && f.bias->is_cuda() && f.bias->get_device() == a.index,
@@ -143,7 +205,7 @@ Tensor multiplied(const Operand& a, const Operand& b, const Finish& f, PyObject*
     p.ld_c = rows_of("out", *f.out, p.M, p.N, f.dtype, a.index);
     c = *f.out;
   } else {
-    c = empty_rows(p.M, p.N, f.dtype, a.index);
+    c = new_rows(p.M, p.N, f.dtype, a.index);
   }
   p.c = c.data_ptr();
   p.ld_a = a.ld;
@@ -170,7 +232,7 @@ Finish finish_of(PyObject* const* p) {
   return f;
 }
 
-// (x, format, transpose, stream) -> (data, scales, row_scale)
+// (x, format, transpose, stream) -> an operand's five values
 PyObject* quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 4);
@@ -179,7 +241,7 @@ PyObject* quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
 }
 
 // (y, residual, weight, format, eps, residual_scale, branch_scale, need_s, s, stream)
-// -> (s or None, data, scales, row_scale)
+// -> (s or None, an operand's five values)
 PyObject* norm_quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 10);
@@ -212,18 +274,18 @@ PyObject* norm_quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
     a.ld_s = rows_of("s", *s_given, a.M, a.D, dtype, index);
     s = *s_given;
   } else if (flag_of(p[7])) {
-    s = empty_rows(a.M, a.D, dtype, index);
+    s = new_rows(a.M, a.D, dtype, index);
   }
   Operand o = empty_operand(a.M, a.D, a.format, index);
   a.y = y.data_ptr();
   a.residual = data_of(residual);
   a.weight = data_of(weight);
-  a.s = pointer(s);
-  a.data = pointer(o.data);
-  a.scales = pointer(o.scales);
-  a.row_scale = static_cast<float*>(pointer(o.row_scale));
-  call(quant_norm, "quant_norm", a, index, p[9], {&s, &o.data, &o.scales, &o.row_scale});
-  return tuple_of({&s, &o.data, &o.scales, &o.row_scale});
+  a.s = s.defined() ? s.data_ptr() : nullptr;
+  a.data = o.data;
+  a.scales = o.scales;
+  a.row_scale = o.row_scale;
+  call(quant_norm, "quant_norm", a, index, p[9], {&s, &o.memory});
+  return operand_tuple(o, &s);
   END_HANDLE_TH_ERRORS
 }
 
@@ -278,7 +340,18 @@ PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-PyMethodDef methods[] = {method<bind>("bind"),       method<quantise>("quantise"), method<norm_quantise>("norm_quantise"),
+// (GemmError, share, {name: code}, names by code)
+PyObject* bind_formats(PyObject* self, PyObject* const* p, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect(n, 4);
+  TORCH_CHECK_TYPE(PyDict_Check(p[2]) && PyTuple_Check(p[3]) && PyTuple_GET_SIZE(p[3]) == 4, "formats");
+  Py_XSETREF(format_codes, Py_NewRef(p[2]));
+  Py_XSETREF(format_names, Py_NewRef(p[3]));
+  return bind(self, p, 2);
+  END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {method<bind_formats>("bind"), method<quantise>("quantise"), method<norm_quantise>("norm_quantise"),
                          method<product>("product"), method<linear>("linear"),     method<linear_backward>("linear_backward"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_quant_calls", nullptr, -1, methods};

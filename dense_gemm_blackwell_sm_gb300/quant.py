@@ -31,7 +31,6 @@ from .gemm import GemmError
 # quant_format_t
 E4M3, MXE4M3, MXFP4, NVFP4 = 0, 1, 2, 3
 FORMATS = {"e4m3": E4M3, "mxe4m3": MXE4M3, "mxfp4": MXFP4, "nvfp4": NVFP4}
-_NAMES = {code: name for name, code in FORMATS.items()}
 _OUT = {torch.bfloat16: ffn.BF16, torch.float32: ffn.F32}
 
 STATIC_B = 1
@@ -70,6 +69,8 @@ class Quantised(collections.namedtuple("Quantised", ["data", "scales", "row_scal
     __slots__ = ()
 
 
+_new = tuple.__new__  # (a call's five values are a Quantised's)
+
 _lib = None
 
 
@@ -101,7 +102,7 @@ def load_calls():
             from . import _quant_calls
         except ImportError as e:
             raise RuntimeError("_quant_calls.so is not built (%s); run __graft_entry__.build() first" % e) from e
-        _quant_calls.bind(GemmError, _share)
+        _quant_calls.bind(GemmError, _share, FORMATS, tuple(FORMATS))
         _calls = _quant_calls
     return _calls
 
@@ -114,17 +115,16 @@ def _out_code(dtype):
 
 
 def _values(q, name):
+    """q itself: its five values are five arguments of a call."""
     if not isinstance(q, Quantised):
         raise TypeError("%s must be a Quantised, not %s" % (name, type(q).__name__))
-    return q.data, q.scales, q.row_scale, _code(FORMATS, q.format, "format"), q.cols
+    return q
 
 
 def quantise(x, format, transpose=False, stream=None):
     """x (rows, cols), float16, bfloat16 or float32, quantised by rows, or with
     ``transpose`` by columns (the operand of x.T): a Quantised."""
-    code = _code(FORMATS, format, "format")
-    data, scales, row_scale = (_calls or load_calls()).quantise(x, code, transpose, stream)
-    return Quantised(data, scales, row_scale, _NAMES[code], x.shape[0] if transpose else x.shape[1])
+    return _new(Quantised, (_calls or load_calls()).quantise(x, format, transpose, stream))
 
 
 def norm_quantise(y, residual=None, weight=None, *, format, eps=1e-6, residual_scale=1.0, branch_scale=1.0,
@@ -138,10 +138,9 @@ def norm_quantise(y, residual=None, weight=None, *, format, eps=1e-6, residual_s
     returns (s, Quantised of n), s None with need_s False.  s may be given, and be y or the
     residual (in place).  weight is (D), of y's type or float32.  Its gradient is that of
     ffn.block_norm with pre_weight=weight."""
-    code = _code(FORMATS, format, "format")
-    s, data, scales, row_scale = (_calls or load_calls()).norm_quantise(
-        y, residual, weight, code, eps, residual_scale, branch_scale, need_s, s, stream)
-    return s, Quantised(data, scales, row_scale, _NAMES[code], y.shape[1])
+    s, *q = (_calls or load_calls()).norm_quantise(y, residual, weight, format, eps, residual_scale, branch_scale,
+                                                   need_s, s, stream)
+    return s, _new(Quantised, q)
 
 
 def product(a, b, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=None, out=None, static_b=False,
@@ -170,8 +169,8 @@ def linear_backward(dy, x, w, *, format, need_dx=True, need_dw=True, out_dtype=t
     operands quantised along the sum: dx = Q(dy) Q(w^T)^T and dw = Q(dy^T) Q(x^T)^T.  The
     roundings are passed by: these are the gradients of the product of the unrounded values,
     made of rounded ones.  Either is None when not needed, and then its operand may be."""
-    return (_calls or load_calls()).linear_backward(dy, x, w, _code(FORMATS, format, "format"), need_dx, need_dw,
-                                                    _out_code(out_dtype), stream, timeout_ns)
+    return (_calls or load_calls()).linear_backward(dy, x, w, format, need_dx, need_dw, _out_code(out_dtype), stream,
+                                                    timeout_ns)
 
 
 def width(cols):
