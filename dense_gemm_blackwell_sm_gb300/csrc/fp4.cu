@@ -74,12 +74,14 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
     s.smem = fp4_pair_smem(nv);
     s.cluster = 2;
   } else {
-    p.tokens = (int32_t)std::min<int64_t>(128, up(a.M, 16) * 16);
-    p.tiles_m = (int32_t)up(a.M, 128);
+    p.tokens = a.M <= 64 ? (int32_t)up(a.M, 16) * 16 : 64;
+    p.tiles_m = (int32_t)up(a.M, p.tokens);
     p.tiles_n = (int32_t)up(a.N, 128);
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    // (all CTAs at once, two an SM)
+    const int64_t slots = 2 * (int64_t)dev.num_sms;
     p.split = 1;
-    while (p.split < 8 && p.split * 2 <= p.blocks && tiles * p.split * 2 <= 2 * dev.num_sms) p.split *= 2;
+    while (p.split < 8 && p.split * 2 <= p.blocks && tiles * p.split * 2 <= slots) p.split *= 2;
     p.stages = fp4_few_stages(nv, p.tokens);
     p.idesc = idesc_fp4(!nv, 128, p.tokens);
     if (!encode_byte_rows(&maps[0], a.a, (uint64_t)a.K / 2, (uint64_t)a.M, (uint64_t)a.ld_a, (uint32_t)p.tokens) ||

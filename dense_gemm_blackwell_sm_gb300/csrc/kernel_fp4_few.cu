@@ -19,27 +19,43 @@ namespace dgb {
 namespace {
 
 constexpr uint32_t kOperand = 128u * 128u;
-constexpr uint32_t kTmemColumns = 256;
-constexpr uint32_t kScaleCol = 128;
-constexpr int kMostStages = 4;
-constexpr uint32_t kRoom = 110u * 1024u;  // of shared memory, for two CTAs on an SM
+constexpr int kMostStages = 6;
+
+// TMEM columns of a CTA, the first of its scales, and the stages those and shared memory hold
+struct FewShape {
+  uint32_t columns, scale_col;
+  int stages;
+};
 
 template <bool NV>
 constexpr uint32_t kSlot = 8u * kScaleBlocks<NV>;  // TMEM columns of a stage's scales
-static_assert(kScaleCol + kMostStages * kSlot<true> <= kTmemColumns, "scales fit TMEM");
 
-__host__ __device__ inline uint32_t stage_bytes(int blocks, int tokens) {
-  return kOperand + (uint32_t)tokens * 128u + 2u * 512u * (uint32_t)blocks;
-}
 
 // Sums [begin, end) of a tile's [token][feature] from the cluster's SPLIT CTAs, in the order of
 // their ranks, to c: V neighbours a time.  What a thread reads from the CTAs is under way
 // together (8 groups of 4 or 8 single values): one after the other, eight reads of distributed
 // shared memory took 2 us.
+__host__ __device__ inline uint32_t stage_bytes(int blocks, int tokens) {
+  return kOperand + (uint32_t)tokens * 128u + 2u * 512u * (uint32_t)blocks;
+}
+
+__host__ __device__ inline FewShape few_shape(int blocks, int tokens) {
+  // (227 KB for two CTAs, 1 KB of each the system's; for three with fewer stages 1 x 14336 x 4096
+  // takes 9.4 us, for two 8.3)
+  const uint32_t room = 111u * 1024u;
+  FewShape f{256u, tokens <= 32 ? 32u : 64u, 0};
+  const int in_tmem = (int)((f.columns - f.scale_col) / (8u * (uint32_t)blocks));
+  const int in_room = (int)((room - 2048u) / stage_bytes(blocks, tokens));
+  f.stages = in_tmem < in_room ? in_tmem : in_room;
+  if (f.stages > kMostStages) f.stages = kMostStages;
+  return f;
+}
+
 template <int V, int SPLIT, typename OutT>
 __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* partial, int32_t begin, int32_t end,
                                            int32_t row0, int32_t col0) {
-  constexpr int U = 8 / SPLIT;
+  constexpr int U = (V == 4 ? 8 : 16) / SPLIT;
+  using Word = typename std::conditional<V == 1, OutT, typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type>::type;
   constexpr int kStep = kFp4FewThreads * V;
   const Fp4Epilogue& e = p.e;
   uint32_t from[SPLIT];
@@ -48,9 +64,14 @@ __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* part
 #pragma unroll 1
   for (int32_t i0 = begin + (int32_t)threadIdx.x * V; i0 < end; i0 += kStep * U) {
     float y[U][SPLIT][V];
+    Word res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int32_t i = min(i0 + u * kStep, end - V);  // (a multiple of V)
+      const int32_t col = col0 + i % 128;
+      if (e.residual != nullptr && col + V <= e.N)
+        res[u] = *reinterpret_cast<const Word*>(reinterpret_cast<const OutT*>(e.residual) +
+                                                (int64_t)(row0 + i / 128) * e.ld_residual + col);
 #pragma unroll
       for (int r = 0; r < SPLIT; ++r) {
         if constexpr (SPLIT == 1) {
@@ -87,26 +108,18 @@ __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* part
         if (e.bias != nullptr) x[j] += __ldg(e.bias + c);
       }
       fp4_act(x, e.act);
-      const OutT* res = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
       OutT* dst = reinterpret_cast<OutT*>(e.c) + (int64_t)row * e.ld_c + col;
-      if (V == 4 && whole) {
-        using Word = typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type;
-        Word word;
-        OutT* t = reinterpret_cast<OutT*>(&word);
-        if (e.residual != nullptr) {
-          word = *reinterpret_cast<const Word*>(res);
+      if (whole) {
+        OutT* t = reinterpret_cast<OutT*>(&res[u]);
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[j] += to_f32(t[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) t[j] = from_f32<OutT>(x[j]);
-        *reinterpret_cast<Word*>(dst) = word;
+        for (int j = 0; j < V; ++j) t[j] = from_f32<OutT>(e.residual != nullptr ? x[j] + to_f32(t[j]) : x[j]);
+        *reinterpret_cast<Word*>(dst) = res[u];
       } else {
+        const OutT* from_res = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           if (col + j >= e.N) break;
-          if (e.residual != nullptr) x[j] += to_f32(res[j]);
-          dst[j] = from_f32<OutT>(x[j]);
+          dst[j] = from_f32<OutT>(e.residual != nullptr ? x[j] + to_f32(from_res[j]) : x[j]);
         }
       }
     }
@@ -125,7 +138,7 @@ __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* part
 }
 
 template <bool NV, typename OutT>
-__global__ void __launch_bounds__(kFp4FewThreads)
+__global__ void __launch_bounds__(kFp4FewThreads, 2)
     k_fp4_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
               const __grid_constant__ Fp4Params p) {
@@ -134,6 +147,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   uint8_t* ring = align_1024(smem_raw);
   const uint32_t S = (uint32_t)p.stages, T = (uint32_t)p.tokens;
   const uint32_t STAGE = stage_bytes((int)NB, (int)T);
+  const FewShape shape = few_shape((int)NB, (int)T);
   uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * STAGE);
   uint64_t* full = bars;
   uint64_t* empty = bars + kMostStages;
@@ -158,7 +172,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
     tma_prefetch_desc(&tmSB);
   }
   if (warp == 0) {
-    tmem_alloc<1>(smem_u32(tmem_slot), kTmemColumns);
+    tmem_alloc<1>(smem_u32(tmem_slot), shape.columns);
     tmem_relinquish<1>();
   }
   tc_fence_before();
@@ -170,6 +184,9 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   const int32_t rank = (int32_t)cluster_ctarank();
   const int32_t tile = (int32_t)(blockIdx.x / (uint32_t)p.split);
   const int32_t tm = tile % p.tiles_m, tn = tile / p.tiles_m;  // tokens, features
+  const int32_t token0 = tm * (int32_t)T;
+  // (64 tokens are half of a block of scales: the second half is its columns 2 and 3)
+  const uint32_t token_col = (uint32_t)(token0 & 127) / 32u;
   const int32_t kb0 = (int32_t)((int64_t)p.blocks * rank / p.split);
   const int32_t nkb = (int32_t)((int64_t)p.blocks * (rank + 1) / p.split) - kb0;
 
@@ -188,8 +205,8 @@ __global__ void __launch_bounds__(kFp4FewThreads)
     };
     auto token_rows = [&](int32_t j, uint32_t s) {
       const uint32_t st = smem_u32(ring + s * STAGE), fb = smem_u32(full + s);
-      tma_load_2d(st + tokens_at, &tmA, fb, (kb0 + j) * 128, tm * 128);
-      tma_load_3d(st + tscales_at, &tmSA, fb, 0, (kb0 + j) * 4 * (int32_t)NB, tm);
+      tma_load_2d(st + tokens_at, &tmA, fb, (kb0 + j) * 128, token0);
+      tma_load_3d(st + tscales_at, &tmSA, fb, 0, (kb0 + j) * 4 * (int32_t)NB, token0 / 128);
     };
     const int32_t first = min(nkb, (int32_t)S);
     if (p.static_b)
@@ -210,7 +227,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
       if (!warp_wait(smem_u32(full + s), (uint32_t)j / S & 1u, w, WAIT_MMA_FULL)) break;
       tc_fence_after();
       const uint32_t st = smem_u32(ring + s * STAGE);
-      const uint32_t sf = tmem + kScaleCol + s * kSlot<NV>;
+      const uint32_t sf = tmem + shape.scale_col + s * kSlot<NV>;
 #pragma unroll
       for (uint32_t i = 0; i < NB; ++i) {
         tmem_cp_32x128b_x4<1>(issue, sf + 4u * i, sdesc_rows16(st + fscales_at + 512u * i));
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
         const uint32_t i = fp4_scale_block<NV>(k);
         if (4 * (kb0 + j) + k < p.steps)
           mma_fp4<1, NV>(issue, tmem, ad + 2 * k, bd + 2 * k, fp4_idesc<NV>(p.idesc, k), sf + 4u * i,
-                         sf + 4u * NB + 4u * i, (uint32_t)(j | k));
+                         sf + 4u * NB + 4u * i + token_col, (uint32_t)(j | k));
       }
       if (issue) mma_commit(smem_u32(empty + s));
       __syncwarp();
@@ -237,7 +254,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   // The partial sums, [token][feature], where the stages were; each CTA of the cluster then
   // adds its share of them.
   float* partial = reinterpret_cast<float*>(ring);
-  const int32_t tokens = min((int32_t)T, p.e.M - tm * 128);
+  const int32_t tokens = min((int32_t)T, p.e.M - token0);
   if (ok) {
     tc_fence_after();
     // (warps 4-7 take every other 16 tokens)
@@ -263,9 +280,9 @@ __global__ void __launch_bounds__(kFp4FewThreads)
     const int32_t share = ((total + p.split - 1) / p.split + 127) / 128 * 128;
     const int32_t begin = rank * share, end = min(total, begin + share);
     if (p.e.vec != 0) {
-      few_finish<4, OutT>(p, partial, begin, end, tm * 128, tn * 128);
+      few_finish<4, OutT>(p, partial, begin, end, token0, tn * 128);
     } else {
-      few_finish<1, OutT>(p, partial, begin, end, tm * 128, tn * 128);
+      few_finish<1, OutT>(p, partial, begin, end, token0, tn * 128);
     }
   }
   if (!ok && threadIdx.x == 0) {
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(kFp4FewThreads)
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc<1>(tmem, kTmemColumns);
+    tmem_dealloc<1>(tmem, shape.columns);
   }
 }
 
@@ -292,9 +309,7 @@ const void* fp4_few_kernel(bool nv, bool out_f32) {
                  : reinterpret_cast<const void*>(k_fp4_few<false, __nv_bfloat16>);
 }
 
-int fp4_few_stages(bool nv, int tokens) {
-  return (int)std::min<uint32_t>(kMostStages, kRoom / stage_bytes(nv ? 4 : 2, tokens));
-}
+int fp4_few_stages(bool nv, int tokens) { return few_shape(nv ? 4 : 2, tokens).stages; }
 
 size_t fp4_few_smem(bool nv, int tokens, int stages) {
   return 1024 + (size_t)stages * stage_bytes(nv ? 4 : 2, tokens) + (2 * kMostStages + 1) * 8 + 16;

@@ -117,24 +117,22 @@ Operand operand_of(const char* name, PyObject* const* p) {
 }
 
 // the five values of a new operand
-PyObject* operand_tuple(const Operand& o, const Tensor* first = nullptr) {
+PyObject* operand_tuple(const Operand& o) {
   const bool four = o.format == QUANT_MXFP4 || o.format == QUANT_NVFP4;
   const uint8_t* base = static_cast<const uint8_t*>(o.memory.data_ptr());
   const Tensor data = part_of(o.memory, 0, four ? at::kByte : at::kFloat8_e4m3fn, {o.rows, o.ld});
   Tensor scales, row_scale;
   if (o.scales) scales = part_of(o.memory, o.scales - base, at::kByte, {o.scale_bytes});
   if (o.row_scale) row_scale = part_of(o.memory, reinterpret_cast<const uint8_t*>(o.row_scale) - base, at::kFloat, {o.rows});
-  const Py_ssize_t n = first != nullptr ? 1 : 0;
-  THPObjectPtr out(PyTuple_New(5 + n));
+  THPObjectPtr out(PyTuple_New(5));
   if (!out) throw python_error();
-  if (first != nullptr) PyTuple_SET_ITEM(out.get(), 0, wrapped(*first));
-  PyTuple_SET_ITEM(out.get(), n, wrapped(data));
-  PyTuple_SET_ITEM(out.get(), n + 1, wrapped(scales));
-  PyTuple_SET_ITEM(out.get(), n + 2, wrapped(row_scale));
-  PyTuple_SET_ITEM(out.get(), n + 3, Py_NewRef(PyTuple_GET_ITEM(format_names, o.format)));
+  PyTuple_SET_ITEM(out.get(), 0, wrapped(data));
+  PyTuple_SET_ITEM(out.get(), 1, wrapped(scales));
+  PyTuple_SET_ITEM(out.get(), 2, wrapped(row_scale));
+  PyTuple_SET_ITEM(out.get(), 3, Py_NewRef(PyTuple_GET_ITEM(format_names, o.format)));
   PyObject* cols = PyLong_FromLongLong(o.cols);
   if (cols == nullptr) throw python_error();
-  PyTuple_SET_ITEM(out.get(), n + 4, cols);
+  PyTuple_SET_ITEM(out.get(), 4, cols);
   return out.release();
 }
 
@@ -241,7 +239,7 @@ PyObject* quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
 }
 
 // (y, residual, weight, format, eps, residual_scale, branch_scale, need_s, s, stream)
-// -> (s or None, an operand's five values)
+// -> (s or None, the operand's five values)
 PyObject* norm_quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 10);
@@ -285,7 +283,11 @@ PyObject* norm_quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
   a.scales = o.scales;
   a.row_scale = o.row_scale;
   call(quant_norm, "quant_norm", a, index, p[9], {&s, &o.memory});
-  return operand_tuple(o, &s);
+  THPObjectPtr q(operand_tuple(o)), out(PyTuple_New(2));
+  if (!out) throw python_error();
+  PyTuple_SET_ITEM(out.get(), 0, wrapped(s));
+  PyTuple_SET_ITEM(out.get(), 1, q.release());
+  return out.release();
   END_HANDLE_TH_ERRORS
 }
 

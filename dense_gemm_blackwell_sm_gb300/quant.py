@@ -138,8 +138,8 @@ def norm_quantise(y, residual=None, weight=None, *, format, eps=1e-6, residual_s
     returns (s, Quantised of n), s None with need_s False.  s may be given, and be y or the
     residual (in place).  weight is (D), of y's type or float32.  Its gradient is that of
     ffn.block_norm with pre_weight=weight."""
-    s, *q = (_calls or load_calls()).norm_quantise(y, residual, weight, format, eps, residual_scale, branch_scale,
-                                                   need_s, s, stream)
+    s, q = (_calls or load_calls()).norm_quantise(y, residual, weight, format, eps, residual_scale, branch_scale,
+                                                  need_s, s, stream)
     return s, _new(Quantised, q)
 
 
