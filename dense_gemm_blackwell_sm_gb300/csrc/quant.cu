@@ -42,7 +42,23 @@ gemm_status_t rows_sizes(const quant_rows_t& a) {
   if (a.transpose != 0 && a.transpose != 1) return GEMM_ERR_INVALID_ARG;
   if (a.rows < 0 || a.cols < 0 || a.rows >= kMaxDim - 32 || a.cols >= kMaxDim - 32) return GEMM_ERR_INVALID_ARG;
   // (one CTA per tile of 256 x 64, in one dimension of the grid)
-  if (a.transpose && ((a.rows + 287) / 256) * ((a.cols + 127) / 64) >= kMaxDim) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  if (a.transpose && ((a.rows + 287) / 256) * ((a.cols + 127) / 64) >= kMaxDim / 8) return GEMM_ERR_UNSUPPORTED_SHAPE;
+  return GEMM_OK;
+}
+
+// Checks a call and resolves its pitches.
+gemm_status_t rows_checked(quant_rows_t* p) {
+  quant_rows_t& a = *p;
+  gemm_status_t st = rows_sizes(a);
+  if (st != GEMM_OK) return st;
+  if (!pitch(&a.ld_x, a.cols) || !pitch(&a.ld_data, bytes_of(width_of(a.transpose ? a.rows : a.cols), a.format)))
+    return GEMM_ERR_INVALID_ARG;
+  if ((a.transpose ? a.cols : a.rows) == 0) return GEMM_OK;
+  if (!a.x && a.rows > 0 && a.cols > 0) return GEMM_ERR_INVALID_ARG;
+  st = operand(a.data, a.scales, a.row_scale, a.format);
+  if (st != GEMM_OK) return st;
+  if (!aligned(a.x, elem(a.dtype)) || a.ld_data % 16 != 0 || !aligned(a.workspace, 16)) return GEMM_ERR_MISALIGNED;
+  if (a.transpose && quant_columns_workspace(a) > 0 && !a.workspace) return GEMM_ERR_INVALID_ARG;
   return GEMM_OK;
 }
 
@@ -67,24 +83,42 @@ int64_t quant_rows_workspace(const quant_rows_t* args) {
   return args->transpose && args->cols > 0 ? (int64_t)quant_columns_workspace(*args) : 0;
 }
 
-gemm_status_t quant_rows(const quant_rows_t* args, gemm_stream_t stream) {
-  if (!args) return GEMM_ERR_INVALID_ARG;
-  quant_rows_t a = *args;
-  gemm_status_t st = rows_sizes(a);
-  if (st != GEMM_OK) return st;
-  if (!pitch(&a.ld_x, a.cols) || !pitch(&a.ld_data, bytes_of(width_of(a.transpose ? a.rows : a.cols), a.format)))
-    return GEMM_ERR_INVALID_ARG;
-  if ((a.transpose ? a.cols : a.rows) == 0) return GEMM_OK;
-  if (!a.x && a.rows > 0 && a.cols > 0) return GEMM_ERR_INVALID_ARG;
-  st = operand(a.data, a.scales, a.row_scale, a.format);
-  if (st != GEMM_OK) return st;
-  if (!aligned(a.x, elem(a.dtype)) || a.ld_data % 16 != 0 || !aligned(a.workspace, 16)) return GEMM_ERR_MISALIGNED;
-  if (a.transpose && quant_columns_workspace(a) > 0 && !a.workspace) return GEMM_ERR_INVALID_ARG;
-  FfnDevice dev;
-  st = device_of_call(1, &dev);
-  if (st != GEMM_OK) return st;
+gemm_status_t quant_rows(const quant_rows_t* args, gemm_stream_t stream) { return quant_rows_many(args, 1, stream); }
+
+gemm_status_t quant_rows_many(const quant_rows_t* args, int32_t count, gemm_stream_t stream) {
+  if (!args || count < 0) return GEMM_ERR_INVALID_ARG;
+  // everything is checked before anything is launched
+  for (int32_t i = 0; i < count; ++i) {
+    quant_rows_t a = args[i];
+    const gemm_status_t st = rows_checked(&a);
+    if (st != GEMM_OK) return st;
+  }
+  FfnDevice dev{};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return launched(a.transpose ? launch_quant_columns(a, dev, s) : launch_quant_rows(a, dev, s));
+  quant_rows_t columns[kQuantColumnTasks];
+  int waiting = 0;
+  cudaError_t e = cudaSuccess;
+  for (int32_t i = 0; i < count && e == cudaSuccess; ++i) {
+    quant_rows_t a = args[i];
+    rows_checked(&a);  // (resolves the pitches)
+    if ((a.transpose ? a.cols : a.rows) == 0) continue;
+    if (dev.status == nullptr) {
+      const gemm_status_t st = device_of_call(1, &dev);
+      if (st != GEMM_OK) return st;
+    }
+    if (!a.transpose) {
+      e = launch_quant_rows(a, dev, s);
+      continue;
+    }
+    // columns of arrays alike go together
+    if (waiting > 0 && (waiting == kQuantColumnTasks || columns[0].dtype != a.dtype || columns[0].format != a.format)) {
+      e = launch_quant_columns(columns, waiting, s);
+      waiting = 0;
+    }
+    columns[waiting++] = a;
+  }
+  if (e == cudaSuccess && waiting > 0) e = launch_quant_columns(columns, waiting, s);
+  return launched(e);
 }
 
 gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream) {

@@ -166,10 +166,10 @@ __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) 
   return b;
 }
 
-// 16 values to codes: 16 bytes (E4M3) or 8 (E2M1) at `dst`.  EXACT: values that may lie
-// nearer to a tie than the reciprocal is exact (32-bit inputs) are divided.
+// 16 values to codes: 4 words (E4M3) or 2 (E2M1).  EXACT: values that may lie nearer to a tie than
+// the reciprocal is exact (32-bit inputs) are divided.
 template <int F, bool EXACT>
-__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
+__device__ __forceinline__ void codes16(uint32_t* w, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
   float t[16];
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
@@ -186,12 +186,26 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], 
   }
   const bool zero = b.inv == 0.f;  // (an infinity times 0 is no 0)
   if constexpr (kFourBit<F>) {
-    *reinterpret_cast<uint2*>(dst) = zero ? make_uint2(0u, 0u) : make_uint2(e2m1x8(t), e2m1x8(t + 8));
+    w[0] = e2m1x8(t);
+    w[1] = e2m1x8(t + 8);
   } else {
-    *reinterpret_cast<uint4*>(dst) =
-        zero ? make_uint4(0u, 0u, 0u, 0u)
-             : make_uint4(e4m3x4(t[0], t[1], t[2], t[3]), e4m3x4(t[4], t[5], t[6], t[7]),
-                          e4m3x4(t[8], t[9], t[10], t[11]), e4m3x4(t[12], t[13], t[14], t[15]));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = e4m3x4(t[4 * j], t[4 * j + 1], t[4 * j + 2], t[4 * j + 3]);
+  }
+  if (zero) {
+#pragma unroll
+    for (int j = 0; j < (kFourBit<F> ? 2 : 4); ++j) w[j] = 0u;
+  }
+}
+// ... stored at `dst`
+template <int F, bool EXACT>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
+  uint32_t w[kFourBit<F> ? 2 : 4];
+  codes16<F, EXACT>(w, v, row, b);
+  if constexpr (kFourBit<F>) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

@@ -13,7 +13,9 @@ namespace dgb {
 // The pitches below are resolved (never 0).
 cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaStream_t st);
 size_t quant_columns_workspace(const quant_rows_t& a);
-cudaError_t launch_quant_columns(const quant_rows_t& a, const FfnDevice& dev, cudaStream_t st);
+// `count` arrays, at most kQuantColumnTasks, of one dtype and format
+constexpr int kQuantColumnTasks = 4;
+cudaError_t launch_quant_columns(const quant_rows_t* args, int count, cudaStream_t st);
 cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaStream_t st);
 cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, cudaStream_t st);
 

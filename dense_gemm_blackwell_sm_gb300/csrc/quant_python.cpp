@@ -136,30 +136,41 @@ PyObject* operand_tuple(const Operand& o) {
   return out.release();
 }
 
-// x's rows or columns, quantised
-Operand quantised(const char* name, const Tensor& x, int32_t format, bool transpose, PyObject* stream) {
+// x's rows or columns, to be quantised by the call whose arguments these are
+Operand to_quantise(quant_rows_t* a, const char* name, const Tensor& x, int32_t format, bool transpose) {
   TORCH_CHECK_VALUE(x.dim() == 2, name, " must be a 2-D tensor, not ", x.sizes());
-  quant_rows_t a{};
   const int index = index_of(x);
   const at::ScalarType dtype = x.scalar_type();
-  a.rows = x.size(0);
-  a.cols = x.size(1);
-  a.dtype = code_of(dtype);
-  TORCH_CHECK_VALUE(a.dtype >= 0, name, " must be float16, bfloat16 or float32, not ", dtype);
-  a.format = format;
-  a.transpose = transpose;
-  a.ld_x = rows_of(name, x, a.rows, a.cols, dtype, index);
+  a->rows = x.size(0);
+  a->cols = x.size(1);
+  a->dtype = code_of(dtype);
+  TORCH_CHECK_VALUE(a->dtype >= 0, name, " must be float16, bfloat16 or float32, not ", dtype);
+  a->format = format;
+  a->transpose = transpose;
+  a->ld_x = rows_of(name, x, a->rows, a->cols, dtype, index);
   // (a refused call asks for -1 bytes and is refused when it is made)
-  const int64_t workspace = std::max<int64_t>(0, quant_rows_workspace(&a));
-  Operand o = empty_operand(transpose ? a.cols : a.rows, transpose ? a.rows : a.cols, format, index, workspace);
-  a.x = x.data_ptr();
-  a.data = o.data;
-  a.scales = o.scales;
-  a.row_scale = o.row_scale;
-  a.workspace = behind(o);
-  call(quant_rows, "quant_rows", a, index, stream, {&o.memory});
+  const int64_t workspace = std::max<int64_t>(0, quant_rows_workspace(a));
+  Operand o = empty_operand(transpose ? a->cols : a->rows, transpose ? a->rows : a->cols, format, index, workspace);
+  a->x = x.data_ptr();
+  a->data = o.data;
+  a->scales = o.scales;
+  a->row_scale = o.row_scale;
+  a->workspace = behind(o);
   return o;
 }
+
+Operand quantised(const char* name, const Tensor& x, int32_t format, bool transpose, PyObject* stream) {
+  quant_rows_t a{};
+  Operand o = to_quantise(&a, name, x, format, transpose);
+  call(quant_rows, "quant_rows", a, o.index, stream, {&o.memory});
+  return o;
+}
+
+struct Several {
+  quant_rows_t args[4];
+  int32_t count;
+};
+gemm_status_t quant_several(const Several* s, gemm_stream_t stream) { return quant_rows_many(s->args, s->count, stream); }
 
 struct Finish {
   const Tensor *bias, *residual, *out;
@@ -336,8 +347,21 @@ PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t n) {
   f.activation = GEMM_ACT_NONE;
   f.timeout_ns = int_of(p[8]);
   Tensor dx, dw;
-  if (need_dx) dx = multiplied(quantised("dy", dy, format, false, p[7]), quantised("w", *w, format, true, p[7]), f, p[7]);
-  if (need_dw) dw = multiplied(quantised("dy", dy, format, true, p[7]), quantised("x", *x, format, true, p[7]), f, p[7]);
+  // (columns one after the other: they go in one launch)
+  Several s{};
+  Operand dy_rows, w_columns, dy_columns, x_columns;
+  if (need_dx) {
+    dy_rows = to_quantise(&s.args[s.count++], "dy", dy, format, false);
+    w_columns = to_quantise(&s.args[s.count++], "w", *w, format, true);
+  }
+  if (need_dw) {
+    dy_columns = to_quantise(&s.args[s.count++], "dy", dy, format, true);
+    x_columns = to_quantise(&s.args[s.count++], "x", *x, format, true);
+  }
+  call(quant_several, "quant_rows_many", s, index, p[7],
+       {&dy_rows.memory, &w_columns.memory, &dy_columns.memory, &x_columns.memory});
+  if (need_dx) dx = multiplied(dy_rows, w_columns, f, p[7]);
+  if (need_dw) dw = multiplied(dy_columns, x_columns, f, p[7]);
   return tuple_of({&dx, &dw});
   END_HANDLE_TH_ERRORS
 }

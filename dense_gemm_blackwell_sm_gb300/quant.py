@@ -82,6 +82,7 @@ def load():
         for name, args in (("quant_rows", RowsArgs), ("quant_norm", NormArgs), ("quant_product", ProductArgs)):
             f = getattr(lib, name)
             f.argtypes, f.restype = [ctypes.POINTER(args), _p], ctypes.c_int  # (a structure is passed by reference)
+        lib.quant_rows_many.argtypes, lib.quant_rows_many.restype = [ctypes.POINTER(RowsArgs), _i32, _p], ctypes.c_int
         lib.quant_rows_workspace.argtypes, lib.quant_rows_workspace.restype = [ctypes.POINTER(RowsArgs)], _i64
         lib.quant_width.argtypes, lib.quant_width.restype = [_i64], _i64
         lib.quant_row_bytes.argtypes, lib.quant_row_bytes.restype = [_i64, _i32], _i64

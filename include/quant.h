@@ -97,6 +97,11 @@ GEMM_API int64_t quant_rows_workspace(const quant_rows_t* args);
 
 GEMM_API gemm_status_t quant_rows(const quant_rows_t* args, gemm_stream_t stream);
 
+/* The same for `count` arrays (0 allowed), each with a workspace of its own; columns of arrays of
+ * one dtype and format that follow one another go in few launches.  All are checked before
+ * anything is launched. */
+GEMM_API gemm_status_t quant_rows_many(const quant_rows_t* args, int32_t count, gemm_stream_t stream);
+
 /* s = residual_scale * residual + branch_scale * y
  * n = s / sqrt(mean(s^2) + eps) * weight, from s before it is rounded, in fp32
  * and n quantised by rows.  Absent (NULL) weight counts as one, an absent residual as

@@ -29,7 +29,7 @@ def lib():
 def test_every_declared_symbol_is_exported(lib):
     text = open(os.path.join(ROOT, "include", "quant.h")).read()
     names = re.findall(r"GEMM_API\s+[\w\s\*]+?\b(quant_\w+)\s*\(", text)
-    assert len(names) == 8
+    assert len(names) == 9
     for n in names:
         assert hasattr(lib, n), n
 
@@ -136,6 +136,15 @@ def product_args(**kw):
     (dict(M=0), gemm.OK), (dict(N=0), gemm.OK)])
 def test_product_refusals(lib, change, status):
     assert lib.quant_product(ctypes.byref(product_args(**change)), None) == status
+
+
+def test_many_rows_refusals(lib):
+    # one refused array refuses all; none is no work
+    two = (quant.RowsArgs * 2)(rows_args(rows=0), rows_args(dtype=3))
+    assert lib.quant_rows_many(two, 2, None) == gemm.ERR_UNSUPPORTED_DTYPE
+    assert lib.quant_rows_many(two, 1, None) == gemm.OK and lib.quant_rows_many(two, 0, None) == gemm.OK
+    assert lib.quant_rows_many(two, -1, None) == gemm.ERR_INVALID_ARG
+    assert lib.quant_rows_many(None, 0, None) == gemm.ERR_INVALID_ARG
 
 
 def test_null_arguments(lib):
