@@ -38,6 +38,15 @@ struct Fp4Params {
   int32_t static_b;
 };
 
+// Tokens that the kernel quantises itself (kernel_fp4_few.cu).
+struct Fp4Tokens {
+  const void* x;
+  const void* x_end;        // the first byte past its last element
+  int64_t ld_x;
+  int32_t K;                // values of a token (the product's K is that padded)
+  int32_t vec;              // rows start on boundaries of: 2 = 32 bytes, 1 = 16, 0 = neither
+};
+
 const void* fp4_pair_kernel(bool nv, bool out_f32);
 size_t fp4_pair_smem(bool nv);
 int fp4_pair_stages(bool nv);
@@ -47,5 +56,10 @@ const void* fp4_few_kernel(bool nv, bool out_f32);
 size_t fp4_few_smem(bool nv, int tokens, int stages);
 int fp4_few_stages(bool nv, int tokens);
 constexpr int kFp4FewThreads = 256;
+
+// the same with the tokens' quantisation; kb: the most stages of K a CTA takes
+const void* fp4_linear_kernel(bool nv, bool out_f32, int dtype);
+int fp4_linear_stages(bool nv, int kb);
+size_t fp4_linear_smem(bool nv, int kb, int stages);
 
 }  // namespace dgb

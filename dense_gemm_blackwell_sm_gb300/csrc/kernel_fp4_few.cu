@@ -7,12 +7,18 @@
 // each takes a part of K, the partial sums meet in distributed shared memory, in a fixed order.
 // Two CTAs fit an SM, so that one's copies run while the other ends.
 //
+// The same body takes up to 16 tokens as they are (k_fp4_linear): while the features are on their
+// way warps 2-7 quantise the CTA's part of the tokens into shared memory, where the MMAs read it.
+// One launch instead of two: 8 x 4096 x 4096 bf16 to MXFP4 7.0 -> 6.5 us on the device, and with
+// calls made one at a time 11.9 -> 6.6; 1 x 14336 x 4096 to NVFP4 12.9 -> 10.1.
+//
 // Warp 0 is the TMA producer, warp 1 copies the scales into TMEM and issues the MMAs, and all
 // eight warps then add, scale and store.
 #include <algorithm>
 #include <type_traits>
 
 #include "fp4_common.cuh"
+#include "kernels_quant_rows.cuh"
 
 namespace dgb {
 
@@ -39,6 +45,21 @@ __host__ __device__ inline uint32_t stage_bytes(int blocks, int tokens) {
   return kOperand + (uint32_t)tokens * 128u + 2u * 512u * (uint32_t)blocks;
 }
 
+// Tokens quantised in the kernel: 16 at most, all of a CTA's K at once (`kb` stages of it)
+constexpr uint32_t kLinearTokens = 16;
+__host__ __device__ inline uint32_t token_bytes(int blocks, int kb) {
+  return (uint32_t)kb * (kLinearTokens * 128u + 512u * (uint32_t)blocks);
+}
+__host__ __device__ inline FewShape linear_shape(int blocks, int kb) {
+  const uint32_t room = 111u * 1024u - 2048u, taken = token_bytes(blocks, kb);
+  FewShape f{256u, 32u, 0};
+  const int in_tmem = (int)((f.columns - f.scale_col) / (8u * (uint32_t)blocks));
+  const int in_room = taken > room ? 0 : (int)((room - taken) / (kOperand + 512u * (uint32_t)blocks));
+  f.stages = in_tmem < in_room ? in_tmem : in_room;
+  if (f.stages > kMostStages) f.stages = kMostStages;
+  return f;
+}
+
 __host__ __device__ inline FewShape few_shape(int blocks, int tokens) {
   // (227 KB for two CTAs, 1 KB of each the system's; for three with fewer stages 1 x 14336 x 4096
   // takes 9.4 us, for two 8.3)
@@ -52,8 +73,8 @@ __host__ __device__ inline FewShape few_shape(int blocks, int tokens) {
 }
 
 template <int V, int SPLIT, typename OutT>
-__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* partial, int32_t begin, int32_t end,
-                                           int32_t row0, int32_t col0) {
+__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* token_scale, const float* partial,
+                                           int32_t begin, int32_t end, int32_t row0, int32_t col0) {
   constexpr int U = (V == 4 ? 8 : 16) / SPLIT;
   using Word = typename std::conditional<V == 1, OutT, typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type>::type;
   constexpr int kStep = kFp4FewThreads * V;
@@ -95,7 +116,7 @@ __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* part
       if (i >= end || col >= e.N) continue;
       // (a group that the matrix' edge cuts goes by single values)
       const bool whole = col + V <= e.N;
-      const float sa = e.row_scale_a != nullptr ? __ldg(e.row_scale_a + row) : 1.f;
+      const float sa = token_scale != nullptr ? token_scale[row] : 1.f;
       float x[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -127,35 +148,143 @@ __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* part
 }
 
 template <int V, typename OutT>
-__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* partial, int32_t begin, int32_t end,
-                                           int32_t row0, int32_t col0) {
+__device__ __forceinline__ void few_finish(const Fp4Params& p, const float* token_scale, const float* partial,
+                                           int32_t begin, int32_t end, int32_t row0, int32_t col0) {
   switch (p.split) {
-    case 1: return few_finish<V, 1, OutT>(p, partial, begin, end, row0, col0);
-    case 2: return few_finish<V, 2, OutT>(p, partial, begin, end, row0, col0);
-    case 4: return few_finish<V, 4, OutT>(p, partial, begin, end, row0, col0);
-    default: return few_finish<V, 8, OutT>(p, partial, begin, end, row0, col0);
+    case 1: return few_finish<V, 1, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    case 2: return few_finish<V, 2, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    case 4: return few_finish<V, 4, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    default: return few_finish<V, 8, OutT>(p, token_scale, partial, begin, end, row0, col0);
   }
 }
 
-template <bool NV, typename OutT>
-__global__ void __launch_bounds__(kFp4FewThreads, 2)
-    k_fp4_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-              const __grid_constant__ Fp4Params p) {
+// the threads that quantise
+constexpr uint32_t kQuantThreads = kFp4FewThreads - 64;
+__device__ __forceinline__ void quantisers_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(kQuantThreads) : "memory"); }
+
+// the tokens' largest magnitudes, as bits, and what comes of them
+struct TokenScales {
+  uint32_t most[kLinearTokens];
+  float scale[kLinearTokens], inv[kLinearTokens];
+};
+
+// Tokens 0 .. M - 1, K-elements [256 kb0, 256 (kb0 + nkb)), into the places of the MMAs' second
+// operand and of its scales.  The threads of warps 2-7 call it together.  Where a token has a
+// scale of its own every CTA finds the largest magnitude of all the token by itself: the tokens
+// are few and in L2, and to tell one another takes the CTAs of a cluster longer (1 x 14336 x 4096
+// 10.5 us where this takes 10.0).
+template <bool NV, typename XT>
+__device__ __forceinline__ void quantise_tokens(const Fp4Params& p, const Fp4Tokens& x, uint8_t* tokens, uint8_t* scales,
+                                                TokenScales* ts, int32_t kb0, int32_t nkb) {
+  constexpr int F = NV ? QUANT_NVFP4 : QUANT_MXFP4;
+  constexpr uint32_t NB = (uint32_t)kScaleBlocks<NV>;
+  constexpr bool EXACT = sizeof(XT) == 4;
+  constexpr int AHEAD = EXACT ? 2 : 4;  // runs of 16 values a thread has on their way
+  const int32_t thread = (int32_t)threadIdx.x - 64;
+  const int32_t runs = nkb * 16, total = runs * p.e.M;
+  const XT* values = reinterpret_cast<const XT*>(x.x);
+  Run<XT> run[AHEAD];
+  auto load = [&](int32_t u) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int32_t at = u + i * (int32_t)kQuantThreads, row = at / runs;
+      if (at < total) {
+        load16<XT>(run[i], values + row * x.ld_x, kb0 * 256 + (at - row * runs) * 16, x.K, x.vec, x.x, x.x_end);
+      } else {
+        run[i].clear();
+      }
+    }
+  };
+  load(thread);
+  if constexpr (NV) {
+    // a warp takes runs of one token at a time
+    const int32_t chunks = (x.K + 511) / 512, tasks = chunks * p.e.M;
+#pragma unroll 1
+    for (int32_t t = thread / 32; t < tasks; t += AHEAD * (int32_t)(kQuantThreads / 32)) {
+      Run<XT> r[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int32_t task = t + i * (int32_t)(kQuantThreads / 32), row = task / chunks;
+        r[i].clear();
+        if (task < tasks)
+          load16<XT>(r[i], values + row * x.ld_x, (task - row * chunks) * 512 + (thread & 31) * 16, x.K, x.vec, x.x, x.x_end);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int32_t task = t + i * (int32_t)(kQuantThreads / 32);
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = r[i][j];
+        // (magnitudes as bits are in order, a NaN's above all)
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(largest16(v)));
+        if (task < tasks && (thread & 31) == 0) atomicMax(&ts->most[task / chunks], most);
+      }
+    }
+    quantisers_sync();
+    if (thread < p.e.M) {
+      const RowUnit unit = row_unit<F>(__uint_as_float(ts->most[thread]));
+      ts->scale[thread] = unit.scale;
+      ts->inv[thread] = unit.inv;
+    }
+    quantisers_sync();
+  }
+#pragma unroll 1
+  for (int32_t u = thread; u < total + (thread & 31); u += AHEAD * (int32_t)kQuantThreads) {
+    if (u != thread) load(u);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int32_t at = u + i * (int32_t)kQuantThreads, row = min(at / runs, p.e.M - 1), c = at - row * runs;
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = run[i][j];
+      float most = largest16(v);
+      // (32 values are two lanes'; all lanes of a warp are here, those behind the end with zeros)
+      if (!NV) most = larger(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      if (at >= total) continue;
+      const RowUnit unit = NV ? RowUnit{ts->scale[row], ts->inv[row]} : row_unit<F>(0.f);
+      const BlockUnit b = block_unit<F, EXACT>(most, unit);
+      uint32_t codes[2];
+      codes16<F, EXACT>(codes, v, unit, b);
+      const uint32_t j = (uint32_t)c / 16u, q = (uint32_t)c % 16u;  // the stage, and its 16 elements
+      *reinterpret_cast<uint2*>(tokens + j * (kLinearTokens * 128u) + sw128_offset((uint32_t)row, q / 2u) + (q & 1u) * 8u) =
+          make_uint2(codes[0], codes[1]);
+      uint8_t* to = scales + j * (512u * NB) + (uint32_t)row * 16u;
+      if constexpr (NV) {
+        to[(q / 4u) * 512u + q % 4u] = (uint8_t)b.byte;
+      } else if ((q & 1u) == 0u) {
+        to[(q / 8u) * 512u + q / 2u % 4u] = (uint8_t)b.byte;
+      }
+    }
+  }
+  fence_proxy_async_smem();  // (the MMAs and the copies into TMEM read them)
+  quantisers_sync();
+}
+
+// XT: the tokens' type where they are quantised here, void where tmA and tmSA bring them.
+template <bool NV, typename OutT, typename XT>
+__device__ __forceinline__ void few_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmSA,
+                                         const CUtensorMap& tmSB, const Fp4Params& p, const Fp4Tokens& x) {
+  constexpr bool LINEAR = !std::is_void<XT>::value;
   constexpr uint32_t NB = (uint32_t)kScaleBlocks<NV>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = align_1024(smem_raw);
-  const uint32_t S = (uint32_t)p.stages, T = (uint32_t)p.tokens;
-  const uint32_t STAGE = stage_bytes((int)NB, (int)T);
-  const FewShape shape = few_shape((int)NB, (int)T);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + S * STAGE);
+  const uint32_t S = (uint32_t)p.stages, T = LINEAR ? kLinearTokens : (uint32_t)p.tokens;
+  const int32_t most_kb = (p.blocks + p.split - 1) / p.split;
+  const uint32_t STAGE = LINEAR ? kOperand + 512u * NB : stage_bytes((int)NB, (int)T);
+  const FewShape shape = LINEAR ? linear_shape((int)NB, most_kb) : few_shape((int)NB, (int)T);
+  uint8_t* tokens_here = ring + S * STAGE;  // LINEAR: the tokens' codes, then their scales
+  uint8_t* token_scales = tokens_here + (uint32_t)most_kb * kLinearTokens * 128u;
+  TokenScales* ts = reinterpret_cast<TokenScales*>(ring + S * STAGE + (LINEAR ? token_bytes((int)NB, most_kb) : 0u));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ts) + (LINEAR ? sizeof(TokenScales) : 0));
   uint64_t* full = bars;
   uint64_t* empty = bars + kMostStages;
   uint64_t* done = bars + 2 * kMostStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* quantised = done + 1;  // LINEAR: the tokens are in place
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 2);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   // (the stage: features, tokens, their scales)
-  const uint32_t tokens_at = kOperand, fscales_at = kOperand + T * 128u, tscales_at = fscales_at + 512u * NB;
+  const uint32_t tokens_at = kOperand, fscales_at = LINEAR ? kOperand : kOperand + T * 128u,
+                 tscales_at = fscales_at + 512u * NB;
 
   const uint32_t warp = warp_idx(), lane = lane_idx();
   if (threadIdx.x == 0) {
@@ -164,13 +293,17 @@ __global__ void __launch_bounds__(kFp4FewThreads, 2)
       mbar_init(smem_u32(empty + s), 1);
     }
     mbar_init(smem_u32(done), 1);
+    mbar_init(smem_u32(quantised), 1);
     *abort_flag = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
+    if constexpr (!LINEAR) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmSA);
+    }
   }
+  if (LINEAR && threadIdx.x >= 64u && threadIdx.x < 64u + kLinearTokens) ts->most[threadIdx.x - 64u] = 0u;
   if (warp == 0) {
     tmem_alloc<1>(smem_u32(tmem_slot), shape.columns);
     tmem_relinquish<1>();
@@ -217,23 +350,31 @@ __global__ void __launch_bounds__(kFp4FewThreads, 2)
       const uint32_t s = (uint32_t)j % S;
       if (j >= first && !mbar_wait(smem_u32(empty + s), ((uint32_t)j / S & 1u) ^ 1u, w, WAIT_PRODUCER_EMPTY)) break;
       if (j >= first || !p.static_b) features(j, s);
-      token_rows(j, s);
+      if constexpr (!LINEAR) token_rows(j, s);
     }
+  } else if (LINEAR && warp >= 2) {
+    // ----------------------------------------------------------- the tokens
+    wait_for_prior_kernel();
+    if constexpr (LINEAR) quantise_tokens<NV, XT>(p, x, tokens_here, token_scales, ts, kb0, nkb);
+    if (threadIdx.x == 64u) mbar_arrive(smem_u32(quantised));
   } else if (warp == 1) {
     // ------------------------------------------------------- scales and MMAs
     const uint32_t issue = elect_lane();
-    for (int32_t j = 0; j < nkb; ++j) {
+    const bool there = !LINEAR || warp_wait(smem_u32(quantised), 0, w, WAIT_MMA_FULL);
+    for (int32_t j = 0; there && j < nkb; ++j) {
       const uint32_t s = (uint32_t)j % S;
       if (!warp_wait(smem_u32(full + s), (uint32_t)j / S & 1u, w, WAIT_MMA_FULL)) break;
       tc_fence_after();
       const uint32_t st = smem_u32(ring + s * STAGE);
+      const uint32_t tk = LINEAR ? smem_u32(tokens_here) + (uint32_t)j * kLinearTokens * 128u : st + tokens_at;
+      const uint32_t tsc = LINEAR ? smem_u32(token_scales) + (uint32_t)j * 512u * NB : st + tscales_at;
       const uint32_t sf = tmem + shape.scale_col + s * kSlot<NV>;
 #pragma unroll
       for (uint32_t i = 0; i < NB; ++i) {
         tmem_cp_32x128b_x4<1>(issue, sf + 4u * i, sdesc_rows16(st + fscales_at + 512u * i));
-        tmem_cp_32x128b_x4<1>(issue, sf + 4u * NB + 4u * i, sdesc_rows16(st + tscales_at + 512u * i));
+        tmem_cp_32x128b_x4<1>(issue, sf + 4u * NB + 4u * i, sdesc_rows16(tsc + 512u * i));
       }
-      const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(st + tokens_at);
+      const uint64_t ad = sdesc_k_sw128(st), bd = sdesc_k_sw128(tk);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t i = fp4_scale_block<NV>(k);
@@ -268,21 +409,23 @@ __global__ void __launch_bounds__(kFp4FewThreads, 2)
       for (int j = 0; j < 16; ++j) partial[(t0 + j) * 128 + feature] = __uint_as_float(v[j]);
     }
   }
+  __syncwarp();
   if (p.split > 1) {
     cluster_sync_all();
   } else {
     __syncthreads();
   }
   if (ok) {
+    const float* token_scale = LINEAR ? (NV ? ts->scale : nullptr) : p.e.row_scale_a;
     // (features of a tile that the matrix has; groups of four, or single ones where rows are not
     // aligned to groups)
     const int32_t total = tokens * 128;
     const int32_t share = ((total + p.split - 1) / p.split + 127) / 128 * 128;
     const int32_t begin = rank * share, end = min(total, begin + share);
     if (p.e.vec != 0) {
-      few_finish<4, OutT>(p, partial, begin, end, token0, tn * 128);
+      few_finish<4, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
     } else {
-      few_finish<1, OutT>(p, partial, begin, end, token0, tn * 128);
+      few_finish<1, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
     }
   }
   if (!ok && threadIdx.x == 0) {
@@ -290,6 +433,7 @@ __global__ void __launch_bounds__(kFp4FewThreads, 2)
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 2000000ull) {}
   }
+  __syncwarp();
   if (p.split > 1) cluster_sync_all();  // no partial sums go away before they are read
   tc_fence_before();
   __syncthreads();
@@ -298,6 +442,32 @@ __global__ void __launch_bounds__(kFp4FewThreads, 2)
     tmem_dealloc<1>(tmem, shape.columns);
   }
 }
+
+template <bool NV, typename OutT>
+__global__ void __launch_bounds__(kFp4FewThreads, 2)
+    k_fp4_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+              const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+              const __grid_constant__ Fp4Params p) {
+  few_body<NV, OutT, void>(tmA, tmB, tmSA, tmSB, p, Fp4Tokens{});
+}
+
+template <bool NV, typename OutT, typename XT>
+__global__ void __launch_bounds__(kFp4FewThreads, 2)
+    k_fp4_linear(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSB,
+                 const __grid_constant__ Fp4Params p, const __grid_constant__ Fp4Tokens x) {
+  few_body<NV, OutT, XT>(tmB, tmB, tmSB, tmSB, p, x);
+}
+
+template <bool NV, typename OutT>
+const void* linear_kernel(int dtype) {
+  switch (dtype) {
+    case FFN_F16: return reinterpret_cast<const void*>(k_fp4_linear<NV, OutT, __half>);
+    case FFN_BF16: return reinterpret_cast<const void*>(k_fp4_linear<NV, OutT, __nv_bfloat16>);
+    default: return reinterpret_cast<const void*>(k_fp4_linear<NV, OutT, float>);
+  }
+}
+
+constexpr size_t kBarriers = (2 * kMostStages + 2) * 8 + 16;
 
 }  // namespace
 
@@ -312,7 +482,20 @@ const void* fp4_few_kernel(bool nv, bool out_f32) {
 int fp4_few_stages(bool nv, int tokens) { return few_shape(nv ? 4 : 2, tokens).stages; }
 
 size_t fp4_few_smem(bool nv, int tokens, int stages) {
-  return 1024 + (size_t)stages * stage_bytes(nv ? 4 : 2, tokens) + (2 * kMostStages + 1) * 8 + 16;
+  return 1024 + (size_t)stages * stage_bytes(nv ? 4 : 2, tokens) + kBarriers;
+}
+
+const void* fp4_linear_kernel(bool nv, bool out_f32, int dtype) {
+  if (nv) return out_f32 ? linear_kernel<true, float>(dtype) : linear_kernel<true, __nv_bfloat16>(dtype);
+  return out_f32 ? linear_kernel<false, float>(dtype) : linear_kernel<false, __nv_bfloat16>(dtype);
+}
+
+int fp4_linear_stages(bool nv, int kb) { return linear_shape(nv ? 4 : 2, kb).stages; }
+
+size_t fp4_linear_smem(bool nv, int kb, int stages) {
+  const int blocks = nv ? 4 : 2;
+  return 1024 + (size_t)stages * (kOperand + 512u * (uint32_t)blocks) + token_bytes(blocks, kb) + sizeof(TokenScales) +
+         kBarriers;
 }
 
 }  // namespace dgb

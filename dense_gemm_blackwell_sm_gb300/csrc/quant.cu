@@ -46,6 +46,28 @@ gemm_status_t rows_sizes(const quant_rows_t& a) {
   return GEMM_OK;
 }
 
+gemm_status_t linear_sizes(const quant_linear_t& a) {
+  if ((a.format != QUANT_MXFP4 && a.format != QUANT_NVFP4) || !is_dtype(a.dtype)) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.out_dtype != FFN_BF16 && a.out_dtype != FFN_F32) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  if (a.M < 0 || a.N < 0 || a.K < 0 || a.M >= kMaxDim || a.N >= kMaxDim || a.K >= kMaxDim - 32 || a.timeout_ns < 0)
+    return GEMM_ERR_INVALID_ARG;
+  if (a.activation < GEMM_ACT_NONE || a.activation > GEMM_ACT_GELU_ERF || (a.flags & ~QUANT_STATIC_B) != 0)
+    return GEMM_ERR_INVALID_ARG;
+  return GEMM_OK;
+}
+
+// where the quantised rows of a linear layer lie in its workspace
+struct LinearWorkspace {
+  size_t scales, row_scale, bytes;
+  explicit LinearWorkspace(const quant_linear_t& a) {
+    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    const int64_t width = width_of(a.K);
+    scales = round((size_t)a.M * (size_t)(width / 2));
+    row_scale = scales + round((size_t)((a.M + 127) / 128) * (size_t)((scales_of(width, a.format) + 3) / 4) * 512);
+    bytes = row_scale + (a.format == QUANT_NVFP4 ? round((size_t)a.M * 4) : 0);
+  }
+};
+
 // Checks a call and resolves its pitches.
 gemm_status_t rows_checked(quant_rows_t* p) {
   quant_rows_t& a = *p;
@@ -168,6 +190,75 @@ gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t stream) {
   const gemm_status_t st = device_of_call(1, &dev);
   if (st != GEMM_OK) return st;
   return launched(launch_fp4_product(a, dev, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t quant_linear_workspace(const quant_linear_t* args) {
+  if (!args || linear_sizes(*args) != GEMM_OK) return -1;
+  if (args->M == 0 || args->N == 0 || fp4_linear_fused(*args)) return 0;
+  return (int64_t)LinearWorkspace(*args).bytes;
+}
+
+gemm_status_t quant_linear(const quant_linear_t* args, gemm_stream_t stream) {
+  if (!args) return GEMM_ERR_INVALID_ARG;
+  quant_linear_t a = *args;
+  gemm_status_t st = linear_sizes(a);
+  if (st != GEMM_OK) return st;
+  const int64_t width = width_of(a.K);
+  if (!pitch(&a.ld_x, a.K) || !pitch(&a.ld_b, width / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N))
+    return GEMM_ERR_INVALID_ARG;
+  if (a.M == 0 || a.N == 0) return GEMM_OK;
+  if ((!a.x && a.K > 0) || !a.b || !a.scales_b || !a.c) return GEMM_ERR_INVALID_ARG;
+  const uintptr_t e = elem(a.out_dtype);
+  if (!aligned(a.x, elem(a.dtype)) || !aligned(a.b, 16) || !aligned(a.scales_b, 16) || a.ld_b % 16 != 0 ||
+      !aligned(a.row_scale_b, 4) || !aligned(a.bias, 4) || !aligned(a.residual, e) || !aligned(a.c, e) ||
+      !aligned(a.workspace, 256))
+    return GEMM_ERR_MISALIGNED;
+  const bool fused = fp4_linear_fused(a);
+  if (!fused && !a.workspace) return GEMM_ERR_INVALID_ARG;
+  FfnDevice dev;
+  st = device_of_call(1, &dev);
+  if (st != GEMM_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (fused) return launched(launch_fp4_linear(a, dev, s));
+  const LinearWorkspace ws(a);
+  uint8_t* base = static_cast<uint8_t*>(a.workspace);
+  quant_rows_t q{};
+  q.rows = a.M;
+  q.cols = a.K;
+  q.dtype = a.dtype;
+  q.format = a.format;
+  q.x = a.x;
+  q.data = base;
+  q.scales = base + ws.scales;
+  q.row_scale = a.format == QUANT_NVFP4 ? reinterpret_cast<float*>(base + ws.row_scale) : nullptr;
+  q.ld_x = a.ld_x;
+  q.ld_data = width / 2;
+  const cudaError_t err = launch_quant_rows(q, dev, s);
+  if (err != cudaSuccess) return launched(err);
+  quant_product_t p{};
+  p.M = a.M;
+  p.N = a.N;
+  p.K = width;
+  p.format = a.format;
+  p.out_dtype = a.out_dtype;
+  p.activation = a.activation;
+  p.flags = a.flags;
+  p.a = q.data;
+  p.b = a.b;
+  p.scales_a = q.scales;
+  p.scales_b = a.scales_b;
+  p.row_scale_a = q.row_scale;
+  p.row_scale_b = a.row_scale_b;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.c = a.c;
+  p.ld_a = q.ld_data;
+  p.ld_b = a.ld_b;
+  p.ld_residual = a.ld_residual;
+  p.ld_c = a.ld_c;
+  p.timeout_ns = a.timeout_ns;
+  p.debug_flags = a.debug_flags;
+  return launched(launch_fp4_product(p, dev, s));
 }
 
 gemm_status_t quant_check(gemm_stream_t stream) { return check_word(1, reinterpret_cast<cudaStream_t>(stream)); }

@@ -17,6 +17,9 @@ size_t quant_columns_workspace(const quant_rows_t& a);
 constexpr int kQuantColumnTasks = 4;
 cudaError_t launch_quant_columns(const quant_rows_t* args, int count, cudaStream_t st);
 cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaStream_t st);
+// whether a linear layer goes in one kernel; if so, its launch
+bool fp4_linear_fused(const quant_linear_t& a);
+cudaError_t launch_fp4_linear(const quant_linear_t& a, const FfnDevice& dev, cudaStream_t st);
 cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, cudaStream_t st);
 
 // elements, scale columns and bytes of a quantised row

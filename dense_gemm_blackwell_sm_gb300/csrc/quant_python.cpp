@@ -159,13 +159,6 @@ Operand to_quantise(quant_rows_t* a, const char* name, const Tensor& x, int32_t 
   return o;
 }
 
-Operand quantised(const char* name, const Tensor& x, int32_t format, bool transpose, PyObject* stream) {
-  quant_rows_t a{};
-  Operand o = to_quantise(&a, name, x, format, transpose);
-  call(quant_rows, "quant_rows", a, o.index, stream, {&o.memory});
-  return o;
-}
-
 struct Several {
   quant_rows_t args[4];
   int32_t count;
@@ -179,48 +172,55 @@ struct Finish {
   int64_t timeout_ns;
 };
 
+// what becomes of the sums, for a product or a linear layer of M x N; the output
+template <typename Args>
+Tensor finish_arguments(Args* a, const Finish& f, int index) {
+  TORCH_CHECK_VALUE(f.dtype == at::kBFloat16 || f.dtype == at::kFloat, "the output must be bfloat16 or float32, not ",
+                    f.dtype);
+  a->out_dtype = code_of(f.dtype);
+  a->activation = f.activation;
+  a->flags = f.flags;
+  a->timeout_ns = f.timeout_ns;
+  a->debug_flags = f.debug_flags;
+  if (f.bias != nullptr) {
+    TORCH_CHECK_VALUE(f.bias->dim() == 1 && f.bias->size(0) == a->N && f.bias->scalar_type() == at::kFloat &&
+                          f.bias->is_contiguous() && f.bias->is_cuda() && f.bias->get_device() == index,
+                      "bias must be ", a->N, " dense values of float32 on cuda:", index);
+    a->bias = static_cast<const float*>(f.bias->data_ptr());
+  }
+  if (f.residual != nullptr) {
+    a->ld_residual = rows_of("residual", *f.residual, a->M, a->N, f.dtype, index);
+    a->residual = f.residual->data_ptr();
+  }
+  Tensor c;
+  if (f.out != nullptr) {
+    a->ld_c = rows_of("out", *f.out, a->M, a->N, f.dtype, index);
+    c = *f.out;
+  } else {
+    c = new_rows(a->M, a->N, f.dtype, index);
+  }
+  a->c = c.data_ptr();
+  return c;
+}
+
 Tensor multiplied(const Operand& a, const Operand& b, const Finish& f, PyObject* stream) {
   TORCH_CHECK_VALUE(a.format == b.format && a.cols == b.cols, "operands must have one format and as many columns, not ",
                     a.cols, " and ", b.cols);
   TORCH_CHECK_VALUE(a.index == b.index, "operands must be on one device");
-  TORCH_CHECK_VALUE(f.dtype == at::kBFloat16 || f.dtype == at::kFloat, "the output must be bfloat16 or float32, not ",
-                    f.dtype);
   quant_product_t p{};
   p.M = a.rows;
   p.N = b.rows;
   p.K = quant_width(a.cols);
   p.format = a.format;
-  p.out_dtype = code_of(f.dtype);
-  p.activation = f.activation;
-  p.flags = f.flags;
   p.a = a.data;
   p.b = b.data;
   p.scales_a = a.scales;
   p.scales_b = b.scales;
   p.row_scale_a = a.row_scale;
   p.row_scale_b = b.row_scale;
-  if (f.bias != nullptr) {
-    TORCH_CHECK_VALUE(f.bias->dim() == 1 && f.bias->size(0) == p.N && f.bias->scalar_type() == at::kFloat &&
-                          f.bias->is_contiguous() && f.bias->is_cuda() && f.bias->get_device() == a.index,
-                      "bias must be ", p.N, " dense values of float32 on cuda:", a.index);
-    p.bias = static_cast<const float*>(f.bias->data_ptr());
-  }
-  if (f.residual != nullptr) {
-    p.ld_residual = rows_of("residual", *f.residual, p.M, p.N, f.dtype, a.index);
-    p.residual = f.residual->data_ptr();
-  }
-  Tensor c;
-  if (f.out != nullptr) {
-    p.ld_c = rows_of("out", *f.out, p.M, p.N, f.dtype, a.index);
-    c = *f.out;
-  } else {
-    c = new_rows(p.M, p.N, f.dtype, a.index);
-  }
-  p.c = c.data_ptr();
   p.ld_a = a.ld;
   p.ld_b = b.ld;
-  p.timeout_ns = f.timeout_ns;
-  p.debug_flags = f.debug_flags;
+  const Tensor c = finish_arguments(&p, f, a.index);
   call(quant_product, "quant_product", p, a.index, stream, {&c});
   return c;
 }
@@ -245,7 +245,10 @@ Finish finish_of(PyObject* const* p) {
 PyObject* quantise(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 4);
-  return operand_tuple(quantised("x", tensor_of(p[0], "x"), format_of(p[1]), flag_of(p[2]), p[3]));
+  quant_rows_t a{};
+  const Operand o = to_quantise(&a, "x", tensor_of(p[0], "x"), format_of(p[1]), flag_of(p[2]));
+  call(quant_rows, "quant_rows", a, o.index, p[3], {&o.memory});
+  return operand_tuple(o);
   END_HANDLE_TH_ERRORS
 }
 
@@ -311,8 +314,7 @@ PyObject* product(PyObject*, PyObject* const* p, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (x, w's five values, and as product from out dtype on) -> y.  The operand made on the way
-// is read by a later call on the same stream, so the first call tells the allocator enough.
+// (x, w's five values, and as product from out dtype on) -> y
 PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 15);
@@ -321,7 +323,25 @@ PyObject* linear(PyObject*, PyObject* const* p, Py_ssize_t n) {
   const Finish f = finish_of(p + 6);
   TORCH_CHECK_VALUE(x.dim() == 2 && x.size(1) == w.cols, "x must be (M, ", w.cols, "), not ", x.sizes());
   TORCH_CHECK_VALUE(index_of(x) == w.index, "x and w must be on one device");
-  return wrapped(multiplied(quantised("x", x, w.format, false, p[12]), w, f, p[12]));
+  const at::ScalarType dtype = x.scalar_type();
+  quant_linear_t a{};
+  a.M = x.size(0);
+  a.N = w.rows;
+  a.K = w.cols;
+  a.dtype = code_of(dtype);
+  TORCH_CHECK_VALUE(a.dtype >= 0, "x must be float16, bfloat16 or float32, not ", dtype);
+  a.format = w.format;
+  a.ld_x = rows_of("x", x, a.M, a.K, dtype, w.index);
+  a.x = x.data_ptr();
+  a.b = w.data;
+  a.scales_b = w.scales;
+  a.row_scale_b = w.row_scale;
+  a.ld_b = w.ld;
+  const Tensor c = finish_arguments(&a, f, w.index);
+  const Tensor workspace = workspace_of(quant_linear_workspace(&a), w.index);
+  a.workspace = workspace.defined() ? workspace.data_ptr() : nullptr;
+  call(quant_linear, "quant_linear", a, w.index, p[12], {&c, &workspace});
+  return wrapped(c);
   END_HANDLE_TH_ERRORS
 }
 

@@ -61,6 +61,13 @@ class ProductArgs(ctypes.Structure):
                 ("reserved", _i32 * 3)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("dtype", _i32), ("format", _i32), ("out_dtype", _i32),
+                ("activation", _i32), ("flags", _i32), ("debug_flags", _i32), ("x", _p), ("b", _p), ("scales_b", _p),
+                ("row_scale_b", _p), ("bias", _p), ("residual", _p), ("c", _p), ("workspace", _p), ("ld_x", _i64),
+                ("ld_b", _i64), ("ld_residual", _i64), ("ld_c", _i64), ("timeout_ns", _i64)]
+
+
 class Quantised(collections.namedtuple("Quantised", ["data", "scales", "row_scale", "format", "cols"])):
     """A quantised operand: ``data`` (rows, row bytes), float8_e4m3fn or two 4-bit codes per
     byte (uint8); ``scales``, the tiled block scales' bytes, None for "e4m3"; ``row_scale``
@@ -79,11 +86,13 @@ def load():
     global _lib
     if _lib is None:
         lib = gemm.load()
-        for name, args in (("quant_rows", RowsArgs), ("quant_norm", NormArgs), ("quant_product", ProductArgs)):
+        for name, args in (("quant_rows", RowsArgs), ("quant_norm", NormArgs), ("quant_product", ProductArgs),
+                           ("quant_linear", LinearArgs)):
             f = getattr(lib, name)
             f.argtypes, f.restype = [ctypes.POINTER(args), _p], ctypes.c_int  # (a structure is passed by reference)
         lib.quant_rows_many.argtypes, lib.quant_rows_many.restype = [ctypes.POINTER(RowsArgs), _i32, _p], ctypes.c_int
         lib.quant_rows_workspace.argtypes, lib.quant_rows_workspace.restype = [ctypes.POINTER(RowsArgs)], _i64
+        lib.quant_linear_workspace.argtypes, lib.quant_linear_workspace.restype = [ctypes.POINTER(LinearArgs)], _i64
         lib.quant_width.argtypes, lib.quant_width.restype = [_i64], _i64
         lib.quant_row_bytes.argtypes, lib.quant_row_bytes.restype = [_i64, _i32], _i64
         lib.quant_scale_bytes.argtypes, lib.quant_scale_bytes.restype = [_i64, _i64, _i32], _i64
@@ -158,7 +167,8 @@ def product(a, b, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=N
 
 def linear(x, w, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=None, out=None, static_b=False,
            stream=None, timeout_ns=0, debug_flags=0):
-    """product(quantise(x, w.format), w, ...) for x (M, K) and a 4-bit weight w (N rows)."""
+    """product(quantise(x, w.format), w, ...) for x (M, K) and a 4-bit weight w (N rows); up to 16
+    tokens go in one kernel where the sizes allow it."""
     return (_calls or load_calls()).linear(x, *_values(w, "w"), _out_code(out_dtype), bias,
                                            _code(ACTIVATIONS, act, "act"), residual, out, static_b, stream,
                                            timeout_ns, debug_flags)

@@ -166,6 +166,38 @@ typedef struct {
 
 GEMM_API gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t stream);
 
+/* A linear layer: x's rows quantised to B's format, then the product,
+ *   C = act(Q(x) B^T + bias) + residual,
+ * with the bits of quant_rows and quant_product.  Up to 16 tokens go in one kernel where the
+ * sizes allow it. */
+typedef struct {
+  int64_t M, N, K;      /* K: values of a row of x; B's rows are quant_width(K) elements */
+  int32_t dtype;        /* ffn_dtype_t of x */
+  int32_t format;       /* QUANT_MXFP4 or QUANT_NVFP4, of B */
+  int32_t out_dtype;    /* as quant_product_t, from here on */
+  int32_t activation;
+  int32_t flags;
+  int32_t debug_flags;
+  const void* x;        /* M x K */
+  const void* b;
+  const void* scales_b;
+  const float* row_scale_b;
+  const float* bias;
+  const void* residual;
+  void* c;
+  void* workspace;      /* quant_linear_workspace bytes, 256-byte aligned; may be NULL if those are 0 */
+  int64_t ld_x;
+  int64_t ld_b;         /* bytes */
+  int64_t ld_residual, ld_c;
+  int64_t timeout_ns;
+} quant_linear_t;
+
+/* Bytes of workspace of this call (it reads sizes, types and format, no array); -1 for sizes it
+ * would refuse. */
+GEMM_API int64_t quant_linear_workspace(const quant_linear_t* args);
+
+GEMM_API gemm_status_t quant_linear(const quant_linear_t* args, gemm_stream_t stream);
+
 /* Synchronise `stream`, then report (and clear) a device-side error recorded by this
  * header's kernels on the current device. */
 GEMM_API gemm_status_t quant_check(gemm_stream_t stream);

@@ -206,3 +206,50 @@ def test_refusals_of_tensors():
     # (without row scales they count as one)
     c = quant.product(a._replace(row_scale=None), b, out_dtype=torch.float32)
     assert torch.equal(c, quant.product(a._replace(row_scale=torch.ones(4, device=DEV)), b, out_dtype=torch.float32))
+
+
+# the tokens' quantisation inside the product (up to 16 of them) and before it: one cluster and
+# several CTAs that share a sum, ragged K and N, strided and misaligned tokens
+LINEAR = [(1, 1, 1), (1, 130, 33), (5, 128, 96), (16, 300, 520), (16, 4096, 2048), (3, 1000, 4096), (8, 257, 4104),
+          (1, 20000, 1000), (17, 130, 96), (4, 9800, 4096),
+          (2, 512, 20000)]
+
+
+@pytest.mark.parametrize("shape", LINEAR)
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_linear_has_the_bits_of_its_parts(shape, fmt, dtype):
+    M, N, K = shape
+    gen = torch.Generator().manual_seed(M * 1000 + N + K)
+    wide = torch.randn(M, K + 13, generator=gen) * 2.0 ** torch.randint(-6, 7, (M, 1), generator=gen)
+    w = quant.quantise(torch.randn(N, K, generator=gen).to(DEV), fmt)
+    bias = torch.randn(N, generator=gen).to(DEV)
+    residual = torch.randn(M, N, generator=gen).to(DEV)
+    for x in (wide[:, :K].contiguous().to(DEV, dtype), wide.to(DEV, dtype)[:, 5:K + 5]):
+        q = quant.quantise(x, fmt)
+        for kw in (dict(), dict(bias=bias, act="silu", residual=residual, out_dtype=torch.float32, static_b=True)):
+            assert torch.equal(quant.linear(x, w, **kw), quant.product(q, w, **kw))
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+def test_linear_with_nan_infinity_and_empty_rows(fmt):
+    x = torch.randn(7, 2100, generator=torch.Generator().manual_seed(5)).to(DEV, torch.bfloat16)
+    x[1, 3] = float("nan")
+    x[2, 2099] = float("inf")
+    x[3] = 0
+    x[4, 1024:1056] = float("-inf")
+    x[5] = -2.0 ** 100
+    w = quant.quantise(torch.randn(600, 2100, generator=torch.Generator().manual_seed(6)).to(DEV), fmt)
+    got, want = quant.linear(x, w), quant.product(quant.quantise(x, fmt), w)
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(), want.nan_to_num())
+    assert got[[1, 2, 4]].isnan().all() and not got[[0, 3, 5, 6]].isnan().any() and (got[3] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+def test_linear_that_waits_too_long_is_reported(fmt):
+    w = quant.quantise(torch.randn(512, 1024, device=DEV), fmt)
+    x = torch.randn(4, 1024, device=DEV, dtype=torch.bfloat16)
+    want = quant.linear(x, w)
+    quant.linear(x, w, timeout_ns=20_000_000, debug_flags=quant.DEBUG_SKIP_ONE_LOAD)
+    assert quant.check() == gemm.ERR_DEVICE_TIMEOUT
+    assert torch.equal(quant.linear(x, w), want) and quant.check() == gemm.OK

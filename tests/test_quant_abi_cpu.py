@@ -29,13 +29,14 @@ def lib():
 def test_every_declared_symbol_is_exported(lib):
     text = open(os.path.join(ROOT, "include", "quant.h")).read()
     names = re.findall(r"GEMM_API\s+[\w\s\*]+?\b(quant_\w+)\s*\(", text)
-    assert len(names) == 9
+    assert len(names) == 11
     for n in names:
         assert hasattr(lib, n), n
 
 
 def test_structures_match_the_header(tmp_path):
-    structs = {"quant_rows_t": quant.RowsArgs, "quant_norm_t": quant.NormArgs, "quant_product_t": quant.ProductArgs}
+    structs = {"quant_rows_t": quant.RowsArgs, "quant_norm_t": quant.NormArgs, "quant_product_t": quant.ProductArgs,
+               "quant_linear_t": quant.LinearArgs}
     lines = ["#include <cstddef>", "#include <cstdio>", '#include "quant.h"', "int main() {"]
     want = []
     for c, py in structs.items():
@@ -138,6 +139,37 @@ def test_product_refusals(lib, change, status):
     assert lib.quant_product(ctypes.byref(product_args(**change)), None) == status
 
 
+def linear_args(**kw):
+    a = dict(M=40, N=8, K=64, dtype=ffn.BF16, format=quant.NVFP4, out_dtype=ffn.BF16, x=P, b=P, scales_b=P, c=P, workspace=P)
+    a.update(kw)
+    return quant.LinearArgs(**a)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(format=quant.MXE4M3), gemm.ERR_UNSUPPORTED_DTYPE), (dict(dtype=3), gemm.ERR_UNSUPPORTED_DTYPE),
+    (dict(out_dtype=ffn.F16), gemm.ERR_UNSUPPORTED_DTYPE), (dict(M=-1), gemm.ERR_INVALID_ARG),
+    (dict(N=BIG), gemm.ERR_INVALID_ARG), (dict(K=-1), gemm.ERR_INVALID_ARG), (dict(K=BIG - 32), gemm.ERR_INVALID_ARG),
+    (dict(activation=-1), gemm.ERR_INVALID_ARG), (dict(flags=4), gemm.ERR_INVALID_ARG),
+    (dict(timeout_ns=-1), gemm.ERR_INVALID_ARG), (dict(x=0), gemm.ERR_INVALID_ARG), (dict(b=0), gemm.ERR_INVALID_ARG),
+    (dict(scales_b=0), gemm.ERR_INVALID_ARG), (dict(c=0), gemm.ERR_INVALID_ARG), (dict(workspace=0), gemm.ERR_INVALID_ARG),
+    (dict(ld_x=63), gemm.ERR_INVALID_ARG), (dict(ld_b=16), gemm.ERR_INVALID_ARG), (dict(ld_b=40), gemm.ERR_MISALIGNED),
+    (dict(ld_c=7), gemm.ERR_INVALID_ARG), (dict(ld_residual=7), gemm.ERR_INVALID_ARG), (dict(x=P + 1), gemm.ERR_MISALIGNED),
+    (dict(b=P + 8), gemm.ERR_MISALIGNED), (dict(scales_b=P + 4), gemm.ERR_MISALIGNED), (dict(c=P + 1), gemm.ERR_MISALIGNED),
+    (dict(bias=P + 2), gemm.ERR_MISALIGNED), (dict(row_scale_b=P + 1), gemm.ERR_MISALIGNED),
+    (dict(residual=P + 1), gemm.ERR_MISALIGNED), (dict(workspace=P + 16), gemm.ERR_MISALIGNED),
+    (dict(M=0), gemm.OK), (dict(N=0), gemm.OK)])
+def test_linear_refusals(lib, change, status):
+    assert lib.quant_linear(ctypes.byref(linear_args(**change)), None) == status
+
+
+def test_linear_workspace(lib):
+    size = lambda **kw: lib.quant_linear_workspace(ctypes.byref(linear_args(**kw)))  # noqa: E731
+    # the quantised rows: codes, tiled scales, row scales, each to 256 bytes; none in one kernel
+    assert size() == 40 * 32 // 256 * 256 + 512 + 256 and size(format=quant.MXFP4) == 1280 + 512
+    assert size(M=16) == 0 and size(M=0) == 0 and size(N=0) == 0 and size(M=-1) == -1
+    assert size(M=8, N=14336, K=65536) > 0 and lib.quant_linear_workspace(None) == -1
+
+
 def test_many_rows_refusals(lib):
     # one refused array refuses all; none is no work
     two = (quant.RowsArgs * 2)(rows_args(rows=0), rows_args(dtype=3))
@@ -148,5 +180,5 @@ def test_many_rows_refusals(lib):
 
 
 def test_null_arguments(lib):
-    for f in (lib.quant_rows, lib.quant_norm, lib.quant_product):
+    for f in (lib.quant_rows, lib.quant_norm, lib.quant_product, lib.quant_linear):
         assert f(None, None) == gemm.ERR_INVALID_ARG
