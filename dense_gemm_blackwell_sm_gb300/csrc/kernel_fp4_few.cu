@@ -2,7 +2,7 @@
 // small layers.
 //
 // The roles of the operands are exchanged: 128 rows of B (a layer's features) are the MMA's M,
-// up to 128 rows of A (tokens) its N, so that a decoded token costs an MMA of 16 columns and
+// up to 64 rows of A (tokens) its N, so that a decoded token costs an MMA of 16 columns and
 // B's rows stream through shared memory once.  A cluster of `split` CTAs shares a tile's sum:
 // each takes a part of K, the partial sums meet in distributed shared memory, in a fixed order.
 // Two CTAs fit an SM, so that one's copies run while the other ends.
@@ -36,11 +36,6 @@ struct FewShape {
 template <bool NV>
 constexpr uint32_t kSlot = 8u * kScaleBlocks<NV>;  // TMEM columns of a stage's scales
 
-
-// Sums [begin, end) of a tile's [token][feature] from the cluster's SPLIT CTAs, in the order of
-// their ranks, to c: V neighbours a time.  What a thread reads from the CTAs is under way
-// together (8 groups of 4 or 8 single values): one after the other, eight reads of distributed
-// shared memory took 2 us.
 __host__ __device__ inline uint32_t stage_bytes(int blocks, int tokens) {
   return kOperand + (uint32_t)tokens * 128u + 2u * 512u * (uint32_t)blocks;
 }
@@ -72,6 +67,10 @@ __host__ __device__ inline FewShape few_shape(int blocks, int tokens) {
   return f;
 }
 
+// Sums [begin, end) of a tile's [token][feature] from the cluster's SPLIT CTAs, in the order of
+// their ranks, to c: V neighbours a time.  What a thread reads from the CTAs is under way
+// together (8 groups of 4 or 8 single values): one after the other, eight reads of distributed
+// shared memory took 2 us.
 template <int V, int SPLIT, typename OutT>
 __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* token_scale, const float* partial,
                                            int32_t begin, int32_t end, int32_t row0, int32_t col0) {

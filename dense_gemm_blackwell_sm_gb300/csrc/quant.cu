@@ -46,14 +46,35 @@ gemm_status_t rows_sizes(const quant_rows_t& a) {
   return GEMM_OK;
 }
 
-gemm_status_t linear_sizes(const quant_linear_t& a) {
-  if ((a.format != QUANT_MXFP4 && a.format != QUANT_NVFP4) || !is_dtype(a.dtype)) return GEMM_ERR_UNSUPPORTED_DTYPE;
+// The sizes and choices of a product or a linear layer (columns past N are counted in 32 bits, and
+// so are tiles).
+template <typename Args>
+gemm_status_t product_sizes(const Args& a) {
+  if (a.format != QUANT_MXFP4 && a.format != QUANT_NVFP4) return GEMM_ERR_UNSUPPORTED_DTYPE;
   if (a.out_dtype != FFN_BF16 && a.out_dtype != FFN_F32) return GEMM_ERR_UNSUPPORTED_DTYPE;
-  if (a.M < 0 || a.N < 0 || a.K < 0 || a.M >= kMaxDim || a.N >= kMaxDim || a.K >= kMaxDim - 32 || a.timeout_ns < 0)
-    return GEMM_ERR_INVALID_ARG;
+  if (a.M < 0 || a.N < 0 || a.M > kMaxDim - 512 || a.N > kMaxDim - 512 || a.timeout_ns < 0) return GEMM_ERR_INVALID_ARG;
   if (a.activation < GEMM_ACT_NONE || a.activation > GEMM_ACT_GELU_ERF || (a.flags & ~QUANT_STATIC_B) != 0)
     return GEMM_ERR_INVALID_ARG;
+  if (((a.M + 255) / 256) * ((a.N + 255) / 256) >= kMaxDim / 4) return GEMM_ERR_UNSUPPORTED_SHAPE;
   return GEMM_OK;
+}
+
+gemm_status_t linear_sizes(const quant_linear_t& a) {
+  if (!is_dtype(a.dtype)) return GEMM_ERR_UNSUPPORTED_DTYPE;
+  const gemm_status_t st = product_sizes(a);
+  if (st != GEMM_OK) return st;
+  return a.K < 0 || a.K >= kMaxDim - 32 ? GEMM_ERR_INVALID_ARG : GEMM_OK;
+}
+
+// Whether rows x (of `x_row` bytes each, `x_pitch` apart) and rows c share a byte: columns of one
+// array's rows do not.
+bool rows_overlap(const void* x, int64_t rows, int64_t x_row, int64_t x_pitch, const void* c, int64_t c_row,
+                  int64_t c_pitch) {
+  const intptr_t x0 = reinterpret_cast<intptr_t>(x), c0 = reinterpret_cast<intptr_t>(c);
+  if (x_row == 0 || c0 >= x0 + (rows - 1) * x_pitch + x_row || x0 >= c0 + (rows - 1) * c_pitch + c_row) return false;
+  if (x_pitch != c_pitch) return true;
+  const int64_t apart = ((c0 - x0) % x_pitch + x_pitch) % x_pitch;
+  return apart < x_row || apart + c_row > x_pitch;
 }
 
 // where the quantised rows of a linear layer lie in its workspace
@@ -170,12 +191,9 @@ gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream) {
 gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t stream) {
   if (!args) return GEMM_ERR_INVALID_ARG;
   quant_product_t a = *args;
-  if (a.format != QUANT_MXFP4 && a.format != QUANT_NVFP4) return GEMM_ERR_UNSUPPORTED_DTYPE;
-  if (a.out_dtype != FFN_BF16 && a.out_dtype != FFN_F32) return GEMM_ERR_UNSUPPORTED_DTYPE;
-  if (a.M < 0 || a.N < 0 || a.K < 32 || a.M >= kMaxDim || a.N >= kMaxDim || a.K >= kMaxDim || a.timeout_ns < 0)
-    return GEMM_ERR_INVALID_ARG;
-  if (a.activation < GEMM_ACT_NONE || a.activation > GEMM_ACT_GELU_ERF || (a.flags & ~QUANT_STATIC_B) != 0)
-    return GEMM_ERR_INVALID_ARG;
+  const gemm_status_t sizes = product_sizes(a);
+  if (sizes != GEMM_OK) return sizes;
+  if (a.K < 32 || a.K >= kMaxDim) return GEMM_ERR_INVALID_ARG;
   if (a.K % 32 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
   if (!pitch(&a.ld_a, a.K / 2) || !pitch(&a.ld_b, a.K / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N))
     return GEMM_ERR_INVALID_ARG;
@@ -213,6 +231,9 @@ gemm_status_t quant_linear(const quant_linear_t* args, gemm_stream_t stream) {
       !aligned(a.row_scale_b, 4) || !aligned(a.bias, 4) || !aligned(a.residual, e) || !aligned(a.c, e) ||
       !aligned(a.workspace, 256))
     return GEMM_ERR_MISALIGNED;
+  if (rows_overlap(a.x, a.M, a.K * (int64_t)elem(a.dtype), a.ld_x * (int64_t)elem(a.dtype), a.c, a.N * (int64_t)e,
+                   a.ld_c * (int64_t)e))
+    return GEMM_ERR_INVALID_ARG;
   const bool fused = fp4_linear_fused(a);
   if (!fused && !a.workspace) return GEMM_ERR_INVALID_ARG;
   FfnDevice dev;

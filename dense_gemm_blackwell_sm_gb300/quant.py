@@ -158,8 +158,7 @@ def product(a, b, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=N
     """act(a @ b.T + bias) + residual for 4-bit operands a (M rows) and b (N rows) of one
     format and as many columns: (M, N), bfloat16 or float32.  bias is (N) float32, residual
     (M, N) of the output's type; it may be ``out``.  With ``static_b`` the kernel may read b
-    while the one before it on the stream still runs: for weights, which that one does not
-    write."""
+    while those before it on the stream still run: for weights, which these do not write."""
     return (_calls or load_calls()).product(*_values(a, "a"), *_values(b, "b"), _out_code(out_dtype), bias,
                                             _code(ACTIVATIONS, act, "act"), residual, out, static_b, stream,
                                             timeout_ns, debug_flags)
@@ -168,7 +167,8 @@ def product(a, b, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=N
 def linear(x, w, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=None, out=None, static_b=False,
            stream=None, timeout_ns=0, debug_flags=0):
     """product(quantise(x, w.format), w, ...) for x (M, K) and a 4-bit weight w (N rows); up to 16
-    tokens go in one kernel where the sizes allow it."""
+    tokens go in one kernel where that is as fast or faster.  ``out`` must not share memory with
+    x."""
     return (_calls or load_calls()).linear(x, *_values(w, "w"), _out_code(out_dtype), bias,
                                            _code(ACTIVATIONS, act, "act"), residual, out, static_b, stream,
                                            timeout_ns, debug_flags)

@@ -104,7 +104,7 @@ GEMM_API gemm_status_t quant_rows_many(const quant_rows_t* args, int32_t count, 
 
 /* s = residual_scale * residual + branch_scale * y
  * n = s / sqrt(mean(s^2) + eps) * weight, from s before it is rounded, in fp32
- * and n quantised by rows.  Absent (NULL) weight counts as one, an absent residual as
+ * and n quantised by rows (a row whose sum of squares passes fp32's range comes as zeros).  Absent (NULL) weight counts as one, an absent residual as
  * zero; s is written if given and may be `residual` or y itself (same pointer and
  * pitch).  The gradient with respect to y, residual and weight is ffn_norm_backward's,
  * dn being what reaches the values that the operand stands for. */
@@ -128,8 +128,8 @@ typedef struct {
 
 GEMM_API gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream);
 
-/* B is not written by the kernel before this one on the stream (weights): it may be read
- * before that kernel has completed. */
+/* B is not written by the kernels just before this one on the stream (weights): it may be
+ * read before they have completed. */
 #define QUANT_STATIC_B 1
 
 /* Test hook: one copy of the first stage is left out, so that a bounded wait runs out and
@@ -140,8 +140,9 @@ GEMM_API gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream
  * for A (M x K) and B (N x K) of one 4-bit format, QUANT_MXFP4 or QUANT_NVFP4, each value
  * in units of its block's scale.  Sums are accumulated in fp32 on the Tensor Core, the
  * epilogue is fp32 and each element is rounded once.  The order of a sum depends on the
- * sizes alone: the same inputs give the same bits.  K is the operands' width, a multiple
- * of 32 below 2^31.  M and N may be 0. */
+ * sizes alone: the same inputs give the same bits.  The sum is multiplied by row_scale_a and
+ * then by row_scale_b, in fp32.  K is the operands' width, a multiple of 32 below 2^31.  M
+ * and N may be 0 and are at most 2^31 - 512. */
 typedef struct {
   int64_t M, N, K;
   int32_t format;       /* QUANT_MXFP4 or QUANT_NVFP4, of both operands */
@@ -168,8 +169,8 @@ GEMM_API gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t 
 
 /* A linear layer: x's rows quantised to B's format, then the product,
  *   C = act(Q(x) B^T + bias) + residual,
- * with the bits of quant_rows and quant_product.  Up to 16 tokens go in one kernel where the
- * sizes allow it. */
+ * with the bits of quant_rows and quant_product.  Up to 16 tokens go in one kernel where that
+ * is as fast or faster.  C must not share a byte with x (a call where it does is refused). */
 typedef struct {
   int64_t M, N, K;      /* K: values of a row of x; B's rows are quant_width(K) elements */
   int32_t dtype;        /* ffn_dtype_t of x */

@@ -140,7 +140,7 @@ def test_product_refusals(lib, change, status):
 
 
 def linear_args(**kw):
-    a = dict(M=40, N=8, K=64, dtype=ffn.BF16, format=quant.NVFP4, out_dtype=ffn.BF16, x=P, b=P, scales_b=P, c=P, workspace=P)
+    a = dict(M=40, N=8, K=64, dtype=ffn.BF16, format=quant.NVFP4, out_dtype=ffn.BF16, x=P, b=P, scales_b=P, c=4 * P, workspace=P)
     a.update(kw)
     return quant.LinearArgs(**a)
 
@@ -157,6 +157,11 @@ def linear_args(**kw):
     (dict(b=P + 8), gemm.ERR_MISALIGNED), (dict(scales_b=P + 4), gemm.ERR_MISALIGNED), (dict(c=P + 1), gemm.ERR_MISALIGNED),
     (dict(bias=P + 2), gemm.ERR_MISALIGNED), (dict(row_scale_b=P + 1), gemm.ERR_MISALIGNED),
     (dict(residual=P + 1), gemm.ERR_MISALIGNED), (dict(workspace=P + 16), gemm.ERR_MISALIGNED),
+    (dict(M=BIG - 511), gemm.ERR_INVALID_ARG), (dict(M=1 << 30, N=1 << 30), gemm.ERR_UNSUPPORTED_SHAPE),
+    # C on x, on its second row, over columns of its rows; beside them and behind them all is well
+    (dict(x=P, c=P), gemm.ERR_INVALID_ARG), (dict(c=P + 128, K=64), gemm.ERR_INVALID_ARG),
+    (dict(ld_x=96, ld_c=96, c=P + 112), gemm.ERR_INVALID_ARG), (dict(ld_x=96, ld_c=80, c=P + 128), gemm.ERR_INVALID_ARG),
+    (dict(ld_x=96, ld_c=96, c=P + 2 * 90), gemm.ERR_INVALID_ARG), (dict(c=P - 16, ld_c=64), gemm.ERR_INVALID_ARG),
     (dict(M=0), gemm.OK), (dict(N=0), gemm.OK)])
 def test_linear_refusals(lib, change, status):
     assert lib.quant_linear(ctypes.byref(linear_args(**change)), None) == status
