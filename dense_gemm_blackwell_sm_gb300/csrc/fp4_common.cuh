@@ -61,16 +61,46 @@ __device__ __forceinline__ void fp4_act(float (&x)[N], int32_t act) {
   }
 }
 
+// 16 bytes of residuals of a row from column col on, zeros behind the last column (rows are aligned)
+template <typename OutT>
+__device__ __forceinline__ uint4 residual16(const Fp4Epilogue& e, int32_t row, int32_t col) {
+  constexpr int n = 16 / (int)sizeof(OutT);
+  const OutT* src = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
+  if (col + n <= e.N) return *reinterpret_cast<const uint4*>(src);
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int j = 0; j < n; ++j)
+    if (col + j < e.N) reinterpret_cast<OutT*>(&u)[j] = src[j];
+  return u;
+}
+
+// A lane's 32 residuals, of its row and of columns col .. col + 31: bf16 ones are loaded ahead of
+// their use, 32 of fp32 leave no registers for that and are loaded where they are added.  (A tile's
+// rows by neighbouring lanes, or fetched to L2 before, gain at most 5 %.)
+template <typename OutT>
+struct Residual32 {
+  uint4 u[4];
+  __device__ __forceinline__ void load(const Fp4Epilogue& e, int32_t row, int32_t col) {
+    if constexpr (sizeof(OutT) == 2) {
+      if (e.residual == nullptr || e.vec == 0 || row >= e.M) return;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u[q] = residual16<OutT>(e, row, col + 8 * q);
+    }
+  }
+};
+
 // 32 x 32 sums, a lane's row in v, of columns col .. col + 31, to c: scaled, finished, rounded
 // into `staging` (4096 bytes of the warp's, 1024-byte aligned) and stored from there, by a TMA
 // copy where c's rows are aligned to 16 bytes (tmC: boxes of 32 x 32, swizzled over 128 bytes for
 // fp32 and 64 for bf16), else by the lanes, each a column, so that they write neighbours.
-// `scale` and `bias`: the columns' values in shared memory.  Every lane of the warp calls it;
-// `buffer` counts the warp's copies: bf16 takes the halves of the staging space in turn.
+// `res`: the residuals; `scale` and `bias`: the columns' values in shared memory.  Every lane of
+// the warp calls it; `buffer` counts the warp's copies: bf16 takes the halves of the staging space
+// in turn.
 template <typename OutT>
 __device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const CUtensorMap* tmC, const uint32_t (&v)[32],
-                                            int32_t row0, int32_t col, float sa, const float* scale, const float* bias,
-                                            uint8_t* staging, uint32_t& buffer, uint32_t lane) {
+                                            const Residual32<OutT>& res, int32_t row0, int32_t col, float sa,
+                                            const float* scale, const float* bias, uint8_t* staging, uint32_t& buffer,
+                                            uint32_t lane) {
   if (row0 >= e.M || col >= e.N) return;
   const int32_t row = row0 + (int32_t)lane;
   float x[32];
@@ -86,40 +116,31 @@ __device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const CUtensor
   if (e.vec != 0) {
     constexpr int per16 = 16 / (int)sizeof(OutT);
     if (e.residual != nullptr && row < e.M) {
-      const OutT* src = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
 #pragma unroll
       for (int q = 0; q < 32 / per16; ++q) {
-        if (col + q * per16 + per16 <= e.N) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src + q * per16);
-          const OutT* w = reinterpret_cast<const OutT*>(&u);
+        uint4 u;
+        if constexpr (sizeof(OutT) == 2) u = res.u[q];
+        else u = residual16<OutT>(e, row, col + q * per16);
+        const OutT* w = reinterpret_cast<const OutT*>(&u);
 #pragma unroll
-          for (int j = 0; j < per16; ++j) x[q * per16 + j] += to_f32(w[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < per16; ++j)
-            if (col + q * per16 + j < e.N) x[q * per16 + j] += to_f32(src[q * per16 + j]);
-        }
+        for (int j = 0; j < per16; ++j) x[q * per16 + j] += to_f32(w[j]);
       }
     }
     uint8_t* buf = staging + (sizeof(OutT) == 2 ? (buffer++ & 1u) * 2048u : 0u);
     // the copy issued from this buffer before has read it
     if (lane == 0) bulk_wait_group_read<sizeof(OutT) == 2 ? 1 : 0>();
     __syncwarp();
-    if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<float4*>(buf + sw128_offset(lane, (uint32_t)j)) =
-            make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-    } else {
+    for (uint32_t j = 0; j < 32 / per16; ++j) {
+      uint32_t o[4];
 #pragma unroll
-      for (uint32_t j = 0; j < 4; ++j) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = pack_bf16x2(__float_as_uint(x[8 * j + 2 * i]), __float_as_uint(x[8 * j + 2 * i + 1]));
-        // 64-byte rows swizzled: the 16-byte piece's index takes bits 1 and 2 of the row
-        *reinterpret_cast<uint4*>(buf + lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(OutT) == 4) o[i] = __float_as_uint(x[4 * j + i]);
+        else o[i] = pack_bf16x2(__float_as_uint(x[8 * j + 2 * i]), __float_as_uint(x[8 * j + 2 * i + 1]));
       }
+      // (64-byte rows swizzled: the 16-byte piece's index takes bits 1 and 2 of the row)
+      const uint32_t at = sizeof(OutT) == 4 ? sw128_offset(lane, j) : lane * 64u + ((j ^ ((lane >> 1) & 3u)) << 4);
+      *reinterpret_cast<uint4*>(buf + at) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_smem();
     __syncwarp();

@@ -367,17 +367,15 @@ PyObject* linear_backward(PyObject*, PyObject* const* p, Py_ssize_t n) {
   f.activation = GEMM_ACT_NONE;
   f.timeout_ns = int_of(p[8]);
   Tensor dx, dw;
-  // (columns one after the other: they go in one launch)
+  // (columns one after the other: they go in few launches)
   Several s{};
   Operand dy_rows, w_columns, dy_columns, x_columns;
-  if (need_dx) {
-    dy_rows = to_quantise(&s.args[s.count++], "dy", dy, format, false);
-    w_columns = to_quantise(&s.args[s.count++], "w", *w, format, true);
-  }
+  if (need_dx) dy_rows = to_quantise(&s.args[s.count++], "dy", dy, format, false);
   if (need_dw) {
     dy_columns = to_quantise(&s.args[s.count++], "dy", dy, format, true);
     x_columns = to_quantise(&s.args[s.count++], "x", *x, format, true);
   }
+  if (need_dx) w_columns = to_quantise(&s.args[s.count++], "w", *w, format, true);
   call(quant_several, "quant_rows_many", s, index, p[7],
        {&dy_rows.memory, &w_columns.memory, &dy_columns.memory, &x_columns.memory});
   if (need_dx) dx = multiplied(dy_rows, w_columns, f, p[7]);

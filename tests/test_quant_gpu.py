@@ -324,3 +324,26 @@ def test_refusals_of_tensors():
         quant.norm_quantise(x, weight=torch.ones(64, device=DEV, dtype=torch.float16), format="e4m3")
     with pytest.raises(gemm.GemmError):
         quant.norm_quantise(torch.zeros(1, 32769, dtype=torch.bfloat16, device=DEV), format="e4m3")
+
+
+# columns with a scale each: one part and many, of unequal length; few columns and many, ragged and
+# off a boundary
+WHOLE = [(1, 3), (64, 65), (130, 70), (512, 20000), (1000, 513), (1025, 100), (2049, 64), (4097, 260), (8193, 40), (14336, 33),
+         (14337, 33), (20000, 70)]
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "nvfp4"])
+@pytest.mark.parametrize("shape", WHOLE)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+def test_columns_are_the_rows_of_the_transpose(fmt, shape, dtype):
+    # (rows are compared with the definition above; columns may differ from them in no bit)
+    gen = torch.Generator().manual_seed(shape[0])
+    wide = torch.randn(shape[0], shape[1] + 9, generator=gen) * 2.0 ** torch.randint(-4, 5, (1, shape[1] + 9), generator=gen)
+    wide[shape[0] // 2, 1:shape[1]:7] = 0
+    wide[:, 2::11] = 0
+    wide[shape[0] - 1, 5::13] = float("nan")
+    wide = wide.to(DEV, dtype)
+    for x in (wide[:, :shape[1]].contiguous(), wide[:, 3:shape[1] + 3]):
+        got, want = quant.quantise(x, fmt, transpose=True), quant.quantise(x.t().contiguous(), fmt)
+        for a, b in ((got.data, want.data), (got.scales, want.scales), (got.row_scale, want.row_scale)):
+            assert (a is None and b is None) or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
