@@ -9,7 +9,12 @@
 // and before that kernel has ended.
 // Up to kTasks arrays go in one launch.
 //
-// Bound by memory: 2 bytes read per element, 0.56 to 1.03 written.
+// Bound by memory: 2 bytes read per element, 0.53 to 1.03 written.  14336 x 4096 bf16: to MXFP8
+// 32.8 us (5.4 TB/s), MXFP4 31.1; with a scale per column (read twice) 54, and 515 x 1097 9 where
+// one kernel takes 6.  8192 x 4096 fp32 34 to 36, with a scale per column 58 and, NVFP4's divisions,
+// 72.  Held whole in the shared memory of a cluster, so that they are read once, columns take
+// longer: loads, the exchange of the magnitudes and the codes then follow one another (14336 x 4096
+// 66 to 77 us).
 #include <algorithm>
 #include <type_traits>
 

@@ -48,7 +48,8 @@ def device(o):
 
 # one token; tails of every kind; K of less than an MMA, of a whole stage, of more; few tiles and many
 SHAPES = [(1, 1, 1), (1, 128, 32), (3, 130, 64), (16, 256, 96), (17, 200, 256), (64, 384, 288), (100, 1000, 512),
-          (129, 128, 1024), (130, 520, 4096), (8, 4096, 2048), (700, 3000, 320), (1100, 2500, 608), (300, 6000, 96)]
+          (129, 128, 1024), (130, 520, 4096), (8, 4096, 2048), (700, 3000, 320), (1100, 2500, 608), (300, 6000, 96),
+          (65, 9800, 64), (512, 2432, 128), (513, 2432, 128)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
