@@ -119,13 +119,16 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
   void** args = few_args;
   if (!encode_scale_blocks(&maps[2], a.scales_a, across, (uint64_t)up(a.M, 128), box_k, 1)) return cudaErrorInvalidValue;
 
-  // Tiles of 64 x 128 with a sum shared by a cluster while they are no more than SMs; above that CTA
-  // pairs, but for M <= 64, where half of a pair's rows or more would be empty.  Few and pair, MXFP4:
+  // Tiles of 64 x 128 with a sum shared by a cluster while they are no more than SMs, or two an SM with
+  // short sums; above that CTA pairs, but for M <= 64, where most of a pair's rows would be empty.
+  // (A pair's CTAs fill their SMs: they start when the kernel before has left.)  Few and pair, MXFP4:
   // 512 x 2048 x 4096 (128 tiles) 8.8 and 10.4 us, 256 x 4096 x 14336 (128) 17.2 and 24.9, 768 x 2048 x
   // 4096 (192) 12.1 and 10.5, 512 x 4096 x 4096 (256) 12.5 and 11.1, 640 x 4096 x 4096 (320) 22.5 and
-  // 11.8; 128 x 14336 x 4096 (224) 13.3 and 13.7, NVFP4 15.6 and 14.5.
+  // 11.8, 512 x 4096 x 1024 (256) 8.0 and 7.2; 128 x 14336 x 4096 (224) 13.3 and 13.7, NVFP4 15.6 and
+  // 14.5; 1097 x 1032 x 544 (162) behind another product 8.6 and 10.4.
   const int64_t pair_tiles = up(a.M, 256) * up(a.N, 256);
-  if (a.M > 64 && up(a.M, 64) * up(a.N, 128) > dev.num_sms) {
+  const int64_t few_tiles = up(a.M, 64) * up(a.N, 128);
+  if (a.M > 64 && few_tiles > (a.K < 1024 ? 2 : 1) * (int64_t)dev.num_sms) {
     p.tiles_m = (int32_t)up(a.M, 256);
     p.tiles_n = (int32_t)up(a.N, 256);
     // (both operands lie in L2 at sizes where that matters: 32 rows of tiles against 8 take 8192 x
