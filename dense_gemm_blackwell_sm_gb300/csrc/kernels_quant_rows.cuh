@@ -11,9 +11,9 @@
 // norm) are read twice.
 //
 // Bound by memory: 2 bytes read and 0.53 to 1.03 written per element (norm: 4 and 2 more).  8192 x
-// 4096 bf16: to E4M3 18.6 us, MXFP8 18.7 (5.4 TB/s), MXFP4 16.5, NVFP4 18.1; the norm to MXFP8 42.5
-// (5.5 TB/s), E4M3 41.1, 4 bits 41.3 and 42.6.  fp32: 25 to 26 us (6.4 TB/s), NVFP4's divisions 34; the
-// norm 63 to 70.  Rows of 4095 columns, off 16-byte boundaries, 24 to 33.  One row of 4096: 1.5 and
+// 4096 bf16: to E4M3 18.3 us, MXFP8 18.5 (5.5 TB/s), MXFP4 16.4, NVFP4 18.0; the norm to all of them 41
+// (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.4 TB/s), NVFP4's divisions 34; the
+// norm 63 to 70.  Rows of 4095 columns, off 16-byte boundaries, 23 to 33.  One row of 4096: 1.5 and
 // 2.6 us, a launch and a row's latency.
 #pragma once
 
@@ -24,8 +24,8 @@
 namespace dgb {
 
 struct QuantRowsParams {
-  int64_t rows;        // of the input
-  int64_t all_rows;    // and of the scale array: rows past the last one get zero bytes
+  uint32_t rows;       // of the input
+  uint32_t all_rows;   // and of the scale array: rows past the last one get zero bytes
   int32_t cols;
   int32_t chunks;      // runs of 16 elements of a padded row
   int32_t all_chunks;  // and of the scale array's columns
@@ -38,7 +38,7 @@ struct QuantRowsParams {
   uint8_t* data;
   uint8_t* scales;
   float* row_scale;
-  int64_t ld_x, ld_residual, ld_s, ld_data;
+  uint32_t ld_x, ld_residual, ld_s, ld_data;  // (below 2^31: an address is one wide multiplication)
   int32_t weight_f32;  // weight is fp32 (else the inputs' type)
   int32_t weight_vec;
   const void* x_end;   // the first byte past the last element of x, of the residual, of the weight
@@ -207,11 +207,11 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
   let_next_kernel_start();
   const int32_t threads = (int32_t)blockDim.x, tx = (int32_t)threadIdx.x;
   const int32_t per = threads * NV;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  const uint32_t step = gridDim.x * blockDim.y;
 
   Run<T> raw[NV], raw_res[NORM ? NV : 1];
-  auto load = [&](int64_t r, int32_t base) {
-    const T* x = reinterpret_cast<const T*>(p.x) + r * p.ld_x;
+  auto load = [&](uint32_t r, int32_t base) {
+    const T* x = reinterpret_cast<const T*>(p.x) + (uint64_t)r * p.ld_x;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int32_t c = base + i * threads + tx;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
       else raw[i].clear();
       if constexpr (NORM) {
         if (in && p.residual != nullptr) {
-          load16<T>(raw_res[i], reinterpret_cast<const T*>(p.residual) + r * p.ld_residual, 16 * c, p.cols, p.vec,
+          load16<T>(raw_res[i], reinterpret_cast<const T*>(p.residual) + (uint64_t)r * p.ld_residual, 16 * c, p.cols, p.vec,
                     p.residual, p.residual_end);
         } else {
           raw_res[i].clear();
@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
   };
 
   uint32_t turn = 0;
-  const int64_t row0 = (int64_t)blockIdx.x * blockDim.y;
+  const uint32_t row0 = blockIdx.x * blockDim.y;
   if (AHEAD) load(row0 + threadIdx.y, 0);
-  for (int64_t r0 = row0; r0 < p.all_rows; r0 += step, turn ^= 1u) {
-    const int64_t r = r0 + threadIdx.y;
+  for (uint32_t r0 = row0; r0 < p.all_rows; r0 += step, turn ^= 1u) {
+    const uint32_t r = r0 + threadIdx.y;
     const bool live = r < p.rows;
     if (!AHEAD) load(r, 0);
     float v[NV][16], most[NV];  // (and each run's largest magnitude)
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
       for (int i = 0; i < NV; ++i) {
         const int32_t c = i * threads + tx;
         if (live && c < p.chunks && p.s != nullptr)
-          store16<T>(reinterpret_cast<T*>(p.s) + r * p.ld_s, v[i], 16 * c, p.cols, p.vec);
+          store16<T>(reinterpret_cast<T*>(p.s) + (uint64_t)r * p.ld_s, v[i], 16 * c, p.cols, p.vec);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) fma2(sum, sum1, v[i][j], v[i][j + 1], v[i][j], v[i][j + 1]);
       }
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 
             *reinterpret_cast<uint32_t*>(p.scales + scale_offset(r, c * 16 / kBlock<F>, p.blocks)) = word;
         }
         if (live && c < p.chunks)
-          store_codes<F, sizeof(T) == 4 && !NORM>(p.data + r * p.ld_data + (int64_t)c * (kFourBit<F> ? 8 : 16), v[i], row, b);
+          store_codes<F, sizeof(T) == 4 && !NORM>(p.data + (uint64_t)r * p.ld_data + (uint32_t)c * (kFourBit<F> ? 8u : 16u), v[i], row, b);
       }
     }
     if (AHEAD && !NORM && p.chunks > per) load(r + step, 0);

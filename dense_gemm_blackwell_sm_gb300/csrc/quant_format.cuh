@@ -210,8 +210,8 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&v)[16], 
 }
 
 // byte offset of the tiled scale of row r, scale column c, of an array with `cb` blocks a row
-__device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t c, int64_t cb) {
-  return ((r >> 7) * cb + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
+__device__ __forceinline__ uint64_t scale_offset(uint32_t r, uint32_t c, uint32_t cb) {
+  return ((uint64_t)(r >> 7) * cb + (c >> 2)) * 512u + (r & 31u) * 16u + ((r >> 5) & 3u) * 4u + (c & 3u);
 }
 
 }  // namespace dgb

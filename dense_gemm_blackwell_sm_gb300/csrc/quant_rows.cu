@@ -22,14 +22,14 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
   p.chunks = (int32_t)(width / 16);
   p.blocks = (int32_t)up(scales, 4);
   p.all_chunks = scales == 0 ? p.chunks : (int32_t)(p.blocks * 4 * (format == QUANT_NVFP4 ? 1 : 2));
-  p.all_rows = scales == 0 ? p.rows : up(p.rows, 128) * 128;
+  p.all_rows = scales == 0 ? p.rows : (uint32_t)(up(p.rows, 128) * 128);
   // One run of 16 columns a thread up to 512 threads a row, then up to four.  4-bit rows that
   // fill the device take two from 64 runs on: half as many threads meet for the row's scale and
   // share a scale word (8192 x 4096 bf16 to NVFP4 22.6 -> 19.1 us, to MXFP4 18.5 -> 16.7; to
   // MXFP8 18.6 -> 20.0, and a norm to NVFP4 43.5 -> 47.6, so these keep one).
   int nv = 1;
   const bool four = format == QUANT_MXFP4 || format == QUANT_NVFP4;
-  if (four && !norm && p.chunks >= 64 && p.chunks * p.rows >= (int64_t)num_sms * 2048) nv = 2;
+  if (four && !norm && p.chunks >= 64 && (int64_t)p.chunks * p.rows >= (int64_t)num_sms * 2048) nv = 2;
   while (nv < 4 && up(p.chunks, nv) > 512) nv *= 2;
   const int threads = (int)std::min<int64_t>(512, up(up(p.chunks, nv), 32) * 32);
   const int rows = std::max(1, (nv == 2 ? 128 : 256) / threads);
@@ -52,7 +52,7 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
 cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int e = a.dtype == FFN_F32 ? 4 : 2;
   QuantRowsParams p{};
-  p.rows = a.rows;
+  p.rows = (uint32_t)a.rows;
   p.cols = (int32_t)a.cols;
   p.vec = alignment_of(a.x, a.ld_x * e);
   p.x = a.x;
@@ -60,15 +60,15 @@ cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaS
   p.data = static_cast<uint8_t*>(a.data);
   p.scales = static_cast<uint8_t*>(a.scales);
   p.row_scale = a.row_scale;
-  p.ld_x = a.ld_x;
-  p.ld_data = a.ld_data;
+  p.ld_x = (uint32_t)a.ld_x;
+  p.ld_data = (uint32_t)a.ld_data;
   return launch(p, a.dtype, a.format, false, dev.num_sms, st);
 }
 
 cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaStream_t st) {
   const int e = a.dtype == FFN_F32 ? 4 : 2;
   QuantRowsParams p{};
-  p.rows = a.M;
+  p.rows = (uint32_t)a.M;
   p.cols = (int32_t)a.D;
   p.vec = std::min({alignment_of(a.y, a.ld_y * e), alignment_of(a.residual, a.ld_residual * e),
                     alignment_of(a.s, a.ld_s * e)});
@@ -82,10 +82,10 @@ cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaS
   p.data = static_cast<uint8_t*>(a.data);
   p.scales = static_cast<uint8_t*>(a.scales);
   p.row_scale = a.row_scale;
-  p.ld_x = a.ld_y;
-  p.ld_residual = a.ld_residual;
-  p.ld_s = a.ld_s;
-  p.ld_data = a.ld_data;
+  p.ld_x = (uint32_t)a.ld_y;
+  p.ld_residual = (uint32_t)a.ld_residual;
+  p.ld_s = (uint32_t)a.ld_s;
+  p.ld_data = (uint32_t)a.ld_data;
   p.weight_f32 = a.param_dtype == FFN_F32;
   p.weight_vec = alignment_of(a.weight, 0);
   p.eps = a.eps;

@@ -172,3 +172,25 @@ def test_odd_pitches_of_the_norm(fmt):
     assert s2.data_ptr() == r.data_ptr() and torch.equal(r, s0) and same(q0, q2)
     none, q3 = quant.norm_quantise(y, s0, None, format=fmt, need_s=False)
     assert none is None and q3.data.shape == q0.data.shape
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("M,N,K", [(3, 40, 0), (40, 40, 0), (0, 40, 64), (3, 0, 64), (0, 0, 0)])
+def test_linear_of_nothing(fmt, M, N, K):
+    x, w = torch.zeros(M, K, device=DEV), quant.quantise(torch.zeros(N, K, device=DEV), fmt)
+    bias, residual = normal(N, seed=1, to=torch.float32), normal(M, N, seed=2, to=torch.float32)
+    y = quant.linear(x, w, bias=bias, residual=residual, out_dtype=torch.float32)
+    assert torch.equal(y, (bias + residual) if M and N else residual)
+    assert quant.check() == gemm.OK
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+def test_linear_of_one_token_and_the_largest_and_smallest_values(fmt):
+    # magnitudes at the ends of the types: the kernel that quantises tokens itself, as rows
+    w = quant.quantise(normal(256, 512, seed=1), fmt)
+    for dtype, values in ((torch.float16, (65504.0, 6e-8)), (torch.bfloat16, (2.0 ** 100, 2.0 ** -120)), (torch.float32, (2.0 ** 100, 2.0 ** -120))):
+        for v in values:
+            x = torch.zeros(1, 512, device=DEV, dtype=dtype)
+            x[0, 7], x[0, 8], x[0, 300] = v, -v, v
+            assert torch.equal(quant.linear(x, w, out_dtype=torch.float32),
+                               quant.product(quant.quantise(x, fmt), w, out_dtype=torch.float32))
