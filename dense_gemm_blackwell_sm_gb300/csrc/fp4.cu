@@ -134,7 +134,6 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
     // (both operands lie in L2 at sizes where that matters: 32 rows of tiles against 8 take 8192 x
     // 14336 x 4096 NVFP4 from 156 to 149 us, 8192^3 from 166 to 162)
     p.raster_group = std::min(32, p.tiles_m);
-    p.stages = fp4_pair_stages(nv);
     p.idesc = idesc_fp4(!nv, 256, 256);
     if (!encode_byte_rows(&maps[0], a.a, (uint64_t)a.K / 2, (uint64_t)a.M, (uint64_t)a.ld_a, 128) ||
         !encode_byte_rows(&maps[1], a.b, (uint64_t)a.K / 2, (uint64_t)a.N, (uint64_t)a.ld_b, 128) ||

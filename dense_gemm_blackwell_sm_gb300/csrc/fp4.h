@@ -27,7 +27,6 @@ struct Fp4Params {
   int32_t steps;            // MMAs of 64 K-elements that a sum takes
   int32_t blocks;           // stages of 256 K-elements
   int32_t tiles_m, tiles_n, raster_group;
-  int32_t stages;
   uint32_t idesc;
   uint32_t debug_flags;
   uint32_t* status;
@@ -36,6 +35,7 @@ struct Fp4Params {
   int32_t tokens;           // columns of an MMA: tokens of a tile
   int32_t split;            // CTAs of a cluster that share a sum
   int32_t static_b;
+  int32_t stages;           // of the ring of copies
 };
 
 // Tokens that the kernel quantises itself (kernel_fp4_few.cu).
@@ -49,7 +49,6 @@ struct Fp4Tokens {
 
 const void* fp4_pair_kernel(bool nv, bool out_f32);
 size_t fp4_pair_smem(bool nv);
-int fp4_pair_stages(bool nv);
 constexpr int kFp4PairThreads = 384;
 
 const void* fp4_few_kernel(bool nv, bool out_f32);

@@ -15,8 +15,8 @@
 // 206 with two), warps 4-11 the epilogue.  Issuing warps walk their loops as a whole and one lane's
 // predicate lets an instruction go (8192^3: 176 us).
 //
-// Bound by the tensor pipe and, with all SMs at it, by the operands' way from L2: a stage takes
-// 590 cycles where its MMAs take 512, a tile's start 1000 more.  8192^3 MXFP4 155 us (7.1 PFLOP/s), NVFP4
+// Bound by the tensor pipe and, with all SMs at it, by the operands' way from L2: a stage (38 KB an SM
+// with a scale per 16, 35 with one per 32) takes 590 cycles where its MMAs take 512, a tile's start 1000 more.  8192^3 MXFP4 155 us (7.1 PFLOP/s), NVFP4
 // 164 (6.7); 8192 x 14336 x 4096 143 and 151 (6.7, 6.4), with fp32 C 190; 4096^3 29 and 30 (4.6: 256 tiles
 // are 3.4 rounds of the pairs).
 //
@@ -349,7 +349,6 @@ const void* fp4_pair_kernel(bool nv, bool out_f32) {
                  : reinterpret_cast<const void*>(k_fp4_pair<false, __nv_bfloat16>);
 }
 
-int fp4_pair_stages(bool nv) { return nv ? stages_of<true>() : stages_of<false>(); }
 size_t fp4_pair_smem(bool nv) {
   return nv ? smem_of<true>(stages_of<true>()) : smem_of<false>(stages_of<false>());
 }
