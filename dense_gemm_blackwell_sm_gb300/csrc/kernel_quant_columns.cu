@@ -3,16 +3,16 @@
 //
 // A CTA takes 256 rows x 64 columns of x through shared memory; a warp then takes 32 of the
 // rows, which are one block of 32 or two of 16 of every column, and a lane two columns, whose
-// codes it stores whole (16 bytes of 4-bit codes or 32 of 8-bit ones).
+// codes (16 bytes of 4-bit ones or 32 of 8-bit ones) meet those of the other warps in shared memory.
 // Where a column has a scale of its own, a first kernel finds the largest magnitudes of
 // parts of the columns; x is then read twice, the second time from its end, which L2 still holds,
 // and before that kernel has ended.
 // Up to kTasks arrays go in one launch.
 //
 // Bound by memory: 2 bytes read per element, 0.53 to 1.03 written.  14336 x 4096 bf16: to MXFP8
-// 32.8 us (5.4 TB/s), MXFP4 31.1; with a scale per column (read twice) 54, and 515 x 1097 9 where
-// one kernel takes 6.  8192 x 4096 fp32 34 to 36, with a scale per column 58 and, NVFP4's divisions,
-// 72.  Held whole in the shared memory of a cluster, so that they are read once, columns take
+// 32.8 us (5.4 TB/s), MXFP4 28.9; with a scale per column (read twice) 53, and 515 x 1097 9 where
+// one kernel takes 6.  8192 x 4096 fp32 33 to 35, with a scale per column 57 and, NVFP4's divisions,
+// 72.  (Persistent CTAs that copy the next tile while they work on one gain nothing.)  Held whole in the shared memory of a cluster, so that they are read once, columns take
 // longer: loads, the exchange of the magnitudes and the codes then follow one another (14336 x 4096
 // 66 to 77 us).
 #include <algorithm>
@@ -40,7 +40,6 @@ struct QuantColumnsTask {
   int32_t row_tiles;
   int32_t strips;           // of 64 columns that x has
   int32_t all_strips;       // and that the scale array's rows have
-  int32_t wide_data;        // the operand's rows start on 32-byte boundaries
   int64_t part_rows;
   const void* x;
   const void* x_end;        // the first byte past x's last element
@@ -283,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4)
   }
   __syncthreads();
   const int warp = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
-  const int64_t k0 = r0 + warp * 32;  // the operand's first column of this warp
   const T* mine = tile + warp * 32 * kPitch<T> + 2 * lane;
   Columns16<T> run[2];
   float most[2][2];
@@ -292,6 +290,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4)
     run[i].load(mine + 16 * i * kPitch<T>);
     run[i].most(most[i]);
   }
+  // The codes of a column meet in shared memory, where the tile was, and go out as whole lines: a
+  // lane's 16 or 32 bytes of a column stored by itself are four times as many requests (14336 x 4096
+  // MXFP4 30.8 -> 28.9 us, NVFP4 54.0 -> 52.9).
+  constexpr int kCodes = kFourBit<F> ? kTileRows / 2 : kTileRows;  // bytes of a column
+  constexpr int kCodesPitch = kCodes + 16;
+  static_assert(kTileCols * kCodesPitch <= kTileRows * kPitch<T> * (int)sizeof(T), "the codes fit the tile");
+  __syncthreads();
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const RowUnit row = units[2 * lane + half];
@@ -308,19 +313,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 4)
       run[i].column(v, half);
       codes16<F, sizeof(T) == 4>(codes + i * kWords, v, row, b);
     }
-    const int64_t c = c0 + 2 * lane + half;
-    if (c >= p.cols || k0 >= p.width) continue;
-    uint8_t* dst = p.data + c * p.ld_data + (kFourBit<F> ? k0 / 2 : k0);
-    if (!kFourBit<F> && p.wide_data) {
-      if constexpr (!kFourBit<F>) st_global_v8(dst, codes);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 2 * kWords; j += 4)
-        *reinterpret_cast<uint4*>(dst + 4 * j) = make_uint4(codes[j], codes[j + 1], codes[j + 2], codes[j + 3]);
+    for (int j = 0; j < 2 * kWords; j += 4)
+      *reinterpret_cast<uint4*>(smem + (2 * lane + half) * kCodesPitch + warp * (kCodes / 8) + 4 * j) =
+          make_uint4(codes[j], codes[j + 1], codes[j + 2], codes[j + 3]);
+  }
+  __syncthreads();
+  {
+    constexpr int kPieces = kCodes / 16;
+    const int64_t first = kFourBit<F> ? r0 / 2 : r0, all = kFourBit<F> ? p.width / 2 : p.width;
+#pragma unroll
+    for (int i = 0; i < kTileCols * kPieces; i += kThreads) {
+      const int col = (i + (int)threadIdx.x) / kPieces, piece = (int)threadIdx.x % kPieces;
+      if (c0 + col < p.cols && first + 16 * piece < all)
+        *reinterpret_cast<uint4*>(p.data + (c0 + col) * p.ld_data + first + 16 * piece) =
+            *reinterpret_cast<const uint4*>(smem + col * kCodesPitch + 16 * piece);
     }
   }
   if constexpr (kBlock<F> != 0) {
-    __syncthreads();
     constexpr int kPer = kBlock<F> / 16;           // runs of a scale
     constexpr int words = kRuns / kPer / 4;        // scale words of a column
     const int64_t scale0 = r0 / kBlock<F>;
@@ -386,7 +396,6 @@ cudaError_t launch_quant_columns(const quant_rows_t* args, int count, cudaStream
     const int64_t scales = scales_of(p.width, a.format);
     p.blocks = (int32_t)up(scales, 4);
     p.vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 && a.ld_x * e % 16 == 0;
-    p.wide_data = ((reinterpret_cast<uintptr_t>(a.data) | (uintptr_t)a.ld_data) & 31u) == 0;
     p.parts = parts_of(a.rows, a.cols);
     p.part_rows = up(a.rows, p.parts);
     p.strips = (int32_t)up(a.cols, kTileCols);
