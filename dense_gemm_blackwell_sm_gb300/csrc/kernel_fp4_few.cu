@@ -72,92 +72,91 @@ __host__ __device__ inline FewShape few_shape(int blocks, int tokens) {
 }
 
 // Sums [begin, end) of a tile's [token][feature] from the cluster's SPLIT CTAs, in the order of
-// their ranks, to c: V neighbours a time.  What a thread reads from the CTAs is under way
-// together (8 groups of 4 or 8 single values): one after the other, eight reads of distributed
-// shared memory took 2 us.
-template <int V, int SPLIT, typename OutT>
+// their ranks, to c: four neighbours a time, which go out together where rows are ALIGNED to that,
+// else one by one.  What a thread reads from the CTAs is under way together (8 groups): one after
+// the other, eight reads of distributed shared memory took 2 us.
+template <bool ALIGNED, int SPLIT, typename OutT>
 __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* token_scale, const float* partial,
                                            int32_t begin, int32_t end, int32_t row0, int32_t col0) {
-  constexpr int U = (V == 4 ? 8 : 16) / SPLIT;
-  using Word = typename std::conditional<V == 1, OutT, typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type>::type;
-  constexpr int kStep = kFp4FewThreads * V;
+  constexpr int U = 8 / SPLIT;
+  union Four {
+    typename std::conditional<sizeof(OutT) == 4, uint4, uint2>::type all;
+    OutT one[4];
+    __device__ __forceinline__ Four() {}
+  };
+  constexpr int kStep = kFp4FewThreads * 4;
   const Fp4Epilogue& e = p.e;
   uint32_t from[SPLIT];
 #pragma unroll
-  for (int r = 0; r < SPLIT; ++r) from[r] = SPLIT == 1 ? smem_u32(partial) : mapa_shared(smem_u32(partial), (uint32_t)r);
+  for (int r = 0; r < SPLIT; ++r) from[r] = mapa_shared(smem_u32(partial), (uint32_t)r);
 #pragma unroll 1
-  for (int32_t i0 = begin + (int32_t)threadIdx.x * V; i0 < end; i0 += kStep * U) {
-    float y[U][SPLIT][V];
-    Word res[U];
+  for (int32_t i0 = begin + (int32_t)threadIdx.x * 4; i0 < end; i0 += kStep * U) {
+    float4 y[U][SPLIT];
+    Four res[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int32_t i = min(i0 + u * kStep, end - V);  // (a multiple of V)
+      const int32_t i = min(i0 + u * kStep, end - 4);  // (a multiple of 4)
       const int32_t col = col0 + i % 128;
-      if (e.residual != nullptr && col + V <= e.N)
-        res[u] = *reinterpret_cast<const Word*>(reinterpret_cast<const OutT*>(e.residual) +
-                                                (int64_t)(row0 + i / 128) * e.ld_residual + col);
-#pragma unroll
-      for (int r = 0; r < SPLIT; ++r) {
-        if constexpr (SPLIT == 1) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) y[u][r][j] = partial[i + j];
-        } else if constexpr (V == 4) {
-          const float4 f = ld_cluster_f32x4(from[r] + 4u * (uint32_t)i);
-          y[u][r][0] = f.x;
-          y[u][r][1] = f.y;
-          y[u][r][2] = f.z;
-          y[u][r][3] = f.w;
+      if (e.residual != nullptr) {
+        const OutT* src = reinterpret_cast<const OutT*>(e.residual) + (int64_t)(row0 + i / 128) * e.ld_residual + col;
+        // (a group that the matrix' edge cuts goes by single values)
+        if (ALIGNED && col + 4 <= e.N) {
+          res[u].all = *reinterpret_cast<const decltype(res[u].all)*>(src);
         } else {
-          y[u][r][0] = __uint_as_float(ld_cluster_u32(from[r] + 4u * (uint32_t)i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < e.N) res[u].one[j] = src[j];
         }
       }
+#pragma unroll
+      for (int r = 0; r < SPLIT; ++r)
+        y[u][r] = SPLIT == 1 ? *reinterpret_cast<const float4*>(partial + i) : ld_cluster_f32x4(from[r] + 4u * (uint32_t)i);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int32_t i = i0 + u * kStep;
       const int32_t row = row0 + i / 128, col = col0 + i % 128;
       if (i >= end || col >= e.N) continue;
-      // (a group that the matrix' edge cuts goes by single values)
-      const bool whole = col + V <= e.N;
       const float sa = token_scale != nullptr ? token_scale[row] : 1.f;
-      float x[V];
+      float x[4] = {y[u][0].x, y[u][0].y, y[u][0].z, y[u][0].w};
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[j] = y[u][0][j];
+      for (int r = 1; r < SPLIT; ++r) {
+        x[0] += y[u][r].x;
+        x[1] += y[u][r].y;
+        x[2] += y[u][r].z;
+        x[3] += y[u][r].w;
+      }
 #pragma unroll
-        for (int r = 1; r < SPLIT; ++r) x[j] += y[u][r][j];
+      for (int j = 0; j < 4; ++j) {
         x[j] *= sa;
         const int32_t c = min(col + j, e.N - 1);
         if (e.row_scale_b != nullptr) x[j] *= __ldg(e.row_scale_b + c);
         if (e.bias != nullptr) x[j] += __ldg(e.bias + c);
       }
       fp4_act(x, e.act);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        res[u].one[j] = from_f32<OutT>(e.residual != nullptr ? x[j] + to_f32(res[u].one[j]) : x[j]);
       OutT* dst = reinterpret_cast<OutT*>(e.c) + (int64_t)row * e.ld_c + col;
-      if (whole) {
-        OutT* t = reinterpret_cast<OutT*>(&res[u]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) t[j] = from_f32<OutT>(e.residual != nullptr ? x[j] + to_f32(t[j]) : x[j]);
-        *reinterpret_cast<Word*>(dst) = res[u];
+      if (ALIGNED && col + 4 <= e.N) {
+        *reinterpret_cast<decltype(res[u].all)*>(dst) = res[u].all;
       } else {
-        const OutT* from_res = reinterpret_cast<const OutT*>(e.residual) + (int64_t)row * e.ld_residual + col;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (col + j >= e.N) break;
-          dst[j] = from_f32<OutT>(e.residual != nullptr ? x[j] + to_f32(from_res[j]) : x[j]);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (col + j < e.N) dst[j] = res[u].one[j];
       }
     }
   }
 }
 
-template <int V, typename OutT>
+template <bool ALIGNED, typename OutT>
 __device__ __forceinline__ void few_finish(const Fp4Params& p, const float* token_scale, const float* partial,
                                            int32_t begin, int32_t end, int32_t row0, int32_t col0) {
   switch (p.split) {
-    case 1: return few_finish<V, 1, OutT>(p, token_scale, partial, begin, end, row0, col0);
-    case 2: return few_finish<V, 2, OutT>(p, token_scale, partial, begin, end, row0, col0);
-    case 4: return few_finish<V, 4, OutT>(p, token_scale, partial, begin, end, row0, col0);
-    default: return few_finish<V, 8, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    case 1: return few_finish<ALIGNED, 1, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    case 2: return few_finish<ALIGNED, 2, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    case 4: return few_finish<ALIGNED, 4, OutT>(p, token_scale, partial, begin, end, row0, col0);
+    default: return few_finish<ALIGNED, 8, OutT>(p, token_scale, partial, begin, end, row0, col0);
   }
 }
 
@@ -426,9 +425,9 @@ __device__ __forceinline__ void few_body(const CUtensorMap& tmA, const CUtensorM
     const int32_t share = ((total + p.split - 1) / p.split + 127) / 128 * 128;
     const int32_t begin = rank * share, end = min(total, begin + share);
     if (p.e.vec != 0) {
-      few_finish<4, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
+      few_finish<true, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
     } else {
-      few_finish<1, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
+      few_finish<false, OutT>(p, token_scale, partial, begin, end, token0, tn * 128);
     }
   }
   if (!ok && threadIdx.x == 0) {

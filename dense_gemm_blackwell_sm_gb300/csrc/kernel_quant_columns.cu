@@ -11,8 +11,7 @@
 //
 // Bound by memory: 2 bytes read per element, 0.53 to 1.03 written.  14336 x 4096 bf16: to MXFP8
 // 32.8 us (5.4 TB/s), MXFP4 28.9; with a scale per column (read twice) 53, and 515 x 1097 9 where
-// one kernel takes 6.  8192 x 4096 fp32 33 to 35, with a scale per column 57 and, NVFP4's divisions,
-// 72.  (Persistent CTAs that copy the next tile while they work on one gain nothing.)  Held whole in the shared memory of a cluster, so that they are read once, columns take
+// one kernel takes 6.  8192 x 4096 fp32 33 to 35, with a scale per column 57 to 61.  (Persistent CTAs that copy the next tile while they work on one gain nothing.)  Held whole in the shared memory of a cluster, so that they are read once, columns take
 // longer: loads, the exchange of the magnitudes and the codes then follow one another (14336 x 4096
 // 66 to 77 us).
 #include <algorithm>

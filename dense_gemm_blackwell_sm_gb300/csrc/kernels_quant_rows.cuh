@@ -12,8 +12,8 @@
 //
 // Bound by memory: 2 bytes read and 0.53 to 1.03 written per element (norm: 4 and 2 more).  8192 x
 // 4096 bf16: to E4M3 18.3 us, MXFP8 18.5 (5.5 TB/s), MXFP4 16.4, NVFP4 18.0; the norm to all of them 41
-// (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.4 TB/s), NVFP4's divisions 34; the
-// norm 63 to 70.  Rows of 4095 columns, off 16-byte boundaries, 23 to 33.  One row of 4096: 1.5 and
+// (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
+// the norm 63 to 68.  Rows of 4095 columns, off 16-byte boundaries, 23 to 33.  One row of 4096: 1.5 and
 // 2.6 us, a launch and a row's latency.
 #pragma once
 

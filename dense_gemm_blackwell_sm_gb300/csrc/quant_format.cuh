@@ -120,16 +120,41 @@ __device__ __forceinline__ RowUnit row_unit(float most) {
 // A block's scale: the byte kept, and what multiplies the block's values.
 struct BlockUnit {
   uint32_t byte;
-  float inv;    // 0 where the values are to be 0
+  float inv;    // 0 where the values are to be 0 (NVFP4 in 32 bits: the scale's reciprocal alone)
   float scale;  // NVFP4 in 32 bits: the scale, to divide by
 };
-// The smallest float not below 1 / s, for s an E4M3 value above 0: one Newton step from the
-// approximate reciprocal (the nearest float to 1 / s), and up where that is below.
-__device__ __forceinline__ float reciprocal_up(float s) {
+// The nearest float to 1 / s, for s an E4M3 value above 0: one Newton step from the approximate
+// reciprocal.
+__device__ __forceinline__ float reciprocal(float s) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  r = fmaf(r, fmaf(-r, s, 1.f), r);
+  return fmaf(r, fmaf(-r, s, 1.f), r);
+}
+// The smallest float not below it
+__device__ __forceinline__ float reciprocal_up(float s) {
+  const float r = reciprocal(s);
   return fmaf(r, s, -1.f) < 0.f ? __uint_as_float(__float_as_uint(r) + 1u) : r;
+}
+
+// v / s with r the nearest float to 1 / s: the product with r, corrected by its remainder, which is
+// exact (Markstein's step).  Rounded to a few bits it goes where the exact quotient does: for a
+// midpoint b of the codes b s is a float, so v = b s gives b, and any other v is a unit in its last
+// place from b s at least, which is more than half a unit of b.  (A division takes a slow way for
+// zeros, of which there are many: 300 x 520 fp32 to NVFP4 4.5 us with divisions, like
+// this 2.0; 8192 x 4096 34 and 25.)
+__device__ __forceinline__ float quotient(float v, float s, float r) {
+  const float q = v * r;
+  return fmaf(fmaf(-q, s, v), r, q);
+}
+__device__ __forceinline__ void quotient2(float& v, float& w, float s, float r) {
+  const float v0 = v, w0 = w;
+  float q0 = v, q1 = w;
+  mul2(q0, q1, r, r);
+  fma2(v, w, q0, q1, -s, -s);
+  const uint32_t sv = __float_as_uint(v0) & 0x80000000u, sw = __float_as_uint(w0) & 0x80000000u;
+  fma2(q0, q1, v, w, r, r);
+  v = __uint_as_float(__float_as_uint(q0) | sv);  // (a zero keeps its sign)
+  w = __uint_as_float(__float_as_uint(q1) | sw);
 }
 
 // EXACT: for 32-bit inputs, whose quotients may lie nearer to a tie than a reciprocal is exact.
@@ -146,7 +171,8 @@ __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) 
   } else if constexpr (F == QUANT_NVFP4) {
     // (for 16-bit magnitudes a product with 1/6 rounded up, rounded towards zero, stays on a tie
     // that the quotient is on: see below)
-    const float q = EXACT ? __fdiv_rn(most * row.inv, 6.f) : __fmul_rz(most * row.inv, 0.166666671633720397949f);
+    constexpr float kSixth = 0.166666671633720397949f;  // (the nearest float, above 1/6)
+    const float q = EXACT ? quotient(most * row.inv, 6.f, kSixth) : __fmul_rz(most * row.inv, kSixth);
     uint32_t byte, half;
     asm("{\n\t.reg .b16 r;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 r, %2, %2;\n\t"
@@ -160,14 +186,14 @@ __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) 
     // the middle between two codes stays there (b * s * r is at least b and below b's
     // neighbour for every scale s and midpoint b), so that ties go to even as for the exact
     // quotient.  16-bit values that are no ties are 2^-11 from them at least.
-    b.inv = b.byte == 0u ? 0.f : reciprocal_up(b.scale) * row.inv;
+    b.inv = b.byte == 0u ? 0.f : EXACT ? reciprocal(b.scale) : reciprocal_up(b.scale) * row.inv;
     if (row.inv == 0.f) b = {0x7fu, 0.f, 1.f};
   }
   return b;
 }
 
 // 16 values to codes: 4 words (E4M3) or 2 (E2M1).  EXACT: values that may lie nearer to a tie than
-// the reciprocal is exact (32-bit inputs) are divided.
+// the reciprocal is exact (32-bit inputs) get their quotients.
 template <int F, bool EXACT>
 __device__ __forceinline__ void codes16(uint32_t* w, const float (&v)[16], const RowUnit& row, const BlockUnit& b) {
   float t[16];
@@ -176,8 +202,8 @@ __device__ __forceinline__ void codes16(uint32_t* w, const float (&v)[16], const
     t[j] = v[j];
     t[j + 1] = v[j + 1];
     if constexpr (F == QUANT_NVFP4 && EXACT) {
-      t[j] = __fdiv_rn(t[j] * row.inv, b.scale);
-      t[j + 1] = __fdiv_rn(t[j + 1] * row.inv, b.scale);
+      mul2(t[j], t[j + 1], row.inv, row.inv);
+      quotient2(t[j], t[j + 1], b.scale, b.inv);
     } else if constexpr (F == QUANT_NVFP4) {
       mul2_rz(t[j], t[j + 1], b.inv, b.inv);
     } else {

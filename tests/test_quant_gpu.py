@@ -347,3 +347,28 @@ def test_columns_are_the_rows_of_the_transpose(fmt, shape, dtype):
         got, want = quant.quantise(x, fmt, transpose=True), quant.quantise(x.t().contiguous(), fmt)
         for a, b in ((got.data, want.data), (got.scales, want.scales), (got.row_scale, want.row_scale)):
             assert (a is None and b is None) or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_fp32_values_beside_every_tie_of_nvfp4(transpose):
+    # every scale s, every midpoint b of the codes: b s and the floats beside it, in blocks whose
+    # largest value is 6 s; then every midpoint of the scales, and beside it, as a block's largest value.
+    # One block holds 2688, so that the row's scale is one.
+    e4m3 = ref.E4M3[1:127]
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    blocks = [np.full(16, 2688.0, np.float32)]
+    for s in e4m3:
+        ties = (mids * s).astype(np.float32)
+        v = np.concatenate([ties, np.nextafter(ties, np.float32(np.inf)), -np.nextafter(ties, np.float32(0))])
+        for part in (v[:15], np.concatenate([v[15:], v[:9]])):
+            blocks.append(np.concatenate([[np.float32(6 * s)], part]).astype(np.float32))
+    middle = ((e4m3[1:] + e4m3[:-1]) / 2 * 6).astype(np.float32)
+    for m in np.concatenate([middle, np.nextafter(middle, np.float32(np.inf)), np.nextafter(middle, np.float32(0))]):
+        blocks.append(np.concatenate([[m], np.linspace(-1, 1, 15) * m]).astype(np.float32))
+    x = np.stack([np.concatenate(blocks), -np.concatenate(blocks)])
+    assert (np.abs(x).max(1) == 2688).all()
+    t = torch.tensor(x, device=DEV)
+    got = quant.quantise(t.t().contiguous() if transpose else t, "nvfp4", transpose=transpose)
+    want = ref.quantise(x.astype(np.float64), "nvfp4")
+    assert (want.row_scale == 1).all()
+    check_operand(got, want)
