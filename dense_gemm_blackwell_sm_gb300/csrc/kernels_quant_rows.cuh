@@ -11,9 +11,9 @@
 // norm) are read twice.
 //
 // Bound by memory: 2 bytes read and 0.53 to 1.03 written per element (norm: 4 and 2 more).  8192 x
-// 4096 bf16: to E4M3 18.3 us, MXFP8 18.5 (5.5 TB/s), MXFP4 16.4, NVFP4 18.0; the norm to all of them 41
-// (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
-// the norm 63 to 68.  Rows of 4095 columns, off 16-byte boundaries, 23 to 33.  One row of 4096: 1.5 and
+// 4096 bf16: to E4M3 18.7 us, MXFP8 17.2 (5.9 TB/s), MXFP4 15.8, NVFP4 18.3; 8192 x 8192 31.6, 32.3 (6.3
+// TB/s), 28.7 and 30.1; the norm of 8192 x 4096 to all of them 41 (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
+// the norm 63 to 68.  Rows of 4095 columns, off 16-byte boundaries, 22 to 28.  One row of 4096: 1.5 and
 // 2.6 us, a launch and a row's latency.
 #pragma once
 
@@ -199,8 +199,17 @@ __device__ __forceinline__ float over_row(float v, float* shared) {
   return over_warp<LARGEST>((lane & 15u) < warps ? mine[lane & 15u] : 0.f, 16);
 }
 
+// Registers a thread, for as many warps an SM as hide a row's steps behind one another: 16-bit rows of
+// one run a thread take 40 (8192 x 4096 to MXFP8 17.2 us, with 48 17.5, with 56 18.6, with 36 and spills
+// 20.6), of two 80 (8192 x 8192 to NVFP4 30.1, with 99 33.1); a norm of 16-bit rows needs 64.
+template <typename T, bool NORM, int NV>
+constexpr int kRowRegisters = NV == 1 && sizeof(T) == 2 ? (NORM ? 64 : 40)
+                              : NV == 1 && !NORM        ? 64
+                              : NV == 2 && sizeof(T) == 2 && !NORM ? 80
+                                                                   : 128;
+
 template <typename T, int F, bool NORM, int NV>
-__global__ void __launch_bounds__(512, NV == 1 && !(NORM && sizeof(T) == 4) ? 2 : 1) k_quant_rows(const QuantRowsParams p) {
+__global__ void __maxnreg__((kRowRegisters<T, NORM, NV>)) k_quant_rows(const QuantRowsParams p) {
   constexpr bool AHEAD = NORM ? NV == 1 : NV <= 2;  // the next row's loads are under way while this one is worked on
   __shared__ float shared[2][2][16];
   wait_for_prior_kernel();

@@ -25,11 +25,12 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
   p.all_rows = scales == 0 ? p.rows : (uint32_t)(up(p.rows, 128) * 128);
   // One run of 16 columns a thread up to 512 threads a row, then up to four.  4-bit rows that
   // fill the device take two from 64 runs on: half as many threads meet for the row's scale and
-  // share a scale word (8192 x 4096 bf16 to NVFP4 22.6 -> 19.1 us, to MXFP4 18.5 -> 16.7; to
-  // MXFP8 18.6 -> 20.0, and a norm to NVFP4 43.5 -> 47.6, so these keep one).
+  // share a scale word (8192 x 4096 bf16 to NVFP4 20.5 -> 18.3 us, to MXFP4 16.9 -> 15.8; to
+  // MXFP8 18.6 -> 20.0, a norm to NVFP4 43.5 -> 47.6, and rows off 16-byte boundaries, 8192 x 4095 to
+  // MXFP4, 22.5 -> 25.1, so these keep one).
   int nv = 1;
   const bool four = format == QUANT_MXFP4 || format == QUANT_NVFP4;
-  if (four && !norm && p.chunks >= 64 && (int64_t)p.chunks * p.rows >= (int64_t)num_sms * 2048) nv = 2;
+  if (four && !norm && p.vec != 0 && p.chunks >= 64 && (int64_t)p.chunks * p.rows >= (int64_t)num_sms * 2048) nv = 2;
   while (nv < 4 && up(p.chunks, nv) > 512) nv *= 2;
   const int threads = (int)std::min<int64_t>(512, up(up(p.chunks, nv), 32) * 32);
   const int rows = std::max(1, (nv == 2 ? 128 : 256) / threads);
