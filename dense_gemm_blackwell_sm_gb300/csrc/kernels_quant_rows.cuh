@@ -11,8 +11,8 @@
 // norm) are read twice.
 //
 // Bound by memory: 2 bytes read and 0.53 to 1.03 written per element (norm: 4 and 2 more).  8192 x
-// 4096 bf16: to E4M3 18.7 us, MXFP8 17.2 (5.9 TB/s), MXFP4 15.8, NVFP4 18.3; 8192 x 8192 31.6, 32.3 (6.3
-// TB/s), 28.7 and 30.1; the norm of 8192 x 4096 to all of them 41 (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
+// 4096 bf16: to E4M3 18.7 us, MXFP8 17.2 (5.9 TB/s), MXFP4 15.4, NVFP4 18.0; 8192 x 8192 31.6, 32.3 (6.3
+// TB/s), 28.6 and 33.1; the norm of 8192 x 4096 to all of them 41 (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
 // the norm 63 to 68.  Rows of 4095 columns, off 16-byte boundaries, 22 to 28.  One row of 4096: 1.5 and
 // 2.6 us, a launch and a row's latency.
 #pragma once
@@ -201,15 +201,18 @@ __device__ __forceinline__ float over_row(float v, float* shared) {
 
 // Registers a thread, for as many warps an SM as hide a row's steps behind one another: 16-bit rows of
 // one run a thread take 40 (8192 x 4096 to MXFP8 17.2 us, with 48 17.5, with 56 18.6, with 36 and spills
-// 20.6), of two 80 (8192 x 8192 to NVFP4 30.1, with 99 33.1); a norm of 16-bit rows needs 64.
-template <typename T, bool NORM, int NV>
+// 20.6), of two 72, so that two CTAs of 448 threads fit (4096 x 14336 to MXFP8 28.5, with 77 34.3).  NVFP4's take
+// what they need: alone they gain from 72 too (26.4 and 32.0), but the gradient of a linear layer, whose
+// other kernels stand beside them, loses (4096 x 14336 x 4096 309 us, with 72 319).  A norm of 16-bit
+// rows needs 64.
+template <typename T, int F, bool NORM, int NV>
 constexpr int kRowRegisters = NV == 1 && sizeof(T) == 2 ? (NORM ? 64 : 40)
                               : NV == 1 && !NORM        ? 64
-                              : NV == 2 && sizeof(T) == 2 && !NORM ? 80
+                              : NV == 2 && sizeof(T) == 2 && !NORM && F != QUANT_NVFP4 ? 72
                                                                    : 128;
 
 template <typename T, int F, bool NORM, int NV>
-__global__ void __maxnreg__((kRowRegisters<T, NORM, NV>)) k_quant_rows(const QuantRowsParams p) {
+__global__ void __maxnreg__((kRowRegisters<T, F, NORM, NV>)) k_quant_rows(const QuantRowsParams p) {
   constexpr bool AHEAD = NORM ? NV == 1 : NV <= 2;  // the next row's loads are under way while this one is worked on
   __shared__ float shared[2][2][16];
   wait_for_prior_kernel();
@@ -359,11 +362,10 @@ __global__ void __maxnreg__((kRowRegisters<T, NORM, NV>)) k_quant_rows(const Qua
 
 template <typename T, int F, bool NORM>
 const void* rows_kernel(int nv) {
-  switch (nv) {
-    case 1: return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 1>);
-    case 2: return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 2>);
-    default: return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 4>);
-  }
+  if (nv == 1) return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 1>);
+  if constexpr (!NORM)
+    if (nv == 2) return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 2>);
+  return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 4>);
 }
 
 template <typename T, bool NORM>

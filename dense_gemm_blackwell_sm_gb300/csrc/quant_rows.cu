@@ -25,13 +25,15 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
   p.all_rows = scales == 0 ? p.rows : (uint32_t)(up(p.rows, 128) * 128);
   // One run of 16 columns a thread up to 512 threads a row, then up to four.  4-bit rows that
   // fill the device take two from 64 runs on: half as many threads meet for the row's scale and
-  // share a scale word (8192 x 4096 bf16 to NVFP4 20.5 -> 18.3 us, to MXFP4 16.9 -> 15.8; to
+  // share a scale word (8192 x 4096 bf16 to NVFP4 20.5 -> 18.0 us, to MXFP4 16.9 -> 15.4; to
   // MXFP8 18.6 -> 20.0, a norm to NVFP4 43.5 -> 47.6, and rows off 16-byte boundaries, 8192 x 4095 to
   // MXFP4, 22.5 -> 25.1, so these keep one).
   int nv = 1;
   const bool four = format == QUANT_MXFP4 || format == QUANT_NVFP4;
   if (four && !norm && p.vec != 0 && p.chunks >= 64 && (int64_t)p.chunks * p.rows >= (int64_t)num_sms * 2048) nv = 2;
-  while (nv < 4 && up(p.chunks, nv) > 512) nv *= 2;
+  // (a norm's longer rows take four: two CTAs of 256 threads fit an SM where one of 512 with two runs a
+  // thread does, 2000 x 16384 bf16 45 us and 49)
+  while (nv < 4 && up(p.chunks, nv) > 512) nv *= norm ? 4 : 2;
   const int threads = (int)std::min<int64_t>(512, up(up(p.chunks, nv), 32) * 32);
   const int rows = std::max(1, (nv == 2 ? 128 : 256) / threads);
   LaunchSpec s;
