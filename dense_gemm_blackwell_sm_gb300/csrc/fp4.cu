@@ -81,7 +81,7 @@ cudaError_t launch_fp4_linear(const quant_linear_t& a, const FfnDevice& dev, cud
   p.idesc = idesc_fp4(!nv, 128, 16);
   Fp4Tokens x{};
   x.x = a.x;
-  x.x_end = static_cast<const uint8_t*>(a.x) + ((a.M - 1) * a.ld_x + a.K) * e;
+  x.x_end = end_of_rows(a.x, a.M, a.ld_x, a.K, e);
   x.ld_x = a.ld_x;
   x.K = (int32_t)a.K;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ld_x * e);

@@ -400,7 +400,7 @@ cudaError_t launch_quant_columns(const quant_rows_t* args, int count, cudaStream
     p.strips = (int32_t)up(a.cols, kTileCols);
     p.row_tiles = (int32_t)up(p.width, kTileRows);
     p.x = a.x;
-    p.x_end = static_cast<const uint8_t*>(a.x) + (a.rows > 0 ? ((a.rows - 1) * a.ld_x + a.cols) * e : 0);
+    p.x_end = end_of_rows(a.x, a.rows, a.ld_x, a.cols, e);
     p.data = static_cast<uint8_t*>(a.data);
     p.scales = static_cast<uint8_t*>(a.scales);
     p.row_scale = a.row_scale;

@@ -98,6 +98,10 @@ __device__ __forceinline__ void load16(Run<T>& v, const T* row, int32_t col, int
     }
     return;
   }
+  if (col >= cols) {  // (padding: nothing is there to load, and a row may have no values at all)
+    v.clear();
+    return;
+  }
   const uintptr_t at = reinterpret_cast<uintptr_t>(row + col), first = at & ~(uintptr_t)15;
   if (first >= reinterpret_cast<uintptr_t>(begin) && first + 16 * sizeof(T) + 16 <= reinterpret_cast<uintptr_t>(end)) {
     uint32_t w[words + 4];

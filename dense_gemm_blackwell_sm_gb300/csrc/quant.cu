@@ -94,7 +94,8 @@ gemm_status_t rows_checked(quant_rows_t* p) {
   quant_rows_t& a = *p;
   gemm_status_t st = rows_sizes(a);
   if (st != GEMM_OK) return st;
-  if (!pitch(&a.ld_x, a.cols) || !pitch(&a.ld_data, bytes_of(width_of(a.transpose ? a.rows : a.cols), a.format)))
+  if (!pitch(&a.ld_x, a.cols) || !pitch(&a.ld_data, bytes_of(width_of(a.transpose ? a.rows : a.cols), a.format)) ||
+      !rows_fit(a.rows, a.ld_x, a.cols, (int64_t)elem(a.dtype)))
     return GEMM_ERR_INVALID_ARG;
   if ((a.transpose ? a.cols : a.rows) == 0) return GEMM_OK;
   if (!a.x && a.rows > 0 && a.cols > 0) return GEMM_ERR_INVALID_ARG;
@@ -174,11 +175,14 @@ gemm_status_t quant_norm(const quant_norm_t* args, gemm_stream_t stream) {
   if (!pitch(&a.ld_y, a.D) || !pitch(&a.ld_residual, a.D) || !pitch(&a.ld_s, a.D) ||
       !pitch(&a.ld_data, bytes_of(width_of(a.D), a.format)))
     return GEMM_ERR_INVALID_ARG;
+  const uintptr_t e = elem(a.dtype);
+  if (!rows_fit(a.M, a.ld_y, a.D, (int64_t)e) || !rows_fit(a.M, a.ld_residual, a.D, (int64_t)e) ||
+      !rows_fit(a.M, a.ld_s, a.D, (int64_t)e))
+    return GEMM_ERR_INVALID_ARG;
   if (a.M == 0) return GEMM_OK;
   if (!a.y) return GEMM_ERR_INVALID_ARG;
   gemm_status_t st = operand(a.data, a.scales, a.row_scale, a.format);
   if (st != GEMM_OK) return st;
-  const uintptr_t e = elem(a.dtype);
   if (!aligned(a.y, e) || !aligned(a.residual, e) || !aligned(a.s, e) || !aligned(a.weight, elem(a.param_dtype)) ||
       a.ld_data % 16 != 0)
     return GEMM_ERR_MISALIGNED;
@@ -195,11 +199,12 @@ gemm_status_t quant_product(const quant_product_t* args, gemm_stream_t stream) {
   if (sizes != GEMM_OK) return sizes;
   if (a.K < 32 || a.K >= kMaxDim) return GEMM_ERR_INVALID_ARG;
   if (a.K % 32 != 0) return GEMM_ERR_UNSUPPORTED_SHAPE;
-  if (!pitch(&a.ld_a, a.K / 2) || !pitch(&a.ld_b, a.K / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N))
+  const uintptr_t e = elem(a.out_dtype);
+  if (!pitch(&a.ld_a, a.K / 2) || !pitch(&a.ld_b, a.K / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N) ||
+      !rows_fit(a.M, a.ld_residual, a.N, (int64_t)e) || !rows_fit(a.M, a.ld_c, a.N, (int64_t)e))
     return GEMM_ERR_INVALID_ARG;
   if (a.M == 0 || a.N == 0) return GEMM_OK;
   if (!a.a || !a.b || !a.scales_a || !a.scales_b || !a.c) return GEMM_ERR_INVALID_ARG;
-  const uintptr_t e = elem(a.out_dtype);
   if (!aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales_a, 16) || !aligned(a.scales_b, 16) ||
       a.ld_a % 16 != 0 || a.ld_b % 16 != 0 || !aligned(a.row_scale_a, 4) || !aligned(a.row_scale_b, 4) ||
       !aligned(a.bias, 4) || !aligned(a.residual, e) || !aligned(a.c, e))
@@ -222,11 +227,13 @@ gemm_status_t quant_linear(const quant_linear_t* args, gemm_stream_t stream) {
   gemm_status_t st = linear_sizes(a);
   if (st != GEMM_OK) return st;
   const int64_t width = width_of(a.K);
-  if (!pitch(&a.ld_x, a.K) || !pitch(&a.ld_b, width / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N))
+  const uintptr_t e = elem(a.out_dtype);
+  if (!pitch(&a.ld_x, a.K) || !pitch(&a.ld_b, width / 2) || !pitch(&a.ld_residual, a.N) || !pitch(&a.ld_c, a.N) ||
+      !rows_fit(a.M, a.ld_x, a.K, (int64_t)elem(a.dtype)) || !rows_fit(a.M, a.ld_residual, a.N, (int64_t)e) ||
+      !rows_fit(a.M, a.ld_c, a.N, (int64_t)e))
     return GEMM_ERR_INVALID_ARG;
   if (a.M == 0 || a.N == 0) return GEMM_OK;
   if ((!a.x && a.K > 0) || !a.b || !a.scales_b || !a.c) return GEMM_ERR_INVALID_ARG;
-  const uintptr_t e = elem(a.out_dtype);
   if (!aligned(a.x, elem(a.dtype)) || !aligned(a.b, 16) || !aligned(a.scales_b, 16) || a.ld_b % 16 != 0 ||
       !aligned(a.row_scale_b, 4) || !aligned(a.bias, 4) || !aligned(a.residual, e) || !aligned(a.c, e) ||
       !aligned(a.workspace, 256))

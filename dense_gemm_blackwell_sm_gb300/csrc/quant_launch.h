@@ -31,4 +31,17 @@ inline int64_t bytes_of(int64_t width, int32_t format) {
   return format == QUANT_MXFP4 || format == QUANT_NVFP4 ? width / 2 : width;
 }
 
+// The first byte past the last element of `rows` rows of `cols` elements, `ld` apart: where rows hold
+// nothing, or there are none, the array's start, whatever the pitch.
+inline const void* end_of_rows(const void* x, int64_t rows, int64_t ld, int64_t cols, int64_t elem) {
+  if (rows <= 0 || cols <= 0) return x;
+  return reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(x) + (uintptr_t)(((rows - 1) * ld + cols) * elem));
+}
+// Whether such rows end within 2^62 bytes, so that the sums above are those of 64 bits: a pitch and a
+// number of rows that no memory has are refused.
+inline bool rows_fit(int64_t rows, int64_t ld, int64_t cols, int64_t elem) {
+  if (rows <= 1) return true;
+  return ld <= (((int64_t)1 << 62) / elem - cols) / (rows - 1);
+}
+
 }  // namespace dgb

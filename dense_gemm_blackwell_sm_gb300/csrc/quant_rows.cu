@@ -59,7 +59,7 @@ cudaError_t launch_quant_rows(const quant_rows_t& a, const FfnDevice& dev, cudaS
   p.cols = (int32_t)a.cols;
   p.vec = alignment_of(a.x, a.ld_x * e);
   p.x = a.x;
-  p.x_end = static_cast<const uint8_t*>(a.x) + ((a.rows - 1) * a.ld_x + a.cols) * e;
+  p.x_end = end_of_rows(a.x, a.rows, a.ld_x, a.cols, e);
   p.data = static_cast<uint8_t*>(a.data);
   p.scales = static_cast<uint8_t*>(a.scales);
   p.row_scale = a.row_scale;
@@ -77,9 +77,9 @@ cudaError_t launch_quant_norm(const quant_norm_t& a, const FfnDevice& dev, cudaS
                     alignment_of(a.s, a.ld_s * e)});
   p.x = a.y;
   p.residual = a.residual;
-  p.x_end = static_cast<const uint8_t*>(a.y) + ((a.M - 1) * a.ld_y + a.D) * e;
-  if (a.residual) p.residual_end = static_cast<const uint8_t*>(a.residual) + ((a.M - 1) * a.ld_residual + a.D) * e;
-  if (a.weight) p.weight_end = static_cast<const uint8_t*>(a.weight) + a.D * (a.param_dtype == FFN_F32 ? 4 : 2);
+  p.x_end = end_of_rows(a.y, a.M, a.ld_y, a.D, e);
+  if (a.residual) p.residual_end = end_of_rows(a.residual, a.M, a.ld_residual, a.D, e);
+  if (a.weight) p.weight_end = end_of_rows(a.weight, 1, a.D, a.D, a.param_dtype == FFN_F32 ? 4 : 2);
   p.weight = a.weight;
   p.s = a.s;
   p.data = static_cast<uint8_t*>(a.data);

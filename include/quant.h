@@ -20,8 +20,10 @@
  * overlap as long as their buffers (workspaces among them) do not.
  *
  * Arrays of elements are row-major with their own row pitch `ld_*` in elements (0
- * means dense: the row's length); elements of a row are adjacent.  Arrays named
- * "output" must not overlap any input unless a comment allows it.
+ * means dense: the row's length); elements of a row are adjacent.  Rows may have no
+ * elements, whatever their pitch: nothing of such an array is read, and it may be NULL.
+ * A pitch and a number of rows whose array would pass 2^62 bytes are refused.  Arrays
+ * named "output" must not overlap any input unless a comment allows it.
  */
 #ifndef DGB_QUANT_H
 #define DGB_QUANT_H

@@ -194,3 +194,39 @@ def test_linear_of_one_token_and_the_largest_and_smallest_values(fmt):
             x[0, 7], x[0, 8], x[0, 300] = v, -v, v
             assert torch.equal(quant.linear(x, w, out_dtype=torch.float32),
                                quant.product(quant.quantise(x, fmt), w, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("fmt", list(quant.FORMATS))
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_of_no_values_with_a_pitch(fmt, transpose, dtype):
+    # (what lies behind the address is NaN, none of it the array's)
+    x = torch.full((100, 64), float("nan"), dtype=dtype, device=DEV)
+    empty = x[:, :0]
+    a, got, _ = rows_call(empty, fmt, transpose)
+    a.ld_x = 64
+    assert a.rows == 100 and a.cols == 0
+    assert quant.load().quant_rows(ctypes.byref(a), gemm._stream_ptr(None)) == gemm.OK
+    assert quant.check() == gemm.OK
+    want = quant.quantise(torch.empty(100, 0, dtype=dtype, device=DEV), fmt, transpose=transpose)
+    assert same(got, quant.Quantised(want.data.view(torch.uint8), *want[1:]))
+    assert not got.data.any() and (transpose or got.data.shape[0] == 100)
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("M", [3, 40])
+def test_linear_of_no_values_with_a_pitch(fmt, M):
+    # (in one kernel and in two)
+    N, lib = 130, quant.load()
+    x = torch.full((M, 64), float("nan"), dtype=torch.bfloat16, device=DEV)
+    w = quant.quantise(torch.empty(N, 0, device=DEV), fmt)
+    bias, c = normal(N, seed=1, to=torch.float32), torch.full((M, N), 7.0, device=DEV)
+    a = quant.LinearArgs(M=M, N=N, K=0, dtype=ffn.BF16, format=quant.FORMATS[fmt], out_dtype=ffn.F32, x=x.data_ptr(),
+                         b=w.data.data_ptr(), scales_b=w.scales.data_ptr(),
+                         row_scale_b=w.row_scale.data_ptr() if w.row_scale is not None else None, bias=bias.data_ptr(),
+                         c=c.data_ptr(), ld_x=64)
+    work = torch.empty(max(256, lib.quant_linear_workspace(ctypes.byref(a))), dtype=torch.uint8, device=DEV)
+    a.workspace = work.data_ptr()
+    assert lib.quant_linear(ctypes.byref(a), gemm._stream_ptr(None)) == gemm.OK
+    assert quant.check() == gemm.OK
+    assert torch.equal(c, bias.expand(M, N))
