@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "fp4_common.cuh"
+#include "fp4_turns.h"
 
 namespace dgb {
 
@@ -76,11 +77,10 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
   uint64_t* empty = bars + kMostStages;      // MMA -> TMA
   uint64_t* ready = bars + 2 * kMostStages;  // scale copies -> MMA
   uint64_t* acc_full = bars + 3 * kMostStages;
-  uint64_t* acc_empty = acc_full + 1;  // the common columns are read
-  uint64_t* own_empty = acc_full + 2;  // the tile's own columns too
-  uint64_t* drain_bar = acc_full + 3;
-  uint64_t* copy_drain = acc_full + 4;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 5);
+  uint64_t* acc_empty = acc_full + 1;  // the common columns are read, and all of the tile before
+  uint64_t* drain_bar = acc_full + 2;
+  uint64_t* copy_drain = acc_full + 3;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 4);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   volatile uint32_t* zero_word = tmem_slot + 2;
   // (the stage's scales follow its operands: A's blocks, B's blocks of rows 0-127, of 128-255)
@@ -97,7 +97,6 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     }
     mbar_init(smem_u32(acc_full), 1);
     mbar_init(smem_u32(acc_empty), 16);
-    mbar_init(smem_u32(own_empty), 16);
     mbar_init(smem_u32(drain_bar), 1);
     mbar_init(smem_u32(copy_drain), 2);
     *abort_flag = 0u;
@@ -174,14 +173,14 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     // ------------------------------------------------------------------ MMA
     // the whole warp walks the loop and one lane issues (see mma_fp4)
     const uint32_t issue = elect_lane();
-    uint32_t stage = 0, sphase = 0, apar = 0, slot = 0;
+    uint32_t stage = 0, sphase = 0, n = 0, slot = 0;
     bool ok = true;
-    for (int32_t tile = cid; ok && tile < tiles; tile += clusters, apar ^= 1u) {
-      // the tile before has handed the common columns back, the one before that its own
-      if (!warp_wait<true>(smem_u32(acc_empty), apar ^ 1u, w, WAIT_MMA_ACC_EMPTY)) break;
-      if (tile >= cid + 2 * clusters && !warp_wait<true>(smem_u32(own_empty), apar, w, WAIT_MMA_ACC_EMPTY)) break;
+    for (int32_t tile = cid; ok && tile < tiles; tile += clusters, ++n) {
+      // the tile before has handed the common columns back, which no warp does before it has read the
+      // own columns of the tile before that (fp4_turns.h)
+      if (!warp_wait<true>(smem_u32(acc_empty), fp4_empty_parity(n), w, WAIT_MMA_ACC_EMPTY)) break;
       tc_fence_after();
-      const uint32_t d = tmem + (apar != 0u ? (uint32_t)kOwn : 0u);
+      const uint32_t d = tmem + (fp4_turn(n) != 0u ? (uint32_t)kOwn : 0u);
       for (int32_t kb = 0; kb < p.blocks; ++kb) {
         // (the copier saw the stage land, so this covers the operands too)
         if (!warp_wait(smem_u32(ready + stage), sphase, w, WAIT_MMA_FULL)) { ok = false; break; }
@@ -255,9 +254,10 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
     const uint32_t group = (warp - 4u) >> 2;
     uint8_t* mine = staging + (warp - 4u) * 4096u;
     const int32_t thread = (int32_t)threadIdx.x - 128;
-    uint32_t apar = 0, buffer = 0;
+    uint32_t n = 0, buffer = 0;
     bool dead = false;
-    for (int32_t tile = cid; tile < tiles; tile += clusters, apar ^= 1u) {
+    for (int32_t tile = cid; tile < tiles; tile += clusters, ++n) {
+      const uint32_t apar = fp4_turn(n);
       int32_t tm, tn;
       raster_tile(tile, p.tiles_m, p.tiles_n, p.raster_group, tm, tn);
       const int32_t row0 = tm * 256 + (int32_t)(rank * 128u + q * 32u), row = row0 + (int32_t)lane;
@@ -282,10 +282,10 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
       if (dead) continue;
       tc_fence_after();
       const uint32_t acc = tmem + ((q * 32u) << 16) + (apar != 0u ? (uint32_t)kOwn : 0u);
-      auto hand_back = [&](uint64_t* bar) {
+      auto hand_back = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(smem_u32(bar), 0));
+        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(smem_u32(acc_empty), 0));
       };
       auto store = [&](const uint32_t(&v)[32], int32_t c, const Residual32<OutT>& r) {
         fp4_store32<OutT>(p.e, &tmC, v, r, row0, col0 + c, sa, columns + c, columns + 256 + c, mine, buffer, lane);
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
         uint32_t v2[32];
         tmem_ld_32x32b_x32(acc + (uint32_t)common + 64u, v2);
         tmem_wait_ld();
-        hand_back(acc_empty);
+        hand_back();
         fetch(rb, common + 32);
         store(v0, common, ra);
         fetch(ra, common + 64);
@@ -306,11 +306,10 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
         store(v2, common + 64, ra);
         tmem_ld_32x32b_x32(acc + (uint32_t)own, v0);
         tmem_wait_ld();
-        hand_back(own_empty);
         store(v0, own, rb);
       } else {
         tmem_wait_ld();
-        hand_back(acc_empty);
+        hand_back();
         fetch(rb, common + 32);
         store(v0, common, ra);
         fetch(ra, own);
@@ -318,7 +317,6 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
         tmem_ld_32x32b_x32(acc + (uint32_t)own, v0);
         tmem_ld_32x32b_x32(acc + (uint32_t)own + 32u, v1);
         tmem_wait_ld();
-        hand_back(own_empty);
         fetch(rb, own + 32);
         store(v0, own, ra);
         store(v1, own + 32, rb);
