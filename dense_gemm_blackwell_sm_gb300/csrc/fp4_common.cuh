@@ -23,7 +23,8 @@ __device__ __forceinline__ uint32_t fp4_idesc(uint32_t idesc, int k) {
 
 // A bounded wait of a whole warp: every lane looks for the phase itself (the acquire is a
 // thread's own) and all leave together.  It calls nothing and no lane runs ahead: what the warp's
-// loop keeps in uniform registers must not live across a call that one lane makes.
+// loop keeps in uniform registers must not live across a call that one lane makes.  All of these
+// kernels' loops wait like this, those that copy among them.
 template <bool CLUSTER_ACQ = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w, uint32_t code) {
   uint64_t since = 0;

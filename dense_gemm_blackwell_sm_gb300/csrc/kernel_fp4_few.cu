@@ -325,17 +325,15 @@ __device__ __forceinline__ void few_body(const CUtensorMap& tmA, const CUtensorM
   const int32_t kb0 = (int32_t)((int64_t)p.blocks * rank / p.split);
   const int32_t nkb = (int32_t)((int64_t)p.blocks * (rank + 1) / p.split) - kb0;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // -------------------------------------------------------------- producer
-    bool skip = (p.debug_flags & QUANT_DEBUG_SKIP_ONE_LOAD) != 0;
+    // the whole warp walks the loop and one lane copies (see warp_wait)
+    const bool skip = (p.debug_flags & QUANT_DEBUG_SKIP_ONE_LOAD) != 0;
     auto features = [&](int32_t j, uint32_t s) {
       const uint32_t st = smem_u32(ring + s * STAGE), fb = smem_u32(full + s);
       mbar_arrive_expect_tx(fb, STAGE);
-      if (skip) {
-        skip = false;  // test hook: this stage's bytes never all arrive
-      } else {
-        tma_load_2d(st, &tmB, fb, (kb0 + j) * 128, tn * 128);
-      }
+      // (test hook: with skip the first stage's bytes never all arrive)
+      if (!skip || j != 0) tma_load_2d(st, &tmB, fb, (kb0 + j) * 128, tn * 128);
       tma_load_3d(st + fscales_at, &tmSB, fb, 0, (kb0 + j) * 4 * (int32_t)NB, tn);
     };
     auto token_rows = [&](int32_t j, uint32_t s) {
@@ -344,15 +342,19 @@ __device__ __forceinline__ void few_body(const CUtensorMap& tmA, const CUtensorM
       tma_load_3d(st + tscales_at, &tmSA, fb, 0, (kb0 + j) * 4 * (int32_t)NB, token0 / 128);
     };
     const int32_t first = min(nkb, (int32_t)S);
-    if (p.static_b)
+    if (p.static_b && lane == 0)
       for (int32_t j = 0; j < first; ++j) features(j, (uint32_t)j);
+    __syncwarp();
     wait_for_prior_kernel();
     let_next_kernel_start();
     for (int32_t j = 0; j < nkb; ++j) {
       const uint32_t s = (uint32_t)j % S;
-      if (j >= first && !mbar_wait(smem_u32(empty + s), ((uint32_t)j / S & 1u) ^ 1u, w, WAIT_PRODUCER_EMPTY)) break;
-      if (j >= first || !p.static_b) features(j, s);
-      if constexpr (!LINEAR) token_rows(j, s);
+      if (j >= first && !warp_wait(smem_u32(empty + s), ((uint32_t)j / S & 1u) ^ 1u, w, WAIT_PRODUCER_EMPTY)) break;
+      if (lane == 0) {
+        if (j >= first || !p.static_b) features(j, s);
+        if constexpr (!LINEAR) token_rows(j, s);
+      }
+      __syncwarp();
     }
   } else if (LINEAR && warp >= 2) {
     // ----------------------------------------------------------- the tokens

@@ -125,49 +125,37 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    if (lane == 0) {
-      uint32_t stage = 0, sphase = 0, issued = 0;
-      bool skip = (p.debug_flags & QUANT_DEBUG_SKIP_ONE_LOAD) != 0;
-      bool ok = true;
-      for (int32_t tile = cid; ok && tile < tiles; tile += clusters) {
-        int32_t tm, tn;
-        raster_tile(tile, p.tiles_m, p.tiles_n, p.raster_group, tm, tn);
-        const int32_t rb = 2 * tm + (int32_t)rank;  // this CTA's 128 rows of A
-        for (int32_t kb = 0; kb < p.blocks; ++kb) {
-          if (!mbar_wait(smem_u32(empty + stage), sphase ^ 1u, w, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
+    // the whole warp walks the loop and one lane copies (see warp_wait)
+    uint32_t stage = 0, sphase = 0;
+    bool skip = (p.debug_flags & QUANT_DEBUG_SKIP_ONE_LOAD) != 0;
+    bool ok = true;
+    for (int32_t tile = cid; ok && tile < tiles; tile += clusters) {
+      int32_t tm, tn;
+      raster_tile(tile, p.tiles_m, p.tiles_n, p.raster_group, tm, tn);
+      const int32_t rb = 2 * tm + (int32_t)rank;  // this CTA's 128 rows of A
+      for (int32_t kb = 0; kb < p.blocks; ++kb) {
+        if (!warp_wait(smem_u32(empty + stage), sphase ^ 1u, w, WAIT_PRODUCER_EMPTY)) { ok = false; break; }
+        if (lane == 0) {
           const uint32_t own = smem_u32(full + stage);
           const uint32_t fb = mapa_shared(own, 0);
           if (leader) mbar_arrive_expect_tx(own, 2u * kStage<NV>);
           const uint32_t st = smem_u32(ring + stage * kStage<NV>);
           tma_load_2d_pair(st, &tmA, fb, kb * 128, rb * 128);
-          if (skip) {
-            skip = false;  // test hook: this stage's bytes never all arrive
-          } else {
-            tma_load_2d_pair(st + kOperand, &tmB, fb, kb * 128, (2 * tn + (int32_t)rank) * 128);
-          }
+          // (test hook: with skip this stage's bytes never all arrive)
+          if (!skip) tma_load_2d_pair(st + kOperand, &tmB, fb, kb * 128, (2 * tn + (int32_t)rank) * 128);
           tma_load_3d_pair(st + kScalesAt, &tmSA, fb, 0, kb * 4 * (int32_t)NB, rb);
           tma_load_3d_pair(st + kScalesAt + 512u * NB, &tmSB, fb, 0, kb * 4 * (int32_t)NB, 2 * tn);
-          ++issued;
-          if (++stage == S) { stage = 0; sphase ^= 1u; }
         }
+        __syncwarp();
+        skip = false;
+        if (++stage == S) { stage = 0; sphase ^= 1u; }
       }
-      if (!ok) {
-        // The copies in flight must land before shared memory is released: the leader
-        // waits for its last issued stages (bounded), the other CTA, which cannot wait
-        // on the leader's barriers, for the same bound in time.
-        volatile uint32_t never = 0u;
-        const WaitCtl wd{&never, nullptr, 2000000ull, 0};
-        if (leader) {
-          const uint32_t n = issued < S ? issued : S;
-          for (uint32_t back = 1; back <= n; ++back) {
-            const uint32_t sb = (stage + S - back) % S;
-            mbar_wait(smem_u32(full + sb), back <= stage ? sphase : sphase ^ 1u, wd, 0u);
-          }
-        } else {
-          const uint64_t t0 = globaltimer_ns();
-          while (globaltimer_ns() - t0 < wd.timeout_ns) {}
-        }
-      }
+    }
+    if (!ok) {
+      // The copies in flight must land before shared memory is released: a bound in time, since the
+      // other CTA cannot wait on the leader's barriers and a stage that was skipped never fills.
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 2000000ull) {}
     }
   } else if (warp == 1 && leader) {
     // ------------------------------------------------------------------ MMA

@@ -64,7 +64,9 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
 
 // The same for a hand-off that passes no memory, such as TMEM columns read with tcgen05.ld: the
 // release is of this CTA's scope (of the cluster's it waits for the thread's stores on their way,
-// about 2000 clocks behind a tile's stores).
+// about 2000 clocks behind a tile's stores).  It orders nothing for the other CTA by itself.  What the
+// hand-off rests on is that the columns have been read when the arrival is issued: tcgen05.wait::ld
+// returns only then, and the arrival follows it in the thread.
 __device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }

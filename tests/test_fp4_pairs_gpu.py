@@ -63,3 +63,19 @@ def test_several_tiles_of_a_cluster(shape, fmt, out):
         c = quant.product(qa, qb, out_dtype=OUT[out])
         assert quant.check() == gemm.OK
         assert torch.equal(c, want), torch.nonzero(c != want)[:3]
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [96, 2080])
+def test_a_wait_that_runs_out_ends_every_role(fmt, out, K):
+    # each CTA's first copy is left out: what waits for it gives up, then what waits for that, over
+    # several tiles; the calls behind it are whole
+    M, N = 4352, 4200
+    a, b = codes(M, K, fmt, 3), codes(N, K, fmt, 4)
+    qa, qb, want = device(a), device(b), times(a, b).to(OUT[out])
+    quant.product(qa, qb, out_dtype=OUT[out], timeout_ns=20_000_000, debug_flags=quant.DEBUG_SKIP_ONE_LOAD)
+    c = quant.product(qa, qb, out_dtype=OUT[out])
+    assert quant.check() == gemm.ERR_DEVICE_TIMEOUT
+    assert torch.equal(c, want) and quant.check() == gemm.OK
+    assert torch.equal(quant.product(qa, qb, out_dtype=OUT[out]), want) and quant.check() == gemm.OK
