@@ -363,6 +363,8 @@ __device__ __forceinline__ void few_body(const CUtensorMap& tmA, const CUtensorM
     if (threadIdx.x == 64u) mbar_arrive(smem_u32(quantised));
   } else if (warp == 1) {
     // ------------------------------------------------------- scales and MMAs
+    // (no wait below begins while the kernel before still runs: its time is not theirs)
+    wait_for_prior_kernel();
     const uint32_t issue = elect_lane();
     const bool there = !LINEAR || warp_wait(smem_u32(quantised), 0, w, WAIT_MMA_FULL);
     for (int32_t j = 0; there && j < nkb; ++j) {

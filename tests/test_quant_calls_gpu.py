@@ -230,3 +230,28 @@ def test_linear_of_no_values_with_a_pitch(fmt, M):
     assert lib.quant_linear(ctypes.byref(a), gemm._stream_ptr(None)) == gemm.OK
     assert quant.check() == gemm.OK
     assert torch.equal(c, bias.expand(M, N))
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+def test_the_time_of_the_kernel_before_is_not_a_wait(fmt):
+    # behind one row that a single CTA takes milliseconds for, so that the next kernel stands beside it:
+    # half a millisecond is enough for calls of ten microseconds
+    row = normal(1, 1 << 20, seed=1).repeat(1, 96)
+    w = quant.quantise(normal(512, 1024, seed=2), fmt)
+    x = normal(4, 1024, seed=3)
+    a = quant.quantise(x, fmt)
+    many = quant.quantise(normal(2304, 1024, seed=4), fmt)  # (with w: CTA pairs)
+    calls = [lambda t: quant.product(a, w, timeout_ns=t, static_b=True), lambda t: quant.product(a, w, timeout_ns=t),
+             lambda t: quant.linear(x, w, timeout_ns=t, static_b=True), lambda t: quant.linear(x, w, timeout_ns=t),
+             lambda t: quant.product(many, many, timeout_ns=t)]
+    want = [f(0) for f in calls]
+    assert quant.check() == gemm.OK
+    for f, c in zip(calls, want):
+        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        begin.record()
+        quant.quantise(row, "e4m3")
+        got = f(500_000)
+        end.record()
+        assert quant.check() == gemm.OK
+        assert begin.elapsed_time(end) > 1.5  # (ms: the row took longer than the limit)
+        assert torch.equal(got, c)
