@@ -288,35 +288,33 @@ __global__ void __maxnreg__((kRowRegisters<T, F, NORM, NV>)) k_quant_rows(const 
 #pragma unroll
         for (int j = 0; j < 16; j += 2) fma2(sum, sum1, v[i][j], v[i][j + 1], v[i][j], v[i][j + 1]);
       }
-      auto weigh = [&]() {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int32_t c = i * threads + tx;
-          auto scale = [&](const auto& e) {
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) mul2(v[i][j], v[i][j + 1], e[j], e[j + 1]);
-          };
-          if (c >= p.chunks || p.weight == nullptr) continue;
-          if (p.weight_f32) {
-            Run<float> e;
-            load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
-            scale(e);
-          } else {
-            Run<T> e;
-            load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
-            scale(e);
-          }
-        }
-      };
-      // (the weight comes while the row's sum is found; 32-bit rows have no registers for that)
-      if (sizeof(T) == 2) weigh();
       sum = over_row<false>(sum + sum1, shared[0][turn]);
       const float unit = __frsqrt_rn(sum / (float)p.cols + p.eps);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 16; j += 2) mul2(v[i][j], v[i][j + 1], unit, unit);
-      if (sizeof(T) == 4) weigh();
+      // (the weight behind the factor: n may be a number where s weight is none.  Multiplied in first, while
+      // the row's sum is found, 16-bit rows take 41.5 us for 8192 x 4096 to MXFP8 where this takes 39.0, and
+      // 4.9 for 512 x 4096 where this takes 5.1.)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int32_t c = i * threads + tx;
+        auto scale = [&](const auto& e) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) mul2(v[i][j], v[i][j + 1], e[j], e[j + 1]);
+        };
+        if (c >= p.chunks || p.weight == nullptr) continue;
+        if (p.weight_f32) {
+          Run<float> e;
+          load16<float>(e, reinterpret_cast<const float*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
+          scale(e);
+        } else {
+          Run<T> e;
+          load16<T>(e, reinterpret_cast<const T*>(p.weight), 16 * c, p.cols, p.weight_vec, p.weight, p.weight_end);
+          scale(e);
+        }
+      }
     }
 
     RowUnit row = row_unit<F>(0.f);
