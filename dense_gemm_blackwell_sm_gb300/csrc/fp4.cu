@@ -119,25 +119,8 @@ cudaError_t launch_fp4_product(const quant_product_t& a, const FfnDevice& dev, c
   void** args = few_args;
   if (!encode_scale_blocks(&maps[2], a.scales_a, across, (uint64_t)up(a.M, 128), box_k, 1)) return cudaErrorInvalidValue;
 
-  // Tiles of 64 x 128 with a sum shared by a cluster while they are no more than SMs, or two an SM with
-  // short sums; above that CTA pairs, but for M <= 64, where most of a pair's rows would be empty.
-  // (A pair's CTAs fill their SMs: they start when the kernel before has left.)  Few and pair, us, products
-  // behind one another:
-  //   up to one an SM: MXFP4 512 x 2048 x 4096 (128 tiles) 8.8 and 10.4, 256 x 4096 x 14336 (128) 17.2 and 24.9
-  //   two an SM, K < 1024: MXFP4 at 160, 162, 180, 192, 224, 250, 256 and 304 tiles (M of 100 to 1216) and K of 64
-  //     to 992 always less, 5.6 to 8.6 and 6.1 to 10.5 (512 x 2560 x 512 6.1 and 7.1, 1024 x 2048 x 256 6.1 and 6.7,
-  //     1216 x 2048 x 736 7.5 and 7.8); NVFP4 alone within 5 % either way up to 256 tiles (7.2 and 7.2,
-  //     7.2 and 6.9) and 9 % more at 304 (7.7 and 7.2), but less where other kernels stand around: gradients
-  //     of a linear layer, with the sums over M there of this kind, MXFP4 and NVFP4, 515 x 1097 x 1032 22.0 and
-  //     25.2, 25.4 and 27.8; 520 x 1200 x 1100 24.3 and 31.5, 29.2 and 35.2; 400 x 2000 x 1032 23.8 and 25.7, 28.7
-  //     and 29.2; 900 x 1097 x 1032 25.5 and 27.5, 30.8 and 32.0
-  //   two an SM, longer sums: gradients 1100 x 1100 x 1200 28.2 and 28.5, 32.8 and 32.3; 2048 x 1100 x 1200 31.7 and
-  //     29.7, 37.5 and 36.4; 4096 x 2048 x 1024 39.5 and 37.4, 50.8 and 47.8; NVFP4 alone 512 x 4096 x 2048 10.0 and
-  //     9.4, 768 x 2048 x 4096 12.5 and 11.7 (MXFP4 alone 8.5 and 9.2, 10.9 and 11.5, from K = 8192 on more)
-  //   more: MXFP4 2048 x 1200 (320 tiles) x 256 10.7 and 6.8, x 2048 15.2 and 9.3; NVFP4 12.7 and 6.9
-  const int64_t pair_tiles = up(a.M, 256) * up(a.N, 256);
-  const int64_t few_tiles = up(a.M, 64) * up(a.N, 128);
-  if (a.M > 64 && few_tiles > (a.K < 1024 ? 2 : 1) * (int64_t)dev.num_sms) {
+  if (fp4_on_pairs(a.M, a.N, a.K, dev.num_sms)) {
+    const int64_t pair_tiles = up(a.M, 256) * up(a.N, 256);
     p.tiles_m = (int32_t)up(a.M, 256);
     p.tiles_n = (int32_t)up(a.N, 256);
     // (both operands lie in L2 at sizes where that matters: 32 rows of tiles against 8 take 8192 x
