@@ -94,6 +94,8 @@ struct Residual32 {
 // into `staging` (4096 bytes of the warp's, 1024-byte aligned) and stored from there, by a TMA
 // copy where c's rows are aligned to 16 bytes (tmC: boxes of 32 x 32, swizzled over 128 bytes for
 // fp32 and 64 for bf16), else by the lanes, each a column, so that they write neighbours.
+// A TMA store writes whole 16-byte pieces, also of a last one that C's columns end inside of; where
+// rows lie in a wider array that is somebody else's memory, so such a run of columns goes by the lanes.
 // `res`: the residuals; `scale` and `bias`: the columns' values in shared memory.  Every lane of
 // the warp calls it; `buffer` counts the warp's copies: bf16 takes the halves of the staging space
 // in turn.
@@ -114,8 +116,8 @@ __device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const CUtensor
     x[4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]) * sa, s.w, b.w);
   }
   fp4_act(x, e.act);
-  if (e.vec != 0) {
-    constexpr int per16 = 16 / (int)sizeof(OutT);
+  constexpr int per16 = 16 / (int)sizeof(OutT);
+  if (e.vec != 0 && (col + 32 <= e.N || e.N % per16 == 0)) {
     if (e.residual != nullptr && row < e.M) {
 #pragma unroll
       for (int q = 0; q < 32 / per16; ++q) {
@@ -152,6 +154,7 @@ __device__ __forceinline__ void fp4_store32(const Fp4Epilogue& e, const CUtensor
     return;
   }
   float* rows = reinterpret_cast<float*>(staging);
+  if (e.vec != 0 && lane == 0) bulk_wait_group_read<0>();  // (copies of other runs have read the space)
   __syncwarp();
 #pragma unroll
   for (uint32_t j = 0; j < 32; ++j) rows[lane * 32u + (j ^ lane)] = x[j];

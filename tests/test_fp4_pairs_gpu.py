@@ -146,6 +146,33 @@ def test_epilogue(shape, fmt, act, out, tiles_a_cluster):
     assert bad == 0, (bad, worst)
 
 
+@pytest.mark.parametrize("M,N", [(1100, 2500), (4352, 4200)])
+@pytest.mark.parametrize("fmt", FOUR)
+def test_strides_out_and_in_place(fmt, M, N, tiles_a_cluster):
+    K = 160
+    assert tiles_a_cluster(M, N, K) >= 1
+    a, b = codes(M, K, fmt, 5), codes(N, K, fmt, 6)
+    qa, qb, exact = device(a), device(b), times(a, b)
+    wide = torch.zeros(M, K // 2 + 48, dtype=torch.uint8, device=DEV)
+    wide[:, 16:16 + K // 2] = qa.data
+    qa = qa._replace(data=wide[:, 16:16 + K // 2])
+    tall = torch.zeros(N, K // 2 + 16, dtype=torch.uint8, device=DEV)
+    tall[:, :K // 2] = qb.data
+    qb = qb._replace(data=tall[:, :K // 2])
+    for dt, pad, off in ((torch.float32, 8, 0), (torch.float32, 5, 2), (torch.bfloat16, 3, 1), (torch.bfloat16, 20, 8)):
+        room = torch.full((M, N + pad), 7.0, device=DEV, dtype=dt)
+        out = room[:, off:off + N]
+        got = quant.product(qa, qb, out_dtype=dt, out=out)
+        assert got.data_ptr() == out.data_ptr()
+        assert torch.equal(out, exact.to(dt))
+        assert (room[:, :off] == 7).all() and (room[:, off + N:] == 7).all()
+        res = torch.randint(-8, 9, (M, N), generator=torch.Generator().manual_seed(1)).to(dt).to(DEV)
+        out.copy_(res)
+        quant.product(qa, qb, out_dtype=dt, out=out, residual=out)
+        assert torch.equal(out, (exact + res.double()).to(dt)) and (room[:, off + N:] == 7).all()
+        assert quant.check() == gemm.OK
+
+
 @pytest.mark.parametrize("fmt", FOUR)
 @pytest.mark.parametrize("M,N", [(1100, 2600), (4352, 4200)])
 def test_nan_and_infinity_stay_in_their_row(fmt, M, N, tiles_a_cluster):
@@ -244,3 +271,23 @@ def test_outputs_past_two_to_the_31_elements(M, N, fmt, tiles_a_cluster):
     x[:, :] = torch.where(x.abs() == 3, x * 2, x)
     c, alone = quant.linear(x, b), quant.linear(x[-rows:], tail(b, cols))
     assert quant.check() == gemm.OK and torch.equal(c[-rows:, -cols:], alone)
+
+
+@pytest.mark.parametrize("M,N", [(1100, 2500), (1100, 2501), (4352, 4203), (4352, 4254)])
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_what_lies_beside_the_output_stays(M, N, fmt, out, tiles_a_cluster):
+    # columns that end inside a 16-byte piece of a wider array whose rows are aligned
+    K, dt = 96, OUT[out]
+    assert tiles_a_cluster(M, N, K) >= 1
+    a, b = codes(M, K, fmt, 5), codes(N, K, fmt, 6)
+    qa, qb, exact = device(a), device(b), times(a, b)
+    room = torch.full((M + 1, (N + 40) // 16 * 16), 7.0, device=DEV, dtype=dt)
+    place = room[:M, 16:16 + N]
+    res = torch.randint(-8, 9, (M, N), generator=torch.Generator().manual_seed(1)).to(dt).to(DEV)
+    for residual in (None, res, place):
+        before = 0 if residual is None else residual.double()
+        quant.product(qa, qb, out_dtype=dt, out=place, residual=residual)
+        assert quant.check() == gemm.OK
+        assert torch.equal(place, (exact + before).to(dt))
+        assert (room[:, :16] == 7).all() and (room[:, 16 + N:] == 7).all() and (room[M] == 7).all()
