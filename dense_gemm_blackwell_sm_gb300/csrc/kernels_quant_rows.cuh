@@ -205,18 +205,17 @@ __device__ __forceinline__ float over_row(float v, float* shared) {
 
 // Registers a thread, for as many warps an SM as hide a row's steps behind one another: 16-bit rows of
 // one run a thread take 40 (8192 x 4096 to MXFP8 17.2 us, with 48 17.5, with 56 18.6, with 36 and spills
-// 20.6), of two 72, so that two CTAs of 448 threads fit (4096 x 14336 to MXFP8 28.5, with 77 34.3).  NVFP4's take
-// what they need: alone they gain from 72 too (26.4 and 32.0), but the gradient of a linear layer, whose
-// other kernels stand beside them, loses (4096 x 14336 x 4096 309 us, with 72 319).  A norm of 16-bit
-// rows needs 64.
-template <typename T, int F, bool NORM, int NV>
-constexpr int kRowRegisters = NV == 1 && sizeof(T) == 2 ? (NORM ? 64 : 40)
-                              : NV == 1 && !NORM        ? 64
-                              : NV == 2 && sizeof(T) == 2 && !NORM && F != QUANT_NVFP4 ? 72
+// 20.6), of two 72, so that two CTAs of 448 threads fit (4096 x 14336 to MXFP8 28.5, with 77 34.3).  NVFP4's
+// two runs need 99: WIDE are those that take what they need, for the rows that quant_rows.cu leaves
+// them.  A norm of 16-bit rows needs 64.
+template <typename T, bool NORM, int NV, bool WIDE>
+constexpr int kRowRegisters = NV == 1 && sizeof(T) == 2            ? (NORM ? 64 : 40)
+                              : NV == 1 && !NORM                   ? 64
+                              : NV == 2 && sizeof(T) == 2 && !WIDE ? 72
                                                                    : 128;
 
-template <typename T, int F, bool NORM, int NV>
-__global__ void __maxnreg__((kRowRegisters<T, F, NORM, NV>)) k_quant_rows(const QuantRowsParams p) {
+template <typename T, int F, bool NORM, int NV, bool WIDE = NV == 2 && F == QUANT_NVFP4>
+__global__ void __maxnreg__((kRowRegisters<T, NORM, NV, WIDE>)) k_quant_rows(const QuantRowsParams p) {
   constexpr bool AHEAD = NORM ? NV == 1 : NV <= 2;  // the next row's loads are under way while this one is worked on
   __shared__ float shared[2][2][16];
   wait_for_prior_kernel();
@@ -363,28 +362,31 @@ __global__ void __maxnreg__((kRowRegisters<T, F, NORM, NV>)) k_quant_rows(const 
 }
 
 template <typename T, int F, bool NORM>
-const void* rows_kernel(int nv) {
+const void* rows_kernel(int nv, bool bounded) {
   if (nv == 1) return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 1>);
-  if constexpr (!NORM)
+  if constexpr (!NORM) {
+    if constexpr (sizeof(T) == 2 && F == QUANT_NVFP4)
+      if (nv == 2 && bounded) return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 2, false>);
     if (nv == 2) return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 2>);
+  }
   return reinterpret_cast<const void*>(k_quant_rows<T, F, NORM, 4>);
 }
 
 template <typename T, bool NORM>
-const void* rows_kernel_of(int format, int nv) {
+const void* rows_kernel_of(int format, int nv, bool bounded) {
   switch (format) {
-    case QUANT_E4M3: return rows_kernel<T, QUANT_E4M3, NORM>(nv);
-    case QUANT_MXE4M3: return rows_kernel<T, QUANT_MXE4M3, NORM>(nv);
-    case QUANT_MXFP4: return rows_kernel<T, QUANT_MXFP4, NORM>(nv);
-    default: return rows_kernel<T, QUANT_NVFP4, NORM>(nv);
+    case QUANT_E4M3: return rows_kernel<T, QUANT_E4M3, NORM>(nv, bounded);
+    case QUANT_MXE4M3: return rows_kernel<T, QUANT_MXE4M3, NORM>(nv, bounded);
+    case QUANT_MXFP4: return rows_kernel<T, QUANT_MXFP4, NORM>(nv, bounded);
+    default: return rows_kernel<T, QUANT_NVFP4, NORM>(nv, bounded);
   }
 }
 
 }  // namespace
 
 // by the inputs' type (kernels_quant_rows_f16.cu and so on)
-const void* quant_rows_f16(int format, bool norm, int nv);
-const void* quant_rows_bf16(int format, bool norm, int nv);
-const void* quant_rows_f32(int format, bool norm, int nv);
+const void* quant_rows_f16(int format, bool norm, int nv, bool bounded);
+const void* quant_rows_bf16(int format, bool norm, int nv, bool bounded);
+const void* quant_rows_f32(int format, bool norm, int nv, bool bounded);
 
 }  // namespace dgb

@@ -3,8 +3,9 @@
 
 namespace dgb {
 
-const void* quant_rows_bf16(int format, bool norm, int nv) {
-  return norm ? rows_kernel_of<__nv_bfloat16, true>(format, nv) : rows_kernel_of<__nv_bfloat16, false>(format, nv);
+const void* quant_rows_bf16(int format, bool norm, int nv, bool bounded) {
+  return norm ? rows_kernel_of<__nv_bfloat16, true>(format, nv, bounded)
+              : rows_kernel_of<__nv_bfloat16, false>(format, nv, bounded);
 }
 
 }  // namespace dgb

@@ -3,8 +3,9 @@
 
 namespace dgb {
 
-const void* quant_rows_f32(int format, bool norm, int nv) {
-  return norm ? rows_kernel_of<float, true>(format, nv) : rows_kernel_of<float, false>(format, nv);
+const void* quant_rows_f32(int format, bool norm, int nv, bool bounded) {
+  return norm ? rows_kernel_of<float, true>(format, nv, bounded)
+              : rows_kernel_of<float, false>(format, nv, bounded);
 }
 
 }  // namespace dgb

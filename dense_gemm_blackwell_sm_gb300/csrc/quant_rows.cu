@@ -36,10 +36,18 @@ cudaError_t launch(QuantRowsParams& p, int32_t dtype, int32_t format, bool norm,
   while (nv < 4 && up(p.chunks, nv) > 512) nv *= norm ? 4 : 2;
   const int threads = (int)std::min<int64_t>(512, up(up(p.chunks, nv), 32) * 32);
   const int rows = std::max(1, (nv == 2 ? 128 : 256) / threads);
+  // NVFP4's two runs in 72 registers a thread or in the 99 they need: many rows of 160 to 448 threads take
+  // the 72, which let a CTA more stand on an SM (two of 448 threads and not one), free and bounded, us:
+  // 4096 x 5120 12.9 and 13.0, 8192 x 5120 23.2 and 22.3, 4096 x 6144 16.5 and 14.8, 8192 x 8192 34.7 and 33.0, 4096 x
+  // 10240 28.8 and 23.1, 4096 x 14336 33.7 and 29.6.  Others lose by it: 8192 x 4096 19.1 and 19.7 (128
+  // threads), 4096 x 15360 35.1 and 37.2 (480: one CTA either way), 1024 x 14336 10.3 and 10.5, 1024 x 8192 6.7 and
+  // 7.0, while 1500 x 10240 gains (12.3 and 10.2).  With a linear layer's gradient around them, 8192 x 10240 x
+  // 2048 289 and 268, 8192 x 12288 x 512 221 and 215, 4096 x 12288 x 4096 268 and 271, 4096 x 14336 x 4096 305 and 310.
+  const bool bounded = threads >= 160 && threads <= 448 && p.rows >= 8u * (uint32_t)num_sms;
   LaunchSpec s;
-  s.func = dtype == FFN_F32    ? quant_rows_f32(format, norm, nv)
-           : dtype == FFN_BF16 ? quant_rows_bf16(format, norm, nv)
-                               : quant_rows_f16(format, norm, nv);
+  s.func = dtype == FFN_F32    ? quant_rows_f32(format, norm, nv, bounded)
+           : dtype == FFN_BF16 ? quant_rows_bf16(format, norm, nv, bounded)
+                               : quant_rows_f16(format, norm, nv, bounded);
   int resident = 0;
   const cudaError_t e = resident_ctas(s.func, threads * rows, 0, 0, &resident);
   if (e != cudaSuccess) return e;

@@ -255,3 +255,20 @@ def test_the_time_of_the_kernel_before_is_not_a_wait(fmt):
         assert quant.check() == gemm.OK
         assert begin.elapsed_time(end) > 1.5  # (ms: the row took longer than the limit)
         assert torch.equal(got, c)
+
+
+@pytest.mark.parametrize("fmt", FOUR)
+@pytest.mark.parametrize("cols", [4096, 5120, 6200, 14336, 15000])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_many_rows_are_as_few(fmt, cols, dtype):
+    # (the rule for the registers of a row's threads goes by the rows and their width)
+    x = normal(1300, cols, seed=cols, to=dtype)
+    x[7, 100], x[1299, cols - 1], x[640] = float("nan"), float("inf"), 0
+    q = quant.quantise(x, fmt)
+    for first in (0, 640, 1280):  # (a scale block's first rows)
+        part = quant.quantise(x[first:first + 20], fmt)
+        assert torch.equal(q.data[first:first + 20], part.data)
+        if fmt == "nvfp4":
+            assert torch.equal(q.row_scale[first:first + 20].view(torch.int32), part.row_scale.view(torch.int32))
+        across = part.scales.numel() // 512
+        assert torch.equal(q.scales.view(-1, across, 32, 16)[first // 128, :, :20, :4], part.scales.view(across, 32, 16)[:, :20, :4])
