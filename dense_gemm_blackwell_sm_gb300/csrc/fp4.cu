@@ -58,7 +58,9 @@ int split_of(int64_t tiles, int32_t blocks, int num_sms) {
 // own does it once.  MXFP4 in one kernel and in two: 1 x 14336 x 4096 (8 stages) 7.8 and 8.6 us, 4
 // tokens (32) 8.3 and 8.7, 8 tokens (64) 9.9 and 8.8; 16 x 4096 x 4096 (32) 7.0 and 7.0.  NVFP4:
 // 1 x 38400 x 2048 (16) 11.0 and 12.5, 1 x 14336 x 4096 (24) 10.0 and 9.6, 1 x 4096 x 14336 (63)
-// 10.0 and 10.1, 4 x 4096 x 4096 (72) 8.2 and 7.0; the host makes one launch for two, 3 us less.
+// 10.0 and 10.1, 4 x 4096 x 4096 (72) 8.2 and 7.0; the host makes one launch for two, 3 us less.  (That
+// decides the cases beside the border: a graph's replay, which pays no launches, would take
+// 1 x 14336 x 4096 NVFP4 in two.)
 bool fp4_linear_fused(const quant_linear_t& a) {
   if (a.M > 16) return false;
   const int64_t blocks = up(width_of(a.K), 256), tiles = up(a.N, 128);

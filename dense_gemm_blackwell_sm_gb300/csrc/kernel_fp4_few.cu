@@ -9,12 +9,13 @@
 //
 // The same body takes up to 16 tokens as they are (k_fp4_linear): while the features are on their
 // way warps 2-7 quantise the CTA's part of the tokens into shared memory, where the MMAs read it.
-// One launch instead of two: 8 x 4096 x 4096 bf16 to MXFP4 7.0 -> 6.5 us on the device, and with
-// calls made one at a time 11.9 -> 6.6; 1 x 14336 x 4096 to NVFP4 12.9 -> 10.1.
+// One launch instead of two: 8 x 4096 x 4096 bf16 to MXFP4 7.0 -> 6.5 us on the device (6.2 over weights
+// in turn), and with calls made one at a time 11.9 -> 6.6; 1 x 14336 x 4096 to NVFP4 12.9 -> 9.7.
 //
-// Bound by the weights' bytes, at 4 to 4.6 TB/s: 1 x 14336 x 4096 7.2 us (MXFP4) and 8.2 (NVFP4), 16 tokens 7.7
-// and 9.0, 64 tokens 9.6 and 11.3; below that by a launch, one CTA's chain of copies and MMAs and the
-// cluster's exchange (1 x 4096 x 4096 5.1 us, 1 x 1024 x 1024 3.3).  1024 x 1024 x 4096 8.8 us.
+// Bound by the weights' bytes, at 3.6 to 3.8 TB/s: 1 x 14336 x 4096 8.2 us (MXFP4) and 9.3 (NVFP4), 16 tokens
+// 8.7 and 9.8, 64 tokens 10.5 and 11.9; below that by a launch, one CTA's chain of copies and MMAs and the
+// cluster's exchange (1 x 4096 x 4096 5.2 us, 1 x 1024 x 1024 3.1).  1024 x 1024 x 4096 8.7 us.  (Launches of
+// one graph over weights in turn, none of which L2 still holds.)
 //
 // Warp 0 is the TMA producer, warp 1 copies the scales into TMEM and issues the MMAs, and all
 // eight warps then add, scale and store.

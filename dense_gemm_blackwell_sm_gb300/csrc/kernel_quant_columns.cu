@@ -11,9 +11,10 @@
 //
 // Bound by memory: 2 bytes read per element, 0.53 to 1.03 written.  14336 x 4096 bf16: to MXFP8
 // 32.8 us (5.4 TB/s), MXFP4 28.9; with a scale per column (read twice) 53, and 515 x 1097 9 where
-// one kernel takes 6.  8192 x 4096 fp32 33 to 35, with a scale per column 57 to 61.  (Persistent CTAs that copy the next tile while they work on one gain nothing.)  Held whole in the shared memory of a cluster, so that they are read once, columns take
-// longer: loads, the exchange of the magnitudes and the codes then follow one another (14336 x 4096
-// 66 to 77 us).
+// one kernel takes 6.  8192 x 4096 fp32 33 to 35, with a scale per column 57 to 61.  (Persistent CTAs
+// that copy the next tile while they work on one gain nothing.)  Held whole in the shared memory of a
+// cluster, so that they are read once, columns take longer: loads, the exchange of the magnitudes and
+// the codes then follow one another (14336 x 4096 66 to 77 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -55,7 +56,8 @@ struct QuantColumnsParams {
 };
 
 // the task of this CTA, and its CTA there
-__device__ __forceinline__ const QuantColumnsTask& task_of(const QuantColumnsParams& q, const uint32_t* first, uint32_t& cta) {
+__device__ __forceinline__ const QuantColumnsTask& task_of(const QuantColumnsParams& q, const uint32_t* first,
+                                                           uint32_t& cta) {
   int t = 0;
 #pragma unroll
   for (int i = 1; i < kTasks; ++i) t += blockIdx.x >= first[i] ? 1 : 0;

@@ -16,9 +16,10 @@
 // predicate lets an instruction go (8192^3: 176 us).
 //
 // Bound by the tensor pipe and, with all SMs at it, by the operands' way from L2: a stage (38 KB an SM
-// with a scale per 16, 35 with one per 32) takes 590 cycles where its MMAs take 512, a tile's start 1000 more.  8192^3 MXFP4 155 us (7.1 PFLOP/s), NVFP4
-// 164 (6.7); 8192 x 14336 x 4096 143 and 151 (6.7, 6.4), with fp32 C 190; 4096^3 29 and 30 (4.6: 256 tiles
-// are 3.4 rounds of the pairs).
+// with a scale per 16, 35 with one per 32) takes 590 cycles where its MMAs take 512, a tile's start
+// 1000 more.  8192^3 MXFP4 150 us (7.3 PFLOP/s), NVFP4 160 (6.9); 8192 x 14336 x 4096 138 and 147 (7.0, 6.5),
+// with fp32 C 180 and 187, with a bf16 residual 209 and 212, rows off 16-byte boundaries 230 and 239;
+// 4096^3 29 and 30 (4.6: 256 tiles are 3.4 rounds of the pairs).
 //
 // Every cluster takes the tiles cid, cid + clusters, ...: results depend on the sizes alone.
 // Every wait is bounded (ptx.cuh); programmatic launches as in ffn_common.cuh.
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
       const int32_t common = (apar != 0u ? 0 : kOwn) + 96 * (int32_t)group;
       const int32_t own = (apar != 0u ? 256 - kOwn : 0) + 32 * (int32_t)group;
       // Residuals come a run ahead, the tile's first ones while its sums are made (8192 x 14336 x
-      // 4096 NVFP4 takes 214 us with them, 232 where they are read when they are added, 151 without).
+      // 4096 NVFP4 takes 212 us with them, 147 without; read when they are added, 18 us more).
       Residual32<OutT> ra, rb;
       auto fetch = [&](Residual32<OutT>& r, int32_t c) { r.load(p.e, row, col0 + c); };
       fetch(ra, common);

@@ -11,10 +11,11 @@
 // norm) are read twice.
 //
 // Bound by memory: 2 bytes read and 0.53 to 1.03 written per element (norm: 4 and 2 more).  8192 x
-// 4096 bf16: to E4M3 18.7 us, MXFP8 17.2 (5.9 TB/s), MXFP4 15.4, NVFP4 18.0; 8192 x 8192 31.6, 32.3 (6.3
-// TB/s), 28.6 and 33.1; the norm of 8192 x 4096 to all of them 41 (5.7 TB/s to MXFP8).  fp32: 25 to 26 us (6.2 to 6.5 TB/s);
-// the norm 63 to 68.  Rows of 4095 columns, off 16-byte boundaries, 22 to 28.  One row of 4096: 1.5 and
-// 2.6 us, a launch and a row's latency.
+// 4096 bf16: to E4M3 19.9 us, MXFP8 18.2 (5.6 TB/s), MXFP4 16.8, NVFP4 19.2; 8192 x 8192 33.7, 33.7 (6.0
+// TB/s), 30.4 and 33.3; 4096 x 14336 29.1, 30.3, 26.5 and 29.6; the norm of 8192 x 4096 41.9, 39.3 (6.0 TB/s),
+// 39.0 and 44.0.  fp32: 26 to 27.5 us (6.0 to 6.2 TB/s); the norm 64 to 70.  Rows of 4095 columns, off 16-byte
+// boundaries, 24 to 30.  One row of 4096: 1.5 and 2.3 to 2.6 us, a launch and a row's latency.  (Launches
+// of one graph over inputs in turn.)
 #pragma once
 
 #include <type_traits>
@@ -354,7 +355,8 @@ __global__ void __maxnreg__((kRowRegisters<T, NORM, NV, WIDE>)) k_quant_rows(con
             *reinterpret_cast<uint32_t*>(p.scales + scale_offset(r, c * 16 / kBlock<F>, p.blocks)) = word;
         }
         if (live && c < p.chunks)
-          store_codes<F, sizeof(T) == 4 && !NORM>(p.data + (uint64_t)r * p.ld_data + (uint32_t)c * (kFourBit<F> ? 8u : 16u), v[i], row, b);
+          store_codes<F, sizeof(T) == 4 && !NORM>(
+              p.data + (uint64_t)r * p.ld_data + (uint32_t)c * (kFourBit<F> ? 8u : 16u), v[i], row, b);
       }
     }
     if (AHEAD && !NORM && p.chunks > per) load(r + step, 0);

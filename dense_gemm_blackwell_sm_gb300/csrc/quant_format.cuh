@@ -157,7 +157,9 @@ __device__ __forceinline__ void quotient2(float& v, float& w, float s, float r) 
   w = __uint_as_float(__float_as_uint(q1) | sw);
 }
 
-// EXACT: for 32-bit inputs, whose quotients may lie nearer to a tie than a reciprocal is exact.
+// EXACT: for 32-bit inputs, whose quotients may lie nearer to a tie than a reciprocal is exact.  (Not for
+// what follows a norm, which is 32 bits wide too: its own rounding errors are as large as the
+// reciprocals', 2^-22.)
 template <int F, bool EXACT>
 __device__ __forceinline__ BlockUnit block_unit(float most, const RowUnit& row) {
   BlockUnit b{0u, row.inv, 1.f};

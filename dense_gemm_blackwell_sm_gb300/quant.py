@@ -10,7 +10,8 @@ marshalling and output allocation only).
 Formats: "e4m3" (a float32 scale per row), "mxe4m3" (E4M3, a power of two per 32 elements),
 "mxfp4" (E2M1, a power of two per 32) and "nvfp4" (E2M1, an E4M3 scale per 16 and a power of
 two per row); include/quant.h defines them.  The products of the 8-bit ones are gemm.Plan's:
-run_epilogue with scale_a and scale_b, and run_mx.
+run_epilogue with scale_a and scale_b, and run_mx.  Rows are kept with their padding, so such a
+plan is made for K = quant.width(columns).
 
 Tensors are CUDA tensors whose rows are dense (last stride 1; the row pitch is free).  Work is
 enqueued on ``stream`` (default: the current stream) of the tensors' device.  As in ``gemm``
@@ -167,8 +168,8 @@ def product(a, b, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=N
 def linear(x, w, *, out_dtype=torch.bfloat16, bias=None, act="none", residual=None, out=None, static_b=False,
            stream=None, timeout_ns=0, debug_flags=0):
     """product(quantise(x, w.format), w, ...) for x (M, K) and a 4-bit weight w (N rows); up to 16
-    tokens go in one kernel where that is as fast or faster.  ``out`` must not share memory with
-    x."""
+    tokens go in one kernel where that is as fast or faster with the launch it saves counted in.
+    ``out`` must not share memory with x."""
     return (_calls or load_calls()).linear(x, *_values(w, "w"), _out_code(out_dtype), bias,
                                            _code(ACTIVATIONS, act, "act"), residual, out, static_b, stream,
                                            timeout_ns, debug_flags)
@@ -179,7 +180,12 @@ def linear_backward(dy, x, w, *, format, need_dx=True, need_dw=True, out_dtype=t
     """(dx, dw) of y = x @ w.T for dy (M, N), x (M, K) and w (N, K), both products with 4-bit
     operands quantised along the sum: dx = Q(dy) Q(w^T)^T and dw = Q(dy^T) Q(x^T)^T.  The
     roundings are passed by: these are the gradients of the product of the unrounded values,
-    made of rounded ones.  Either is None when not needed, and then its operand may be."""
+    made of rounded ones.  Either is None when not needed, and then its operand may be.
+
+    It is the product's gradient alone: dy is what reaches x @ w.T.  Of ``linear``'s other parts the
+    bias's gradient is dy's sum over the rows and the residual's is dy itself; with an activation
+    dy has to have been multiplied by its derivative, for which a training step keeps what the
+    activation is applied to (linear without ``act``, then the activation)."""
     return (_calls or load_calls()).linear_backward(dy, x, w, format, need_dx, need_dw, _out_code(out_dtype), stream,
                                                     timeout_ns)
 

@@ -180,3 +180,23 @@ def test_a_block_in_a_graph(M):
     for pair in first + second:
         assert all(torch.equal(a, b) for a, b in zip(pair, want))
     assert quant.check() == gemm.OK
+
+
+@pytest.mark.parametrize("D", [1001, 97, 33])
+@pytest.mark.parametrize("fmt", ["e4m3", "mxe4m3"])
+def test_ragged_eight_bit_operands_into_gemm(fmt, D):
+    # rows are kept with their padding: the plan's K is their width
+    M, N, K = 130, 264, quant.width(D)
+    assert K == -(-D // 32) * 32
+    x, w = normal(M, D, seed=1), normal(N, D, seed=2, std=D ** -0.5)
+    a, b = quant.quantise(x, fmt), quant.quantise(w, fmt)
+    assert a.data.shape == (M, K) and a.cols == D
+    c = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    plan = gemm.Plan(M, N, K, gemm.dtype_code(fmt, "bf16"))
+    if fmt == "e4m3":
+        plan.run_epilogue(a.data, b.data, c, scale_a=a.row_scale, scale_b=b.row_scale)
+    else:
+        plan.run_mx(a.data, b.data, c, a.scales, b.scales)
+    assert plan.check() == gemm.OK
+    bad, worst = bounds.outside(f64(c), ref.product(ref.quantise(f64(x), fmt), ref.quantise(f64(w), fmt), "bf16"))
+    assert bad == 0, (bad, worst)
